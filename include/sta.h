@@ -1,8 +1,10 @@
 /*
  * sta.h -- C ABI of libsta: masked multi-head attention over a two-level
  * (BSR + bitmap) mask, split-KV decode (GQA over packed or paged KV, and
- * against a shared latent KV cache) with a log-sum-exp merge, and the fused
- * operators that follow the attention, for NVIDIA GB300 (sm_103a).
+ * against a shared latent KV cache) with a log-sum-exp merge, the fused
+ * operators that follow the attention, and serving over a paged KV cache
+ * (rotary positions, the write of new tokens, the attention of chunks of new
+ * tokens, page bookkeeping), for NVIDIA GB300 (sm_103a).
  *
  * Sources of the operations:
  *  - "Accelerating Sparse Transformer Inference on GPU" (STOF):
@@ -442,6 +444,176 @@ sta_status sta_decode_splitkv_noalloc(const void* q, const void* k, const void* 
  *   Asynchronous on `stream`. */
 sta_status sta_merge_lse(const float* part_o, const float* part_lse, int n_rows, int s, int d, void* o,
                          sta_dtype o_dtype, float* lse, sta_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* Serving over a paged KV cache                                             */
+/* ------------------------------------------------------------------------ */
+/* The cache is that of sta_decode_splitkv_paged: k_pages, v_pages [n_pages,
+ * page_size, Hkv, d], and per request a list of pages (page_indptr [n_req+1],
+ * page_indices). A list may have room for more entries than its request uses:
+ * a request of n tokens HOLDS the first ceil(n / page_size) entries of its list.
+ * New tokens of a step are packed: request r owns rows q_indptr[r] ..
+ * q_indptr[r+1]-1, and they are the LAST tokens of its sequence, whose length
+ * kv_indptr[r+1] - kv_indptr[r] counts them: row q_indptr[r] + i has position
+ * length - (number of new tokens) + i. Rows at or past q_indptr[n_req] (a padded
+ * batch) are neither read nor written. (The pages have no counterpart for these
+ * calls: they are what a serving step needs around the paged decode.) */
+
+/* Which elements of a head form pair p of the rot_dim / 2 pairs that turn. */
+#define STA_ROPE_HALF 0        /* p and p + rot_dim / 2 */
+#define STA_ROPE_INTERLEAVED 1 /* 2 p and 2 p + 1       */
+/* How the turning speeds are scaled for contexts longer than the trained one. */
+#define STA_ROPE_SCALE_NONE 0
+#define STA_ROPE_SCALE_LINEAR 1 /* f / factor */
+#define STA_ROPE_SCALE_BLEND 2  /* g f + (1 - g) f / factor, g = clamp((orig_len f / 2 pi -      */
+                                /* low_turns) / (high_turns - low_turns), 0, 1): pairs that turn */
+                                /* often within orig_len tokens keep their speed                 */
+typedef struct {
+  int32_t rot_dim;  /* leading elements of each head that turn: even, 2 .. d; the rest is copied */
+  int32_t layout;   /* STA_ROPE_HALF / STA_ROPE_INTERLEAVED                                      */
+  int32_t scaling;  /* STA_ROPE_SCALE_*                                                          */
+  float mscale;     /* > 0: factor on cosine and sine (1 for a pure rotation)                    */
+  double base;      /* > 1: pair p turns by f_p = base^(-2 p / rot_dim) radians a token          */
+  double factor;    /* > 0, for LINEAR and BLEND                                                 */
+  double orig_len, low_turns, high_turns; /* for BLEND; high_turns > low_turns                   */
+  const double* freqs; /* host [rot_dim / 2] or NULL: radians a token of each pair, used as they */
+                       /* are (base and scaling are then ignored)                                */
+} sta_rope_params;
+
+/* sta_rope -- rotary positions: element pair (a, b) of pair p at position t becomes
+ *   (a cos - b sin, a sin + b cos) * mscale,  angle t f_p,
+ * or with transpose != 0 the transposed turn (a cos + b sin, b cos - a sin) * mscale,
+ * which takes the gradient of the result to the gradient of the input. The angle is
+ * reduced exactly at any int32 position; arithmetic in fp32, one rounding to dtype.
+ *
+ *   x, y       [n_tokens, H, d] dtype (device), x_stride / y_stride >= H d elements
+ *              between tokens, heads d apart. y may be x (equal strides); other
+ *              overlap is not allowed. y's elements between tokens are not touched.
+ *   positions  int32 [n_tokens] (device), any values
+ *   d          2 .. 512; H 1 .. 65536; dtype STA_BF16 or STA_F32; transpose 0 or 1
+ * Any d, rot_dim and stride is taken; 16-byte vectors are used when x, y, the
+ * strides, d and rot_dim (HALF: rot_dim / 2) are whole multiples of 16 bytes.
+ * n_tokens == 0 launches nothing. One launch, asynchronous on `stream`. */
+sta_status sta_rope(const void* x, void* y, const int32_t* positions_dev, const sta_rope_params* rope,
+                    int64_t n_tokens, int H, int d, int64_t x_stride, int64_t y_stride, int transpose,
+                    sta_dtype dtype, sta_stream stream);
+
+/* sta_rope_append_paged -- turns the queries and keys of a step's new tokens and
+ * writes the keys and values to their places in the paged cache.
+ *
+ *   q, k, v    [n_tokens, Hq | Hkv | Hkv, d] bf16 (device), q_stride / k_stride /
+ *              v_stride elements between tokens (views of one packed projection
+ *              output will do). Hq == 0 with q == q_out == NULL: keys and values only
+ *   q_out      [n_tokens, Hq, d] bf16 (device, written; may be q when q_stride ==
+ *              Hq d, and must not overlap k or v)
+ *   positions  int32 [n_tokens] (device) for the rotation, or NULL: each token's
+ *              position in its sequence. The place in the cache is always the latter
+ *   rope       NULL: nothing turns (q is copied to q_out)
+ *   n_tokens   rows of q, k, v: at least q_indptr[n_req]; the rest is padding
+ * A token that its (shorter) sequence does not reach, and one whose page the list
+ * does not have (0x604 in the device error word) or whose page number is outside
+ * [0, n_pages) (0x110), is not written to the cache. Two requests that write to one
+ * shared page slot race: fork first (sta_pages_fork gives each its own last page).
+ * d 2 .. 512; dtype STA_BF16 (else STA_ERR_UNSUPPORTED). One launch, asynchronous on
+ * `stream`. */
+sta_status sta_rope_append_paged(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                                 int64_t v_stride, void* q_out, void* k_pages, void* v_pages, int page_size,
+                                 int n_pages, const int32_t* page_indptr_dev, const int32_t* page_indices_dev,
+                                 const int32_t* q_indptr_dev, const int32_t* kv_indptr_dev,
+                                 const int32_t* positions_dev, const sta_rope_params* rope, int64_t n_tokens, int n_req,
+                                 int Hq, int Hkv, int d, sta_dtype dtype, sta_stream stream);
+
+/* sta_chunk_fwd_paged -- attention of each request's new tokens (one, a few, or a
+ * whole prompt) over its sequence in the paged cache, whose last tokens they are:
+ * O = softmax(Q K^T * scale + mask) V and its LSE. GQA as in the decode: query head h
+ * reads kv head h / (Hq / Hkv).
+ *
+ *   q          [N, Hq, d] bf16 (device), q_stride elements between tokens (0: Hq d;
+ *              a multiple of 8), N = q_indptr_host[n_req]
+ *   q_indptr, kv_indptr  int32 [n_req+1], device and host copies, non-decreasing from
+ *              0. The host copies size the launch; the kernels go by the device's. A
+ *              captured call may be replayed with other kv lengths, pages and fewer new
+ *              tokens a request; more new tokens than the host copy had are not
+ *              computed (0x606 in the device error word)
+ *   page_indptr / page_indices  as for sta_decode_splitkv_paged; a page number outside
+ *              [0, n_pages), or a list shorter than its sequence, reads page 0 and sets
+ *              the device error word to 0x110
+ *   pattern    NULL: causal; else a STA_MASK_PATTERN source (host) over positions:
+ *              token at position i sees key j when (!causal || j <= i) && ((win_lo <=
+ *              j - i && j - i <= win_hi) || j < n_global_cols). A token that sees no key
+ *              gets O = 0, LSE = -inf
+ *   Hq % Hkv == 0, Hq / Hkv <= 128, d 64 or 128, dtype STA_BF16, scale > 0, any
+ *   page_size >= 1, n_pages * page_size < 2^31
+ *   num_splits 0: the library cuts long sequences into chunks where that balances the
+ *              work; 1..1024: every sequence is cut into that many; merged by LSE
+ *   o          [N, Hq, d] bf16 (device, written); lse [N, Hq] f32 (device, written; may
+ *              be NULL)
+ *   workspace  device scratch for the chunks' partials, 256-byte aligned; NULL sets
+ *              *workspace_bytes and returns
+ * Keys and values of a sequence's tokens must be finite; what pages hold behind the
+ * sequence is never used. Asynchronous on `stream`. */
+sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages, int page_size,
+                               int n_pages, const int32_t* page_indptr_dev, const int32_t* page_indices_dev,
+                               const int32_t* q_indptr_dev, const int32_t* q_indptr_host, const int32_t* kv_indptr_dev,
+                               const int32_t* kv_indptr_host, int n_req, int Hq, int Hkv, int d, sta_dtype dtype,
+                               float scale, const sta_mask_src* pattern, int num_splits, void* o, float* lse,
+                               void* workspace, size_t* workspace_bytes, sta_stream stream);
+
+/* Page bookkeeping on the device. ref is int32 [n_pages] (device): how many lists hold
+ * each page, 0 for a free one; page_indptr, page_indices and kv_indptr (the sequences'
+ * lengths) as above, all on the device. Buffers (K and V of every layer, say) are a
+ * host array of device pointers, each [n_pages] pages of page_bytes (a multiple of 16,
+ * pointers 16-byte aligned); n_bufs may be 0 where only the lists change. Free pages are
+ * taken lowest number first, in the order of the requests or forks. status (int32 [2],
+ * device) may be NULL. Codes in the device error word: 0x601 a page number outside
+ * [0, n_pages), 0x602 a request number outside [0, n_req) (or a parent that is its own
+ * child), 0x603 a free page freed, 0x604 a list too short, 0x605 a child that holds pages
+ * or is named twice; the entry, fork or request concerned is then left as it was. All are
+ * asynchronous on `stream` and synchronise nothing; workspace (256-byte aligned) follows
+ * the usual protocol: NULL sets *workspace_bytes and returns. n_pages <= 2^30. */
+
+/* sta_pages_copy -- page src[i] onto page dst[i] of every buffer, i < n (src, dst int32
+ * [n], device; a negative number: no copy). Pages of dst must be distinct and none of
+ * them may be a page of src (but src[i] == dst[i] is left alone): pairs are copied in no
+ * particular order. */
+sta_status sta_pages_copy(void* const* bufs_host, int n_bufs, size_t page_bytes, int n_pages, const int32_t* src_dev,
+                          const int32_t* dst_dev, int n, sta_stream stream);
+
+/* sta_pages_grow -- gives each request the free pages that it needs to go from the lengths
+ * of kv_indptr to those of new_kv_indptr (a shorter new length gives and takes nothing).
+ * status: {pages taken, pages that were wanted but not there}; an entry without a page is
+ * -1. A request whose list has no room for the new length gets nothing (0x604). */
+sta_status sta_pages_grow(int32_t* ref_dev, int n_pages, const int32_t* page_indptr_dev, int32_t* page_indices_dev,
+                          const int32_t* kv_indptr_dev, const int32_t* new_kv_indptr_dev, int n_req, int page_size,
+                          int32_t* status_dev, void* workspace, size_t* workspace_bytes, sta_stream stream);
+
+/* sta_pages_fork -- request child[i] becomes a copy of request parent[i], i < n_forks <=
+ * n_req (int32, device): whole pages are shared (one more holder each), and a last, partly
+ * filled page is copied, in every buffer, onto a free page of the child's own, so that
+ * both can grow. A parent may be forked many times; a child must hold nothing (length 0 in
+ * kv_indptr), and of two forks onto one child the first counts. The caller gives the child
+ * its parent's length in the next kv_indptr. status: {pages taken, pages that were wanted
+ * but not there}; a child without its last page has -1 there. */
+sta_status sta_pages_fork(void* const* bufs_host, int n_bufs, size_t page_bytes, int32_t* ref_dev, int n_pages,
+                          const int32_t* page_indptr_dev, int32_t* page_indices_dev, const int32_t* kv_indptr_dev,
+                          int n_req, int page_size, const int32_t* parent_dev, const int32_t* child_dev, int n_forks,
+                          int32_t* status_dev, void* workspace, size_t* workspace_bytes, sta_stream stream);
+
+/* sta_pages_free -- the requests reqs[0 .. n) (int32, device) let go of the pages they
+ * hold: each page loses a holder, their held entries become -1. A request named twice is
+ * freed once. */
+sta_status sta_pages_free(int32_t* ref_dev, int n_pages, const int32_t* page_indptr_dev, int32_t* page_indices_dev,
+                          const int32_t* kv_indptr_dev, int n_req, int page_size, const int32_t* reqs_dev, int n,
+                          sta_stream stream);
+
+/* sta_pages_compact -- with U pages in use, moves those numbered U or more onto the free
+ * pages below U (both ascending): page data in every buffer, ref, and the held list
+ * entries of every request. page_map (int32 [n_pages], device, written): each used page's
+ * new number, -1 for a free one, for lists kept elsewhere. status: {U, pages moved}. */
+sta_status sta_pages_compact(void* const* bufs_host, int n_bufs, size_t page_bytes, int32_t* ref_dev, int n_pages,
+                             const int32_t* page_indptr_dev, int32_t* page_indices_dev, const int32_t* kv_indptr_dev,
+                             int n_req, int page_size, int32_t* page_map_dev, int32_t* status_dev, void* workspace,
+                             size_t* workspace_bytes, sta_stream stream);
 
 /* Static string describing a status code. */
 const char* sta_status_string(sta_status status);

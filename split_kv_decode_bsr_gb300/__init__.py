@@ -14,6 +14,9 @@ Operations (sources):
   * ``sta_decode_splitkv`` / ``sta_merge_lse`` -- Cleave's Split operator on the KV
     reduction of GQA decode with a log-sum-exp merge ("Cleave: Scaling Tensor
     Program Optimization ...", Split演算子によるSplit-Kの対応).
+  * ``sta_rope``, ``sta_rope_append_paged``, ``sta_chunk_fwd_paged``, ``sta_pages_*`` --
+    serving over the paged KV cache of the paged decode: rotary positions, the write of new
+    tokens, the attention of chunks of new tokens, and the bookkeeping of pages.
 """
 
 from __future__ import annotations
@@ -35,12 +38,16 @@ STA_BF16, STA_F32 = 0, 1
 STA_MASK_PATTERN, STA_MASK_DENSE_U8, STA_MASK_DENSE_BITS = 0, 1, 2
 STA_KERNEL_AUTO, STA_KERNEL_BLOCK, STA_KERNEL_ROW, STA_KERNEL_MIXED = 0, 1, 2, 3
 STA_O_BHLD, STA_O_BLHD = 0, 1
+STA_ROPE_HALF, STA_ROPE_INTERLEAVED = 0, 1
+STA_ROPE_SCALE_NONE, STA_ROPE_SCALE_LINEAR, STA_ROPE_SCALE_BLEND = 0, 1, 2
 _KERNELS = {"auto": STA_KERNEL_AUTO, "block": STA_KERNEL_BLOCK, "row": STA_KERNEL_ROW}
 
 EXPORTED = ("sta_encode_mask", "sta_tile_lists_bytes", "sta_mha_fwd", "sta_mha_fwd_splitkv", "sta_mha_fwd_layout",
             "sta_bias_residual_layernorm", "sta_validate_mask", "sta_mla_decode", "sta_mha_select_kernel", "sta_decode_splitkv",
             "sta_decode_splitkv_noalloc", "sta_decode_splitkv_paged", "sta_merge_lse", "sta_status_string", "sta_device_error",
-            "sta_check_bounded_wait", "sta_last_cuda_error", "sta_last_cuda_error_string")
+            "sta_check_bounded_wait", "sta_last_cuda_error", "sta_last_cuda_error_string", "sta_rope",
+            "sta_rope_append_paged", "sta_chunk_fwd_paged", "sta_pages_copy", "sta_pages_grow", "sta_pages_fork",
+            "sta_pages_free", "sta_pages_compact")
 
 BIG = 1 << 40
 
@@ -66,6 +73,12 @@ class _BsrMask(C.Structure):
                 ("part_row_ptr", C.c_void_p), ("part_col_idx", C.c_void_p), ("part_bitmap", C.c_void_p),
                 ("n_full", C.c_int64), ("n_part", C.c_int64), ("n_valid", C.c_int64),
                 ("head_tiles", C.c_void_p), ("tile_lists", C.c_void_p), ("head_valid", C.c_void_p)]
+
+
+class _RopeParams(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("layout", C.c_int32), ("scaling", C.c_int32), ("mscale", C.c_float),
+                ("base", C.c_double), ("factor", C.c_double), ("orig_len", C.c_double), ("low_turns", C.c_double),
+                ("high_turns", C.c_double), ("freqs", C.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -98,6 +111,17 @@ def lib():
                                                    P, P, P, sz, P]
             h.sta_decode_splitkv_noalloc.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i32, f32, i32, P, P, P]
             h.sta_merge_lse.argtypes = [P, P, i32, i32, i32, P, i32, P, P]
+            i64, R = C.c_int64, C.POINTER(_RopeParams)
+            h.sta_rope.argtypes = [P, P, P, R, i64, i32, i32, i64, i64, i32, i32, P]
+            h.sta_rope_append_paged.argtypes = [P, P, P, i64, i64, i64, P, P, P, i32, i32, P, P, P, P, P, R, i64, i32,
+                                                i32, i32, i32, i32, P]
+            h.sta_chunk_fwd_paged.argtypes = [P, i64, P, P, i32, i32, P, P, P, P, P, P, i32, i32, i32, i32, i32, f32,
+                                              C.POINTER(_MaskSrc), i32, P, P, P, sz, P]
+            h.sta_pages_copy.argtypes = [P, i32, C.c_size_t, i32, P, P, i32, P]
+            h.sta_pages_grow.argtypes = [P, i32, P, P, P, P, i32, i32, P, P, sz, P]
+            h.sta_pages_fork.argtypes = [P, i32, C.c_size_t, P, i32, P, P, P, i32, i32, P, P, i32, P, P, sz, P]
+            h.sta_pages_free.argtypes = [P, i32, P, P, P, i32, i32, P, i32, P]
+            h.sta_pages_compact.argtypes = [P, i32, C.c_size_t, P, i32, P, P, P, i32, i32, P, P, P, sz, P]
             h.sta_status_string.argtypes = [i32]
             h.sta_status_string.restype = C.c_char_p
             h.sta_device_error.argtypes = [C.POINTER(C.c_int), i32]
@@ -577,6 +601,334 @@ def sta_merge_lse(part_o: torch.Tensor, part_lse: torch.Tensor, o_dtype=torch.bf
     _check("sta_merge_lse", lib().sta_merge_lse(_ptr(part_o.contiguous()), _ptr(part_lse.contiguous()), n_rows, s, d,
                                                 _ptr(o), _dtype_code(o.dtype), _ptr(lse), _stream(stream)))
     return o, lse
+
+
+# ---------------------------------------------------------------------------
+# serving over a paged KV cache
+
+
+def _need(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _place(dev: torch.device, *tensors):
+    """Every tensor given (None allowed) lies on CUDA device `dev`."""
+    _need(dev.type == "cuda", f"tensors must be on a CUDA device, not {dev}")
+    for t in tensors:
+        _need(t is None or t.device == dev, "tensors on different devices")
+
+
+def _i32(dev: torch.device, **tensors):
+    """The named index tensors: contiguous int32 on `dev`."""
+    for name, t in tensors.items():
+        _need(t.dtype == torch.int32 and t.is_contiguous() and t.device == dev, f"{name}: contiguous int32 on {dev}")
+
+
+class _Launch:
+    """The device a call launches on, made current, and its stream, made torch's current one so that
+    what the call allocates belongs to that stream."""
+
+    def __init__(self, dev: torch.device, stream):
+        cur = torch.cuda.current_device()
+        self._outer = [torch.cuda.device(dev)] if dev.index is not None and dev.index != cur else []
+        self._stream, self._dev = stream, dev
+
+    def __enter__(self):
+        for c in self._outer:
+            c.__enter__()
+        s = self._stream
+        if s is None:
+            return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+        if not isinstance(s, torch.cuda.Stream):
+            s = torch.cuda.ExternalStream(int(s), device=self._dev) if int(s) else torch.cuda.default_stream(self._dev)
+        c = torch.cuda.stream(s)
+        c.__enter__()
+        self._outer.append(c)
+        return C.c_void_p(s.cuda_stream)
+
+    def __exit__(self, *exc):
+        for c in reversed(self._outer):
+            c.__exit__(*exc)
+        return False
+
+
+def _workspace(need: int, workspace: Optional[torch.Tensor], dev: torch.device) -> torch.Tensor:
+    """The caller's scratch when it is large enough, else one of `need` bytes."""
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    _need(workspace.dtype == torch.uint8 and workspace.is_contiguous() and workspace.device == dev,
+          f"workspace: contiguous uint8 on {dev}")
+    _need(workspace.numel() >= need, f"workspace: {need} bytes needed, {workspace.numel()} given")
+    return workspace
+
+
+def _host_i32(x, n: int, what: str):
+    """Host int32 values as a pointer, and what keeps them alive."""
+    import numpy as np
+
+    a = np.ascontiguousarray(x.numpy() if isinstance(x, torch.Tensor) else x, dtype=np.int32)
+    _need(a.shape == (n,), f"{what}: {n} values")
+    return C.c_void_p(a.ctypes.data), a
+
+
+class Rope:
+    """Rotary positions of a model's heads (sta_rope_params).
+
+    The leading rot_dim elements of each head turn, in pairs (p, p + rot_dim / 2) or, interleaved,
+    (2p, 2p + 1), pair p by base^(-2p / rot_dim) radians a token. scaling "linear" divides the
+    speeds by factor; "blend" does so only for pairs that turn less than low_turns times within
+    orig_len tokens, and by a blend up to high_turns. mscale multiplies cosine and sine. freqs:
+    rot_dim / 2 speeds in radians a token, in place of base and scaling.
+    """
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, orig_len: float = 0.0, low_turns: float = 1.0, high_turns: float = 32.0,
+                 mscale: float = 1.0, freqs: Optional[Sequence[float]] = None):
+        kinds = {"none": STA_ROPE_SCALE_NONE, "linear": STA_ROPE_SCALE_LINEAR, "blend": STA_ROPE_SCALE_BLEND}
+        _need(scaling in kinds, f"scaling: one of {sorted(kinds)}")
+        self._freqs = None
+        if freqs is not None:
+            _need(len(freqs) == rot_dim // 2, "freqs: rot_dim / 2 values")
+            self._freqs = (C.c_double * len(freqs))(*[float(f) for f in freqs])
+        self.rot_dim = int(rot_dim)
+        self.struct = _RopeParams(int(rot_dim), STA_ROPE_INTERLEAVED if interleaved else STA_ROPE_HALF, kinds[scaling],
+                                  float(mscale), float(base), float(factor), float(orig_len), float(low_turns),
+                                  float(high_turns), C.cast(self._freqs, C.c_void_p) if self._freqs else None)
+
+
+def _heads_view(t: torch.Tensor, what: str):
+    """[n, H, d] with contiguous heads: the token stride."""
+    _need(t.dim() == 3, f"{what}: [tokens, heads, d]")
+    n, H, d = t.shape
+    _need(n == 0 or ((d == 1 or t.stride(2) == 1) and (H == 1 or t.stride(1) == d)),
+          f"{what}: a token's heads must be contiguous")
+    return t.stride(0) if n > 1 else H * d
+
+
+def sta_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope, transpose: bool = False,
+             y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rotary positions: x [n, H, d] bf16 or float32 (any token stride), positions int32 [n].
+
+    transpose turns the other way: the gradient of the input from the gradient of the result.
+    y may be x (in place); otherwise a new [n, H, d] tensor is returned.
+    """
+    xs = _heads_view(x, "x")
+    n, H, d = x.shape
+    dev = x.device
+    _place(dev, y)
+    _i32(dev, positions=positions)
+    _need(positions.shape == (n,), "positions: one a token")
+    code = _dtype_code(x.dtype)
+    with _Launch(dev, stream) as st:
+        y = torch.empty((n, H, d), dtype=x.dtype, device=dev) if y is None else y
+        _need(y.shape == x.shape and y.dtype == x.dtype, "y: x's shape and dtype")
+        _check("sta_rope", lib().sta_rope(_ptr(x), _ptr(y), _ptr(positions), C.byref(rope.struct), n, H, d, xs,
+                                          _heads_view(y, "y"), int(bool(transpose)), code, st))
+    return y
+
+
+def sta_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
+                          v_pages: torch.Tensor, page_indptr_dev: torch.Tensor, page_indices_dev: torch.Tensor,
+                          q_indptr_dev: torch.Tensor, kv_indptr_dev: torch.Tensor, rope: Optional[Rope] = None,
+                          positions: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, stream=None):
+    """Turns q [n, Hq, d] and k [n, Hkv, d] of a step's new tokens (any token strides, bf16) and
+    writes k and v to their places in k_pages / v_pages [n_pages, page_size, Hkv, d].
+
+    Request r's new tokens are rows q_indptr[r] .. q_indptr[r+1]-1, the last ones of its sequence of
+    kv_indptr[r+1] - kv_indptr[r] tokens (both int32, device). rope None: nothing turns. q None: keys
+    and values only. Returns the turned q [n, Hq, d] (rows of a padded batch's padding unwritten).
+    """
+    dev = k.device
+    _place(dev, q, v, k_pages, v_pages, q_out)
+    n_pages, page_size, Hkv, d = k_pages.shape
+    n = k.shape[0]
+    _need(v_pages.shape == k_pages.shape and k_pages.is_contiguous() and v_pages.is_contiguous(),
+          "k_pages, v_pages: contiguous [n_pages, page_size, Hkv, d]")
+    _need(k.shape == (n, Hkv, d) and v.shape == k.shape, "k, v: [n, Hkv, d]")
+    ks, vs = _heads_view(k, "k"), _heads_view(v, "v")
+    Hq, qs = 0, 0
+    if q is not None:
+        qs = _heads_view(q, "q")
+        Hq = q.shape[1]
+        _need(q.shape == (n, Hq, d), "q: [n, Hq, d]")
+    for t in (q, k, v, k_pages, v_pages, q_out):
+        _need(t is None or t.dtype == torch.bfloat16, "bf16 only")
+    _i32(dev, page_indptr=page_indptr_dev, page_indices=page_indices_dev, q_indptr=q_indptr_dev, kv_indptr=kv_indptr_dev)
+    n_req = q_indptr_dev.numel() - 1
+    _need(kv_indptr_dev.numel() == n_req + 1 and page_indptr_dev.numel() == n_req + 1, "indptr: n_req + 1 values each")
+    if positions is not None:
+        _i32(dev, positions=positions)
+        _need(positions.shape == (n,), "positions: one a token")
+    with _Launch(dev, stream) as st:
+        if q is not None and q_out is None:
+            q_out = torch.empty((n, Hq, d), dtype=q.dtype, device=dev)
+        if q_out is not None:
+            _need(q is not None and q_out.shape == q.shape and q_out.is_contiguous(), "q_out: contiguous, q's shape")
+        _check("sta_rope_append_paged", lib().sta_rope_append_paged(
+            _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(q_out), _ptr(k_pages), _ptr(v_pages), page_size, n_pages,
+            _ptr(page_indptr_dev), _ptr(page_indices_dev), _ptr(q_indptr_dev), _ptr(kv_indptr_dev), _ptr(positions),
+            C.byref(rope.struct) if rope is not None else None, n, n_req, Hq, Hkv, d, STA_BF16, st))
+    return q_out
+
+
+def sta_chunk_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_indptr_dev: torch.Tensor,
+                        page_indices_dev: torch.Tensor, q_indptr_dev: torch.Tensor, q_indptr_host,
+                        kv_indptr_dev: torch.Tensor, kv_indptr_host, scale=None, pattern: Optional[MaskSource] = None,
+                        num_splits: int = 0, o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of each request's new tokens over its sequence in the paged cache.
+
+    q [n, Hq, d] bf16 (any token stride that is a multiple of 8), request r's rows q_indptr[r] ..
+    q_indptr[r+1]-1 being the last tokens of its sequence of kv_indptr[r+1] - kv_indptr[r] tokens;
+    indptr int32 [n_req + 1], device and host. pattern: None (causal) or a MaskSource.pattern over
+    positions. Rows past q_indptr[n_req] are left as they are. Returns O [n, Hq, d] and LSE
+    [n, Hq] float32 (-inf for a token that sees no key).
+    """
+    qs = _heads_view(q, "q")
+    n, Hq, d = q.shape
+    dev = q.device
+    _place(dev, k_pages, v_pages, o, lse)
+    n_pages, page_size, Hkv, dk = k_pages.shape
+    _need(dk == d and v_pages.shape == k_pages.shape and k_pages.is_contiguous() and v_pages.is_contiguous(),
+          "k_pages, v_pages: contiguous [n_pages, page_size, Hkv, d]")
+    _need(q.dtype == k_pages.dtype == v_pages.dtype, "q, k_pages, v_pages: one dtype")
+    _i32(dev, page_indptr=page_indptr_dev, page_indices=page_indices_dev, q_indptr=q_indptr_dev, kv_indptr=kv_indptr_dev)
+    n_req = q_indptr_dev.numel() - 1
+    _need(kv_indptr_dev.numel() == n_req + 1 and page_indptr_dev.numel() == n_req + 1, "indptr: n_req + 1 values each")
+    qh, keep_q = _host_i32(q_indptr_host, n_req + 1, "q_indptr_host")
+    kh, keep_k = _host_i32(kv_indptr_host, n_req + 1, "kv_indptr_host")
+    _need(0 <= int(keep_q[-1]) <= n, "q_indptr: past q's rows")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    pat = None if pattern is None else _src_array([pattern])
+    h = lib()
+    with _Launch(dev, stream) as st:
+        o = torch.empty((n, Hq, d), dtype=q.dtype, device=dev) if o is None else o
+        lse = torch.empty((n, Hq), dtype=torch.float32, device=dev) if lse is None else lse
+        _need(o.shape == q.shape and o.dtype == q.dtype and o.is_contiguous(), "o: contiguous, q's shape and dtype")
+        _need(lse.shape == (n, Hq) and lse.dtype == torch.float32 and lse.is_contiguous(), "lse: contiguous float32 [n, Hq]")
+        need = C.c_size_t(0)
+
+        def call(ws):
+            _check("sta_chunk_fwd_paged", h.sta_chunk_fwd_paged(
+                _ptr(q), qs, _ptr(k_pages), _ptr(v_pages), page_size, n_pages, _ptr(page_indptr_dev),
+                _ptr(page_indices_dev), _ptr(q_indptr_dev), qh, _ptr(kv_indptr_dev), kh, n_req, Hq, Hkv, d,
+                _dtype_code(q.dtype), scale, pat, num_splits, _ptr(o), _ptr(lse), _ptr(ws), C.byref(need), st))
+
+        call(None)
+        workspace = _workspace(need.value, workspace, dev)
+        need.value = workspace.numel()
+        call(workspace)
+    return o, lse
+
+
+def _buf_array(bufs: Sequence[torch.Tensor], dev: torch.device, n_pages: Optional[int] = None):
+    """The buffers' device pointers (host array), their number, bytes a page and pages."""
+    bufs = list(bufs)
+    page_bytes = 0
+    for b in bufs:
+        _need(b.device == dev and b.is_contiguous() and b.dim() >= 1, f"buffers: contiguous on {dev}")
+        n_pages = b.shape[0] if n_pages is None else n_pages
+        _need(b.shape[0] == n_pages and n_pages > 0, "buffers: [n_pages, ...] each")
+        nb = b.numel() // n_pages * b.element_size()
+        _need(page_bytes in (0, nb), "buffers: the same bytes a page")
+        page_bytes = nb
+    return (C.c_void_p * max(len(bufs), 1))(*[b.data_ptr() for b in bufs]), len(bufs), page_bytes, n_pages
+
+
+def _lists(ref, page_indptr, page_indices, kv_indptr):
+    dev = ref.device
+    _place(dev)
+    _i32(dev, ref=ref, page_indptr=page_indptr, page_indices=page_indices, kv_indptr=kv_indptr)
+    n_req = kv_indptr.numel() - 1
+    _need(page_indptr.numel() == n_req + 1, "page_indptr, kv_indptr: n_req + 1 values each")
+    return dev, n_req
+
+
+def sta_pages_copy(bufs: Sequence[torch.Tensor], src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """Page src[i] onto page dst[i] of every buffer [n_pages, ...] (int32, device; negative: no copy).
+    Pages of dst must be distinct and not among src."""
+    bufs = list(bufs)
+    _need(bufs, "at least one buffer")
+    dev = bufs[0].device
+    _place(dev)
+    _i32(dev, src=src, dst=dst)
+    _need(src.dim() == 1 and src.shape == dst.shape, "src, dst: [n] each")
+    arr, nb, page_bytes, n_pages = _buf_array(bufs, dev)
+    with _Launch(dev, stream) as st:
+        _check("sta_pages_copy", lib().sta_pages_copy(arr, nb, page_bytes, n_pages, _ptr(src), _ptr(dst), src.numel(), st))
+
+
+def sta_pages_grow(ref: torch.Tensor, page_indptr: torch.Tensor, page_indices: torch.Tensor, kv_indptr: torch.Tensor,
+                   new_kv_indptr: torch.Tensor, page_size: int, stream=None) -> torch.Tensor:
+    """Gives each request the free pages (lowest first) it needs to go from kv_indptr's lengths to
+    new_kv_indptr's; updates ref and page_indices, returns status int32 [2] {taken, missing}."""
+    dev, n_req = _lists(ref, page_indptr, page_indices, kv_indptr)
+    _i32(dev, new_kv_indptr=new_kv_indptr)
+    _need(new_kv_indptr.numel() == n_req + 1, "new_kv_indptr: n_req + 1 values")
+    h, need = lib(), C.c_size_t(0)
+    with _Launch(dev, stream) as st:
+        status = torch.empty(2, dtype=torch.int32, device=dev)
+        args = (_ptr(ref), ref.numel(), _ptr(page_indptr), _ptr(page_indices), _ptr(kv_indptr), _ptr(new_kv_indptr), n_req,
+                page_size, _ptr(status))
+        _check("sta_pages_grow", h.sta_pages_grow(*args, None, C.byref(need), st))
+        ws = _workspace(need.value, None, dev)
+        _check("sta_pages_grow", h.sta_pages_grow(*args, _ptr(ws), C.byref(need), st))
+    return status
+
+
+def sta_pages_fork(bufs: Sequence[torch.Tensor], ref: torch.Tensor, page_indptr: torch.Tensor,
+                   page_indices: torch.Tensor, kv_indptr: torch.Tensor, parent: torch.Tensor, child: torch.Tensor,
+                   page_size: int, stream=None) -> torch.Tensor:
+    """Request child[i] becomes a copy of request parent[i]: whole pages shared, a last, partly filled
+    page copied onto a free one in every buffer. A child must hold nothing. Updates ref and
+    page_indices, returns status int32 [2] {pages taken, missing}."""
+    dev, n_req = _lists(ref, page_indptr, page_indices, kv_indptr)
+    _i32(dev, parent=parent, child=child)
+    _need(parent.dim() == 1 and parent.shape == child.shape, "parent, child: [n_forks] each")
+    arr, nb, page_bytes, _ = _buf_array(bufs, dev, ref.numel())
+    h, need = lib(), C.c_size_t(0)
+    with _Launch(dev, stream) as st:
+        status = torch.empty(2, dtype=torch.int32, device=dev)
+        args = (arr, nb, page_bytes, _ptr(ref), ref.numel(), _ptr(page_indptr), _ptr(page_indices), _ptr(kv_indptr), n_req,
+                page_size, _ptr(parent), _ptr(child), parent.numel(), _ptr(status))
+        _check("sta_pages_fork", h.sta_pages_fork(*args, None, C.byref(need), st))
+        ws = _workspace(need.value, None, dev)
+        _check("sta_pages_fork", h.sta_pages_fork(*args, _ptr(ws), C.byref(need), st))
+    return status
+
+
+def sta_pages_free(ref: torch.Tensor, page_indptr: torch.Tensor, page_indices: torch.Tensor, kv_indptr: torch.Tensor,
+                   reqs: torch.Tensor, page_size: int, stream=None) -> None:
+    """The listed requests (int32, device) let go of the pages they hold; their entries become -1."""
+    dev, n_req = _lists(ref, page_indptr, page_indices, kv_indptr)
+    _i32(dev, reqs=reqs)
+    with _Launch(dev, stream) as st:
+        _check("sta_pages_free", lib().sta_pages_free(_ptr(ref), ref.numel(), _ptr(page_indptr), _ptr(page_indices),
+                                                      _ptr(kv_indptr), n_req, page_size, _ptr(reqs), reqs.numel(), st))
+
+
+def sta_pages_compact(bufs: Sequence[torch.Tensor], ref: torch.Tensor, page_indptr: torch.Tensor,
+                      page_indices: torch.Tensor, kv_indptr: torch.Tensor, page_size: int, stream=None):
+    """Moves the used pages to the lowest numbers: page data in every buffer, ref and the lists.
+    Returns page_map int32 [n_pages] (each used page's new number, -1: free) and status int32 [2]
+    {pages in use, pages moved}."""
+    dev, n_req = _lists(ref, page_indptr, page_indices, kv_indptr)
+    arr, nb, page_bytes, _ = _buf_array(bufs, dev, ref.numel())
+    h, need = lib(), C.c_size_t(0)
+    with _Launch(dev, stream) as st:
+        page_map = torch.empty(ref.numel(), dtype=torch.int32, device=dev)
+        status = torch.empty(2, dtype=torch.int32, device=dev)
+        args = (arr, nb, page_bytes, _ptr(ref), ref.numel(), _ptr(page_indptr), _ptr(page_indices), _ptr(kv_indptr), n_req,
+                page_size, _ptr(page_map), _ptr(status))
+        _check("sta_pages_compact", h.sta_pages_compact(*args, None, C.byref(need), st))
+        ws = _workspace(need.value, None, dev)
+        _check("sta_pages_compact", h.sta_pages_compact(*args, _ptr(ws), C.byref(need), st))
+    return page_map, status
+
+
+# ---------------------------------------------------------------------------
+# failure detection
 
 
 def sta_check_bounded_wait(limit_ns: int, stream=None) -> int:
