@@ -1,87 +1,716 @@
-// Attention of chunks of new tokens over a paged KV cache.
+// Attention of chunks of new tokens over a paged KV cache, for sm_103a.
 //
-// First form: one warp per (new token, query head). The lanes share the head's elements; the
-// keys that the token may see are visited one by one with the online softmax
-// m' = max(m, s), l' = l e^(m - m') + e^(s - m'), O' = O e^(m - m') + e^(s - m') v.
+// Rows. The G = Hq / Hkv query heads that share a KV head, of 128 / G consecutive new tokens, are
+// the 128 rows of a query tile (row = token * G + head of the group; a last few rows are unused
+// when G does not divide 128). K and V of a KV head are then read once for the whole group, and a
+// causal tile spans few positions. A CTA works on one item: two neighbouring query tiles of one
+// (request, KV head), in two slots that share every K / V tile (128 keys) in shared memory; when
+// a request has one tile left, both slots take that tile and every other key tile each, and the
+// two results are merged at the end (a single token's long cache is then two interleaved
+// streams). The key tiles of an item are those that some of its tokens see: [0, n_global) and the
+// window, as two ranges of tile numbers. Items of few rows over a long cache are further cut into
+// chunks of their tile list, whose normalised fp32 partials a second kernel merges by
+// log-sum-exp.
+//
+// Roles (12 warps, one CTA an SM): warps 0..3 and 4..7 the softmax of slots 0 and 1 (a thread a
+// row), warps 8 and 9 issue the MMAs of slots 0 and 1, warp 10 loads K and V, warp 11 loads Q.
+// S = Q K^T (M 128, N 128) and O += P V (P bf16 over the first half of S in tensor memory) run as
+// tcgen05.mma; a slot's order on the tensor core is PV(j), QK(j + 1), and one slot's MMAs run
+// under the other's softmax. S and O of both slots fill the 512 TMEM columns. The softmax is the
+// online one with a lazy maximum: O is rescaled only when a row's maximum grows by more than 2^8.
+//
+// Pages. A page of P tokens is copied by TMA in boxes of gcd(P, 128) tokens when that is a
+// multiple of 8 (whole swizzle atoms); for other page sizes the loading warp copies 16 bytes a
+// lane (cp.async) to the same swizzled places. Rows of V behind the sequence are set to zero,
+// since what a page holds there may be NaN; rows of K there only reach masked scores.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <cmath>
+#include <numeric>
+#include <vector>
 
-#include "common.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
 namespace sta {
 namespace {
 
+constexpr int kBM = 128;  // rows of a query tile
+constexpr int kBN = 128;  // keys of a tile
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kKvWarp = 10, kQWarp = 11;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int kCpLag = 2;                  // cp.async stages in flight behind the one being issued
+
 struct ChunkArgs {
-  const __nv_bfloat16* q;  // [N, Hq, d], q_stride elements between tokens
-  const __nv_bfloat16* k;  // [n_pages, page_size, Hkv, d]
+  __nv_bfloat16* o;  // [N, Hq, d]
+  float* lse;        // [N, Hq] or null
+  const __nv_bfloat16* k;
   const __nv_bfloat16* v;
-  __nv_bfloat16* o;        // [N, Hq, d]
-  float* lse;              // [N, Hq] or null
   const int32_t* page_indptr;
   const int32_t* page_indices;
   const int32_t* q_indptr;
   const int32_t* kv_indptr;
-  int64_t q_stride;
-  int n_tokens, n_req, Hq, Hkv, d, page_size, n_pages;
+  float* part_o;     // [partial rows, d]
+  float* part_lse;   // [partial rows]
+  int N, Hq, Hkv, G, TQ;  // TQ tokens a query tile
+  int page_size, n_pages;
+  int box;                // tokens of a TMA box, or 0: cp.async
   float scale_log2;
   int causal;
-  int64_t win_lo, win_hi, n_global;  // key j of position p: (win_lo <= j - p <= win_hi or j < n_global) and, if causal, j <= p
+  int64_t win_lo, win_hi, n_global;
   int* err;
 };
 
+// What the host planned: requests in launch order (heaviest first). Rank k has the items base[k] ..
+// base[k+1]-1: ((u, from the last pair of query tiles down) * Hkv + KV head) * ns + chunk.
+template <int CAP>
+struct Plan {
+  int n;                // requests
+  int32_t base[CAP + 1];
+  int32_t rows[CAP];    // first merged row of a request that is cut (those come first)
+  int32_t part[CAP];    // first partial row
+  int32_t qn[CAP];      // new tokens on the host
+  uint16_t req[CAP];    // request, from the launch's first
+  uint16_t ns[CAP];     // chunks
+};
+
+struct Item {
+  int r, hk, c, ns, rank;
+  int q0;          // first row of the request in q
+  int n;           // new tokens computed
+  int t0;          // first token of slot 0 (slot 1: t0 + TQ when dual)
+  int dual;
+  int len;         // tokens of the sequence
+  int pos0;        // position of the request's token 0
+  int gt, wl;      // tile list: [0, gt), then wl, wl + 1, ...
+  int j0, j1;      // this chunk's part of it
+  int j1a;         // slot 0's end in dual items (its last tokens come earlier)
+  __device__ int tile(int j) const { return j < gt ? j : wl + (j - gt); }
+  __device__ int count(int slot) const {
+    return dual ? (slot == 1 ? j1 - j0 : j1a - j0) : (j1 - j0 + 1 - slot) / 2;
+  }
+};
+
+// Ranges of keys that tokens at positions p0 .. p1 see among them.
+struct Seen {
+  int g1;      // last key seen as a global one, or -1
+  int lo, hi;  // first and last key of the window, hi < lo: none
+};
+template <class A>
+__host__ __device__ inline Seen seen(const A& a, int64_t p0, int64_t p1, int64_t len) {
+  const int64_t jmax = a.causal && p1 < len - 1 ? p1 : len - 1;
+  int64_t g = a.n_global - 1 < jmax ? a.n_global - 1 : jmax, lo = p0 + a.win_lo, hi = p1 + a.win_hi;
+  if (lo < 0) lo = 0;
+  if (hi > jmax) hi = jmax;
+  Seen s;
+  s.g1 = (int)(g < -1 ? -1 : g);
+  s.lo = (int)(lo > INT32_MAX ? INT32_MAX : lo);
+  s.hi = (int)(hi < -1 ? -1 : hi);
+  return s;
+}
+__host__ __device__ inline int tile_list(const Seen& s, int& gt, int& wl) {
+  gt = s.g1 >= 0 ? s.g1 / kBN + 1 : 0;
+  wl = s.lo / kBN > gt ? s.lo / kBN : gt;
+  const int wh = s.hi >= s.lo ? s.hi / kBN : -1;
+  return gt + (wh >= wl ? wh - wl + 1 : 0);
+}
+
+template <int CAP>
+__device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP>& P, int req0, int item, Item& it) {
+  int lo = 0, hi = P.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (P.base[mid] <= item) lo = mid;
+    else hi = mid;
+  }
+  it.rank = lo;
+  it.ns = P.ns[lo];
+  const int x = item - P.base[lo], per_u = A.Hkv * it.ns, units = (P.base[lo + 1] - P.base[lo]) / per_u;
+  const int u = units - 1 - x / per_u, y = x - (x / per_u) * per_u;
+  it.hk = y / it.ns;
+  it.c = y - it.hk * it.ns;
+  it.r = req0 + P.req[lo];
+  const int q0 = __ldg(A.q_indptr + it.r), q1 = __ldg(A.q_indptr + it.r + 1);
+  const int64_t len = (int64_t)__ldg(A.kv_indptr + it.r + 1) - __ldg(A.kv_indptr + it.r);
+  int n = q1 - q0;
+  if (n > P.qn[lo]) {
+    record_error(A.err, 0x606);
+    n = P.qn[lo];
+  }
+  if (q0 < 0 || n < 0 || q0 > A.N - n || len < 0 || len > INT32_MAX - 2 * kBN) {
+    record_error(A.err, 0x111);
+    return false;
+  }
+  it.q0 = q0;
+  it.n = n;
+  it.t0 = 2 * u * A.TQ;
+  if (it.t0 >= n) return false;
+  it.dual = it.t0 + A.TQ < n;
+  it.len = (int)len;
+  it.pos0 = (int)(len - (q1 - q0));
+  const int te = min(n, it.t0 + (it.dual ? 2 : 1) * A.TQ);
+  const Seen s = seen(A, it.pos0 + it.t0, it.pos0 + te - 1, len);
+  const int nt = tile_list(s, it.gt, it.wl);
+  it.j0 = (int)((int64_t)it.c * nt / it.ns);
+  it.j1 = (int)((int64_t)(it.c + 1) * nt / it.ns);
+  it.j1a = it.j1;
+  if (it.dual) {  // tiles past what slot 0's tokens see
+    const Seen a = seen(A, it.pos0 + it.t0, it.pos0 + it.t0 + A.TQ - 1, len);
+    const int last = max(a.g1, a.hi >= a.lo ? a.hi : -1);
+    const int lt = last >= 0 ? last / kBN : -1;  // last tile of slot 0
+    const int na = lt < 0 ? 0 : (lt < it.gt ? lt + 1 : it.gt + max(0, lt - it.wl + 1));
+    it.j1a = max(it.j0, min(it.j1, na));
+  }
+  return true;
+}
+
 template <int D>
-__global__ void __launch_bounds__(256) chunk_kernel(const ChunkArgs A) {
-  constexpr int E = D / 32;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= (int64_t)A.n_tokens * A.Hq) return;
-  const int t = (int)(row / A.Hq), h = (int)(row % A.Hq), hk = h / (A.Hq / A.Hkv);
-  int lo = 0, hi = A.n_req - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(A.q_indptr + mid) <= t) lo = mid;
-    else hi = mid - 1;
+struct Cfg {
+  static constexpr int KH = D / 64;            // 128-byte column blocks of a row
+  static constexpr int TILE = kBN * D * 2;     // a Q, K or V tile
+  static constexpr int STAGES = D == 128 ? 5 : 10;
+  static constexpr int OFF_Q = 0;              // two tiles
+  static constexpr int OFF_KV = 2 * TILE;
+  static constexpr int OFF_X = OFF_KV + STAGES * TILE;  // slot 1's row maximum and sum, for the merge of a single tile
+  static constexpr int SMEM = 1024 + OFF_X + kBM * 8;
+  static constexpr uint32_t IDESC_QK = umma_idesc_bf16(kBM, kBN, 0, 0);
+  static constexpr uint32_t IDESC_PV = umma_idesc_bf16(kBM, D, 0, 1);
+  static constexpr int S_COL = 0;              // slot s: + 128 s; P over its first 64 columns
+  static constexpr int O_COL = 256;            // slot s: + 128 s
+};
+
+// 128 consecutive TMEM columns of this thread's lane, loaded and waited for in one statement.
+#define STA_R(i) "=r"(r[i])
+#define STA_R8(i) STA_R(i), STA_R(i + 1), STA_R(i + 2), STA_R(i + 3), STA_R(i + 4), STA_R(i + 5), STA_R(i + 6), STA_R(i + 7)
+#define STA_R32X(i) STA_R8(i), STA_R8(i + 8), STA_R8(i + 16), STA_R8(i + 24)
+__device__ __forceinline__ void tmem_ld128_sync(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, "
+      "%37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, "
+      "%59, %60, %61, %62, %63, %64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, "
+      "%81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, %101, "
+      "%102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, "
+      "%120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : STA_R32X(0), STA_R32X(32), STA_R32X(64), STA_R32X(96)
+      : "r"(taddr)
+      : "memory");
+}
+#undef STA_R32X
+#undef STA_R8
+#undef STA_R
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Bits of keys k0 .. k0 + 31 that lie in [lo, hi].
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int k0) {
+  const int a = lo - k0, b = hi - k0;
+  if (a > 31 || b < 0 || b < a) return 0u;
+  return (a <= 0 ? ~0u : ~0u << a) & (b >= 31 ? ~0u : (2u << b) - 1u);
+}
+
+// Page of token `tok` of the sequence: a number outside the cache reads page 0 and is reported.
+__device__ __forceinline__ int page_of(const ChunkArgs& A, int pb, int pe, int tok) {
+  const int64_t o = (int64_t)pb + tok / A.page_size;
+  int pg = o >= 0 && o < pe ? __ldg(A.page_indices + o) : -1;
+  if (pg < 0 || pg >= A.n_pages) {
+    record_error(A.err, 0x110);
+    pg = 0;
   }
-  const int r = lo, q1 = __ldg(A.q_indptr + r + 1);
-  if (t >= q1) return;
-  const int64_t len = max((int64_t)0, (int64_t)__ldg(A.kv_indptr + r + 1) - __ldg(A.kv_indptr + r));
-  const int64_t pos = len - (q1 - t);
-  const int64_t jmax = min(len - 1, A.causal ? pos : len - 1);
-  const int64_t w0 = max((int64_t)0, pos + A.win_lo), w1 = min(jmax, pos + A.win_hi);
-  const int64_t g1 = min(A.n_global - 1, jmax);
-  const int pb = __ldg(A.page_indptr + r), pe = __ldg(A.page_indptr + r + 1);
-  float q[E], acc[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(A.q[t * A.q_stride + (int64_t)h * D + lane * E + e]) * A.scale_log2;
-    acc[e] = 0.f;
-  }
-  for (int64_t j = g1 >= 0 ? 0 : w0; j <= max(g1, w1); ++j) {
-    if (j > g1 && j < w0) j = w0;
-    if (j > g1 && j > w1) break;
-    const int64_t ord = pb + j / A.page_size;
-    int page = ord < pe ? __ldg(A.page_indices + ord) : -1;
-    if (page < 0 || page >= A.n_pages) {
-      record_error(A.err, 0x110);
-      page = 0;
+  return pg;
+}
+
+template <int D, int CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ChunkArgs A,
+                 const __grid_constant__ Plan<CAP> P, int req0) {
+  using C = Cfg<D>;
+  constexpr int ST = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  // full[s] / empty[s]: a K or V tile is in stage s / may be overwritten (an arrival of each slot). s_full[x]: S of slot x is in TMEM (and all its
+  // earlier MMAs are done); p_full[x]: its P is (128 threads); o_full[x]: its last PV is done.
+  __shared__ __align__(8) uint64_t full[ST], empty[ST], s_full[2], p_full[2], o_full[2], q_full, tail, drain[2];
+  __shared__ uint32_t s_tmem;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Item it;
+  if (!get_item(A, P, req0, blockIdx.x, it)) return;
+
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  float2* s_x = reinterpret_cast<float2*>(smem + C::OFF_X);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 2);
     }
-    const int64_t at = (((int64_t)page * A.page_size + j % A.page_size) * A.Hkv + hk) * D + lane * E;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], __bfloat162float(A.k[at + e]), s);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s), a = exp2f(m - mn), p = exp2f(s - mn);
-    m = mn;
-    l = l * a + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + p * __bfloat162float(A.v[at + e]);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 128);
+      mbar_init(&o_full[x], 1);
+      mbar_init(&drain[x], 1);
+    }
+    mbar_init(&q_full, 1);
+    mbar_init(&tail, 1);
+    fence_mbar_init();
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (warp == kMmaWarp) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int nj = it.j1 - it.j0;
+
+  if (warp == kQWarp) {
+    // ------------------------------------------------------------ Q
+    if (lane == 0 && nj > 0) {
+      const uint32_t bytes = (uint32_t)(A.G * A.TQ * 128 * C::KH);
+      mbar_arrive_expect_tx(&q_full, bytes * (it.dual ? 2 : 1));
+      for (int x = 0; x <= it.dual; ++x)
 #pragma unroll
-  for (int e = 0; e < E; ++e) A.o[row * D + lane * E + e] = __float2bfloat16_rn(acc[e] * inv);
-  if (A.lse && lane == 0) A.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        for (int kh = 0; kh < C::KH; ++kh)
+          tma_load_3d(smem + C::OFF_Q + x * C::TILE + kh * (kBM * 128), &tm_q, kh * 64, it.hk * A.G,
+                      it.q0 + it.t0 + x * A.TQ, &q_full);
+      mbar_wait(&q_full, 0, A.err, 0x620);  // shared memory is not released under the copy
+    }
+  } else if (warp == kKvWarp) {
+    // ------------------------------------------------------------ K and V
+    const int pb = __ldg(A.page_indptr + it.r), pe = __ldg(A.page_indptr + it.r + 1);
+    int n_issued = 0;
+    bool ok = true;
+    for (int x = 0; x < 2 * nj; ++x) {
+      const int s = x % ST, tok0 = it.tile(it.j0 + (x >> 1)) * kBN;
+      const bool is_v = x & 1;
+      const bool tail_v = is_v && tok0 + kBN > it.len;  // rows behind the sequence
+      if (lane == 0) ok = mbar_wait(&empty[s], ((x / ST) & 1u) ^ 1u, A.err, 0x621);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      uint8_t* dst = smem + C::OFF_KV + s * C::TILE;
+      if (A.box > 0) {
+        const int boxes = kBN / A.box, in = min(boxes, (it.len - tok0 + A.box - 1) / A.box);  // boxes with tokens
+        uint64_t* bar = tail_v ? &tail : &full[s];
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(in * A.box * 128 * C::KH));
+        __syncwarp();
+        const int b = lane / C::KH, kh = lane % C::KH;
+        if (b < in) {
+          const int tok = tok0 + b * A.box;
+          const int row = page_of(A, pb, pe, tok) * A.page_size + tok % A.page_size;
+          tma_load_3d(dst + kh * (kBN * 128) + b * A.box * 128, is_v ? &tm_v : &tm_k, kh * 64, it.hk, row, bar);
+        }
+        if (tail_v) {
+          // (one tail tile an item: the last one of its list at most)
+          ok = mbar_wait(&tail, 0, A.err, 0x622);
+          for (int i = (it.len - tok0) * 8 + lane; i < kBN * 8; i += 32)
+#pragma unroll
+            for (int h = 0; h < C::KH; ++h) *reinterpret_cast<uint4*>(dst + h * (kBN * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+        }
+      } else {
+        constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an instruction
+        const int ch = lane % LPR;
+        const __nv_bfloat16* src = (is_v ? A.v : A.k) + (int64_t)it.hk * D + ch * 8;
+        uint8_t* d0 = dst + (ch >> 3) * (kBN * 128);
+#pragma unroll 4
+        for (int r0 = 0; r0 < kBN; r0 += RPI) {
+          const int row = r0 + lane / LPR, tok = tok0 + row;
+          uint8_t* d = d0 + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+          if (tok < it.len) {
+            const int64_t at = (int64_t)page_of(A, pb, pe, tok) * A.page_size + tok % A.page_size;
+            cp_async16(smem_u32(d), src + at * A.Hkv * D);
+          } else if (is_v) {
+            *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        cp_async_commit();
+        if (x >= kCpLag) {
+          cp_async_wait<kCpLag>();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[(x - kCpLag) % ST]);
+        }
+      }
+      ++n_issued;
+    }
+    if (A.box == 0) {  // the last stages
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0)
+        for (int x = max(0, n_issued - kCpLag); x < n_issued; ++x) mbar_arrive(&full[x % ST]);
+    }
+    if (lane == 0)  // shared memory is not released under a copy
+      for (int x = max(0, n_issued - ST); x < n_issued; ++x) mbar_wait(&full[x % ST], (x / ST) & 1u, A.err, 0x623);
+  } else if (warp >= kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue of one slot
+    const int x = warp - kMmaWarp;
+    const int cnt = it.count(x);
+    if (lane == 0 && nj > 0) {
+      const uint32_t sQ = smem_u32(smem + C::OFF_Q) + (it.dual ? x * C::TILE : 0);
+      const uint64_t a0 = umma_sdesc_sw128(sQ, 16, 1024);
+      const uint64_t k0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_KV), 16, 1024);
+      const uint64_t v0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_KV), kBN * 128, 1024);
+      const uint32_t tS = tmem + C::S_COL + x * 128, tO = tmem + C::O_COL + x * 128;
+      bool ok = mbar_wait(&q_full, 0, A.err, 0x624);
+      // Both slots pass every stage in order: a stage that the other slot alone uses is waited for
+      // and given back at once, so that neither slot's view of its phase falls behind.
+      auto skip = [&](int y) -> bool {
+        if (!mbar_wait(&full[y % ST], (y / ST) & 1u, A.err, 0x625)) return false;
+        mbar_arrive(&empty[y % ST]);
+        return true;
+      };
+      auto qk = [&](int i) -> bool {
+        const int y = 2 * i, s = y % ST;  // list entry j0 + i: stages 2i (K) and 2i + 1 (V)
+        if (!mbar_wait(&full[s], (y / ST) & 1u, A.err, 0x625)) return false;
+        tc_fence_after();
+        const uint64_t b = k0 + (uint64_t)((s * C::TILE) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int off = (kk >> 2) * (kBN * 128) + (kk & 3) * 32;
+          umma_bf16(tS, a0 + (uint64_t)(off >> 4), b + (uint64_t)(off >> 4), C::IDESC_QK, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[x]);
+        umma_commit(&empty[s]);
+        return true;
+      };
+      const int step = it.dual ? 1 : 2;
+      int i = it.dual ? 0 : x;  // this slot's entry
+      for (int y = 0; ok && y < 2 * min(i, nj); ++y) ok = skip(y);
+      if (ok && cnt > 0) ok = qk(i);
+      for (int n = 0; ok && n < cnt; ++n) {
+        const int y = 2 * i + 1, s = y % ST;
+        if (!(ok = mbar_wait(&p_full[x], n & 1u, A.err, 0x626))) break;
+        if (!(ok = mbar_wait(&full[s], (y / ST) & 1u, A.err, 0x627))) break;
+        tc_fence_after();
+        const uint64_t b = v0 + (uint64_t)((s * C::TILE) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk)
+          umma_bf16_ts(tO, tS + kk * 8, b + (uint64_t)((kk * 2048) >> 4), C::IDESC_PV, (n > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&empty[s]);
+        if (n + 1 == cnt) umma_commit(&o_full[x]);
+        const int next = n + 1 < cnt ? i + step : nj;
+        for (int z = y + 1; ok && z < 2 * next; ++z) ok = skip(z);
+        i = next;
+        if (ok && n + 1 < cnt) ok = qk(i);
+      }
+      if (cnt == 0)
+        for (int y = 2 * min(i, nj); ok && y < 2 * nj; ++y) ok = skip(y);
+      if (!ok) {  // TMEM is not freed under an MMA
+        umma_commit(&drain[x]);
+        mbar_wait(&drain[x], 0, A.err, 0x628);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax of one slot
+    const int x = warp >> 2, qd = warp & 3, m = qd * 32 + lane;
+    const uint32_t t_lane = tmem + ((uint32_t)(qd * 32) << 16);
+    const uint32_t tS = t_lane + C::S_COL + x * 128, tO = t_lane + C::O_COL + x * 128;
+    const int cnt = it.count(x);
+    const int tt = m / A.G, t = it.t0 + (it.dual ? x * A.TQ : 0) + tt, h = it.hk * A.G + (m - tt * A.G);
+    const bool live = tt < A.TQ && t < it.n;
+    const bool warp_live = __any_sync(0xffffffffu, live);
+    const int pos = it.pos0 + t;
+    const Seen sn = seen(A, pos, pos, it.len);
+    const float c = A.scale_log2;
+    float m_ref = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int n = 0; n < cnt; ++n) {
+      const int k0 = it.tile(it.j0 + (it.dual ? n : 2 * n + x)) * kBN;
+      if (!mbar_wait(&s_full[x], n & 1u, A.err, 0x629)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (warp_live) {
+        float s[128];
+        tmem_ld128_sync(tS, s);
+        const bool all = (k0 >= sn.lo && k0 + kBN - 1 <= sn.hi) || k0 + kBN - 1 <= sn.g1 || !live;
+        if (!__all_sync(0xffffffffu, all)) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t bits = range_bits(sn.lo, sn.hi, k0 + 32 * w) | range_bits(0, sn.g1, k0 + 32 * w);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[32 * w + e] = (bits & (1u << e)) ? s[32 * w + e] : -INFINITY;
+          }
+        }
+        float m8[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          m8[y] = fmax3(s[y], s[y + 8], s[y + 16]);
+#pragma unroll
+          for (int z = 24; z < 120; z += 16) m8[y] = fmax3(m8[y], s[y + z], s[y + z + 8]);
+          m8[y] = fmaxf(m8[y], s[y + 120]);
+        }
+        const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * c;
+        float alpha = 1.f;
+        bool need = false;
+        if (mx > m_ref + kRescaleThreshold) {
+          if (m_ref != -INFINITY) {
+            alpha = ex2(m_ref - mx);
+            need = true;
+          }
+          m_ref = mx;
+        }
+        if (__any_sync(0xffffffffu, need)) {  // (S of this tile is there: the earlier PV is done)
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tmem_ld32_sync(tO + c0, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tmem_st32_sync(tO + c0, reinterpret_cast<const uint32_t*>(o));
+          }
+        }
+        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+        const uint64_t c2 = f32x2_pack(c, c), nm2 = f32x2_pack(neg_m, neg_m);
+        uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float a0, a1;
+            f32x2_unpack(f32x2_fma(f32x2_pack(s[64 * half + 2 * e], s[64 * half + 2 * e + 1]), c2, nm2), a0, a1);
+            const float p0 = ex2(a0), p1 = ex2(a1);
+            l2[e & 3] = f32x2_add(l2[e & 3], f32x2_pack(p0, p1));
+            pk[e] = pack_bf16x2(p0, p1);  // rounded for the MMA; the sum takes the fp32 values
+          }
+          tmem_st32_sync(tS + 32 * half, pk);
+        }
+        float lp[8];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) f32x2_unpack(l2[y], lp[2 * y], lp[2 * y + 1]);
+        l = l * alpha + (((lp[0] + lp[1]) + (lp[2] + lp[3])) + ((lp[4] + lp[5]) + (lp[6] + lp[7])));
+      }
+      tc_fence_before();
+      mbar_arrive(&p_full[x]);
+    }
+    // ---- result
+    if (ok && cnt > 0) mbar_wait(&o_full[x], 0, A.err, 0x62a);
+    tc_fence_after();
+    float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and, for a single tile, of slot 1's
+    bool other = false;
+    if (!it.dual) {
+      if (x == 1) s_x[m] = make_float2(cnt > 0 ? m_ref : -INFINITY, l);
+      tc_fence_before();
+      named_bar_sync(1, 256);
+      tc_fence_after();
+      if (x == 0) {
+        const float2 ml = s_x[m];
+        other = it.count(1) > 0;
+        const float M = fmaxf(m_ref, ml.x);
+        if (M != -INFINITY) {
+          w0 = exp2f(m_ref - M);
+          w1 = exp2f(ml.x - M);
+          l = l * w0 + ml.y * w1;
+          m_ref = M;
+        }
+      }
+    }
+    if (warp_live && (it.dual || x == 0)) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float row_lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+      w0 *= inv;
+      w1 *= inv;
+      const int64_t row = (int64_t)(it.q0 + t) * A.Hq + h;
+      const int64_t prow = it.ns > 1 ? P.part[it.rank] + ((int64_t)it.c * P.qn[it.rank] + t) * A.Hq + h : 0;
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        float o[32];
+        if (cnt > 0) {
+          tmem_ld32_sync(tO + c0, o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= w0;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+        if (other) {
+          float o1[32];
+          tmem_ld32_sync(tO + 128 + c0, o1);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], w1, o[e]);
+        }
+        if (live) {
+          if (it.ns > 1) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(A.part_o + prow * D + c0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(A.o + row * D + c0 + e) =
+                  make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]), pack_bf16x2(o[e + 4], o[e + 5]),
+                             pack_bf16x2(o[e + 6], o[e + 7]));
+          }
+        }
+      }
+      if (live) {
+        if (it.ns > 1) A.part_lse[prow] = row_lse;
+        else if (A.lse) A.lse[row] = row_lse;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// One warp per (new token, query head) of the requests that were cut.
+template <int D, int CAP>
+__global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant__ ChunkArgs A,
+                                                          const __grid_constant__ Plan<CAP> P, int req0, int n_cut,
+                                                          int n_rows) {
+  constexpr int E = D / 32;
+  const int64_t mr = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (mr >= n_rows) return;
+  int lo = 0, hi = n_cut;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (P.rows[mid] <= mr) lo = mid;
+    else hi = mid;
+  }
+  const int y = (int)mr - P.rows[lo], r = req0 + P.req[lo], t = y / A.Hq;
+  const int q0 = __ldg(A.q_indptr + r), n = __ldg(A.q_indptr + r + 1) - q0;
+  if (q0 < 0 || t >= n || q0 > A.N - min(n, P.qn[lo])) return;
+  const int64_t pr = (int64_t)P.part[lo] + y;
+  const size_t stride = (size_t)P.qn[lo] * A.Hq;
+  float out[E];
+  const float L = merge_row<E>(A.part_o + pr * D, stride * D, A.part_lse + pr, stride, P.ns[lo], lane, out);
+  const int64_t row = (int64_t)(q0 + t) * A.Hq + y % A.Hq;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(A.o + row * D + lane * E + e) = pack_bf16x2(out[e], out[e + 1]);
+  if (A.lse && lane == 0) A.lse[row] = L;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p)
+               : nullptr;
+  }();
+  return fn;
+}
+
+// [rows, heads, d] bf16 as a 3-D tensor (d, heads, rows), `stride` elements between rows; box (64, bh, br).
+bool make_map(CUtensorMap* m, const void* base, int d, int heads, int64_t rows, int64_t stride, int bh, int br) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)bh, (cuuint32_t)br}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Requests [r0, r1) as one launch: launch order, chunks, items and partial rows.
+struct Group {
+  int r0 = 0, n = 0, n_cut = 0;
+  int64_t items = 0, rows = 0, parts = 0;  // items; merged rows; partial rows
+  std::vector<int> req, qn, ns;
+  std::vector<int64_t> base, row0, part0;
+};
+
+constexpr int kSmallPlan = 64, kLargePlan = 1024;
+
+sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, int r0, int r1, int num_splits, int sms,
+                      Group& g) {
+  // Chunks. A CTA an SM, items heaviest first: an item longer than a third of an SM's share of the
+  // key tiles would show in the tail, so it is cut into pieces of about that; pieces below kMinTiles
+  // tiles cost more in prologue and merge than they gain.
+  constexpr int kMinTiles = 8, kMaxAuto = 256;
+  g.r0 = r0;
+  std::vector<int> tiles(r1 - r0), units(r1 - r0), idx;
+  double work = 0;
+  for (int r = r0; r < r1; ++r) {
+    const int n = qi[r + 1] - qi[r];
+    const int64_t len = (int64_t)ki[r + 1] - ki[r];
+    if (n == 0) continue;
+    const int nt = (n + a.TQ - 1) / a.TQ, u = (nt + 1) / 2;
+    const int64_t p0 = len - n;
+    auto count = [&](int v) {  // key tiles of pair v
+      int gt, wl;
+      const int64_t t0 = (int64_t)2 * v * a.TQ, te = std::min<int64_t>(n, t0 + 2 * a.TQ);
+      return tile_list(seen(a, p0 + t0, p0 + te - 1, len), gt, wl);
+    };
+    tiles[r - r0] = std::max(count(u - 1), count(0));
+    units[r - r0] = u;
+    work += (double)a.Hkv * u * (count(0) + count(u - 1)) / 2.0;
+    idx.push_back(r - r0);
+  }
+  std::stable_sort(idx.begin(), idx.end(), [&](int x, int y) { return tiles[x] > tiles[y]; });
+  const int piece = std::max(kMinTiles, (int)std::ceil(work / sms / 3.0));
+  for (int i : idx) {
+    const int n = qi[r0 + i + 1] - qi[r0 + i];
+    int ns = num_splits;
+    if (ns == 0) ns = std::min(kMaxAuto, std::max(1, (tiles[i] + piece - 1) / piece));
+    g.req.push_back(i);
+    g.qn.push_back(n);
+    g.ns.push_back(ns);
+    g.base.push_back(g.items);
+    g.row0.push_back(g.rows);
+    g.part0.push_back(g.parts);
+    g.items += (int64_t)units[i] * a.Hkv * ns;
+    if (ns > 1) {
+      g.n_cut = (int)g.req.size();  // tiles descend, so those that are cut come first
+      g.rows += (int64_t)n * a.Hq;
+      g.parts += (int64_t)n * a.Hq * ns;
+    }
+  }
+  g.n = (int)g.req.size();
+  if (g.items > INT32_MAX || g.parts > INT32_MAX / 2) return STA_ERR_UNSUPPORTED;
+  return STA_OK;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+template <int D, int CAP>
+sta_status launch_group(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a,
+                        const Group& g, cudaStream_t st) {
+  Plan<CAP> p{};
+  p.n = g.n;
+  for (int i = 0; i < g.n; ++i) {
+    p.base[i] = (int32_t)g.base[i];
+    p.rows[i] = (int32_t)g.row0[i];
+    p.part[i] = (int32_t)g.part0[i];
+    p.qn[i] = g.qn[i];
+    p.req[i] = (uint16_t)g.req[i];
+    p.ns[i] = (uint16_t)g.ns[i];
+  }
+  p.base[g.n] = (int32_t)g.items;
+  auto kern = chunk_kernel<D, CAP>;
+  STA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM));
+  kern<<<(unsigned)g.items, kThreads, Cfg<D>::SMEM, st>>>(tq, tk, tv, a, p, g.r0);
+  STA_LAUNCH_CHECK();
+  if (g.n_cut > 0) {
+    chunk_merge_kernel<D, CAP><<<(unsigned)cdiv(g.rows, 8), 256, 0, st>>>(a, p, g.r0, g.n_cut, (int)g.rows);
+    STA_LAUNCH_CHECK();
+  }
+  return STA_OK;
 }
 
 }  // namespace
@@ -96,17 +725,18 @@ extern "C" sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const
                                           const int32_t* kv_indptr_host, int n_req, int Hq, int Hkv, int d,
                                           sta_dtype dtype, float scale, const sta_mask_src* pattern, int num_splits,
                                           void* o, float* lse, void* workspace, size_t* workspace_bytes,
-                                          sta_stream stream) {
+                                          sta_stream stream) try {
   constexpr int64_t kFar = (int64_t)1 << 31;  // beyond any distance between two tokens
   if (!workspace_bytes || !q_indptr_host || !kv_indptr_host || n_req < 1 || Hq < 1 || Hkv < 1 || page_size < 1 ||
       n_pages < 1 || num_splits < 0 || num_splits > 1024)
     return STA_ERR_INVALID_ARG;
   if (Hq % Hkv != 0 || !(scale > 0.f) || !std::isfinite(scale)) return STA_ERR_INVALID_ARG;
-  if (dtype != STA_BF16 || (d != 64 && d != 128) || Hq / Hkv > 128 || Hq > 65535) return STA_ERR_UNSUPPORTED;
+  if (dtype != STA_BF16 || (d != 64 && d != 128) || Hq / Hkv > kBM || Hq > 65535) return STA_ERR_UNSUPPORTED;
   if ((int64_t)n_pages * page_size > INT32_MAX) return STA_ERR_UNSUPPORTED;
   if (q_indptr_host[0] != 0 || kv_indptr_host[0] != 0) return STA_ERR_INVALID_ARG;
   for (int r = 0; r < n_req; ++r)
     if (q_indptr_host[r + 1] < q_indptr_host[r] || kv_indptr_host[r + 1] < kv_indptr_host[r]) return STA_ERR_INVALID_ARG;
+  if (kv_indptr_host[n_req] > INT32_MAX - 2 * kBN) return STA_ERR_UNSUPPORTED;
   ChunkArgs a{};
   a.causal = 1;
   a.win_lo = -kFar;
@@ -120,44 +750,72 @@ extern "C" sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const
   }
   if (q_stride == 0) q_stride = (int64_t)Hq * d;
   if (q_stride < (int64_t)Hq * d || (q_stride & 7)) return q_stride & 7 ? STA_ERR_UNSUPPORTED : STA_ERR_INVALID_ARG;
-  const size_t need = 256;
+  a.N = q_indptr_host[n_req];
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.TQ = kBM / a.G;
+  a.page_size = page_size;
+  a.n_pages = n_pages;
+  const int box = std::gcd(page_size, kBN);
+  a.box = box % 8 == 0 ? box : 0;
+  a.scale_log2 = scale * kLog2e;
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaGetLastError();  // a size query also works where there is no device
+  std::vector<Group> groups;
+  int64_t parts = 0;
+  for (int r0 = 0; r0 < n_req; r0 += kLargePlan) {
+    Group g;
+    const sta_status st = plan_group(a, q_indptr_host, kv_indptr_host, r0, std::min(n_req, r0 + kLargePlan), num_splits, sms, g);
+    if (st != STA_OK) return st;
+    parts = std::max(parts, g.parts);
+    groups.push_back(std::move(g));
+  }
+  const size_t o_bytes = align256((size_t)parts * d * sizeof(float));
+  const size_t need = std::max<size_t>(256, o_bytes + align256((size_t)parts * sizeof(float)));
   if (!workspace) {
     *workspace_bytes = need;
     return STA_OK;
   }
   if (*workspace_bytes < need) return STA_ERR_WORKSPACE;
   if ((uintptr_t)workspace & 255) return STA_ERR_UNSUPPORTED;
-  const int N = q_indptr_host[n_req];
-  if (N == 0) return STA_OK;
+  if (a.N == 0) return STA_OK;
   if (!q || !k_pages || !v_pages || !page_indptr_dev || !page_indices_dev || !q_indptr_dev || !kv_indptr_dev || !o)
     return STA_ERR_INVALID_ARG;
   if (((uintptr_t)q | (uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)o) & 15) return STA_ERR_UNSUPPORTED;
   if (((uintptr_t)page_indptr_dev | (uintptr_t)page_indices_dev | (uintptr_t)q_indptr_dev | (uintptr_t)kv_indptr_dev |
        (uintptr_t)lse) & 3)
     return STA_ERR_UNSUPPORTED;
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.k = static_cast<const __nv_bfloat16*>(k_pages);
-  a.v = static_cast<const __nv_bfloat16*>(v_pages);
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
+  a.k = static_cast<const __nv_bfloat16*>(k_pages);
+  a.v = static_cast<const __nv_bfloat16*>(v_pages);
   a.page_indptr = page_indptr_dev;
   a.page_indices = page_indices_dev;
   a.q_indptr = q_indptr_dev;
   a.kv_indptr = kv_indptr_dev;
-  a.q_stride = q_stride;
-  a.n_tokens = N;
-  a.n_req = n_req;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.d = d;
-  a.page_size = page_size;
-  a.n_pages = n_pages;
-  a.scale_log2 = scale * kLog2e;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + o_bytes);
   a.err = device_error_word();
-  const int64_t blocks = cdiv((int64_t)N * Hq, 8);
-  if (blocks > INT32_MAX) return STA_ERR_UNSUPPORTED;
-  if (d == 64) chunk_kernel<64><<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(a);
-  else chunk_kernel<128><<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(a);
-  STA_LAUNCH_CHECK();
+  CUtensorMap tq, tk, tv;
+  const int64_t rows = (int64_t)n_pages * page_size, kv_stride = (int64_t)Hkv * d;
+  const int kv_box = a.box > 0 ? a.box : 8;  // (the maps of K and V are not used by cp.async)
+  if (!make_map(&tq, q, d, Hq, a.N, q_stride, a.G, a.TQ) || !make_map(&tk, k_pages, d, Hkv, rows, kv_stride, 1, kv_box) ||
+      !make_map(&tv, v_pages, d, Hkv, rows, kv_stride, 1, kv_box)) {
+    note_cuda_error(cudaErrorInvalidValue);  // tensor-map encoding refused
+    return STA_ERR_CUDA;
+  }
+  const cudaStream_t s = (cudaStream_t)stream;
+  for (const Group& g : groups) {
+    if (g.items == 0) continue;
+    const sta_status st = g.n <= kSmallPlan ? (d == 64 ? launch_group<64, kSmallPlan>(tq, tk, tv, a, g, s)
+                                                       : launch_group<128, kSmallPlan>(tq, tk, tv, a, g, s))
+                                            : (d == 64 ? launch_group<64, kLargePlan>(tq, tk, tv, a, g, s)
+                                                       : launch_group<128, kLargePlan>(tq, tk, tv, a, g, s));
+    if (st != STA_OK) return st;
+  }
   return STA_OK;
+} catch (...) {  // no memory for the plan
+  return STA_ERR_INVALID_ARG;
 }

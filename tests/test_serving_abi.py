@@ -131,6 +131,14 @@ def test_chunk_refusals(lib):
     assert _chunk(lib, ws=P, ws_bytes=1 << 30, lse=P + 2)[0] == UNSUPPORTED
 
 
+def test_chunk_workspace_grows_with_the_splits(lib):
+    # s chunks of (new tokens x query heads) rows, d floats and an LSE each
+    st, n = _chunk(lib, splits=5)
+    rows = 5 * 4 * 8
+    assert st == OK and n >= rows * (64 + 1) * 4
+    assert _chunk(lib, splits=1)[1] == 256
+
+
 def _bufs(n=2, at=P):
     return (C.c_void_p * max(n, 1))(*[at + 4096 * i for i in range(n)])
 

@@ -370,6 +370,16 @@ def test_chunk_replayed_with_other_lengths(dev):
             x[k].copy_(v)
 
 
+def test_chunk_more_new_tokens_than_planned_is_reported(dev):
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = PagedCase(21, [400, 1], [400, 10], 4, 2, 64, 16)
+    x = c.dev(dev)
+    x["q_indptr_host"] = np.array([0, 1, 401], np.int32)  # 1 and 400 on the host, 400 and 1 on the device
+    sta.sta_chunk_fwd_paged(**x)
+    assert sta.sta_device_error(reset=True) == 0x606
+
+
 def test_chunk_on_another_stream(dev):
     import torch
 
