@@ -13,7 +13,7 @@
 // log-sum-exp.
 //
 // Roles (12 warps, one CTA an SM): warps 0..3 and 4..7 the softmax of slots 0 and 1 (a thread a
-// row), warps 8 and 9 issue the MMAs of slots 0 and 1, warp 10 loads K and V, warp 11 loads Q.
+// row), warp 8 issues the MMAs, warps 9, 10 and 11 load V, K and Q.
 // S = Q K^T (M 128, N 128) and O += P V (P bf16 over the first half of S in tensor memory) run as
 // tcgen05.mma; a slot's order on the tensor core is PV(j), QK(j + 1), and one slot's MMAs run
 // under the other's softmax. S and O of both slots fill the 512 TMEM columns. The softmax is the
@@ -39,9 +39,9 @@ namespace {
 constexpr int kBM = 128;  // rows of a query tile
 constexpr int kBN = 128;  // keys of a tile
 constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kKvWarp = 10, kQWarp = 11;
+constexpr int kMmaWarp = 8, kVWarp = 9, kKWarp = 10, kQWarp = 11;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr int kCpLag = 2;                  // cp.async stages in flight behind the one being issued
+constexpr int kCpLag = 1;                  // cp.async tiles of K, and of V, in flight behind the one being issued
 
 struct ChunkArgs {
   __nv_bfloat16* o;  // [N, Hq, d]
@@ -220,17 +220,6 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int k0) {
   return (a <= 0 ? ~0u : ~0u << a) & (b >= 31 ? ~0u : (2u << b) - 1u);
 }
 
-// Page of token `tok` of the sequence: a number outside the cache reads page 0 and is reported.
-__device__ __forceinline__ int page_of(const ChunkArgs& A, int pb, int pe, int tok) {
-  const int64_t o = (int64_t)pb + tok / A.page_size;
-  int pg = o >= 0 && o < pe ? __ldg(A.page_indices + o) : -1;
-  if (pg < 0 || pg >= A.n_pages) {
-    record_error(A.err, 0x110);
-    pg = 0;
-  }
-  return pg;
-}
-
 template <int D, int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -239,9 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   constexpr int ST = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
-  // full[s] / empty[s]: a K or V tile is in stage s / may be overwritten (an arrival of each slot). s_full[x]: S of slot x is in TMEM (and all its
-  // earlier MMAs are done); p_full[x]: its P is (128 threads); o_full[x]: its last PV is done.
-  __shared__ __align__(8) uint64_t full[ST], empty[ST], s_full[2], p_full[2], o_full[2], q_full, tail, drain[2];
+  // full[s] / empty[s]: a K or V tile is in stage s / may be overwritten. s_full[x]: S of slot x is in
+  // TMEM (and every earlier MMA is done); p_half[x], p_full[x]: the P of its first 64 keys, of all of
+  // them is (128 threads each); o_full[x]: its last PV is done.
+  __shared__ __align__(8) uint64_t full[ST], empty[ST], s_full[2], p_half[2], p_full[2], o_full[2], q_full, tail, drain;
   __shared__ uint32_t s_tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Item it;
@@ -253,14 +243,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 2);
+      mbar_init(&empty[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
+      mbar_init(&p_half[x], 128);
       mbar_init(&p_full[x], 128);
       mbar_init(&o_full[x], 1);
-      mbar_init(&drain[x], 1);
     }
+    mbar_init(&drain, 1);
     mbar_init(&q_full, 1);
     mbar_init(&tail, 1);
     fence_mbar_init();
@@ -287,132 +278,166 @@ __global__ void __launch_bounds__(kThreads, 1)
                       it.q0 + it.t0 + x * A.TQ, &q_full);
       mbar_wait(&q_full, 0, A.err, 0x620);  // shared memory is not released under the copy
     }
-  } else if (warp == kKvWarp) {
-    // ------------------------------------------------------------ K and V
+  } else if (warp == kKWarp || warp == kVWarp) {
+    // ------------------------------------------------------------ K or V: ring stages 2i and 2i + 1
+    const bool is_v = warp == kVWarp;
     const int pb = __ldg(A.page_indptr + it.r), pe = __ldg(A.page_indptr + it.r + 1);
-    int n_issued = 0;
+    const int P0 = A.page_size;
+    auto page_at = [&](int tok) -> int {  // list entry of a token, unchecked; -1 behind the list
+      const int o = pb + tok / P0;
+      return o >= 0 && o < pe ? __ldg(A.page_indices + o) : -1;
+    };
+    auto row_at = [&](int page, int tok) -> int {  // cache row; a page outside the cache reads page 0
+      if (page < 0 || page >= A.n_pages) {
+        record_error(A.err, 0x110);
+        page = 0;
+      }
+      return page * P0 + tok % P0;
+    };
     bool ok = true;
-    for (int x = 0; x < 2 * nj; ++x) {
-      const int s = x % ST, tok0 = it.tile(it.j0 + (x >> 1)) * kBN;
-      const bool is_v = x & 1;
-      const bool tail_v = is_v && tok0 + kBN > it.len;  // rows behind the sequence
-      if (lane == 0) ok = mbar_wait(&empty[s], ((x / ST) & 1u) ^ 1u, A.err, 0x621);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      uint8_t* dst = smem + C::OFF_KV + s * C::TILE;
-      if (A.box > 0) {
-        const int boxes = kBN / A.box, in = min(boxes, (it.len - tok0 + A.box - 1) / A.box);  // boxes with tokens
+    int i = 0;
+    if (A.box > 0) {
+      // a lane per TMA box (column block kh of box b); the next tile's page numbers are fetched
+      // while this tile's stage is waited for
+      const int b = lane / C::KH, kh = lane % C::KH, off = b * A.box;
+      const int boxes = kBN / A.box;
+      int pg = nj > 0 && b < boxes ? page_at(it.tile(it.j0) * kBN + off) : -1;
+      for (; i < nj; ++i) {
+        const int y = 2 * i + is_v, s = y % ST, tok0 = it.tile(it.j0 + i) * kBN, page = pg;
+        if (i + 1 < nj && b < boxes) pg = page_at(it.tile(it.j0 + i + 1) * kBN + off);
+        const int in = min(boxes, (it.len - tok0 + A.box - 1) / A.box);  // boxes with tokens
+        const bool tail_v = is_v && tok0 + kBN > it.len;                 // rows behind the sequence
+        if (lane == 0) ok = mbar_wait(&empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        uint8_t* dst = smem + C::OFF_KV + s * C::TILE;
         uint64_t* bar = tail_v ? &tail : &full[s];
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(in * A.box * 128 * C::KH));
         __syncwarp();
-        const int b = lane / C::KH, kh = lane % C::KH;
-        if (b < in) {
-          const int tok = tok0 + b * A.box;
-          const int row = page_of(A, pb, pe, tok) * A.page_size + tok % A.page_size;
-          tma_load_3d(dst + kh * (kBN * 128) + b * A.box * 128, is_v ? &tm_v : &tm_k, kh * 64, it.hk, row, bar);
-        }
-        if (tail_v) {
-          // (one tail tile an item: the last one of its list at most)
-          ok = mbar_wait(&tail, 0, A.err, 0x622);
-          for (int i = (it.len - tok0) * 8 + lane; i < kBN * 8; i += 32)
+        if (b < in)
+          tma_load_3d(dst + kh * (kBN * 128) + off * 128, is_v ? &tm_v : &tm_k, kh * 64, it.hk, row_at(page, tok0 + off), bar);
+        if (tail_v) {  // (the last tile of a list at most)
+          mbar_wait(&tail, 0, A.err, 0x622);
+          for (int z = (it.len - tok0) * 8 + lane; z < kBN * 8; z += 32)
 #pragma unroll
-            for (int h = 0; h < C::KH; ++h) *reinterpret_cast<uint4*>(dst + h * (kBN * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < C::KH; ++k) *reinterpret_cast<uint4*>(dst + k * (kBN * 128) + z * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[s]);
         }
-      } else {
-        constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an instruction
-        const int ch = lane % LPR;
-        const __nv_bfloat16* src = (is_v ? A.v : A.k) + (int64_t)it.hk * D + ch * 8;
-        uint8_t* d0 = dst + (ch >> 3) * (kBN * 128);
-#pragma unroll 4
-        for (int r0 = 0; r0 < kBN; r0 += RPI) {
-          const int row = r0 + lane / LPR, tok = tok0 + row;
-          uint8_t* d = d0 + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-          if (tok < it.len) {
-            const int64_t at = (int64_t)page_of(A, pb, pe, tok) * A.page_size + tok % A.page_size;
-            cp_async16(smem_u32(d), src + at * A.Hkv * D);
-          } else if (is_v) {
-            *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
+      }
+    } else {
+      // 16 bytes a lane: lane l looks up the rows of tokens l, l + 32, .. of the tile, which the
+      // copies take from it by shuffles
+      constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an instruction
+      const int ch = lane % LPR;
+      const __nv_bfloat16* src = (is_v ? A.v : A.k) + (int64_t)it.hk * D + ch * 8;
+      const int64_t row_elems = (int64_t)A.Hkv * D;
+      int pg[kBN / 32];
+#pragma unroll
+      for (int g = 0; g < kBN / 32; ++g) {
+        const int tok = nj > 0 ? it.tile(it.j0) * kBN + 32 * g + lane : it.len;
+        pg[g] = tok < it.len ? page_at(tok) : -1;
+      }
+      for (; i < nj; ++i) {
+        const int y = 2 * i + is_v, s = y % ST, tok0 = it.tile(it.j0 + i) * kBN;
+        int row[kBN / 32];
+#pragma unroll
+        for (int g = 0; g < kBN / 32; ++g) {
+          const int tok = tok0 + 32 * g + lane;
+          row[g] = tok < it.len ? row_at(pg[g], tok) : -1;
+          const int next = i + 1 < nj ? it.tile(it.j0 + i + 1) * kBN + 32 * g + lane : it.len;
+          pg[g] = next < it.len ? page_at(next) : -1;
+        }
+        if (lane == 0) ok = mbar_wait(&empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        const uint32_t dst = smem_u32(smem + C::OFF_KV + s * C::TILE) + (ch >> 3) * (kBN * 128);
+#pragma unroll
+        for (int g = 0; g < kBN / 32; ++g) {
+#pragma unroll 8
+          for (int r0 = 0; r0 < 32; r0 += RPI) {
+            const int rr = r0 + lane / LPR, at = __shfl_sync(0xffffffffu, row[g], rr), m = 32 * g + rr;
+            const uint32_t d = dst + m * 128 + (((ch & 7) ^ (m & 7)) << 4);
+            if (at >= 0) cp_async16(d, src + at * row_elems);
+            else if (is_v) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(d), "r"(0) : "memory");
           }
         }
         cp_async_commit();
-        if (x >= kCpLag) {
+        if (i >= kCpLag) {
           cp_async_wait<kCpLag>();
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[(x - kCpLag) % ST]);
+          if (lane == 0) mbar_arrive(&full[(y - 2 * kCpLag) % ST]);
         }
       }
-      ++n_issued;
-    }
-    if (A.box == 0) {  // the last stages
-      cp_async_wait<0>();
+      cp_async_wait<0>();  // the last tiles
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0)
-        for (int x = max(0, n_issued - kCpLag); x < n_issued; ++x) mbar_arrive(&full[x % ST]);
+        for (int k = max(0, i - kCpLag); k < i; ++k) mbar_arrive(&full[(2 * k + is_v) % ST]);
     }
     if (lane == 0)  // shared memory is not released under a copy
-      for (int x = max(0, n_issued - ST); x < n_issued; ++x) mbar_wait(&full[x % ST], (x / ST) & 1u, A.err, 0x623);
-  } else if (warp >= kMmaWarp) {
-    // ------------------------------------------------------------ MMA issue of one slot
-    const int x = warp - kMmaWarp;
-    const int cnt = it.count(x);
+      for (int k = max(0, i - (ST + 1) / 2); k < i; ++k) {
+        const int y = 2 * k + is_v;
+        if (y + ST >= 2 * i) mbar_wait(&full[y % ST], (y / ST) & 1u, A.err, 0x623);
+      }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    // One thread issues both slots' products in turn, PV(j) and QK(j + 1) of slot 0, then of slot 1, so
+    // that each slot's softmax has the time of the other's products. (An issuing thread for each slot
+    // let the two fall into step, both in the softmax at once and then both on the tensor core: 538 us
+    // against 413 us for the 8192-token prompt.)
     if (lane == 0 && nj > 0) {
-      const uint32_t sQ = smem_u32(smem + C::OFF_Q) + (it.dual ? x * C::TILE : 0);
-      const uint64_t a0 = umma_sdesc_sw128(sQ, 16, 1024);
+      const uint64_t q0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
       const uint64_t k0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_KV), 16, 1024);
       const uint64_t v0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_KV), kBN * 128, 1024);
-      const uint32_t tS = tmem + C::S_COL + x * 128, tO = tmem + C::O_COL + x * 128;
       bool ok = mbar_wait(&q_full, 0, A.err, 0x624);
-      // Both slots pass every stage in order: a stage that the other slot alone uses is waited for
-      // and given back at once, so that neither slot's view of its phase falls behind.
-      auto skip = [&](int y) -> bool {
-        if (!mbar_wait(&full[y % ST], (y / ST) & 1u, A.err, 0x625)) return false;
-        mbar_arrive(&empty[y % ST]);
-        return true;
-      };
-      auto qk = [&](int i) -> bool {
-        const int y = 2 * i, s = y % ST;  // list entry j0 + i: stages 2i (K) and 2i + 1 (V)
-        if (!mbar_wait(&full[s], (y / ST) & 1u, A.err, 0x625)) return false;
+      // slot x takes list entry j0 + i: ring stages 2i (K) and 2i + 1 (V)
+      auto takes = [&](int x, int i) { return i < nj && (it.dual ? (x == 1 || it.j0 + i < it.j1a) : (i & 1) == x); };
+      auto qk = [&](int x, int i) {
+        const int y = 2 * i, s = y % ST;
+        if (!(ok = ok && mbar_wait(&full[s], (y / ST) & 1u, A.err, 0x625))) return;
         tc_fence_after();
-        const uint64_t b = k0 + (uint64_t)((s * C::TILE) >> 4);
+        const uint64_t a = q0 + (uint64_t)((it.dual && x ? C::TILE : 0) >> 4), b = k0 + (uint64_t)((s * C::TILE) >> 4);
+        const uint32_t tS = tmem + C::S_COL + x * 128;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const int off = (kk >> 2) * (kBN * 128) + (kk & 3) * 32;
-          umma_bf16(tS, a0 + (uint64_t)(off >> 4), b + (uint64_t)(off >> 4), C::IDESC_QK, kk > 0 ? 1u : 0u);
+          umma_bf16(tS, a + (uint64_t)(off >> 4), b + (uint64_t)(off >> 4), C::IDESC_QK, kk > 0 ? 1u : 0u);
         }
         umma_commit(&s_full[x]);
-        umma_commit(&empty[s]);
-        return true;
+        if (!it.dual || x == 1) umma_commit(&empty[s]);
+      };
+      auto pv = [&](int x, int i, int n) {  // n: this slot's tiles before
+        const int y = 2 * i + 1, s = y % ST;
+        const uint64_t b = v0 + (uint64_t)((s * C::TILE) >> 4);
+        const uint32_t tS = tmem + C::S_COL + x * 128, tO = tmem + C::O_COL + x * 128;
+        if (!(ok = ok && mbar_wait(&full[s], (y / ST) & 1u, A.err, 0x627))) return;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!(ok = mbar_wait(half ? &p_full[x] : &p_half[x], n & 1u, A.err, 0x626))) return;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = half * (kBN / 32); kk < (half + 1) * (kBN / 32); ++kk)
+            umma_bf16_ts(tO, tS + kk * 8, b + (uint64_t)((kk * 2048) >> 4), C::IDESC_PV, (n > 0 || kk > 0) ? 1u : 0u);
+        }
+        if (!it.dual || x == 1) umma_commit(&empty[s]);
       };
       const int step = it.dual ? 1 : 2;
-      int i = it.dual ? 0 : x;  // this slot's entry
-      for (int y = 0; ok && y < 2 * min(i, nj); ++y) ok = skip(y);
-      if (ok && cnt > 0) ok = qk(i);
-      for (int n = 0; ok && n < cnt; ++n) {
-        const int y = 2 * i + 1, s = y % ST;
-        if (!(ok = mbar_wait(&p_full[x], n & 1u, A.err, 0x626))) break;
-        if (!(ok = mbar_wait(&full[s], (y / ST) & 1u, A.err, 0x627))) break;
-        tc_fence_after();
-        const uint64_t b = v0 + (uint64_t)((s * C::TILE) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
-          umma_bf16_ts(tO, tS + kk * 8, b + (uint64_t)((kk * 2048) >> 4), C::IDESC_PV, (n > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&empty[s]);
-        if (n + 1 == cnt) umma_commit(&o_full[x]);
-        const int next = n + 1 < cnt ? i + step : nj;
-        for (int z = y + 1; ok && z < 2 * next; ++z) ok = skip(z);
-        i = next;
-        if (ok && n + 1 < cnt) ok = qk(i);
-      }
-      if (cnt == 0)
-        for (int y = 2 * min(i, nj); ok && y < 2 * nj; ++y) ok = skip(y);
+      for (int x = 0; x < 2; ++x)
+        if (takes(x, it.dual ? 0 : x)) qk(x, it.dual ? 0 : x);
+      for (int n = 0; ok && n * step < nj; ++n)
+        for (int x = 0; x < 2; ++x) {
+          const int e = n * step + (it.dual ? 0 : x);
+          if (!takes(x, e)) continue;
+          pv(x, e, n);
+          if (takes(x, e + step)) qk(x, e + step);
+          else if (ok) umma_commit(&o_full[x]);
+        }
       if (!ok) {  // TMEM is not freed under an MMA
-        umma_commit(&drain[x]);
-        mbar_wait(&drain[x], 0, A.err, 0x628);
+        umma_commit(&drain);
+        mbar_wait(&drain, 0, A.err, 0x628);
       }
     }
   } else {
@@ -491,12 +516,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[e] = pack_bf16x2(p0, p1);  // rounded for the MMA; the sum takes the fp32 values
           }
           tmem_st32_sync(tS + 32 * half, pk);
+          if (half == 0) {
+            tc_fence_before();
+            mbar_arrive(&p_half[x]);
+          }
         }
         float lp[8];
 #pragma unroll
         for (int y = 0; y < 4; ++y) f32x2_unpack(l2[y], lp[2 * y], lp[2 * y + 1]);
         l = l * alpha + (((lp[0] + lp[1]) + (lp[2] + lp[3])) + ((lp[4] + lp[5]) + (lp[6] + lp[7])));
       }
+      if (!warp_live) mbar_arrive(&p_half[x]);
       tc_fence_before();
       mbar_arrive(&p_full[x]);
     }
