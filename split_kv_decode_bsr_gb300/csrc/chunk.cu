@@ -213,6 +213,14 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// True in one lane of the (whole, converged) warp. Unlike lane == 0 it tells the compiler that a
+// single thread runs what follows, so that the operands of its MMAs stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Bits of keys k0 .. k0 + 31 that lie in [lo, hi].
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int k0) {
   const int a = lo - k0, b = hi - k0;
@@ -388,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // that each slot's softmax has the time of the other's products. (An issuing thread for each slot
     // let the two fall into step, both in the softmax at once and then both on the tensor core: 538 us
     // against 413 us for the 8192-token prompt.)
-    if (lane == 0 && nj > 0) {
+    if (nj > 0 && elect_one()) {
       const uint64_t q0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
       const uint64_t k0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_KV), 16, 1024);
       const uint64_t v0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_KV), kBN * 128, 1024);
