@@ -41,7 +41,6 @@ constexpr int kBN = 128;  // keys of a tile
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kVWarp = 9, kKWarp = 10, kQWarp = 11;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr int kCpLag = 1;                  // cp.async tiles of K, and of V, in flight behind the one being issued
 
 struct ChunkArgs {
   __nv_bfloat16* o;  // [N, Hq, d]
@@ -77,6 +76,7 @@ struct Plan {
 };
 
 struct Item {
+  int end;         // no more items
   int r, hk, c, ns, rank;
   int q0;          // first row of the request in q
   int n;           // new tokens computed
@@ -92,6 +92,16 @@ struct Item {
     return dual ? (slot == 1 ? j1 - j0 : j1a - j0) : (j1 - j0 + 1 - slot) / 2;
   }
 };
+
+// An item out of shared memory, by a whole warp: a word a lane, then broadcasts, which tell the
+// compiler that the fields are the same in every lane (the MMA operands that follow from them then
+// stay in uniform registers).
+__device__ __forceinline__ Item read_item(const Item* s) {
+  static_assert(sizeof(Item) == 17 * 4, "one word a lane");
+  const int lane = threadIdx.x & 31, v = lane < 17 ? reinterpret_cast<const int*>(s)[lane] : 0;
+  auto f = [&](int i) { return __shfl_sync(0xffffffffu, v, i); };
+  return Item{f(0), f(1), f(2), f(3), f(4), f(5), f(6), f(7), f(8), f(9), f(10), f(11), f(12), f(13), f(14), f(15), f(16)};
+}
 
 // Ranges of keys that tokens at positions p0 .. p1 see among them.
 struct Seen {
@@ -125,6 +135,7 @@ __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP>& P,
     if (P.base[mid] <= item) lo = mid;
     else hi = mid;
   }
+  it.end = 0;
   it.rank = lo;
   it.ns = P.ns[lo];
   const int x = item - P.base[lo], per_u = A.Hkv * it.ns, units = (P.base[lo + 1] - P.base[lo]) / per_u;
@@ -204,13 +215,13 @@ __device__ __forceinline__ void tmem_ld128_sync(uint32_t taddr, float* v) {
 #undef STA_R8
 #undef STA_R
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes, or 16 zero bytes where `some` is false.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// One arrival of this thread on `bar` once all its cp.async so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // True in one lane of the (whole, converged) warp. Unlike lane == 0 it tells the compiler that a
@@ -219,6 +230,28 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
+}
+
+// Asks for one CTA of this grid that has not started yet, to do its work here: the answer (16 bytes)
+// arrives on `bar`.
+__device__ __forceinline__ void clc_request(void* answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// blockIdx.x of the CTA that was taken over, or -1: none is left (no further request may be made).
+__device__ __forceinline__ int clc_answer(const void* answer) {
+  uint32_t got, x = 0;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\tld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}"
+      : "=&r"(got), "=&r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return got ? (int)x : -1;
 }
 
 // Bits of keys k0 .. k0 + 31 that lie in [lo, hi].
@@ -238,19 +271,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   // full[s] / empty[s]: a K or V tile is in stage s / may be overwritten. s_full[x]: S of slot x is in
   // TMEM (and every earlier MMA is done); p_half[x], p_full[x]: the P of its first 64 keys, of all of
-  // them is (128 threads each); o_full[x]: its last PV is done.
-  __shared__ __align__(8) uint64_t full[ST], empty[ST], s_full[2], p_half[2], p_full[2], o_full[2], q_full, tail, drain;
+  // them is (128 threads each); o_full[x]: the item's last PV of slot x is done; o_free[x]: its O has
+  // been read (128 threads); x_full: slot 1's row maxima and sums are in s_x; item_full / item_empty:
+  // s_item holds an item / has been read by the softmax, MMA, K and V warps.
+  __shared__ __align__(16) uint4 s_clc;
+  __shared__ __align__(8) uint64_t full[ST], empty[ST], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], q_full,
+      q_empty, x_full, tail, drain, clc_full, item_full[2], item_empty[2];
+  __shared__ Item s_item[2];
   __shared__ uint32_t s_tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Item it;
-  if (!get_item(A, P, req0, blockIdx.x, it)) return;
 
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   float2* s_x = reinterpret_cast<float2*>(smem + C::OFF_X);
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], A.box > 0 ? 1 : 32);  // TMA bytes, or the copying lanes
       mbar_init(&empty[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -258,10 +294,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_half[x], 128);
       mbar_init(&p_full[x], 128);
       mbar_init(&o_full[x], 1);
+      mbar_init(&o_free[x], 128);
+      mbar_init(&item_full[x], 1);
+      mbar_init(&item_empty[x], 11);
     }
-    mbar_init(&drain, 1);
     mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    mbar_init(&x_full, 128);
     mbar_init(&tail, 1);
+    mbar_init(&drain, 1);
+    mbar_init(&clc_full, 1);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -272,25 +314,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const int nj = it.j1 - it.j0;
 
+  // Every role runs over the same items: item k is in s_item[k & 1]. A wait that runs out ends the
+  // role's loop, and then, by their own waits, the others'.
   if (warp == kQWarp) {
-    // ------------------------------------------------------------ Q
-    if (lane == 0 && nj > 0) {
-      const uint32_t bytes = (uint32_t)(A.G * A.TQ * 128 * C::KH);
-      mbar_arrive_expect_tx(&q_full, bytes * (it.dual ? 2 : 1));
-      for (int x = 0; x <= it.dual; ++x)
+    // ------------------------------------------------------------ items and Q
+    // The CTA starts with its own item and takes over those of CTAs that have not started yet, in
+    // the grid's order (heaviest first), one ahead of the work.
+    if (lane == 0) {
+      bool ok = true;
+      int item = blockIdx.x, k = 0, nq = 0;
+      Item it;
+      for (int n = 0; ok && item >= 0; ++n) {
+        clc_request(&s_clc, &clc_full);
+        if (get_item(A, P, req0, item, it)) {
+          if (k >= 2) ok = mbar_wait(&item_empty[k & 1], ((k >> 1) & 1u) ^ 1u, A.err, 0x62b);
+          if (ok) {
+            s_item[k & 1] = it;
+            mbar_arrive(&item_full[k & 1]);
+            ++k;
+          }
+          if (ok && it.j1 > it.j0) {
+            if (nq > 0) ok = mbar_wait(&q_empty, (nq - 1) & 1u, A.err, 0x620);
+            if (ok) {
+              const uint32_t bytes = (uint32_t)(A.G * A.TQ * 128 * C::KH);
+              mbar_arrive_expect_tx(&q_full, bytes * (it.dual ? 2 : 1));
+              for (int x = 0; x <= it.dual; ++x)
 #pragma unroll
-        for (int kh = 0; kh < C::KH; ++kh)
-          tma_load_3d(smem + C::OFF_Q + x * C::TILE + kh * (kBM * 128), &tm_q, kh * 64, it.hk * A.G,
-                      it.q0 + it.t0 + x * A.TQ, &q_full);
-      mbar_wait(&q_full, 0, A.err, 0x620);  // shared memory is not released under the copy
+                for (int kh = 0; kh < C::KH; ++kh)
+                  tma_load_3d(smem + C::OFF_Q + x * C::TILE + kh * (kBM * 128), &tm_q, kh * 64, it.hk * A.G,
+                              it.q0 + it.t0 + x * A.TQ, &q_full);
+              ++nq;
+            }
+          }
+        }
+        item = mbar_wait(&clc_full, n & 1u, A.err, 0x62c) ? clc_answer(&s_clc) : -1;
+        fence_proxy_async_smem();  // the answer has been read before the next one is written
+      }
+      if (ok && k >= 2) ok = mbar_wait(&item_empty[k & 1], ((k >> 1) & 1u) ^ 1u, A.err, 0x62b);
+      if (ok) {
+        s_item[k & 1].end = 1;
+        mbar_arrive(&item_full[k & 1]);
+      }
+      if (nq > 0) mbar_wait(&q_full, (nq - 1) & 1u, A.err, 0x620);  // shared memory is not released under a copy
     }
   } else if (warp == kKWarp || warp == kVWarp) {
     // ------------------------------------------------------------ K or V: ring stages 2i and 2i + 1
     const bool is_v = warp == kVWarp;
-    const int pb = __ldg(A.page_indptr + it.r), pe = __ldg(A.page_indptr + it.r + 1);
     const int P0 = A.page_size;
+    int pb = 0, pe = 0;
     auto page_at = [&](int tok) -> int {  // list entry of a token, unchecked; -1 behind the list
       const int o = pb + tok / P0;
       return o >= 0 && o < pe ? __ldg(A.page_indices + o) : -1;
@@ -303,254 +375,331 @@ __global__ void __launch_bounds__(kThreads, 1)
       return page * P0 + tok % P0;
     };
     bool ok = true;
-    int i = 0;
-    if (A.box > 0) {
-      // a lane per TMA box (column block kh of box b); the next tile's page numbers are fetched
-      // while this tile's stage is waited for
-      const int b = lane / C::KH, kh = lane % C::KH, off = b * A.box;
-      const int boxes = kBN / A.box;
-      int pg = nj > 0 && b < boxes ? page_at(it.tile(it.j0) * kBN + off) : -1;
-      for (; i < nj; ++i) {
-        const int y = 2 * i + is_v, s = y % ST, tok0 = it.tile(it.j0 + i) * kBN, page = pg;
-        if (i + 1 < nj && b < boxes) pg = page_at(it.tile(it.j0 + i + 1) * kBN + off);
-        const int in = min(boxes, (it.len - tok0 + A.box - 1) / A.box);  // boxes with tokens
-        const bool tail_v = is_v && tok0 + kBN > it.len;                 // rows behind the sequence
-        if (lane == 0) ok = mbar_wait(&empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        uint8_t* dst = smem + C::OFF_KV + s * C::TILE;
-        uint64_t* bar = tail_v ? &tail : &full[s];
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(in * A.box * 128 * C::KH));
-        __syncwarp();
-        if (b < in)
-          tma_load_3d(dst + kh * (kBN * 128) + off * 128, is_v ? &tm_v : &tm_k, kh * 64, it.hk, row_at(page, tok0 + off), bar);
-        if (tail_v) {  // (the last tile of a list at most)
-          mbar_wait(&tail, 0, A.err, 0x622);
-          for (int z = (it.len - tok0) * 8 + lane; z < kBN * 8; z += 32)
-#pragma unroll
-            for (int k = 0; k < C::KH; ++k) *reinterpret_cast<uint4*>(dst + k * (kBN * 128) + z * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
+    int T = 0, n_tail = 0;  // tiles of earlier items; tail tiles so far
+    for (int k = 0; ok; ++k) {
+      if (!mbar_wait(&item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
+      const Item it = read_item(&s_item[k & 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+      if (it.end) break;
+      const int nj = it.j1 - it.j0;
+      int i = 0;
+      if (nj > 0) {
+        pb = __ldg(A.page_indptr + it.r);
+        pe = __ldg(A.page_indptr + it.r + 1);
+      }
+      if (A.box > 0) {
+        // a lane per TMA box (column block kh of box b); the next tile's page numbers are fetched
+        // while this tile's stage is waited for
+        const int b = lane / C::KH, kh = lane % C::KH, off = b * A.box;
+        const int boxes = kBN / A.box;
+        int pg = nj > 0 && b < boxes ? page_at(it.tile(it.j0) * kBN + off) : -1;
+        for (; i < nj; ++i) {
+          const int y = 2 * (T + i) + is_v, s = y % ST, tok0 = it.tile(it.j0 + i) * kBN, page = pg;
+          if (i + 1 < nj && b < boxes) pg = page_at(it.tile(it.j0 + i + 1) * kBN + off);
+          const int in = min(boxes, (it.len - tok0 + A.box - 1) / A.box);  // boxes with tokens
+          const bool tail_v = is_v && tok0 + kBN > it.len;                 // rows behind the sequence
+          if (lane == 0) ok = mbar_wait(&empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          uint8_t* dst = smem + C::OFF_KV + s * C::TILE;
+          uint64_t* bar = tail_v ? &tail : &full[s];
+          if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(in * A.box * 128 * C::KH));
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[s]);
-        }
-      }
-    } else {
-      // 16 bytes a lane: lane l looks up the rows of tokens l, l + 32, .. of the tile, which the
-      // copies take from it by shuffles
-      constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an instruction
-      const int ch = lane % LPR;
-      const __nv_bfloat16* src = (is_v ? A.v : A.k) + (int64_t)it.hk * D + ch * 8;
-      const int64_t row_elems = (int64_t)A.Hkv * D;
-      int pg[kBN / 32];
+          if (b < in)
+            tma_load_3d(dst + kh * (kBN * 128) + off * 128, is_v ? &tm_v : &tm_k, kh * 64, it.hk, row_at(page, tok0 + off), bar);
+          if (tail_v) {  // (the last tile of a list at most)
+            mbar_wait(&tail, n_tail++ & 1u, A.err, 0x622);
+            for (int z = (it.len - tok0) * 8 + lane; z < kBN * 8; z += 32)
 #pragma unroll
-      for (int g = 0; g < kBN / 32; ++g) {
-        const int tok = nj > 0 ? it.tile(it.j0) * kBN + 32 * g + lane : it.len;
-        pg[g] = tok < it.len ? page_at(tok) : -1;
-      }
-      for (; i < nj; ++i) {
-        const int y = 2 * i + is_v, s = y % ST, tok0 = it.tile(it.j0 + i) * kBN;
-        int row[kBN / 32];
-#pragma unroll
-        for (int g = 0; g < kBN / 32; ++g) {
-          const int tok = tok0 + 32 * g + lane;
-          row[g] = tok < it.len ? row_at(pg[g], tok) : -1;
-          const int next = i + 1 < nj ? it.tile(it.j0 + i + 1) * kBN + 32 * g + lane : it.len;
-          pg[g] = next < it.len ? page_at(next) : -1;
-        }
-        if (lane == 0) ok = mbar_wait(&empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        const uint32_t dst = smem_u32(smem + C::OFF_KV + s * C::TILE) + (ch >> 3) * (kBN * 128);
-#pragma unroll
-        for (int g = 0; g < kBN / 32; ++g) {
-#pragma unroll 8
-          for (int r0 = 0; r0 < 32; r0 += RPI) {
-            const int rr = r0 + lane / LPR, at = __shfl_sync(0xffffffffu, row[g], rr), m = 32 * g + rr;
-            const uint32_t d = dst + m * 128 + (((ch & 7) ^ (m & 7)) << 4);
-            if (at >= 0) cp_async16(d, src + at * row_elems);
-            else if (is_v) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(d), "r"(0) : "memory");
+              for (int k = 0; k < C::KH; ++k) *reinterpret_cast<uint4*>(dst + k * (kBN * 128) + z * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
           }
         }
-        cp_async_commit();
-        if (i >= kCpLag) {
-          cp_async_wait<kCpLag>();
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[(y - 2 * kCpLag) % ST]);
+      } else {
+        // 16 bytes a lane: lane l looks up the rows of tokens l, l + 32, .. of the tile, which the
+        // copies take from it by shuffles
+        constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an instruction
+        const int ch = lane % LPR;
+        const __nv_bfloat16* src = (is_v ? A.v : A.k) + (int64_t)it.hk * D + ch * 8;
+        const int64_t row_elems = (int64_t)A.Hkv * D;
+        int pg[kBN / 32];
+#pragma unroll
+        for (int g = 0; g < kBN / 32; ++g) {
+          const int tok = nj > 0 ? it.tile(it.j0) * kBN + 32 * g + lane : it.len;
+          pg[g] = tok < it.len ? page_at(tok) : -1;
+        }
+        for (; i < nj; ++i) {
+          const int y = 2 * (T + i) + is_v, s = y % ST, tok0 = it.tile(it.j0 + i) * kBN;
+          int row[kBN / 32];
+#pragma unroll
+          for (int g = 0; g < kBN / 32; ++g) {
+            const int tok = tok0 + 32 * g + lane;
+            row[g] = tok < it.len ? row_at(pg[g], tok) : -1;
+            const int next = i + 1 < nj ? it.tile(it.j0 + i + 1) * kBN + 32 * g + lane : it.len;
+            pg[g] = next < it.len ? page_at(next) : -1;
+          }
+          if (lane == 0) ok = mbar_wait(&empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          const uint32_t dst = smem_u32(smem + C::OFF_KV + s * C::TILE) + (ch >> 3) * (kBN * 128);
+#pragma unroll
+          for (int g = 0; g < kBN / 32; ++g) {
+            int at[32 / RPI];
+#pragma unroll
+            for (int r = 0; r < 32 / RPI; ++r) at[r] = __shfl_sync(0xffffffffu, row[g], r * RPI + lane / LPR);
+#pragma unroll
+            for (int r = 0; r < 32 / RPI; ++r) {
+              const int m = 32 * g + r * RPI + lane / LPR;  // rows behind the sequence: zeros
+              cp_async16(dst + m * 128 + (((ch & 7) ^ (m & 7)) << 4), src + max(at[r], 0) * row_elems, at[r] >= 0);
+            }
+          }
+          cp_async_arrive(&full[s]);
         }
       }
-      cp_async_wait<0>();  // the last tiles
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0)
-        for (int k = max(0, i - kCpLag); k < i; ++k) mbar_arrive(&full[(2 * k + is_v) % ST]);
+      T += i;
     }
     if (lane == 0)  // shared memory is not released under a copy
-      for (int k = max(0, i - (ST + 1) / 2); k < i; ++k) {
-        const int y = 2 * k + is_v;
-        if (y + ST >= 2 * i) mbar_wait(&full[y % ST], (y / ST) & 1u, A.err, 0x623);
+      for (int i = max(0, T - (ST + 1) / 2); i < T; ++i) {
+        const int y = 2 * i + is_v;
+        if (y + ST >= 2 * T) mbar_wait(&full[y % ST], (y / ST) & 1u, A.err, 0x623);
       }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
     // One thread issues both slots' products in turn, PV(j) and QK(j + 1) of slot 0, then of slot 1, so
     // that each slot's softmax has the time of the other's products. (An issuing thread for each slot
-    // let the two fall into step, both in the softmax at once and then both on the tensor core: 538 us
-    // against 413 us for the 8192-token prompt.)
-    if (nj > 0 && elect_one()) {
-      const uint64_t q0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-      const uint64_t k0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_KV), 16, 1024);
-      const uint64_t v0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_KV), kBN * 128, 1024);
-      bool ok = mbar_wait(&q_full, 0, A.err, 0x624);
-      // slot x takes list entry j0 + i: ring stages 2i (K) and 2i + 1 (V)
-      auto takes = [&](int x, int i) { return i < nj && (it.dual ? (x == 1 || it.j0 + i < it.j1a) : (i & 1) == x); };
-      auto qk = [&](int x, int i) {
-        const int y = 2 * i, s = y % ST;
-        if (!(ok = ok && mbar_wait(&full[s], (y / ST) & 1u, A.err, 0x625))) return;
-        tc_fence_after();
-        const uint64_t a = q0 + (uint64_t)((it.dual && x ? C::TILE : 0) >> 4), b = k0 + (uint64_t)((s * C::TILE) >> 4);
-        const uint32_t tS = tmem + C::S_COL + x * 128;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const int off = (kk >> 2) * (kBN * 128) + (kk & 3) * 32;
-          umma_bf16(tS, a + (uint64_t)(off >> 4), b + (uint64_t)(off >> 4), C::IDESC_QK, kk > 0 ? 1u : 0u);
-        }
-        umma_commit(&s_full[x]);
-        if (!it.dual || x == 1) umma_commit(&empty[s]);
-      };
-      auto pv = [&](int x, int i, int n) {  // n: this slot's tiles before
-        const int y = 2 * i + 1, s = y % ST;
-        const uint64_t b = v0 + (uint64_t)((s * C::TILE) >> 4);
-        const uint32_t tS = tmem + C::S_COL + x * 128, tO = tmem + C::O_COL + x * 128;
-        if (!(ok = ok && mbar_wait(&full[s], (y / ST) & 1u, A.err, 0x627))) return;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!(ok = mbar_wait(half ? &p_full[x] : &p_half[x], n & 1u, A.err, 0x626))) return;
+    // let the two fall into step, both in the softmax at once and then both on the tensor core: 542 us
+    // against 470 us for an 8192-token prompt, before the elected lane issued.)
+    const uint64_t q0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+    const uint64_t k0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_KV), 16, 1024);
+    const uint64_t v0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_KV), kBN * 128, 1024);
+    bool ok = true;
+    int T = 0, nq = 0;                       // tiles and Q loads of earlier items
+    int np0 = 0, np1 = 0, nf0 = 0, nf1 = 0;  // tiles, and items with tiles, of each slot so far
+    const bool by_lanes = A.box == 0;
+    for (int k = 0; ok; ++k) {
+      if (!mbar_wait(&item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
+      const Item it = read_item(&s_item[k & 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+      if (it.end) break;
+      const bool dual = it.dual;
+      const int nj = it.j1 - it.j0, na = it.j1a - it.j0;
+      if (elect_one() && nj > 0) {
+        // a wait that has run out fails the later ones at once; the products then issued read
+        // nothing but shared and tensor memory, and their results are not used
+        auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
+          if (!mbar_try_wait(bar, parity)) ok = ok && mbar_wait(bar, parity, A.err, code);
+        };
+        auto wait_full = [&](int y) {  // ring entry y: K of list entry y / 2, or V
+          wait(&full[y % ST], (y / ST) & 1u, 0x625);
+          if (by_lanes) fence_proxy_async_smem();  // cp.async wrote through the generic proxy
+        };
+        auto qk = [&](int x, int y) {
+          const uint64_t a = q0 + (uint64_t)((dual && x ? C::TILE : 0) >> 4), b = k0 + (uint64_t)((y % ST * C::TILE) >> 4);
+          const uint32_t tS = tmem + C::S_COL + x * 128;
           tc_fence_after();
 #pragma unroll
-          for (int kk = half * (kBN / 32); kk < (half + 1) * (kBN / 32); ++kk)
-            umma_bf16_ts(tO, tS + kk * 8, b + (uint64_t)((kk * 2048) >> 4), C::IDESC_PV, (n > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const int off = (kk >> 2) * (kBN * 128) + (kk & 3) * 32;
+            umma_bf16(tS, a + (uint64_t)(off >> 4), b + (uint64_t)(off >> 4), C::IDESC_QK, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[x]);
+        };
+        auto pv = [&](int x, int y, uint32_t parity, bool first) {
+          const uint64_t b = v0 + (uint64_t)((y % ST * C::TILE) >> 4);
+          const uint32_t tS = tmem + C::S_COL + x * 128, tO = tmem + C::O_COL + x * 128;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            wait(half ? &p_full[x] : &p_half[x], parity, 0x626);
+            tc_fence_after();
+#pragma unroll
+            for (int kk = half * (kBN / 32); kk < (half + 1) * (kBN / 32); ++kk)
+              umma_bf16_ts(tO, tS + kk * 8, b + (uint64_t)((kk * 2048) >> 4), C::IDESC_PV, (kk > 0 || !first) ? 1u : 0u);
+          }
+        };
+        wait(&q_full, nq & 1u, 0x624);
+        int y = 2 * T;  // ring entry of the K of the current tile
+        if (dual) {
+          wait_full(y);
+          if (na > 0) qk(0, y);
+          qk(1, y);
+          umma_commit(&empty[y % ST]);
+          if (nj == 1) umma_commit(&q_empty);
+          if (nf0 > 0 && na > 0) wait(&o_free[0], (nf0 - 1) & 1u, 0x62e);
+          if (nf1 > 0) wait(&o_free[1], (nf1 - 1) & 1u, 0x62e);
+          for (int n = 0; ok && n < nj; ++n, y += 2) {
+            wait_full(y + 1);
+            if (n < na) {
+              pv(0, y + 1, (np0 + n) & 1u, n == 0);
+              if (n + 1 < na) {
+                wait_full(y + 2);
+                qk(0, y + 2);
+              } else {
+                umma_commit(&o_full[0]);
+              }
+            }
+            pv(1, y + 1, (np1 + n) & 1u, n == 0);
+            umma_commit(&empty[(y + 1) % ST]);
+            if (n + 1 < nj) {
+              if (n + 1 >= na) wait_full(y + 2);
+              qk(1, y + 2);
+              umma_commit(&empty[(y + 2) % ST]);
+              if (n + 2 == nj) umma_commit(&q_empty);
+            } else {
+              umma_commit(&o_full[1]);
+            }
+          }
+        } else {
+          for (int x = 0; x < 2 && x < nj; ++x) {
+            wait_full(y + 2 * x);
+            qk(x, y + 2 * x);
+            umma_commit(&empty[(y + 2 * x) % ST]);
+            if (x + 1 == nj) umma_commit(&q_empty);
+          }
+          if (nf0 > 0) wait(&o_free[0], (nf0 - 1) & 1u, 0x62e);
+          if (nf1 > 0 && nj > 1) wait(&o_free[1], (nf1 - 1) & 1u, 0x62e);
+          for (int e = 0; ok && e < nj; ++e, y += 2) {
+            const int x = e & 1;
+            wait_full(y + 1);
+            pv(x, y + 1, ((x ? np1 : np0) + (e >> 1)) & 1u, e < 2);
+            umma_commit(&empty[(y + 1) % ST]);
+            if (e + 2 < nj) {
+              wait_full(y + 4);
+              qk(x, y + 4);
+              umma_commit(&empty[(y + 4) % ST]);
+              if (e + 3 == nj) umma_commit(&q_empty);
+            } else {
+              umma_commit(&o_full[x]);
+            }
+          }
         }
-        if (!it.dual || x == 1) umma_commit(&empty[s]);
-      };
-      const int step = it.dual ? 1 : 2;
-      for (int x = 0; x < 2; ++x)
-        if (takes(x, it.dual ? 0 : x)) qk(x, it.dual ? 0 : x);
-      for (int n = 0; ok && n * step < nj; ++n)
-        for (int x = 0; x < 2; ++x) {
-          const int e = n * step + (it.dual ? 0 : x);
-          if (!takes(x, e)) continue;
-          pv(x, e, n);
-          if (takes(x, e + step)) qk(x, e + step);
-          else if (ok) umma_commit(&o_full[x]);
+        if (!ok) {  // TMEM is not freed under an MMA
+          umma_commit(&drain);
+          mbar_wait(&drain, 0, A.err, 0x628);
         }
-      if (!ok) {  // TMEM is not freed under an MMA
-        umma_commit(&drain);
-        mbar_wait(&drain, 0, A.err, 0x628);
       }
+      ok = !__any_sync(0xffffffffu, !ok);
+      T += nj;
+      nq += nj > 0;
+      np0 += it.count(0);
+      np1 += it.count(1);
+      nf0 += it.count(0) > 0;
+      nf1 += it.count(1) > 0;
     }
   } else {
     // ------------------------------------------------------------ softmax of one slot
     const int x = warp >> 2, qd = warp & 3, m = qd * 32 + lane;
     const uint32_t t_lane = tmem + ((uint32_t)(qd * 32) << 16);
     const uint32_t tS = t_lane + C::S_COL + x * 128, tO = t_lane + C::O_COL + x * 128;
-    const int cnt = it.count(x);
-    const int tt = m / A.G, t = it.t0 + (it.dual ? x * A.TQ : 0) + tt, h = it.hk * A.G + (m - tt * A.G);
-    const bool live = tt < A.TQ && t < it.n;
-    const bool warp_live = __any_sync(0xffffffffu, live);
-    const int pos = it.pos0 + t;
-    const Seen sn = seen(A, pos, pos, it.len);
     const float c = A.scale_log2;
-    float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int n = 0; n < cnt; ++n) {
-      const int k0 = it.tile(it.j0 + (it.dual ? n : 2 * n + x)) * kBN;
-      if (!mbar_wait(&s_full[x], n & 1u, A.err, 0x629)) {
-        ok = false;
-        break;
+    uint32_t ns = 0, no = 0, nx = 0;  // tiles, results and merges of this slot so far
+    for (int k = 0; ok; ++k) {
+      if (!mbar_wait(&item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
+      const Item it = read_item(&s_item[k & 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+      if (it.end) break;
+      const int cnt = it.count(x);
+      const int tt = m / A.G, t = it.t0 + (it.dual ? x * A.TQ : 0) + tt, h = it.hk * A.G + (m - tt * A.G);
+      const bool live = tt < A.TQ && t < it.n;
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      const int pos = it.pos0 + t;
+      const Seen sn = seen(A, pos, pos, it.len);
+      float m_ref = -INFINITY, l = 0.f;
+      for (int n = 0; n < cnt; ++n) {
+        const int k0 = it.tile(it.j0 + (it.dual ? n : 2 * n + x)) * kBN;
+        if (!mbar_wait(&s_full[x], ns++ & 1u, A.err, 0x629)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (warp_live) {
+          float s[128];
+          tmem_ld128_sync(tS, s);
+          const bool all = (k0 >= sn.lo && k0 + kBN - 1 <= sn.hi) || k0 + kBN - 1 <= sn.g1 || !live;
+          if (!__all_sync(0xffffffffu, all)) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t bits = range_bits(sn.lo, sn.hi, k0 + 32 * w) | range_bits(0, sn.g1, k0 + 32 * w);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[32 * w + e] = (bits & (1u << e)) ? s[32 * w + e] : -INFINITY;
+            }
+          }
+          float m8[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            m8[y] = fmax3(s[y], s[y + 8], s[y + 16]);
+#pragma unroll
+            for (int z = 24; z < 120; z += 16) m8[y] = fmax3(m8[y], s[y + z], s[y + z + 8]);
+            m8[y] = fmaxf(m8[y], s[y + 120]);
+          }
+          const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * c;
+          float alpha = 1.f;
+          bool need = false;
+          if (mx > m_ref + kRescaleThreshold) {
+            if (m_ref != -INFINITY) {
+              alpha = ex2(m_ref - mx);
+              need = true;
+            }
+            m_ref = mx;
+          }
+          if (__any_sync(0xffffffffu, need)) {  // (S of this tile is there: the earlier PV is done)
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              float o[32];
+              tmem_ld32_sync(tO + c0, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= alpha;
+              tmem_st32_sync(tO + c0, reinterpret_cast<const uint32_t*>(o));
+            }
+          }
+          const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+          const uint64_t c2 = f32x2_pack(c, c), nm2 = f32x2_pack(neg_m, neg_m);
+          uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float a0, a1;
+              f32x2_unpack(f32x2_fma(f32x2_pack(s[64 * half + 2 * e], s[64 * half + 2 * e + 1]), c2, nm2), a0, a1);
+              const float p0 = ex2(a0), p1 = ex2(a1);
+              l2[e & 3] = f32x2_add(l2[e & 3], f32x2_pack(p0, p1));
+              pk[e] = pack_bf16x2(p0, p1);  // rounded for the MMA; the sum takes the fp32 values
+            }
+            tmem_st32_sync(tS + 32 * half, pk);
+            if (half == 0) {
+              tc_fence_before();
+              mbar_arrive(&p_half[x]);
+            }
+          }
+          float lp[8];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) f32x2_unpack(l2[y], lp[2 * y], lp[2 * y + 1]);
+          l = l * alpha + (((lp[0] + lp[1]) + (lp[2] + lp[3])) + ((lp[4] + lp[5]) + (lp[6] + lp[7])));
+        }
+        if (!warp_live) mbar_arrive(&p_half[x]);
+        tc_fence_before();
+        mbar_arrive(&p_full[x]);
       }
+      // ---- result
+      if (ok && cnt > 0) ok = mbar_wait(&o_full[x], no++ & 1u, A.err, 0x62a);
       tc_fence_after();
-      if (warp_live) {
-        float s[128];
-        tmem_ld128_sync(tS, s);
-        const bool all = (k0 >= sn.lo && k0 + kBN - 1 <= sn.hi) || k0 + kBN - 1 <= sn.g1 || !live;
-        if (!__all_sync(0xffffffffu, all)) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t bits = range_bits(sn.lo, sn.hi, k0 + 32 * w) | range_bits(0, sn.g1, k0 + 32 * w);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[32 * w + e] = (bits & (1u << e)) ? s[32 * w + e] : -INFINITY;
-          }
-        }
-        float m8[8];
-#pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          m8[y] = fmax3(s[y], s[y + 8], s[y + 16]);
-#pragma unroll
-          for (int z = 24; z < 120; z += 16) m8[y] = fmax3(m8[y], s[y + z], s[y + z + 8]);
-          m8[y] = fmaxf(m8[y], s[y + 120]);
-        }
-        const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * c;
-        float alpha = 1.f;
-        bool need = false;
-        if (mx > m_ref + kRescaleThreshold) {
-          if (m_ref != -INFINITY) {
-            alpha = ex2(m_ref - mx);
-            need = true;
-          }
-          m_ref = mx;
-        }
-        if (__any_sync(0xffffffffu, need)) {  // (S of this tile is there: the earlier PV is done)
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float o[32];
-            tmem_ld32_sync(tO + c0, o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-            tmem_st32_sync(tO + c0, reinterpret_cast<const uint32_t*>(o));
-          }
-        }
-        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
-        const uint64_t c2 = f32x2_pack(c, c), nm2 = f32x2_pack(neg_m, neg_m);
-        uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float a0, a1;
-            f32x2_unpack(f32x2_fma(f32x2_pack(s[64 * half + 2 * e], s[64 * half + 2 * e + 1]), c2, nm2), a0, a1);
-            const float p0 = ex2(a0), p1 = ex2(a1);
-            l2[e & 3] = f32x2_add(l2[e & 3], f32x2_pack(p0, p1));
-            pk[e] = pack_bf16x2(p0, p1);  // rounded for the MMA; the sum takes the fp32 values
-          }
-          tmem_st32_sync(tS + 32 * half, pk);
-          if (half == 0) {
-            tc_fence_before();
-            mbar_arrive(&p_half[x]);
-          }
-        }
-        float lp[8];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) f32x2_unpack(l2[y], lp[2 * y], lp[2 * y + 1]);
-        l = l * alpha + (((lp[0] + lp[1]) + (lp[2] + lp[3])) + ((lp[4] + lp[5]) + (lp[6] + lp[7])));
+      float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and, for a single tile, of slot 1's
+      const bool other = !it.dual && x == 0 && it.count(1) > 0;
+      if (!it.dual && x == 1 && cnt > 0) {
+        s_x[m] = make_float2(m_ref, l);
+        tc_fence_before();
+        mbar_arrive(&x_full);
       }
-      if (!warp_live) mbar_arrive(&p_half[x]);
-      tc_fence_before();
-      mbar_arrive(&p_full[x]);
-    }
-    // ---- result
-    if (ok && cnt > 0) mbar_wait(&o_full[x], 0, A.err, 0x62a);
-    tc_fence_after();
-    float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and, for a single tile, of slot 1's
-    bool other = false;
-    if (!it.dual) {
-      if (x == 1) s_x[m] = make_float2(cnt > 0 ? m_ref : -INFINITY, l);
-      tc_fence_before();
-      named_bar_sync(1, 256);
-      tc_fence_after();
-      if (x == 0) {
+      if (other) {
+        if (ok) ok = mbar_wait(&x_full, nx++ & 1u, A.err, 0x62f);
+        tc_fence_after();
         const float2 ml = s_x[m];
-        other = it.count(1) > 0;
         const float M = fmaxf(m_ref, ml.x);
         if (M != -INFINITY) {
           w0 = exp2f(m_ref - M);
@@ -559,49 +708,53 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_ref = M;
         }
       }
-    }
-    if (warp_live && (it.dual || x == 0)) {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float row_lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
-      w0 *= inv;
-      w1 *= inv;
-      const int64_t row = (int64_t)(it.q0 + t) * A.Hq + h;
-      const int64_t prow = it.ns > 1 ? P.part[it.rank] + ((int64_t)it.c * P.qn[it.rank] + t) * A.Hq + h : 0;
+      if (warp_live && (it.dual || x == 0)) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float row_lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+        w0 *= inv;
+        w1 *= inv;
+        const int64_t row = (int64_t)(it.q0 + t) * A.Hq + h;
+        const int64_t prow = it.ns > 1 ? P.part[it.rank] + ((int64_t)it.c * P.qn[it.rank] + t) * A.Hq + h : 0;
 #pragma unroll
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        float o[32];
-        if (cnt > 0) {
-          tmem_ld32_sync(tO + c0, o);
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          float o[32];
+          if (cnt > 0) {
+            tmem_ld32_sync(tO + c0, o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= w0;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
-        }
-        if (other) {
-          float o1[32];
-          tmem_ld32_sync(tO + 128 + c0, o1);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], w1, o[e]);
-        }
-        if (live) {
-          if (it.ns > 1) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(A.part_o + prow * D + c0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 32; ++e) o[e] *= w0;
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(A.o + row * D + c0 + e) =
-                  make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]), pack_bf16x2(o[e + 4], o[e + 5]),
-                             pack_bf16x2(o[e + 6], o[e + 7]));
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (other) {
+            float o1[32];
+            tmem_ld32_sync(tO + 128 + c0, o1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], w1, o[e]);
+          }
+          if (live) {
+            if (it.ns > 1) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(A.part_o + prow * D + c0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                *reinterpret_cast<uint4*>(A.o + row * D + c0 + e) =
+                    make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]), pack_bf16x2(o[e + 4], o[e + 5]),
+                               pack_bf16x2(o[e + 6], o[e + 7]));
+            }
           }
         }
+        if (live) {
+          if (it.ns > 1) A.part_lse[prow] = row_lse;
+          else if (A.lse) A.lse[row] = row_lse;
+        }
       }
-      if (live) {
-        if (it.ns > 1) A.part_lse[prow] = row_lse;
-        else if (A.lse) A.lse[row] = row_lse;
-      }
+      // what has been read of O may be overwritten by the slot's next item
+      tc_fence_before();
+      if ((it.dual || x == 0) && cnt > 0) mbar_arrive(&o_free[x]);
+      if (other) mbar_arrive(&o_free[1]);
     }
   }
   tc_fence_before();
