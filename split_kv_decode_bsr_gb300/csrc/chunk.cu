@@ -12,8 +12,8 @@
 // chunks of their tile list, whose normalised fp32 partials a second kernel merges by
 // log-sum-exp.
 //
-// Roles (12 warps, one CTA an SM): warps 0..3 and 4..7 the softmax of slots 0 and 1 (a thread a
-// row), warp 8 issues the MMAs, warps 9, 10 and 11 load V, K and Q.
+// Roles (20 warps, one CTA an SM): warps 0..7 and 8..15 the softmax of slots 0 and 1 (two threads a
+// row), warp 16 issues the MMAs, warps 17 and 18 load V and K, warp 19 finds items and loads Q.
 // S = Q K^T (M 128, N 128) and O += P V (P bf16 over the first half of S in tensor memory) run as
 // tcgen05.mma; a slot's order on the tensor core is PV(j), QK(j + 1), and one slot's MMAs run
 // under the other's softmax. S and O of both slots fill the 512 TMEM columns. The softmax is the
@@ -38,8 +38,8 @@ namespace {
 
 constexpr int kBM = 128;  // rows of a query tile
 constexpr int kBN = 128;  // keys of a tile
-constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kVWarp = 9, kKWarp = 10, kQWarp = 11;
+constexpr int kThreads = 640;
+constexpr int kMmaWarp = 16, kVWarp = 17, kKWarp = 18, kQWarp = 19;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 struct ChunkArgs {
@@ -177,6 +177,23 @@ __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP>& P,
   return true;
 }
 
+// Behind the tiles in shared memory.
+template <int ST>
+struct Shared {
+  uint4 clc;  // answer to a request for another CTA's item
+  // full[s] / empty[s]: a K or V tile is in stage s / may be overwritten. s_full[x]: S of slot x is in
+  // TMEM (and every earlier MMA is done); p_half[x], p_full[x]: the P of its first, its last 64 keys is
+  // (128 threads each); o_full[x]: the item's last PV of slot x is done; o_free[x]: its O has been
+  // read (256 threads); x_full: slot 1's row maxima and sums of a single tile are in row; item_full /
+  // item_empty: item holds an item / has been read by the softmax, MMA, K and V warps.
+  uint64_t full[ST], empty[ST], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], q_full, q_empty, x_full, tail,
+      drain, clc_full, item_full[2], item_empty[2];
+  Item item[2];
+  uint32_t tmem;
+  uint8_t ok[2][2][2][4];    // [item & 1][slot][half][quadrant]: the warp's waits held
+  float row[2][2][kBM];      // [slot][half][row]: a value from one of a row's two threads to the other
+};
+
 template <int D>
 struct Cfg {
   static constexpr int KH = D / 64;            // 128-byte column blocks of a row
@@ -184,36 +201,40 @@ struct Cfg {
   static constexpr int STAGES = D == 128 ? 5 : 10;
   static constexpr int OFF_Q = 0;              // two tiles
   static constexpr int OFF_KV = 2 * TILE;
-  static constexpr int OFF_X = OFF_KV + STAGES * TILE;  // slot 1's row maximum and sum, for the merge of a single tile
-  static constexpr int SMEM = 1024 + OFF_X + kBM * 8;
+  static constexpr int OFF_S = OFF_KV + STAGES * TILE;  // Shared
+  static constexpr int SMEM = OFF_S + (int)sizeof(Shared<STAGES>);
+  static_assert(SMEM <= 227 * 1024, "one CTA an SM");
   static constexpr uint32_t IDESC_QK = umma_idesc_bf16(kBM, kBN, 0, 0);
   static constexpr uint32_t IDESC_PV = umma_idesc_bf16(kBM, D, 0, 1);
   static constexpr int S_COL = 0;              // slot s: + 128 s; P over its first 64 columns
   static constexpr int O_COL = 256;            // slot s: + 128 s
 };
 
-// 128 consecutive TMEM columns of this thread's lane, loaded and waited for in one statement.
-#define STA_R(i) "=r"(r[i])
-#define STA_R8(i) STA_R(i), STA_R(i + 1), STA_R(i + 2), STA_R(i + 3), STA_R(i + 4), STA_R(i + 5), STA_R(i + 6), STA_R(i + 7)
-#define STA_R32X(i) STA_R8(i), STA_R8(i + 8), STA_R8(i + 16), STA_R8(i + 24)
-__device__ __forceinline__ void tmem_ld128_sync(uint32_t taddr, float* v) {
+// 16 (8) consecutive TMEM columns of this thread's lane, accessed and waited for in one statement.
+__device__ __forceinline__ void tmem_ld8_sync(uint32_t taddr, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, "
-      "%37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, "
-      "%59, %60, %61, %62, %63, %64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, "
-      "%81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, %101, "
-      "%102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, "
-      "%120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : STA_R32X(0), STA_R32X(32), STA_R32X(64), STA_R32X(96)
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
       : "r"(taddr)
       : "memory");
 }
-#undef STA_R32X
-#undef STA_R8
-#undef STA_R
+__device__ __forceinline__ void tmem_st8_sync(uint32_t taddr, const float* v) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16_sync(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 
 // 16 bytes, or 16 zero bytes where `some` is false.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool some) {
@@ -268,54 +289,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ Plan<CAP> P, int req0) {
   using C = Cfg<D>;
   constexpr int ST = C::STAGES;
-  extern __shared__ uint8_t smem_raw[];
-  // full[s] / empty[s]: a K or V tile is in stage s / may be overwritten. s_full[x]: S of slot x is in
-  // TMEM (and every earlier MMA is done); p_half[x], p_full[x]: the P of its first 64 keys, of all of
-  // them is (128 threads each); o_full[x]: the item's last PV of slot x is done; o_free[x]: its O has
-  // been read (128 threads); x_full: slot 1's row maxima and sums are in s_x; item_full / item_empty:
-  // s_item holds an item / has been read by the softmax, MMA, K and V warps.
-  __shared__ __align__(16) uint4 s_clc;
-  __shared__ __align__(8) uint64_t full[ST], empty[ST], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], q_full,
-      q_empty, x_full, tail, drain, clc_full, item_full[2], item_empty[2];
-  __shared__ Item s_item[2];
-  __shared__ uint32_t s_tmem;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Shared<ST>& sh = *reinterpret_cast<Shared<ST>*>(smem + C::OFF_S);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  const uint32_t raw = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  float2* s_x = reinterpret_cast<float2*>(smem + C::OFF_X);
+  if (smem_u32(smem) & 1023) {  // swizzle atoms start on 1024-byte boundaries
+    record_error(A.err, 0x607);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&full[s], A.box > 0 ? 1 : 32);  // TMA bytes, or the copying lanes
-      mbar_init(&empty[s], 1);
+      mbar_init(&sh.full[s], A.box > 0 ? 1 : 32);  // TMA bytes, or the copying lanes
+      mbar_init(&sh.empty[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&s_full[x], 1);
-      mbar_init(&p_half[x], 128);
-      mbar_init(&p_full[x], 128);
-      mbar_init(&o_full[x], 1);
-      mbar_init(&o_free[x], 128);
-      mbar_init(&item_full[x], 1);
-      mbar_init(&item_empty[x], 11);
+      mbar_init(&sh.s_full[x], 1);
+      mbar_init(&sh.p_half[x], 128);
+      mbar_init(&sh.p_full[x], 128);
+      mbar_init(&sh.o_full[x], 1);
+      mbar_init(&sh.o_free[x], 256);
+      mbar_init(&sh.item_full[x], 1);
+      mbar_init(&sh.item_empty[x], kMmaWarp + 3);
     }
-    mbar_init(&q_full, 1);
-    mbar_init(&q_empty, 1);
-    mbar_init(&x_full, 128);
-    mbar_init(&tail, 1);
-    mbar_init(&drain, 1);
-    mbar_init(&clc_full, 1);
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.x_full, 128);
+    mbar_init(&sh.tail, 1);
+    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.clc_full, 1);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(&s_tmem, 512);
+    tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = sh.tmem;
 
-  // Every role runs over the same items: item k is in s_item[k & 1]. A wait that runs out ends the
+  // Every role runs over the same items: item k is in sh.item[k & 1]. A wait that runs out ends the
   // role's loop, and then, by their own waits, the others'.
   if (warp == kQWarp) {
     // ------------------------------------------------------------ items and Q
@@ -326,37 +338,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       int item = blockIdx.x, k = 0, nq = 0;
       Item it;
       for (int n = 0; ok && item >= 0; ++n) {
-        clc_request(&s_clc, &clc_full);
+        clc_request(&sh.clc, &sh.clc_full);
         if (get_item(A, P, req0, item, it)) {
-          if (k >= 2) ok = mbar_wait(&item_empty[k & 1], ((k >> 1) & 1u) ^ 1u, A.err, 0x62b);
+          if (k >= 2) ok = mbar_wait(&sh.item_empty[k & 1], ((k >> 1) & 1u) ^ 1u, A.err, 0x62b);
           if (ok) {
-            s_item[k & 1] = it;
-            mbar_arrive(&item_full[k & 1]);
+            sh.item[k & 1] = it;
+            mbar_arrive(&sh.item_full[k & 1]);
             ++k;
           }
           if (ok && it.j1 > it.j0) {
-            if (nq > 0) ok = mbar_wait(&q_empty, (nq - 1) & 1u, A.err, 0x620);
+            if (nq > 0) ok = mbar_wait(&sh.q_empty, (nq - 1) & 1u, A.err, 0x620);
             if (ok) {
               const uint32_t bytes = (uint32_t)(A.G * A.TQ * 128 * C::KH);
-              mbar_arrive_expect_tx(&q_full, bytes * (it.dual ? 2 : 1));
+              mbar_arrive_expect_tx(&sh.q_full, bytes * (it.dual ? 2 : 1));
               for (int x = 0; x <= it.dual; ++x)
 #pragma unroll
                 for (int kh = 0; kh < C::KH; ++kh)
                   tma_load_3d(smem + C::OFF_Q + x * C::TILE + kh * (kBM * 128), &tm_q, kh * 64, it.hk * A.G,
-                              it.q0 + it.t0 + x * A.TQ, &q_full);
+                              it.q0 + it.t0 + x * A.TQ, &sh.q_full);
               ++nq;
             }
           }
         }
-        item = mbar_wait(&clc_full, n & 1u, A.err, 0x62c) ? clc_answer(&s_clc) : -1;
+        item = mbar_wait(&sh.clc_full, n & 1u, A.err, 0x62c) ? clc_answer(&sh.clc) : -1;
         fence_proxy_async_smem();  // the answer has been read before the next one is written
       }
-      if (ok && k >= 2) ok = mbar_wait(&item_empty[k & 1], ((k >> 1) & 1u) ^ 1u, A.err, 0x62b);
+      if (ok && k >= 2) ok = mbar_wait(&sh.item_empty[k & 1], ((k >> 1) & 1u) ^ 1u, A.err, 0x62b);
       if (ok) {
-        s_item[k & 1].end = 1;
-        mbar_arrive(&item_full[k & 1]);
+        sh.item[k & 1].end = 1;
+        mbar_arrive(&sh.item_full[k & 1]);
       }
-      if (nq > 0) mbar_wait(&q_full, (nq - 1) & 1u, A.err, 0x620);  // shared memory is not released under a copy
+      if (nq > 0) mbar_wait(&sh.q_full, (nq - 1) & 1u, A.err, 0x620);  // shared memory is not released under a copy
     }
   } else if (warp == kKWarp || warp == kVWarp) {
     // ------------------------------------------------------------ K or V: ring stages 2i and 2i + 1
@@ -377,10 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int T = 0, n_tail = 0;  // tiles of earlier items; tail tiles so far
     for (int k = 0; ok; ++k) {
-      if (!mbar_wait(&item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
-      const Item it = read_item(&s_item[k & 1]);
+      if (!mbar_wait(&sh.item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
+      const Item it = read_item(&sh.item[k & 1]);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+      if (lane == 0) mbar_arrive(&sh.item_empty[k & 1]);
       if (it.end) break;
       const int nj = it.j1 - it.j0;
       int i = 0;
@@ -399,23 +411,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i + 1 < nj && b < boxes) pg = page_at(it.tile(it.j0 + i + 1) * kBN + off);
           const int in = min(boxes, (it.len - tok0 + A.box - 1) / A.box);  // boxes with tokens
           const bool tail_v = is_v && tok0 + kBN > it.len;                 // rows behind the sequence
-          if (lane == 0) ok = mbar_wait(&empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
+          if (lane == 0) ok = mbar_wait(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
           uint8_t* dst = smem + C::OFF_KV + s * C::TILE;
-          uint64_t* bar = tail_v ? &tail : &full[s];
+          uint64_t* bar = tail_v ? &sh.tail : &sh.full[s];
           if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(in * A.box * 128 * C::KH));
           __syncwarp();
           if (b < in)
             tma_load_3d(dst + kh * (kBN * 128) + off * 128, is_v ? &tm_v : &tm_k, kh * 64, it.hk, row_at(page, tok0 + off), bar);
           if (tail_v) {  // (the last tile of a list at most)
-            mbar_wait(&tail, n_tail++ & 1u, A.err, 0x622);
+            mbar_wait(&sh.tail, n_tail++ & 1u, A.err, 0x622);
             for (int z = (it.len - tok0) * 8 + lane; z < kBN * 8; z += 32)
 #pragma unroll
               for (int k = 0; k < C::KH; ++k) *reinterpret_cast<uint4*>(dst + k * (kBN * 128) + z * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full[s]);
+            if (lane == 0) mbar_arrive(&sh.full[s]);
           }
         }
       } else {
@@ -441,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int next = i + 1 < nj ? it.tile(it.j0 + i + 1) * kBN + 32 * g + lane : it.len;
             pg[g] = next < it.len ? page_at(next) : -1;
           }
-          if (lane == 0) ok = mbar_wait(&empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
+          if (lane == 0) ok = mbar_wait(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
           const uint32_t dst = smem_u32(smem + C::OFF_KV + s * C::TILE) + (ch >> 3) * (kBN * 128);
@@ -456,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               cp_async16(dst + m * 128 + (((ch & 7) ^ (m & 7)) << 4), src + max(at[r], 0) * row_elems, at[r] >= 0);
             }
           }
-          cp_async_arrive(&full[s]);
+          cp_async_arrive(&sh.full[s]);
         }
       }
       T += i;
@@ -464,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0)  // shared memory is not released under a copy
       for (int i = max(0, T - (ST + 1) / 2); i < T; ++i) {
         const int y = 2 * i + is_v;
-        if (y + ST >= 2 * T) mbar_wait(&full[y % ST], (y / ST) & 1u, A.err, 0x623);
+        if (y + ST >= 2 * T) mbar_wait(&sh.full[y % ST], (y / ST) & 1u, A.err, 0x623);
       }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
@@ -480,10 +492,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int np0 = 0, np1 = 0, nf0 = 0, nf1 = 0;  // tiles, and items with tiles, of each slot so far
     const bool by_lanes = A.box == 0;
     for (int k = 0; ok; ++k) {
-      if (!mbar_wait(&item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
-      const Item it = read_item(&s_item[k & 1]);
+      if (!mbar_wait(&sh.item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
+      const Item it = read_item(&sh.item[k & 1]);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+      if (lane == 0) mbar_arrive(&sh.item_empty[k & 1]);
       if (it.end) break;
       const bool dual = it.dual;
       const int nj = it.j1 - it.j0, na = it.j1a - it.j0;
@@ -494,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!mbar_try_wait(bar, parity)) ok = ok && mbar_wait(bar, parity, A.err, code);
         };
         auto wait_full = [&](int y) {  // ring entry y: K of list entry y / 2, or V
-          wait(&full[y % ST], (y / ST) & 1u, 0x625);
+          wait(&sh.full[y % ST], (y / ST) & 1u, 0x625);
           if (by_lanes) fence_proxy_async_smem();  // cp.async wrote through the generic proxy
         };
         auto qk = [&](int x, int y) {
@@ -506,30 +518,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int off = (kk >> 2) * (kBN * 128) + (kk & 3) * 32;
             umma_bf16(tS, a + (uint64_t)(off >> 4), b + (uint64_t)(off >> 4), C::IDESC_QK, kk > 0 ? 1u : 0u);
           }
-          umma_commit(&s_full[x]);
+          umma_commit(&sh.s_full[x]);
         };
         auto pv = [&](int x, int y, uint32_t parity, bool first) {
           const uint64_t b = v0 + (uint64_t)((y % ST * C::TILE) >> 4);
           const uint32_t tS = tmem + C::S_COL + x * 128, tO = tmem + C::O_COL + x * 128;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            wait(half ? &p_full[x] : &p_half[x], parity, 0x626);
+            wait(half ? &sh.p_full[x] : &sh.p_half[x], parity, 0x626);
             tc_fence_after();
 #pragma unroll
             for (int kk = half * (kBN / 32); kk < (half + 1) * (kBN / 32); ++kk)
               umma_bf16_ts(tO, tS + kk * 8, b + (uint64_t)((kk * 2048) >> 4), C::IDESC_PV, (kk > 0 || !first) ? 1u : 0u);
           }
         };
-        wait(&q_full, nq & 1u, 0x624);
+        wait(&sh.q_full, nq & 1u, 0x624);
         int y = 2 * T;  // ring entry of the K of the current tile
         if (dual) {
           wait_full(y);
           if (na > 0) qk(0, y);
           qk(1, y);
-          umma_commit(&empty[y % ST]);
-          if (nj == 1) umma_commit(&q_empty);
-          if (nf0 > 0 && na > 0) wait(&o_free[0], (nf0 - 1) & 1u, 0x62e);
-          if (nf1 > 0) wait(&o_free[1], (nf1 - 1) & 1u, 0x62e);
+          umma_commit(&sh.empty[y % ST]);
+          if (nj == 1) umma_commit(&sh.q_empty);
+          if (nf0 > 0 && na > 0) wait(&sh.o_free[0], (nf0 - 1) & 1u, 0x62e);
+          if (nf1 > 0) wait(&sh.o_free[1], (nf1 - 1) & 1u, 0x62e);
           for (int n = 0; ok && n < nj; ++n, y += 2) {
             wait_full(y + 1);
             if (n < na) {
@@ -538,47 +550,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait_full(y + 2);
                 qk(0, y + 2);
               } else {
-                umma_commit(&o_full[0]);
+                umma_commit(&sh.o_full[0]);
               }
             }
             pv(1, y + 1, (np1 + n) & 1u, n == 0);
-            umma_commit(&empty[(y + 1) % ST]);
+            umma_commit(&sh.empty[(y + 1) % ST]);
             if (n + 1 < nj) {
               if (n + 1 >= na) wait_full(y + 2);
               qk(1, y + 2);
-              umma_commit(&empty[(y + 2) % ST]);
-              if (n + 2 == nj) umma_commit(&q_empty);
+              umma_commit(&sh.empty[(y + 2) % ST]);
+              if (n + 2 == nj) umma_commit(&sh.q_empty);
             } else {
-              umma_commit(&o_full[1]);
+              umma_commit(&sh.o_full[1]);
             }
           }
         } else {
           for (int x = 0; x < 2 && x < nj; ++x) {
             wait_full(y + 2 * x);
             qk(x, y + 2 * x);
-            umma_commit(&empty[(y + 2 * x) % ST]);
-            if (x + 1 == nj) umma_commit(&q_empty);
+            umma_commit(&sh.empty[(y + 2 * x) % ST]);
+            if (x + 1 == nj) umma_commit(&sh.q_empty);
           }
-          if (nf0 > 0) wait(&o_free[0], (nf0 - 1) & 1u, 0x62e);
-          if (nf1 > 0 && nj > 1) wait(&o_free[1], (nf1 - 1) & 1u, 0x62e);
+          if (nf0 > 0) wait(&sh.o_free[0], (nf0 - 1) & 1u, 0x62e);
+          if (nf1 > 0 && nj > 1) wait(&sh.o_free[1], (nf1 - 1) & 1u, 0x62e);
           for (int e = 0; ok && e < nj; ++e, y += 2) {
             const int x = e & 1;
             wait_full(y + 1);
             pv(x, y + 1, ((x ? np1 : np0) + (e >> 1)) & 1u, e < 2);
-            umma_commit(&empty[(y + 1) % ST]);
+            umma_commit(&sh.empty[(y + 1) % ST]);
             if (e + 2 < nj) {
               wait_full(y + 4);
               qk(x, y + 4);
-              umma_commit(&empty[(y + 4) % ST]);
-              if (e + 3 == nj) umma_commit(&q_empty);
+              umma_commit(&sh.empty[(y + 4) % ST]);
+              if (e + 3 == nj) umma_commit(&sh.q_empty);
             } else {
-              umma_commit(&o_full[x]);
+              umma_commit(&sh.o_full[x]);
             }
           }
         }
         if (!ok) {  // TMEM is not freed under an MMA
-          umma_commit(&drain);
-          mbar_wait(&drain, 0, A.err, 0x628);
+          umma_commit(&sh.drain);
+          mbar_wait(&sh.drain, 0, A.err, 0x628);
         }
       }
       ok = !__any_sync(0xffffffffu, !ok);
@@ -590,40 +602,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       nf1 += it.count(1) > 0;
     }
   } else {
-    // ------------------------------------------------------------ softmax of one slot
-    const int x = warp >> 2, qd = warp & 3, m = qd * 32 + lane;
+    // ------------------------------------------------------------ softmax of half the columns of one slot
+    // Two threads a row: `half` takes keys 64 half .. of every tile and columns D / 2 * half .. of O. The
+    // two warps of a row quadrant meet on a named barrier of their own. Both always run the same tiles:
+    // a warp whose wait ran out goes on without waiting, and both leave before the next item.
+    const int x = warp >> 3, half = (warp >> 2) & 1, qd = warp & 3, m = qd * 32 + lane;
+    const int bar = 1 + x * 4 + qd;
     const uint32_t t_lane = tmem + ((uint32_t)(qd * 32) << 16);
-    const uint32_t tS = t_lane + C::S_COL + x * 128, tO = t_lane + C::O_COL + x * 128;
+    const uint32_t tS = t_lane + C::S_COL + x * 128, tO = t_lane + C::O_COL + x * 128 + half * (D / 2);
+    float* mine = &sh.row[x][half][m];
+    const float* theirs = &sh.row[x][half ^ 1][m];
     const float c = A.scale_log2;
-    bool ok = true;
     uint32_t ns = 0, no = 0, nx = 0;  // tiles, results and merges of this slot so far
-    for (int k = 0; ok; ++k) {
-      if (!mbar_wait(&item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
-      const Item it = read_item(&s_item[k & 1]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+    bool ok = true;
+    for (int k = 0;; ++k) {
+      ok = mbar_wait(&sh.item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d) && ok;
+      if (lane == 0) sh.ok[k & 1][x][half][qd] = ok;
+      named_bar_sync(bar, 64);
+      if (!sh.ok[k & 1][x][0][qd] || !sh.ok[k & 1][x][1][qd]) break;
+      const Item& it = sh.item[k & 1];  // given back at the end: few registers are left beside S
       if (it.end) break;
-      const int cnt = it.count(x);
-      const int tt = m / A.G, t = it.t0 + (it.dual ? x * A.TQ : 0) + tt, h = it.hk * A.G + (m - tt * A.G);
+      const int cnt = it.count(x), dual = it.dual;
+      const int tt = m / A.G, t = it.t0 + (dual ? x * A.TQ : 0) + tt;
       const bool live = tt < A.TQ && t < it.n;
       const bool warp_live = __any_sync(0xffffffffu, live);
       const int pos = it.pos0 + t;
       const Seen sn = seen(A, pos, pos, it.len);
       float m_ref = -INFINITY, l = 0.f;
       for (int n = 0; n < cnt; ++n) {
-        const int k0 = it.tile(it.j0 + (it.dual ? n : 2 * n + x)) * kBN;
-        if (!mbar_wait(&s_full[x], ns++ & 1u, A.err, 0x629)) {
-          ok = false;
-          break;
-        }
+        const int k0 = it.tile(it.j0 + (dual ? n : 2 * n + x)) * kBN + 64 * half;
+        ok = ok && mbar_wait(&sh.s_full[x], ns & 1u, A.err, 0x629);
+        ++ns;
         tc_fence_after();
         if (warp_live) {
-          float s[128];
-          tmem_ld128_sync(tS, s);
-          const bool all = (k0 >= sn.lo && k0 + kBN - 1 <= sn.hi) || k0 + kBN - 1 <= sn.g1 || !live;
+          float s[64];
+          tmem_ld64_sync(tS + 64 * half, s);
+          const bool all = (k0 >= sn.lo && k0 + 63 <= sn.hi) || k0 + 63 <= sn.g1 || !live;
           if (!__all_sync(0xffffffffu, all)) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < 2; ++w) {
               const uint32_t bits = range_bits(sn.lo, sn.hi, k0 + 32 * w) | range_bits(0, sn.g1, k0 + 32 * w);
 #pragma unroll
               for (int e = 0; e < 32; ++e) s[32 * w + e] = (bits & (1u << e)) ? s[32 * w + e] : -INFINITY;
@@ -633,11 +650,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int y = 0; y < 8; ++y) {
             m8[y] = fmax3(s[y], s[y + 8], s[y + 16]);
-#pragma unroll
-            for (int z = 24; z < 120; z += 16) m8[y] = fmax3(m8[y], s[y + z], s[y + z + 8]);
-            m8[y] = fmaxf(m8[y], s[y + 120]);
+            m8[y] = fmax3(m8[y], s[y + 24], s[y + 32]);
+            m8[y] = fmax3(m8[y], s[y + 40], s[y + 48]);
+            m8[y] = fmaxf(m8[y], s[y + 56]);
           }
-          const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * c;
+          float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+          // the row's maximum over both halves. (The value is overwritten after this thread's next
+          // S is there, which takes the other's P of this tile, written after it has read.) Past the
+          // barrier both have read their S, which P goes over.
+          *mine = mx;
+          tc_fence_before();
+          named_bar_sync(bar, 64);
+          tc_fence_after();
+          mx = fmaxf(mx, *theirs) * c;
           float alpha = 1.f;
           bool need = false;
           if (mx > m_ref + kRescaleThreshold) {
@@ -648,75 +673,87 @@ __global__ void __launch_bounds__(kThreads, 1)
             m_ref = mx;
           }
           if (__any_sync(0xffffffffu, need)) {  // (S of this tile is there: the earlier PV is done)
+#pragma unroll 1
+            for (int c0 = 0; c0 < D / 2; c0 += 8) {  // rare, and S is in registers
+              float o[8];
+              tmem_ld8_sync(tO + c0, o);
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              float o[32];
-              tmem_ld32_sync(tO + c0, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= alpha;
-              tmem_st32_sync(tO + c0, reinterpret_cast<const uint32_t*>(o));
+              for (int e = 0; e < 8; ++e) o[e] *= alpha;
+              tmem_st8_sync(tO + c0, o);
             }
+            tc_fence_before();
+            named_bar_sync(bar, 64);  // all of O is scaled before the first half's PV
+            tc_fence_after();
           }
           const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
           const uint64_t c2 = f32x2_pack(c, c), nm2 = f32x2_pack(neg_m, neg_m);
-          uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
+          uint64_t l2[2] = {0ull, 0ull};
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t pk[32];
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 16; ++e) {
               float a0, a1;
-              f32x2_unpack(f32x2_fma(f32x2_pack(s[64 * half + 2 * e], s[64 * half + 2 * e + 1]), c2, nm2), a0, a1);
+              f32x2_unpack(f32x2_fma(f32x2_pack(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]), c2, nm2), a0, a1);
               const float p0 = ex2(a0), p1 = ex2(a1);
-              l2[e & 3] = f32x2_add(l2[e & 3], f32x2_pack(p0, p1));
+              l2[e & 1] = f32x2_add(l2[e & 1], f32x2_pack(p0, p1));
               pk[e] = pack_bf16x2(p0, p1);  // rounded for the MMA; the sum takes the fp32 values
             }
-            tmem_st32_sync(tS + 32 * half, pk);
-            if (half == 0) {
-              tc_fence_before();
-              mbar_arrive(&p_half[x]);
-            }
+            tmem_st16_sync(tS + 32 * half + 16 * q, pk);
           }
-          float lp[8];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) f32x2_unpack(l2[y], lp[2 * y], lp[2 * y + 1]);
-          l = l * alpha + (((lp[0] + lp[1]) + (lp[2] + lp[3])) + ((lp[4] + lp[5]) + (lp[6] + lp[7])));
+          float l0, l1, l3, l4;
+          f32x2_unpack(l2[0], l0, l1);
+          f32x2_unpack(l2[1], l3, l4);
+          l = l * alpha + ((l0 + l1) + (l3 + l4));
         }
-        if (!warp_live) mbar_arrive(&p_half[x]);
         tc_fence_before();
-        mbar_arrive(&p_full[x]);
+        mbar_arrive(half ? &sh.p_full[x] : &sh.p_half[x]);
       }
       // ---- result
-      if (ok && cnt > 0) ok = mbar_wait(&o_full[x], no++ & 1u, A.err, 0x62a);
+      if (cnt > 0) {
+        ok = ok && mbar_wait(&sh.o_full[x], no & 1u, A.err, 0x62a);
+        ++no;
+        *mine = l;  // (the other has read the last maximum: its P, and the PV since, say so)
+        named_bar_sync(bar, 64);
+        l += *theirs;
+      }
       tc_fence_after();
       float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and, for a single tile, of slot 1's
-      const bool other = !it.dual && x == 0 && it.count(1) > 0;
-      if (!it.dual && x == 1 && cnt > 0) {
-        s_x[m] = make_float2(m_ref, l);
-        tc_fence_before();
-        mbar_arrive(&x_full);
+      const bool other = !dual && x == 0 && it.count(1) > 0;
+      if (!dual && x == 1 && cnt > 0) {
+        named_bar_sync(bar, 64);  // both have the sum
+        if (half == 0) {
+          sh.row[1][0][m] = m_ref;
+          sh.row[1][1][m] = l;
+          tc_fence_before();
+          mbar_arrive(&sh.x_full);
+        }
+        // sh.row[1] and O are read by slot 0
+        ok = ok && mbar_wait(&sh.o_free[1], (no - 1) & 1u, A.err, 0x62e);
       }
       if (other) {
-        if (ok) ok = mbar_wait(&x_full, nx++ & 1u, A.err, 0x62f);
+        ok = ok && mbar_wait(&sh.x_full, nx & 1u, A.err, 0x62f);
+        ++nx;
         tc_fence_after();
-        const float2 ml = s_x[m];
-        const float M = fmaxf(m_ref, ml.x);
+        const float m1 = sh.row[1][0][m], l1 = sh.row[1][1][m], M = fmaxf(m_ref, m1);
         if (M != -INFINITY) {
           w0 = exp2f(m_ref - M);
-          w1 = exp2f(ml.x - M);
-          l = l * w0 + ml.y * w1;
+          w1 = exp2f(m1 - M);
+          l = l * w0 + l1 * w1;
           m_ref = M;
         }
       }
-      if (warp_live && (it.dual || x == 0)) {
+      if (warp_live && (dual || x == 0)) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const float row_lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
         w0 *= inv;
         w1 *= inv;
+        const int h = it.hk * A.G + (m - tt * A.G);
         const int64_t row = (int64_t)(it.q0 + t) * A.Hq + h;
         const int64_t prow = it.ns > 1 ? P.part[it.rank] + ((int64_t)it.c * P.qn[it.rank] + t) * A.Hq + h : 0;
+        const int col = half * (D / 2);
 #pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
+        for (int c0 = 0; c0 < D / 2; c0 += 32) {
           float o[32];
           if (cnt > 0) {
             tmem_ld32_sync(tO + c0, o);
@@ -736,25 +773,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it.ns > 1) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(A.part_o + prow * D + c0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                *reinterpret_cast<float4*>(A.part_o + prow * D + col + c0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             } else {
 #pragma unroll
               for (int e = 0; e < 32; e += 8)
-                *reinterpret_cast<uint4*>(A.o + row * D + c0 + e) =
+                *reinterpret_cast<uint4*>(A.o + row * D + col + c0 + e) =
                     make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]), pack_bf16x2(o[e + 4], o[e + 5]),
                                pack_bf16x2(o[e + 6], o[e + 7]));
             }
           }
         }
-        if (live) {
+        if (live && half == 0) {
           if (it.ns > 1) A.part_lse[prow] = row_lse;
           else if (A.lse) A.lse[row] = row_lse;
         }
       }
       // what has been read of O may be overwritten by the slot's next item
       tc_fence_before();
-      if ((it.dual || x == 0) && cnt > 0) mbar_arrive(&o_free[x]);
-      if (other) mbar_arrive(&o_free[1]);
+      if ((dual || x == 0) && cnt > 0) mbar_arrive(&sh.o_free[x]);
+      if (other) mbar_arrive(&sh.o_free[1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.item_empty[k & 1]);
     }
   }
   tc_fence_before();
