@@ -177,6 +177,20 @@ __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP>& P,
   return true;
 }
 
+// A position in the ring of K and V stages, and the parity of its use.
+template <int ST>
+struct Ring {
+  int s = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ Ring next(int n) const {  // n <= ST
+    Ring r;
+    const bool wrap = s + n >= ST;
+    r.s = wrap ? s + n - ST : s + n;
+    r.parity = wrap ? parity ^ 1u : parity;
+    return r;
+  }
+};
+
 // Behind the tiles in shared memory.
 template <int ST>
 struct Shared {
@@ -488,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t k0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_KV), 16, 1024);
     const uint64_t v0 = umma_sdesc_sw128(smem_u32(smem + C::OFF_KV), kBN * 128, 1024);
     bool ok = true;
-    int T = 0, nq = 0;                       // tiles and Q loads of earlier items
+    Ring<ST> ring;                           // the next item's first K
+    int nq = 0;                              // Q loads of earlier items
     int np0 = 0, np1 = 0, nf0 = 0, nf1 = 0;  // tiles, and items with tiles, of each slot so far
     const bool by_lanes = A.box == 0;
     for (int k = 0; ok; ++k) {
@@ -505,12 +520,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
           if (!mbar_try_wait(bar, parity)) ok = ok && mbar_wait(bar, parity, A.err, code);
         };
-        auto wait_full = [&](int y) {  // ring entry y: K of list entry y / 2, or V
-          wait(&sh.full[y % ST], (y / ST) & 1u, 0x625);
+        auto wait_full = [&](const Ring<ST>& r) {
+          wait(&sh.full[r.s], r.parity, 0x625);
           if (by_lanes) fence_proxy_async_smem();  // cp.async wrote through the generic proxy
         };
-        auto qk = [&](int x, int y) {
-          const uint64_t a = q0 + (uint64_t)((dual && x ? C::TILE : 0) >> 4), b = k0 + (uint64_t)((y % ST * C::TILE) >> 4);
+        auto qk = [&](int x, const Ring<ST>& r) {
+          const uint64_t a = q0 + (uint64_t)((dual && x ? C::TILE : 0) >> 4), b = k0 + (uint64_t)((r.s * C::TILE) >> 4);
           const uint32_t tS = tmem + C::S_COL + x * 128;
           tc_fence_after();
 #pragma unroll
@@ -520,8 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           umma_commit(&sh.s_full[x]);
         };
-        auto pv = [&](int x, int y, uint32_t parity, bool first) {
-          const uint64_t b = v0 + (uint64_t)((y % ST * C::TILE) >> 4);
+        auto pv = [&](int x, const Ring<ST>& r, uint32_t parity, bool first) {
+          const uint64_t b = v0 + (uint64_t)((r.s * C::TILE) >> 4);
           const uint32_t tS = tmem + C::S_COL + x * 128, tO = tmem + C::O_COL + x * 128;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -533,55 +548,63 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         wait(&sh.q_full, nq & 1u, 0x624);
-        int y = 2 * T;  // ring entry of the K of the current tile
+        Ring<ST> r = ring;  // the current tile's K; its V is the next entry
         if (dual) {
-          wait_full(y);
-          if (na > 0) qk(0, y);
-          qk(1, y);
-          umma_commit(&sh.empty[y % ST]);
+          wait_full(r);
+          if (na > 0) qk(0, r);
+          qk(1, r);
+          umma_commit(&sh.empty[r.s]);
           if (nj == 1) umma_commit(&sh.q_empty);
           if (nf0 > 0 && na > 0) wait(&sh.o_free[0], (nf0 - 1) & 1u, 0x62e);
           if (nf1 > 0) wait(&sh.o_free[1], (nf1 - 1) & 1u, 0x62e);
-          for (int n = 0; ok && n < nj; ++n, y += 2) {
-            wait_full(y + 1);
+          uint32_t par0 = np0 & 1u, par1 = np1 & 1u;
+          for (int n = 0; ok && n < nj; ++n) {
+            const Ring<ST> v = r.next(1);
+            r = r.next(2);
+            wait_full(v);
             if (n < na) {
-              pv(0, y + 1, (np0 + n) & 1u, n == 0);
+              pv(0, v, par0, n == 0);
               if (n + 1 < na) {
-                wait_full(y + 2);
-                qk(0, y + 2);
+                wait_full(r);
+                qk(0, r);
               } else {
                 umma_commit(&sh.o_full[0]);
               }
             }
-            pv(1, y + 1, (np1 + n) & 1u, n == 0);
-            umma_commit(&sh.empty[(y + 1) % ST]);
+            pv(1, v, par1, n == 0);
+            umma_commit(&sh.empty[v.s]);
             if (n + 1 < nj) {
-              if (n + 1 >= na) wait_full(y + 2);
-              qk(1, y + 2);
-              umma_commit(&sh.empty[(y + 2) % ST]);
+              if (n + 1 >= na) wait_full(r);
+              qk(1, r);
+              umma_commit(&sh.empty[r.s]);
               if (n + 2 == nj) umma_commit(&sh.q_empty);
             } else {
               umma_commit(&sh.o_full[1]);
             }
+            par0 ^= 1u;
+            par1 ^= 1u;
           }
         } else {
           for (int x = 0; x < 2 && x < nj; ++x) {
-            wait_full(y + 2 * x);
-            qk(x, y + 2 * x);
-            umma_commit(&sh.empty[(y + 2 * x) % ST]);
+            const Ring<ST> e = x ? r.next(2) : r;
+            wait_full(e);
+            qk(x, e);
+            umma_commit(&sh.empty[e.s]);
             if (x + 1 == nj) umma_commit(&sh.q_empty);
           }
           if (nf0 > 0) wait(&sh.o_free[0], (nf0 - 1) & 1u, 0x62e);
           if (nf1 > 0 && nj > 1) wait(&sh.o_free[1], (nf1 - 1) & 1u, 0x62e);
-          for (int e = 0; ok && e < nj; ++e, y += 2) {
+          for (int e = 0; ok && e < nj; ++e) {
             const int x = e & 1;
-            wait_full(y + 1);
-            pv(x, y + 1, ((x ? np1 : np0) + (e >> 1)) & 1u, e < 2);
-            umma_commit(&sh.empty[(y + 1) % ST]);
+            const Ring<ST> v = r.next(1), f = r.next(4);
+            r = r.next(2);
+            wait_full(v);
+            pv(x, v, ((x ? np1 : np0) + (e >> 1)) & 1u, e < 2);
+            umma_commit(&sh.empty[v.s]);
             if (e + 2 < nj) {
-              wait_full(y + 4);
-              qk(x, y + 4);
-              umma_commit(&sh.empty[(y + 4) % ST]);
+              wait_full(f);
+              qk(x, f);
+              umma_commit(&sh.empty[f.s]);
               if (e + 3 == nj) umma_commit(&sh.q_empty);
             } else {
               umma_commit(&sh.o_full[x]);
@@ -594,7 +617,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       ok = !__any_sync(0xffffffffu, !ok);
-      T += nj;
+      {
+        const int y = ring.s + 2 * nj, turns = y / ST;
+        ring.s = y - turns * ST;
+        ring.parity ^= turns & 1u;
+      }
       nq += nj > 0;
       np0 += it.count(0);
       np1 += it.count(1);
