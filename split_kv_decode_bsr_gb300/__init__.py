@@ -22,6 +22,7 @@ Operations (sources):
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 import os
 import threading
@@ -612,40 +613,49 @@ def _need(ok, what: str):
         raise ValueError(what)
 
 
-def _place(dev: torch.device, *tensors):
+def _on(dev: torch.device, *tensors):
     """Every tensor given (None allowed) lies on CUDA device `dev`."""
-    _need(dev.type == "cuda", f"tensors must be on a CUDA device, not {dev}")
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, not {dev}")
     for t in tensors:
-        _need(t is None or t.device == dev, "tensors on different devices")
+        if t is not None and t.device != dev:
+            raise ValueError("tensors on different devices")
 
 
 def _i32(dev: torch.device, **tensors):
     """The named index tensors: contiguous int32 on `dev`."""
     for name, t in tensors.items():
-        _need(t.dtype == torch.int32 and t.is_contiguous() and t.device == dev, f"{name}: contiguous int32 on {dev}")
+        if t.dtype is not torch.int32 or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name}: contiguous int32 on {dev}")
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 class _Launch:
     """The device a call launches on, made current, and its stream, made torch's current one so that
-    what the call allocates belongs to that stream."""
+    what the call allocates belongs to that stream. Entering gives the stream's handle."""
+    __slots__ = ("_dev", "_stream", "_outer")
 
     def __init__(self, dev: torch.device, stream):
-        cur = torch.cuda.current_device()
-        self._outer = [torch.cuda.device(dev)] if dev.index is not None and dev.index != cur else []
-        self._stream, self._dev = stream, dev
+        self._dev, self._stream, self._outer = dev, stream, ()
 
     def __enter__(self):
-        for c in self._outer:
-            c.__enter__()
-        s = self._stream
+        dev, s = self._dev, self._stream
+        if s is None and dev.index == torch._C._cuda_getDevice():
+            return torch._C._cuda_getCurrentRawStream(dev.index)
+        outer = [torch.cuda.device(dev)]
+        outer[0].__enter__()
         if s is None:
-            return C.c_void_p(torch.cuda.current_stream().cuda_stream)
-        if not isinstance(s, torch.cuda.Stream):
-            s = torch.cuda.ExternalStream(int(s), device=self._dev) if int(s) else torch.cuda.default_stream(self._dev)
-        c = torch.cuda.stream(s)
-        c.__enter__()
-        self._outer.append(c)
-        return C.c_void_p(s.cuda_stream)
+            s = torch.cuda.current_stream(dev)
+        else:
+            if not isinstance(s, torch.cuda.Stream):
+                s = torch.cuda.ExternalStream(int(s), device=dev) if int(s) else torch.cuda.default_stream(dev)
+            outer.append(torch.cuda.stream(s))
+            outer[1].__enter__()
+        self._outer = outer
+        return s.cuda_stream
 
     def __exit__(self, *exc):
         for c in reversed(self._outer):
@@ -664,12 +674,14 @@ def _workspace(need: int, workspace: Optional[torch.Tensor], dev: torch.device) 
 
 
 def _host_i32(x, n: int, what: str):
-    """Host int32 values as a pointer, and what keeps them alive."""
+    """Host int32 values: their address, and the array that keeps them alive."""
     import numpy as np
 
-    a = np.ascontiguousarray(x.numpy() if isinstance(x, torch.Tensor) else x, dtype=np.int32)
+    a = x.numpy() if isinstance(x, torch.Tensor) else x
+    if not (isinstance(a, np.ndarray) and a.dtype == np.int32 and a.flags.c_contiguous):
+        a = np.ascontiguousarray(a, dtype=np.int32)
     _need(a.shape == (n,), f"{what}: {n} values")
-    return C.c_void_p(a.ctypes.data), a
+    return a.__array_interface__["data"][0], a
 
 
 class Rope:
@@ -716,14 +728,14 @@ def sta_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope, transpose: bo
     xs = _heads_view(x, "x")
     n, H, d = x.shape
     dev = x.device
-    _place(dev, y)
+    _on(dev, y)
     _i32(dev, positions=positions)
     _need(positions.shape == (n,), "positions: one a token")
     code = _dtype_code(x.dtype)
     with _Launch(dev, stream) as st:
         y = torch.empty((n, H, d), dtype=x.dtype, device=dev) if y is None else y
         _need(y.shape == x.shape and y.dtype == x.dtype, "y: x's shape and dtype")
-        _check("sta_rope", lib().sta_rope(_ptr(x), _ptr(y), _ptr(positions), C.byref(rope.struct), n, H, d, xs,
+        _check("sta_rope", lib().sta_rope(_addr(x), _addr(y), _addr(positions), C.byref(rope.struct), n, H, d, xs,
                                           _heads_view(y, "y"), int(bool(transpose)), code, st))
     return y
 
@@ -740,7 +752,7 @@ def sta_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
     and values only. Returns the turned q [n, Hq, d] (rows of a padded batch's padding unwritten).
     """
     dev = k.device
-    _place(dev, q, v, k_pages, v_pages, q_out)
+    _on(dev, q, v, k_pages, v_pages, q_out)
     n_pages, page_size, Hkv, d = k_pages.shape
     n = k.shape[0]
     _need(v_pages.shape == k_pages.shape and k_pages.is_contiguous() and v_pages.is_contiguous(),
@@ -766,8 +778,8 @@ def sta_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
         if q_out is not None:
             _need(q is not None and q_out.shape == q.shape and q_out.is_contiguous(), "q_out: contiguous, q's shape")
         _check("sta_rope_append_paged", lib().sta_rope_append_paged(
-            _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(q_out), _ptr(k_pages), _ptr(v_pages), page_size, n_pages,
-            _ptr(page_indptr_dev), _ptr(page_indices_dev), _ptr(q_indptr_dev), _ptr(kv_indptr_dev), _ptr(positions),
+            _addr(q), _addr(k), _addr(v), qs, ks, vs, _addr(q_out), _addr(k_pages), _addr(v_pages), page_size, n_pages,
+            _addr(page_indptr_dev), _addr(page_indices_dev), _addr(q_indptr_dev), _addr(kv_indptr_dev), _addr(positions),
             C.byref(rope.struct) if rope is not None else None, n, n_req, Hq, Hkv, d, STA_BF16, st))
     return q_out
 
@@ -788,7 +800,7 @@ def sta_chunk_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
     qs = _heads_view(q, "q")
     n, Hq, d = q.shape
     dev = q.device
-    _place(dev, k_pages, v_pages, o, lse)
+    _on(dev, k_pages, v_pages, o, lse)
     n_pages, page_size, Hkv, dk = k_pages.shape
     _need(dk == d and v_pages.shape == k_pages.shape and k_pages.is_contiguous() and v_pages.is_contiguous(),
           "k_pages, v_pages: contiguous [n_pages, page_size, Hkv, d]")
@@ -807,19 +819,46 @@ def sta_chunk_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
         lse = torch.empty((n, Hq), dtype=torch.float32, device=dev) if lse is None else lse
         _need(o.shape == q.shape and o.dtype == q.dtype and o.is_contiguous(), "o: contiguous, q's shape and dtype")
         _need(lse.shape == (n, Hq) and lse.dtype == torch.float32 and lse.is_contiguous(), "lse: contiguous float32 [n, Hq]")
-        need = C.c_size_t(0)
-
-        def call(ws):
-            _check("sta_chunk_fwd_paged", h.sta_chunk_fwd_paged(
-                _ptr(q), qs, _ptr(k_pages), _ptr(v_pages), page_size, n_pages, _ptr(page_indptr_dev),
-                _ptr(page_indices_dev), _ptr(q_indptr_dev), qh, _ptr(kv_indptr_dev), kh, n_req, Hq, Hkv, d,
-                _dtype_code(q.dtype), scale, pat, num_splits, _ptr(o), _ptr(lse), _ptr(ws), C.byref(need), st))
-
-        call(None)
-        workspace = _workspace(need.value, workspace, dev)
-        need.value = workspace.numel()
-        call(workspace)
+        args = (q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), page_size, n_pages, page_indptr_dev.data_ptr(),
+                page_indices_dev.data_ptr(), q_indptr_dev.data_ptr(), qh, kv_indptr_dev.data_ptr(), kh, n_req, Hq, Hkv, d,
+                _dtype_code(q.dtype), scale, pat, num_splits, o.data_ptr(), lse.data_ptr())
+        # most calls cut nothing and need the least scratch there is: one that needs more says how much
+        ws = _workspace(256, workspace, dev)
+        size = C.c_size_t(ws.numel())
+        status = h.sta_chunk_fwd_paged(*args, ws.data_ptr(), C.byref(size), st)
+        if status == STA_ERR_WORKSPACE:
+            ws = _workspace(size.value, workspace, dev)
+            status = h.sta_chunk_fwd_paged(*args, ws.data_ptr(), C.byref(size), st)
+        _check("sta_chunk_fwd_paged", status)
     return o, lse
+
+
+def chunk_workspace_bytes(q_indptr, kv_indptr, n_req: int, Hq: int, Hkv: int, d: int, page_size: int = 16,
+                          pattern: Optional[MaskSource] = None, num_splits: int = 0) -> int:
+    """Workspace size sta_chunk_fwd_paged needs for these requests (host only, never 0)."""
+    n = C.c_size_t(0)
+    qh, keep_q = _host_i32(q_indptr, n_req + 1, "q_indptr")
+    kh, keep_k = _host_i32(kv_indptr, n_req + 1, "kv_indptr")
+    _check("sta_chunk_fwd_paged", lib().sta_chunk_fwd_paged(
+        None, 0, None, None, page_size, 1, None, None, None, qh, None, kh, n_req, Hq, Hkv, d, STA_BF16, 1.0,
+        None if pattern is None else _src_array([pattern]), num_splits, None, None, None, C.byref(n), None))
+    return int(n.value)
+
+
+@functools.lru_cache(maxsize=None)
+def _pages_ws(fn: str, n_pages: int, n_req: int, n_forks: int) -> int:
+    """Workspace size of a page call (it depends on these alone)."""
+    n = C.c_size_t(0)
+    h = lib()
+    if fn == "sta_pages_grow":
+        st = h.sta_pages_grow(None, n_pages, None, None, None, None, n_req, 1, None, None, C.byref(n), None)
+    elif fn == "sta_pages_fork":
+        st = h.sta_pages_fork(None, 0, 0, None, n_pages, None, None, None, n_req, 1, None, None, n_forks, None, None,
+                              C.byref(n), None)
+    else:
+        st = h.sta_pages_compact(None, 0, 0, None, n_pages, None, None, None, n_req, 1, None, None, None, C.byref(n), None)
+    _check(fn, st)
+    return int(n.value)
 
 
 def _buf_array(bufs: Sequence[torch.Tensor], dev: torch.device, n_pages: Optional[int] = None):
@@ -838,7 +877,7 @@ def _buf_array(bufs: Sequence[torch.Tensor], dev: torch.device, n_pages: Optiona
 
 def _lists(ref, page_indptr, page_indices, kv_indptr):
     dev = ref.device
-    _place(dev)
+    _on(dev)
     _i32(dev, ref=ref, page_indptr=page_indptr, page_indices=page_indices, kv_indptr=kv_indptr)
     n_req = kv_indptr.numel() - 1
     _need(page_indptr.numel() == n_req + 1, "page_indptr, kv_indptr: n_req + 1 values each")
@@ -851,12 +890,12 @@ def sta_pages_copy(bufs: Sequence[torch.Tensor], src: torch.Tensor, dst: torch.T
     bufs = list(bufs)
     _need(bufs, "at least one buffer")
     dev = bufs[0].device
-    _place(dev)
+    _on(dev)
     _i32(dev, src=src, dst=dst)
     _need(src.dim() == 1 and src.shape == dst.shape, "src, dst: [n] each")
     arr, nb, page_bytes, n_pages = _buf_array(bufs, dev)
     with _Launch(dev, stream) as st:
-        _check("sta_pages_copy", lib().sta_pages_copy(arr, nb, page_bytes, n_pages, _ptr(src), _ptr(dst), src.numel(), st))
+        _check("sta_pages_copy", lib().sta_pages_copy(arr, nb, page_bytes, n_pages, _addr(src), _addr(dst), src.numel(), st))
 
 
 def sta_pages_grow(ref: torch.Tensor, page_indptr: torch.Tensor, page_indices: torch.Tensor, kv_indptr: torch.Tensor,
@@ -866,14 +905,12 @@ def sta_pages_grow(ref: torch.Tensor, page_indptr: torch.Tensor, page_indices: t
     dev, n_req = _lists(ref, page_indptr, page_indices, kv_indptr)
     _i32(dev, new_kv_indptr=new_kv_indptr)
     _need(new_kv_indptr.numel() == n_req + 1, "new_kv_indptr: n_req + 1 values")
-    h, need = lib(), C.c_size_t(0)
     with _Launch(dev, stream) as st:
         status = torch.empty(2, dtype=torch.int32, device=dev)
-        args = (_ptr(ref), ref.numel(), _ptr(page_indptr), _ptr(page_indices), _ptr(kv_indptr), _ptr(new_kv_indptr), n_req,
-                page_size, _ptr(status))
-        _check("sta_pages_grow", h.sta_pages_grow(*args, None, C.byref(need), st))
-        ws = _workspace(need.value, None, dev)
-        _check("sta_pages_grow", h.sta_pages_grow(*args, _ptr(ws), C.byref(need), st))
+        args = (_addr(ref), ref.numel(), _addr(page_indptr), _addr(page_indices), _addr(kv_indptr), _addr(new_kv_indptr), n_req,
+                page_size, _addr(status))
+        ws = torch.empty(_pages_ws("sta_pages_grow", ref.numel(), n_req, 0), dtype=torch.uint8, device=dev)
+        _check("sta_pages_grow", lib().sta_pages_grow(*args, ws.data_ptr(), C.byref(C.c_size_t(ws.numel())), st))
     return status
 
 
@@ -887,14 +924,12 @@ def sta_pages_fork(bufs: Sequence[torch.Tensor], ref: torch.Tensor, page_indptr:
     _i32(dev, parent=parent, child=child)
     _need(parent.dim() == 1 and parent.shape == child.shape, "parent, child: [n_forks] each")
     arr, nb, page_bytes, _ = _buf_array(bufs, dev, ref.numel())
-    h, need = lib(), C.c_size_t(0)
     with _Launch(dev, stream) as st:
         status = torch.empty(2, dtype=torch.int32, device=dev)
-        args = (arr, nb, page_bytes, _ptr(ref), ref.numel(), _ptr(page_indptr), _ptr(page_indices), _ptr(kv_indptr), n_req,
-                page_size, _ptr(parent), _ptr(child), parent.numel(), _ptr(status))
-        _check("sta_pages_fork", h.sta_pages_fork(*args, None, C.byref(need), st))
-        ws = _workspace(need.value, None, dev)
-        _check("sta_pages_fork", h.sta_pages_fork(*args, _ptr(ws), C.byref(need), st))
+        args = (arr, nb, page_bytes, _addr(ref), ref.numel(), _addr(page_indptr), _addr(page_indices), _addr(kv_indptr), n_req,
+                page_size, _addr(parent), _addr(child), parent.numel(), _addr(status))
+        ws = torch.empty(_pages_ws("sta_pages_fork", ref.numel(), n_req, parent.numel()), dtype=torch.uint8, device=dev)
+        _check("sta_pages_fork", lib().sta_pages_fork(*args, ws.data_ptr(), C.byref(C.c_size_t(ws.numel())), st))
     return status
 
 
@@ -904,8 +939,8 @@ def sta_pages_free(ref: torch.Tensor, page_indptr: torch.Tensor, page_indices: t
     dev, n_req = _lists(ref, page_indptr, page_indices, kv_indptr)
     _i32(dev, reqs=reqs)
     with _Launch(dev, stream) as st:
-        _check("sta_pages_free", lib().sta_pages_free(_ptr(ref), ref.numel(), _ptr(page_indptr), _ptr(page_indices),
-                                                      _ptr(kv_indptr), n_req, page_size, _ptr(reqs), reqs.numel(), st))
+        _check("sta_pages_free", lib().sta_pages_free(_addr(ref), ref.numel(), _addr(page_indptr), _addr(page_indices),
+                                                      _addr(kv_indptr), n_req, page_size, _addr(reqs), reqs.numel(), st))
 
 
 def sta_pages_compact(bufs: Sequence[torch.Tensor], ref: torch.Tensor, page_indptr: torch.Tensor,
@@ -915,15 +950,13 @@ def sta_pages_compact(bufs: Sequence[torch.Tensor], ref: torch.Tensor, page_indp
     {pages in use, pages moved}."""
     dev, n_req = _lists(ref, page_indptr, page_indices, kv_indptr)
     arr, nb, page_bytes, _ = _buf_array(bufs, dev, ref.numel())
-    h, need = lib(), C.c_size_t(0)
     with _Launch(dev, stream) as st:
         page_map = torch.empty(ref.numel(), dtype=torch.int32, device=dev)
         status = torch.empty(2, dtype=torch.int32, device=dev)
-        args = (arr, nb, page_bytes, _ptr(ref), ref.numel(), _ptr(page_indptr), _ptr(page_indices), _ptr(kv_indptr), n_req,
-                page_size, _ptr(page_map), _ptr(status))
-        _check("sta_pages_compact", h.sta_pages_compact(*args, None, C.byref(need), st))
-        ws = _workspace(need.value, None, dev)
-        _check("sta_pages_compact", h.sta_pages_compact(*args, _ptr(ws), C.byref(need), st))
+        args = (arr, nb, page_bytes, _addr(ref), ref.numel(), _addr(page_indptr), _addr(page_indices), _addr(kv_indptr), n_req,
+                page_size, _addr(page_map), _addr(status))
+        ws = torch.empty(_pages_ws("sta_pages_compact", ref.numel(), n_req, 0), dtype=torch.uint8, device=dev)
+        _check("sta_pages_compact", lib().sta_pages_compact(*args, ws.data_ptr(), C.byref(C.c_size_t(ws.numel())), st))
     return page_map, status
 
 

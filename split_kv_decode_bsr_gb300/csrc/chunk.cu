@@ -12,8 +12,8 @@
 // chunks of their tile list, whose normalised fp32 partials a second kernel merges by
 // log-sum-exp.
 //
-// Roles (20 warps, one CTA an SM): warps 0..7 and 8..15 the softmax of slots 0 and 1 (two threads a
-// row), warp 16 issues the MMAs, warps 17 and 18 load V and K, warp 19 finds items and loads Q.
+// Roles (12 warps, one CTA an SM): warps 0..3 and 4..7 the softmax of slots 0 and 1 (a thread a
+// row), warp 8 issues the MMAs, warps 9 and 10 load V and K, warp 11 finds items and loads Q.
 // S = Q K^T (M 128, N 128) and O += P V (P bf16 over the first half of S in tensor memory) run as
 // tcgen05.mma; a slot's order on the tensor core is PV(j), QK(j + 1), and one slot's MMAs run
 // under the other's softmax. S and O of both slots fill the 512 TMEM columns. The softmax is the
@@ -38,8 +38,8 @@ namespace {
 
 constexpr int kBM = 128;  // rows of a query tile
 constexpr int kBN = 128;  // keys of a tile
-constexpr int kThreads = 640;
-constexpr int kMmaWarp = 16, kVWarp = 17, kKWarp = 18, kQWarp = 19;
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kVWarp = 9, kKWarp = 10, kQWarp = 11;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 struct ChunkArgs {
@@ -196,16 +196,15 @@ template <int ST>
 struct Shared {
   uint4 clc;  // answer to a request for another CTA's item
   // full[s] / empty[s]: a K or V tile is in stage s / may be overwritten. s_full[x]: S of slot x is in
-  // TMEM (and every earlier MMA is done); p_half[x], p_full[x]: the P of its first, its last 64 keys is
-  // (128 threads each); o_full[x]: the item's last PV of slot x is done; o_free[x]: its O has been
-  // read (256 threads); x_full: slot 1's row maxima and sums of a single tile are in row; item_full /
+  // TMEM (and every earlier MMA is done); p_half[x], p_full[x]: the P of its first 64 keys, of all of
+  // them is (4 warps each); o_full[x]: the item's last PV of slot x is done; o_free[x]: its O has been
+  // read (4 warps); x_full: slot 1's row maxima and sums of a single tile are in row; item_full /
   // item_empty: item holds an item / has been read by the softmax, MMA, K and V warps.
   uint64_t full[ST], empty[ST], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], q_full, q_empty, x_full, tail,
       drain, clc_full, item_full[2], item_empty[2];
   Item item[2];
   uint32_t tmem;
-  uint8_t ok[2][2][2][4];    // [item & 1][slot][half][quadrant]: the warp's waits held
-  float row[2][2][kBM];      // [slot][half][row]: a value from one of a row's two threads to the other
+  float2 row[kBM];           // slot 1's row maxima (base 2) and sums, for the merge of a single tile
 };
 
 template <int D>
@@ -224,7 +223,7 @@ struct Cfg {
   static constexpr int O_COL = 256;            // slot s: + 128 s
 };
 
-// 16 (8) consecutive TMEM columns of this thread's lane, accessed and waited for in one statement.
+// 8 consecutive TMEM columns of this thread's lane, accessed and waited for in one statement.
 __device__ __forceinline__ void tmem_ld8_sync(uint32_t taddr, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
@@ -241,14 +240,28 @@ __device__ __forceinline__ void tmem_st8_sync(uint32_t taddr, const float* v) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16_sync(uint32_t taddr, const uint32_t* r) {
+// 128 consecutive TMEM columns of this thread's lane, loaded and waited for in one statement.
+#define STA_R(i) "=r"(r[i])
+#define STA_R8(i) STA_R(i), STA_R(i + 1), STA_R(i + 2), STA_R(i + 3), STA_R(i + 4), STA_R(i + 5), STA_R(i + 6), STA_R(i + 7)
+#define STA_R32X(i) STA_R8(i), STA_R8(i + 8), STA_R8(i + 16), STA_R8(i + 24)
+__device__ __forceinline__ void tmem_ld128_sync(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, "
+      "%37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, "
+      "%59, %60, %61, %62, %63, %64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, "
+      "%81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, %101, "
+      "%102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, "
+      "%120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : STA_R32X(0), STA_R32X(32), STA_R32X(64), STA_R32X(96)
+      : "r"(taddr)
       : "memory");
 }
+#undef STA_R32X
+#undef STA_R8
+#undef STA_R
 
 // 16 bytes, or 16 zero bytes where `some` is false.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool some) {
@@ -317,16 +330,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sh.s_full[x], 1);
-      mbar_init(&sh.p_half[x], 128);
-      mbar_init(&sh.p_full[x], 128);
+      mbar_init(&sh.p_half[x], 4);
+      mbar_init(&sh.p_full[x], 4);
       mbar_init(&sh.o_full[x], 1);
-      mbar_init(&sh.o_free[x], 256);
+      mbar_init(&sh.o_free[x], 4);
       mbar_init(&sh.item_full[x], 1);
       mbar_init(&sh.item_empty[x], kMmaWarp + 3);
     }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
-    mbar_init(&sh.x_full, 128);
+    mbar_init(&sh.x_full, 4);
     mbar_init(&sh.tail, 1);
     mbar_init(&sh.drain, 1);
     mbar_init(&sh.clc_full, 1);
@@ -629,24 +642,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       nf1 += it.count(1) > 0;
     }
   } else {
-    // ------------------------------------------------------------ softmax of half the columns of one slot
-    // Two threads a row: `half` takes keys 64 half .. of every tile and columns D / 2 * half .. of O. The
-    // two warps of a row quadrant meet on a named barrier of their own. Both always run the same tiles:
-    // a warp whose wait ran out goes on without waiting, and both leave before the next item.
-    const int x = warp >> 3, half = (warp >> 2) & 1, qd = warp & 3, m = qd * 32 + lane;
-    const int bar = 1 + x * 4 + qd;
+    // ------------------------------------------------------------ softmax of one slot, a thread a row
+    const int x = warp >> 2, qd = warp & 3, m = qd * 32 + lane;
     const uint32_t t_lane = tmem + ((uint32_t)(qd * 32) << 16);
-    const uint32_t tS = t_lane + C::S_COL + x * 128, tO = t_lane + C::O_COL + x * 128 + half * (D / 2);
-    float* mine = &sh.row[x][half][m];
-    const float* theirs = &sh.row[x][half ^ 1][m];
+    const uint32_t tS = t_lane + C::S_COL + x * 128, tO = t_lane + C::O_COL + x * 128;
     const float c = A.scale_log2;
-    uint32_t ns = 0, no = 0, nx = 0;  // tiles, results and merges of this slot so far
+    // an arrival of the whole warp
+    auto arrive = [&](uint64_t* bar) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
     bool ok = true;
-    for (int k = 0;; ++k) {
-      ok = mbar_wait(&sh.item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d) && ok;
-      if (lane == 0) sh.ok[k & 1][x][half][qd] = ok;
-      named_bar_sync(bar, 64);
-      if (!sh.ok[k & 1][x][0][qd] || !sh.ok[k & 1][x][1][qd]) break;
+    uint32_t ns = 0, no = 0, nx = 0;  // tiles, results and merges of this slot so far
+    for (int k = 0; ok; ++k) {
+      if (!mbar_wait(&sh.item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
       const Item& it = sh.item[k & 1];  // given back at the end: few registers are left beside S
       if (it.end) break;
       const int cnt = it.count(x), dual = it.dual;
@@ -656,18 +666,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = it.pos0 + t;
       const Seen sn = seen(A, pos, pos, it.len);
       float m_ref = -INFINITY, l = 0.f;
-      for (int n = 0; n < cnt; ++n) {
-        const int k0 = it.tile(it.j0 + (dual ? n : 2 * n + x)) * kBN + 64 * half;
-        ok = ok && mbar_wait(&sh.s_full[x], ns & 1u, A.err, 0x629);
-        ++ns;
+      for (int n = 0; ok && n < cnt; ++n) {
+        const int k0 = it.tile(it.j0 + (dual ? n : 2 * n + x)) * kBN;
+        if (!(ok = mbar_wait(&sh.s_full[x], ns++ & 1u, A.err, 0x629))) break;
         tc_fence_after();
         if (warp_live) {
-          float s[64];
-          tmem_ld64_sync(tS + 64 * half, s);
-          const bool all = (k0 >= sn.lo && k0 + 63 <= sn.hi) || k0 + 63 <= sn.g1 || !live;
+          float s[128];
+          tmem_ld128_sync(tS, s);
+          const bool all = (k0 >= sn.lo && k0 + kBN - 1 <= sn.hi) || k0 + kBN - 1 <= sn.g1 || !live;
           if (!__all_sync(0xffffffffu, all)) {
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
+            for (int w = 0; w < 4; ++w) {
               const uint32_t bits = range_bits(sn.lo, sn.hi, k0 + 32 * w) | range_bits(0, sn.g1, k0 + 32 * w);
 #pragma unroll
               for (int e = 0; e < 32; ++e) s[32 * w + e] = (bits & (1u << e)) ? s[32 * w + e] : -INFINITY;
@@ -677,19 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int y = 0; y < 8; ++y) {
             m8[y] = fmax3(s[y], s[y + 8], s[y + 16]);
-            m8[y] = fmax3(m8[y], s[y + 24], s[y + 32]);
-            m8[y] = fmax3(m8[y], s[y + 40], s[y + 48]);
-            m8[y] = fmaxf(m8[y], s[y + 56]);
+#pragma unroll
+            for (int z = 24; z < 120; z += 16) m8[y] = fmax3(m8[y], s[y + z], s[y + z + 8]);
+            m8[y] = fmaxf(m8[y], s[y + 120]);
           }
-          float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-          // the row's maximum over both halves. (The value is overwritten after this thread's next
-          // S is there, which takes the other's P of this tile, written after it has read.) Past the
-          // barrier both have read their S, which P goes over.
-          *mine = mx;
-          tc_fence_before();
-          named_bar_sync(bar, 64);
-          tc_fence_after();
-          mx = fmaxf(mx, *theirs) * c;
+          const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * c;
           float alpha = 1.f;
           bool need = false;
           if (mx > m_ref + kRescaleThreshold) {
@@ -701,72 +702,58 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (__any_sync(0xffffffffu, need)) {  // (S of this tile is there: the earlier PV is done)
 #pragma unroll 1
-            for (int c0 = 0; c0 < D / 2; c0 += 8) {  // rare, and S is in registers
+            for (int c0 = 0; c0 < D; c0 += 8) {  // rare, and S is in registers
               float o[8];
               tmem_ld8_sync(tO + c0, o);
 #pragma unroll
               for (int e = 0; e < 8; ++e) o[e] *= alpha;
               tmem_st8_sync(tO + c0, o);
             }
-            tc_fence_before();
-            named_bar_sync(bar, 64);  // all of O is scaled before the first half's PV
-            tc_fence_after();
           }
           const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
           const uint64_t c2 = f32x2_pack(c, c), nm2 = f32x2_pack(neg_m, neg_m);
-          uint64_t l2[2] = {0ull, 0ull};
+          uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t pk[16];
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[32];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 32; ++e) {
               float a0, a1;
-              f32x2_unpack(f32x2_fma(f32x2_pack(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]), c2, nm2), a0, a1);
+              f32x2_unpack(f32x2_fma(f32x2_pack(s[64 * half + 2 * e], s[64 * half + 2 * e + 1]), c2, nm2), a0, a1);
               const float p0 = ex2(a0), p1 = ex2(a1);
-              l2[e & 1] = f32x2_add(l2[e & 1], f32x2_pack(p0, p1));
+              l2[e & 3] = f32x2_add(l2[e & 3], f32x2_pack(p0, p1));
               pk[e] = pack_bf16x2(p0, p1);  // rounded for the MMA; the sum takes the fp32 values
             }
-            tmem_st16_sync(tS + 32 * half + 16 * q, pk);
+            tmem_st32_sync(tS + 32 * half, pk);
+            arrive(half ? &sh.p_full[x] : &sh.p_half[x]);
           }
-          float l0, l1, l3, l4;
-          f32x2_unpack(l2[0], l0, l1);
-          f32x2_unpack(l2[1], l3, l4);
-          l = l * alpha + ((l0 + l1) + (l3 + l4));
+          float lp[8];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) f32x2_unpack(l2[y], lp[2 * y], lp[2 * y + 1]);
+          l = l * alpha + (((lp[0] + lp[1]) + (lp[2] + lp[3])) + ((lp[4] + lp[5]) + (lp[6] + lp[7])));
+        } else if (lane == 0) {
+          mbar_arrive(&sh.p_half[x]);
+          mbar_arrive(&sh.p_full[x]);
         }
-        tc_fence_before();
-        mbar_arrive(half ? &sh.p_full[x] : &sh.p_half[x]);
       }
       // ---- result
-      if (cnt > 0) {
-        ok = ok && mbar_wait(&sh.o_full[x], no & 1u, A.err, 0x62a);
-        ++no;
-        *mine = l;  // (the other has read the last maximum: its P, and the PV since, say so)
-        named_bar_sync(bar, 64);
-        l += *theirs;
-      }
+      if (ok && cnt > 0) ok = mbar_wait(&sh.o_full[x], no++ & 1u, A.err, 0x62a);
       tc_fence_after();
       float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and, for a single tile, of slot 1's
       const bool other = !dual && x == 0 && it.count(1) > 0;
-      if (!dual && x == 1 && cnt > 0) {
-        named_bar_sync(bar, 64);  // both have the sum
-        if (half == 0) {
-          sh.row[1][0][m] = m_ref;
-          sh.row[1][1][m] = l;
-          tc_fence_before();
-          mbar_arrive(&sh.x_full);
-        }
-        // sh.row[1] and O are read by slot 0
-        ok = ok && mbar_wait(&sh.o_free[1], (no - 1) & 1u, A.err, 0x62e);
+      if (!dual && x == 1 && cnt > 0) {  // (slot 0 gives O, and with it row, back)
+        sh.row[m] = make_float2(m_ref, l);
+        arrive(&sh.x_full);
       }
       if (other) {
-        ok = ok && mbar_wait(&sh.x_full, nx & 1u, A.err, 0x62f);
-        ++nx;
+        if (ok) ok = mbar_wait(&sh.x_full, nx++ & 1u, A.err, 0x62f);
         tc_fence_after();
-        const float m1 = sh.row[1][0][m], l1 = sh.row[1][1][m], M = fmaxf(m_ref, m1);
+        const float2 ml = sh.row[m];
+        const float M = fmaxf(m_ref, ml.x);
         if (M != -INFINITY) {
           w0 = exp2f(m_ref - M);
-          w1 = exp2f(m1 - M);
-          l = l * w0 + l1 * w1;
+          w1 = exp2f(ml.x - M);
+          l = l * w0 + ml.y * w1;
           m_ref = M;
         }
       }
@@ -778,9 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int h = it.hk * A.G + (m - tt * A.G);
         const int64_t row = (int64_t)(it.q0 + t) * A.Hq + h;
         const int64_t prow = it.ns > 1 ? P.part[it.rank] + ((int64_t)it.c * P.qn[it.rank] + t) * A.Hq + h : 0;
-        const int col = half * (D / 2);
 #pragma unroll
-        for (int c0 = 0; c0 < D / 2; c0 += 32) {
+        for (int c0 = 0; c0 < D; c0 += 32) {
           float o[32];
           if (cnt > 0) {
             tmem_ld32_sync(tO + c0, o);
@@ -800,25 +786,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it.ns > 1) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(A.part_o + prow * D + col + c0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                *reinterpret_cast<float4*>(A.part_o + prow * D + c0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             } else {
 #pragma unroll
               for (int e = 0; e < 32; e += 8)
-                *reinterpret_cast<uint4*>(A.o + row * D + col + c0 + e) =
+                *reinterpret_cast<uint4*>(A.o + row * D + c0 + e) =
                     make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]), pack_bf16x2(o[e + 4], o[e + 5]),
                                pack_bf16x2(o[e + 6], o[e + 7]));
             }
           }
         }
-        if (live && half == 0) {
+        if (live) {
           if (it.ns > 1) A.part_lse[prow] = row_lse;
           else if (A.lse) A.lse[row] = row_lse;
         }
       }
       // what has been read of O may be overwritten by the slot's next item
-      tc_fence_before();
-      if ((dual || x == 0) && cnt > 0) mbar_arrive(&sh.o_free[x]);
-      if (other) mbar_arrive(&sh.o_free[1]);
+      if ((dual || x == 0) && cnt > 0) arrive(&sh.o_free[x]);
+      if (other) arrive(&sh.o_free[1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.item_empty[k & 1]);
     }
@@ -1035,7 +1020,10 @@ extern "C" sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const
     *workspace_bytes = need;
     return STA_OK;
   }
-  if (*workspace_bytes < need) return STA_ERR_WORKSPACE;
+  if (*workspace_bytes < need) {
+    *workspace_bytes = need;
+    return STA_ERR_WORKSPACE;
+  }
   if ((uintptr_t)workspace & 255) return STA_ERR_UNSUPPORTED;
   if (a.N == 0) return STA_OK;
   if (!q || !k_pages || !v_pages || !page_indptr_dev || !page_indices_dev || !q_indptr_dev || !kv_indptr_dev || !o)

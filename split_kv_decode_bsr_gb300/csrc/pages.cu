@@ -63,11 +63,24 @@ __device__ __forceinline__ int block_scan(int v, int& total, int* s_warp) {
   return before + incl - v;
 }
 
-// Copies page src[i] onto page dst[i] of every buffer (a negative number: no copy).
+// Copies page src[i] onto page dst[i] of every buffer (a negative number: no copy). With page_map,
+// first the entries that the requests hold take their pages' new numbers, a warp per request.
 __global__ void __launch_bounds__(kThreads) pages_copy_kernel(const __grid_constant__ PageBufs bufs, int n_bufs,
                                                               int64_t page_bytes, int n_pages, const int32_t* src,
                                                               const int32_t* dst, int n, const int32_t* n_dev,
-                                                              int* err) {
+                                                              const Lists L, const int32_t* page_map, int* err) {
+  if (page_map) {
+    const int lane = threadIdx.x & 31, warps = gridDim.x * (kThreads / 32);
+    for (int r = (blockIdx.x * kThreads + threadIdx.x) >> 5; r < L.n_req; r += warps) {
+      const int b = __ldg(L.indptr + r);
+      const int held = min(pages_of(tokens_of(L.kv_indptr, r), L.page_size), __ldg(L.indptr + r + 1) - b);
+      for (int k = lane; k < held; k += 32) {
+        const int page = L.indices[b + k];
+        if (page < 0 || page >= n_pages) record_error(err, 0x601);
+        else L.indices[b + k] = __ldg(page_map + page);
+      }
+    }
+  }
   const int slices = (int)((page_bytes + kSlice - 1) / kSlice);
   const int64_t pairs = n_dev ? min(n, __ldg(n_dev)) : n;
   const int64_t items = pairs * n_bufs * slices;
@@ -94,25 +107,35 @@ __global__ void __launch_bounds__(kThreads) pages_copy_kernel(const __grid_const
   }
 }
 
-// The lowest free pages, ascending, into taken[0 .. want): returns how many there are.
+// Bit e: page p + e (of 16) is there and its count is 0 (free) or, with `live`, above 0.
+__device__ __forceinline__ uint32_t page_bits(const Lists& L, int p, bool live) {
+  uint32_t bits = 0;
+  if (p + 16 <= L.n_pages && !((uintptr_t)L.ref & 15)) {
+    int4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const int4*>(L.ref + p + 4 * i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bits |= (uint32_t)(live ? x[e] > 0 : x[e] == 0) << (4 * i + e);
+    }
+  } else {
+    for (int e = 0; e < 16 && p + e < L.n_pages; ++e) bits |= (uint32_t)(live ? L.ref[p + e] > 0 : L.ref[p + e] == 0) << e;
+  }
+  return bits;
+}
+
+// The lowest free pages, ascending, into taken[0 .. want): returns how many there are. 16 pages a
+// thread and step.
 __device__ int take_free(const Lists& L, int want, int32_t* taken, int* s_warp) {
   int found = 0;
-  for (int p0 = 0; p0 < L.n_pages && found < want; p0 += 4 * kScanThreads) {
-    int f[4], n = 0;
-    const int p = p0 + 4 * (int)threadIdx.x;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[e] = p + e < L.n_pages && L.ref[p + e] == 0;
-      n += f[e];
-    }
+  for (int64_t p0 = 0; p0 < L.n_pages && found < want; p0 += 16 * kScanThreads) {
+    const int p = (int)min(p0 + 16 * (int)threadIdx.x, (int64_t)L.n_pages);
+    uint32_t bits = page_bits(L, p, false);
     int total;
-    int k = found + block_scan(n, total, s_warp);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (f[e]) {
-        if (k < want) taken[k] = p + e;
-        ++k;
-      }
+    int k = found + block_scan(__popc(bits), total, s_warp);
+    for (; bits && k < want; bits &= bits - 1, ++k) taken[k] = p + __ffs(bits) - 1;
     found += total;
   }
   __syncthreads();
@@ -134,24 +157,31 @@ __device__ __forceinline__ int grow_want(const Lists& L, const int32_t* now, int
 __global__ void __launch_bounds__(kScanThreads) pages_grow_kernel(const Lists L, const int32_t* now, int32_t* taken,
                                                                   int32_t* status) {
   __shared__ int s_warp[32];
-  int want = 0;
+  // the requests' wants, 1024 at a time; a batch of no more needs them only once
+  const bool once = L.n_req <= kScanThreads;
+  int want = 0, n = 0, k0 = 0, first = 0;
   for (int r0 = 0; r0 < L.n_req; r0 += kScanThreads) {
     const int r = r0 + threadIdx.x;
-    int first, total;
-    block_scan(r < L.n_req ? grow_want(L, now, r, first) : 0, total, s_warp);
+    int total;
+    n = r < L.n_req ? grow_want(L, now, r, first) : 0;
+    k0 = block_scan(n, total, s_warp);
     want += total;
   }
   const int got = take_free(L, want, taken, s_warp);
   int base = 0;
   for (int r0 = 0; r0 < L.n_req; r0 += kScanThreads) {
     const int r = r0 + threadIdx.x;
-    int first = 0, total;
-    const int n = r < L.n_req ? grow_want(L, now, r, first) : 0;
-    const int k0 = base + block_scan(n, total, s_warp);
-    base += total;
+    if (!once) {
+      int total;
+      n = r < L.n_req ? grow_want(L, now, r, first) : 0;
+      k0 = base + block_scan(n, total, s_warp);
+      base += total;
+    }
+    if (n == 0) continue;
+    int32_t* list = L.indices + __ldg(L.indptr + r) + first;
     for (int k = 0; k < n; ++k) {
       const int page = k0 + k < got ? taken[k0 + k] : -1;
-      L.indices[__ldg(L.indptr + r) + first + k] = page;
+      list[k] = page;
       if (page >= 0) L.ref[page] = 1;
     }
   }
@@ -298,28 +328,26 @@ __global__ void __launch_bounds__(kScanThreads) pages_plan_compact_kernel(const 
                                                                           int32_t* status) {
   __shared__ int s_warp[32];
   int used = 0;
-  for (int p0 = 0; p0 < L.n_pages; p0 += kScanThreads) {
-    const int p = p0 + threadIdx.x;
-    int total;
-    block_scan(p < L.n_pages && L.ref[p] > 0, total, s_warp);
-    used += total;
-  }
+  for (int64_t p0 = 16 * threadIdx.x; p0 < L.n_pages; p0 += 16 * kScanThreads) used += __popc(page_bits(L, (int)p0, true));
+  int all;
+  block_scan(used, all, s_warp);
+  used = all;
   int holes = 0, movers = 0;
-  for (int p0 = 0; p0 < L.n_pages; p0 += kScanThreads) {
-    const int p = p0 + threadIdx.x;
-    const bool live = p < L.n_pages && L.ref[p] > 0, hole = p < used && !live, mover = live && p >= used;
+  for (int64_t r0 = 0; r0 < L.n_pages; r0 += 16 * kScanThreads) {
+    const int p = (int)min(r0 + 16 * (int)threadIdx.x, (int64_t)L.n_pages);
+    const uint32_t in = p + 16 <= L.n_pages ? 0xffffu : (1u << (L.n_pages - p)) - 1u;
+    const uint32_t live = page_bits(L, p, true);
+    const uint32_t low = used >= p + 16 ? 0xffffu : (used <= p ? 0u : (1u << (used - p)) - 1u);  // below `used`
+    uint32_t hole = in & low & ~live, mover = live & ~low;
+    // both counts in one scan: at most 16384 of each a round
     int total;
-    // holes come before `used` and movers from it on: both counts in one scan (at most 2^30 pages)
-    const int k = block_scan(hole || mover, total, s_warp);
-    // pages below `used` in this round are all before those past it
-    const int below = min(max(used - p0, 0), kScanThreads);
-    int nh;
-    block_scan(hole && (int)threadIdx.x < below, nh, s_warp);
-    if (hole) dst[holes + k] = p;
-    if (mover) src[movers + k - nh] = p;
-    holes += nh;
-    movers += total - nh;
-    if (p < L.n_pages) page_map[p] = live ? p : -1;
+    const int k = block_scan(__popc(hole) | (__popc(mover) << 16), total, s_warp);
+    int32_t *h = dst + holes + (k & 0xffff), *m = src + movers + (k >> 16);
+    for (; hole; hole &= hole - 1) *h++ = p + __ffs(hole) - 1;
+    for (; mover; mover &= mover - 1) *m++ = p + __ffs(mover) - 1;
+    holes += total & 0xffff;
+    movers += total >> 16;
+    for (int e = 0; e < 16 && p + e < L.n_pages; ++e) page_map[p + e] = (live >> e) & 1 ? p + e : -1;
   }
   __syncthreads();
   for (int k = threadIdx.x; k < movers; k += kScanThreads) {
@@ -333,21 +361,6 @@ __global__ void __launch_bounds__(kScanThreads) pages_plan_compact_kernel(const 
       status[0] = used;
       status[1] = movers;
     }
-  }
-}
-
-// A warp per request: the entries it holds take their pages' new numbers.
-__global__ void __launch_bounds__(kThreads) pages_remap_kernel(const Lists L, const int32_t* page_map) {
-  const int r = (blockIdx.x * kThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  if (r >= L.n_req) return;
-  const int b = __ldg(L.indptr + r), held = min(pages_of(tokens_of(L.kv_indptr, r), L.page_size), __ldg(L.indptr + r + 1) - b);
-  for (int k = lane; k < held; k += 32) {
-    const int page = L.indices[b + k];
-    if (page < 0 || page >= L.n_pages) {
-      record_error(L.err, 0x601);
-      continue;
-    }
-    L.indices[b + k] = __ldg(page_map + page);
   }
 }
 
@@ -371,16 +384,19 @@ sta_status check_bufs(void* const* bufs, int n_bufs, size_t page_bytes) {
 
 // n: pairs at most (the grid is sized by it), n_dev: their number on the device, or null.
 sta_status launch_copy(void* const* bufs, int n_bufs, size_t page_bytes, int n_pages, const int32_t* src,
-                       const int32_t* dst, int n, const int32_t* n_dev, int* err, cudaStream_t st) {
+                       const int32_t* dst, int n, const int32_t* n_dev, const Lists& L, const int32_t* page_map, int* err,
+                       cudaStream_t st) {
   const int64_t slices = cdiv((int64_t)page_bytes, kSlice);
-  for (int b0 = 0; b0 < n_bufs; b0 += kMaxBufs) {
+  const unsigned remap = page_map ? (unsigned)std::min<int64_t>(cdiv(L.n_req, kThreads / 32), 152 * 8) : 0;
+  for (int b0 = 0; b0 == 0 || b0 < n_bufs; b0 += kMaxBufs) {
     PageBufs pb;
     const int nb = std::min(kMaxBufs, n_bufs - b0);
     for (int b = 0; b < nb; ++b) pb.p[b] = static_cast<uint8_t*>(bufs[b0 + b]);
     const int64_t items = (int64_t)n * nb * slices;
-    const unsigned grid = (unsigned)std::min<int64_t>(items, 152 * 8);
+    const unsigned grid = std::max((unsigned)std::min<int64_t>(items, 152 * 8), b0 == 0 ? remap : 0u);
     if (grid == 0) continue;
-    pages_copy_kernel<<<grid, kThreads, 0, st>>>(pb, nb, (int64_t)page_bytes, n_pages, src, dst, n, n_dev, err);
+    pages_copy_kernel<<<grid, kThreads, 0, st>>>(pb, nb, (int64_t)page_bytes, n_pages, src, dst, n, n_dev, L,
+                                                 b0 == 0 ? page_map : nullptr, err);
     STA_LAUNCH_CHECK();
   }
   return STA_OK;
@@ -419,8 +435,8 @@ extern "C" sta_status sta_pages_copy(void* const* bufs_host, int n_bufs, size_t 
   if (n == 0 || n_bufs == 0) return STA_OK;
   if (!src_dev || !dst_dev) return STA_ERR_INVALID_ARG;
   if (!aligned4({src_dev, dst_dev})) return STA_ERR_UNSUPPORTED;
-  return launch_copy(bufs_host, n_bufs, page_bytes, n_pages, src_dev, dst_dev, n, nullptr, device_error_word(),
-                     (cudaStream_t)stream);
+  return launch_copy(bufs_host, n_bufs, page_bytes, n_pages, src_dev, dst_dev, n, nullptr, Lists{}, nullptr,
+                     device_error_word(), (cudaStream_t)stream);
 }
 
 extern "C" sta_status sta_pages_grow(int32_t* ref_dev, int n_pages, const int32_t* page_indptr_dev,
@@ -468,7 +484,7 @@ extern "C" sta_status sta_pages_fork(void* const* bufs_host, int n_bufs, size_t 
   pages_fork_kernel<<<1 + (unsigned)std::min<int64_t>(cdiv(n_forks, 32), 151), kScanThreads, 0, s>>>(
       L, parent_dev, child_dev, n_forks, taken, src, dst, reinterpret_cast<int32_t*>(ws + 3 * part), status_dev);
   STA_LAUNCH_CHECK();
-  return launch_copy(bufs_host, n_bufs, page_bytes, n_pages, src, dst, n_forks, nullptr, L.err, s);
+  return launch_copy(bufs_host, n_bufs, page_bytes, n_pages, src, dst, n_forks, nullptr, L, nullptr, L.err, s);
 }
 
 extern "C" sta_status sta_pages_free(int32_t* ref_dev, int n_pages, const int32_t* page_indptr_dev,
@@ -512,7 +528,5 @@ extern "C" sta_status sta_pages_compact(void* const* bufs_host, int n_bufs, size
   int32_t* n_moves = reinterpret_cast<int32_t*>(ws + 2 * part);
   pages_plan_compact_kernel<<<1, kScanThreads, 0, s>>>(L, page_map_dev, src, dst, n_moves, status_dev);
   STA_LAUNCH_CHECK();
-  pages_remap_kernel<<<(unsigned)cdiv(n_req, kThreads / 32), kThreads, 0, s>>>(L, page_map_dev);
-  STA_LAUNCH_CHECK();
-  return launch_copy(bufs_host, n_bufs, page_bytes, n_pages, src, dst, (int)most, n_moves, L.err, s);
+  return launch_copy(bufs_host, n_bufs, page_bytes, n_pages, src, dst, (int)most, n_moves, L, page_map_dev, L.err, s);
 }

@@ -10,8 +10,8 @@
 // A CTA takes a few tokens: it puts their cosines and sines (times the magnitude) into shared
 // memory once, then its threads run over the tokens' heads, a unit of work being the 16-byte
 // vector (half layout: the two vectors half a rotation apart) that one thread turns. All
-// loads of a thread's units are issued before the first store. Every element is read and
-// written once, so HBM bounds it.
+// loads of a thread's first four units are issued before the table is computed. Every element
+// is read and written once, so HBM bounds it.
 #include <cmath>
 
 #include "common.cuh"
@@ -79,11 +79,11 @@ struct alignas(W * sizeof(T) == 16 ? 16 : sizeof(T)) Vec {
   }
 };
 
-// Where a new token goes: its position and its cache row, -1 when it goes nowhere.
-__device__ __forceinline__ void token_place(const RopeArgs& A, int64_t t, int& pos, int64_t& row) {
+// Where a new token goes: its position and its cache row, -1 when it goes nowhere. False for padding.
+__device__ __forceinline__ bool token_place(const RopeArgs& A, int64_t t, int& pos, int64_t& row) {
   pos = 0;
   row = -1;
-  if (t < __ldg(A.q_indptr) || t >= __ldg(A.q_indptr + A.n_req)) return;  // padding
+  if (t < __ldg(A.q_indptr) || t >= __ldg(A.q_indptr + A.n_req)) return false;
   int lo = 0, hi = A.n_req - 1;  // the last request that starts at or before t
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -94,20 +94,21 @@ __device__ __forceinline__ void token_place(const RopeArgs& A, int64_t t, int& p
   const int64_t p = len - (q1 - t);
   if (p < 0 || t >= q1) {  // the sequence is shorter than its chunk: this token is not in it
     pos = (int)(p < INT32_MIN ? INT32_MIN : p);
-    return;
+    return true;
   }
   pos = (int)p;
   const int64_t e = (int64_t)__ldg(A.page_indptr + lo) + p / A.page_size;
   if (e >= __ldg(A.page_indptr + lo + 1)) {
     record_error(A.err, 0x604);
-    return;
+    return true;
   }
   const int page = __ldg(A.page_indices + e);
   if (page < 0 || page >= A.n_pages) {
     record_error(A.err, 0x110);
-    return;
+    return true;
   }
   row = (int64_t)page * A.page_size + p % A.page_size;
+  return true;
 }
 
 // W: elements of a vector (1: unaligned data, element by element); IL: interleaved pairs;
@@ -123,88 +124,50 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs A, const 
   const int half = A.rot >> 1;
   const int64_t t0 = (int64_t)blockIdx.x * A.tokens;
   const int nt = (int)min((int64_t)A.tokens, A.n_tokens - t0);
-  if ((int)threadIdx.x < nt) {
-    int pos;
-    int64_t row = 0;
-    s_live[threadIdx.x] = 1;
-    if constexpr (APPEND) {
-      token_place(A, t0 + threadIdx.x, pos, row);
-      s_live[threadIdx.x] = t0 + threadIdx.x >= __ldg(A.q_indptr) && t0 + threadIdx.x < __ldg(A.q_indptr + A.n_req);
-      if (A.positions) pos = __ldg(A.positions + t0 + threadIdx.x);
-    } else {
-      pos = __ldg(A.positions + t0 + threadIdx.x);
-    }
-    s_pos[threadIdx.x] = pos;
-    s_row[threadIdx.x] = row;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const int t = i / half, p = i - t * half;
-    const uint64_t turn = (uint64_t)(int64_t)s_pos[t] * tab.turn[p];
-    float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-    s_cs[i] = make_float2(c * A.mscale, (A.transpose ? -s : s) * A.mscale);
-  }
-  __syncthreads();
   const int per_token = A.H * A.units, total = nt * per_token;
-  for (int i0 = threadIdx.x; i0 < total; i0 += U * kThreads) {
-    Vec<T, WI> a[U], b[U];
-    T* out[U];
-    int tk[U], un[U], off[U];
+  Vec<T, WI> a[U], b[U];
+  int at[U];           // token << 20 | head (of q, k and v together); -1: none
+  int off[U];          // first element of the vector
+  bool turn[U];
+  // One round of U units a thread: their loads, and, once the table is there, the turn and the stores.
+  auto load = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kThreads;
-      out[u] = nullptr;
+      at[u] = -1;
       if (i >= total) continue;
-      const int t = i / per_token, x = i - t * per_token;
-      int h = x / A.units;
-      const int unit = x - h * A.units;
-      int g = 0;
-      if constexpr (APPEND) {
-        if (!s_live[t]) continue;
-        if (h >= A.heads[0]) {
-          h -= A.heads[0];
-          g = 1;
-          if (h >= A.heads[1]) {
-            h -= A.heads[1];
-            g = 2;
-          }
-          if (s_row[t] < 0) continue;
-        }
-      }
-      const T* src = reinterpret_cast<const T*>(A.src[g] + (t0 + t) * A.src_stride[g]) + (int64_t)h * A.d;
-      out[u] = reinterpret_cast<T*>(A.dst[g] + (g ? s_row[t] : t0 + t) * A.dst_stride[g]) + (int64_t)h * A.d;
-      tk[u] = t;
-      un[u] = g == 2 ? -1 : unit;
-      if (unit < A.rot_units) {
-        off[u] = unit * WI;
-        a[u].load(src + off[u]);
-        if (!IL) b[u].load(src + off[u] + half);
+      const int t = i / per_token, x = i - t * per_token, h = x / A.units, unit = x - h * A.units;
+      at[u] = (t << 20) | h;
+      turn[u] = unit < A.rot_units;
+      off[u] = turn[u] ? unit * WI : A.rot + (unit - A.rot_units) * WI;
+      const int g = !APPEND || h < A.heads[0] ? 0 : (h < A.heads[0] + A.heads[1] ? 1 : 2);
+      const int hg = h - (g > 0 ? A.heads[0] : 0) - (g > 1 ? A.heads[1] : 0);
+      const T* src = reinterpret_cast<const T*>(A.src[g] + (t0 + t) * A.src_stride[g]) + (int64_t)hg * A.d + off[u];
+      if (W == 1 && IL && !turn[u]) {  // the last element of an odd rest is alone
+        a[u].v[0] = src[0];
+        if (off[u] + 1 < A.d) a[u].v[1] = src[1];
       } else {
-        un[u] = -2;
-        off[u] = A.rot + (unit - A.rot_units) * WI;
-        if (W == 1 && IL) {
-          a[u].v[0] = src[off[u]];
-          if (off[u] + 1 < A.d) a[u].v[1] = src[off[u] + 1];
-        } else {
-          a[u].load(src + off[u]);
-        }
+        a[u].load(src);
       }
+      if (!IL && turn[u]) b[u].load(src + half);
     }
+  };
+  auto store = [&]() {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (!out[u]) continue;
-      if (un[u] == -2) {  // behind the rotated part: copied
-        if (W == 1 && IL) {
-          out[u][off[u]] = a[u].v[0];
-          if (off[u] + 1 < A.d) out[u][off[u] + 1] = a[u].v[1];
-        } else {
-          a[u].store(out[u] + off[u]);
-        }
+      if (at[u] < 0) continue;
+      const int t = at[u] >> 20, h = at[u] & 0xfffff;
+      const int g = !APPEND || h < A.heads[0] ? 0 : (h < A.heads[0] + A.heads[1] ? 1 : 2);
+      const int hg = h - (g > 0 ? A.heads[0] : 0) - (g > 1 ? A.heads[1] : 0);
+      if (APPEND && (!s_live[t] || (g > 0 && s_row[t] < 0))) continue;
+      T* out = reinterpret_cast<T*>(A.dst[g] + (g ? s_row[t] : t0 + t) * A.dst_stride[g]) + (int64_t)hg * A.d + off[u];
+      if (W == 1 && IL && !turn[u]) {
+        out[0] = a[u].v[0];
+        if (off[u] + 1 < A.d) out[1] = a[u].v[1];
         continue;
       }
-      if (un[u] >= 0) {
-        const float2* cs = s_cs + tk[u] * half + (IL ? off[u] >> 1 : off[u]);
+      if (turn[u] && g < 2) {
+        const float2* cs = s_cs + t * half + (IL ? off[u] >> 1 : off[u]);
         if constexpr (IL) {
 #pragma unroll
           for (int e = 0; e < WI / 2; ++e) {
@@ -221,9 +184,38 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs A, const 
           }
         }
       }
-      a[u].store(out[u] + off[u]);
-      if (!IL) b[u].store(out[u] + off[u] + half);
+      a[u].store(out);
+      if (!IL && turn[u]) b[u].store(out + half);
     }
+  };
+  load(threadIdx.x);  // under the table's latency
+  if ((int)threadIdx.x < nt) {
+    int pos;
+    int64_t row = 0;
+    bool live = true;
+    if constexpr (APPEND) {
+      live = token_place(A, t0 + threadIdx.x, pos, row);
+      if (A.positions) pos = __ldg(A.positions + t0 + threadIdx.x);
+    } else {
+      pos = __ldg(A.positions + t0 + threadIdx.x);
+    }
+    s_pos[threadIdx.x] = pos;
+    s_row[threadIdx.x] = row;
+    s_live[threadIdx.x] = live;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+    const int t = i / half, p = i - t * half;
+    const uint64_t phase = (uint64_t)(int64_t)s_pos[t] * tab.turn[p];
+    float s, c;
+    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
+    s_cs[i] = make_float2(c * A.mscale, (A.transpose ? -s : s) * A.mscale);
+  }
+  __syncthreads();
+  store();
+  for (int i0 = threadIdx.x + U * kThreads; i0 < total; i0 += U * kThreads) {
+    load(i0);
+    store();
   }
 }
 
@@ -279,10 +271,18 @@ sta_status launch_rope(RopeArgs& a, const RopeTable& tab, bool interleaved, cuda
   a.rot_units = interleaved ? a.rot / wi : a.rot / 2 / wi;
   a.units = a.rot_units + (a.d - a.rot + wi - 1) / wi;
   a.H = a.heads[0] + a.heads[1] + a.heads[2];
-  // tokens of a CTA: about 8 units a thread while that leaves several CTAs to every SM
+  // Tokens of a CTA: the number whose units fill rounds of 4 a thread best, the larger of two as good,
+  // while two CTAs are left to every SM.
+  const int64_t per_token = (int64_t)a.H * a.units, round = 4 * kThreads;
   int tokens = 1;
-  while (tokens < kMaxTokens && 2 * tokens * a.H * a.units <= 8 * kThreads && a.n_tokens >= (int64_t)2 * tokens * 152 * 4)
-    tokens *= 2;
+  double best = 0;
+  for (int t = 1; t <= kMaxTokens && t * per_token <= 2 * round && (t == 1 || a.n_tokens >= (int64_t)t * 152 * 2); ++t) {
+    const double fill = (double)(t * per_token) / (double)(cdiv(t * per_token, round) * round);
+    if (fill >= best) {
+      best = fill;
+      tokens = t;
+    }
+  }
   a.tokens = tokens;
   const int64_t blocks = cdiv(a.n_tokens, tokens);
   if (blocks > INT32_MAX || (int64_t)tokens * a.H * a.units > INT32_MAX / 2) return STA_ERR_INVALID_ARG;
