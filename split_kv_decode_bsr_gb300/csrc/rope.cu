@@ -10,7 +10,7 @@
 // A CTA takes a few tokens: it puts their cosines and sines (times the magnitude) into shared
 // memory once, then its threads run over the tokens' heads, a unit of work being the 16-byte
 // vector (half layout: the two vectors half a rotation apart) that one thread turns. All
-// loads of a thread's first four units are issued before the table is computed. Every element
+// loads of a thread's first two units are issued before the table is computed. Every element
 // is read and written once, so HBM bounds it.
 #include <cmath>
 
@@ -114,10 +114,14 @@ __device__ __forceinline__ bool token_place(const RopeArgs& A, int64_t t, int& p
 // W: elements of a vector (1: unaligned data, element by element); IL: interleaved pairs;
 // APPEND: q, k, v with k and v going to pages.
 template <typename T, int W, bool IL, bool APPEND>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs A, const __grid_constant__ RopeTable tab) {
+__global__ void __launch_bounds__(kThreads, 6) rope_kernel(const RopeArgs A, const __grid_constant__ RopeTable tab) {
   constexpr int WI = IL && W == 1 ? 2 : W;  // elements of a vector: whole pairs when interleaved
-  constexpr int U = 4;                      // units of a thread in flight
-  extern __shared__ float2 s_cs[];          // [tokens][rot / 2] cosine, sine
+  // units of a thread in flight: 2, and 6 CTAs an SM (16384 x 40 x 128 in bf16: 58 us; 4 with 3 CTAs 67)
+  constexpr int U = 2;
+  constexpr int PP = IL ? WI / 2 : WI;      // pairs of a unit
+  // cosine and sine, two pairs in 16 bytes: [tokens][PP / 2][units][2], so that neighbouring threads
+  // read neighbouring words (a unit's pairs side by side would meet in the same banks four times)
+  extern __shared__ __align__(16) float2 s_cs[];
   __shared__ int64_t s_row[kMaxTokens];
   __shared__ int s_pos[kMaxTokens];
   __shared__ int s_live[kMaxTokens];
@@ -167,7 +171,18 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs A, const 
         continue;
       }
       if (turn[u] && g < 2) {
-        const float2* cs = s_cs + t * half + (IL ? off[u] >> 1 : off[u]);
+        float2 cs[PP];
+        if constexpr (PP == 1) {
+          cs[0] = s_cs[t * half + (IL ? off[u] >> 1 : off[u])];
+        } else {
+          const float4* c4 = reinterpret_cast<const float4*>(s_cs + t * half) + off[u] / WI;
+#pragma unroll
+          for (int j = 0; j < PP / 2; ++j) {
+            const float4 w = c4[j * A.rot_units];
+            cs[2 * j] = make_float2(w.x, w.y);
+            cs[2 * j + 1] = make_float2(w.z, w.w);
+          }
+        }
         if constexpr (IL) {
 #pragma unroll
           for (int e = 0; e < WI / 2; ++e) {
@@ -209,7 +224,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs A, const 
     const uint64_t phase = (uint64_t)(int64_t)s_pos[t] * tab.turn[p];
     float s, c;
     sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-    s_cs[i] = make_float2(c * A.mscale, (A.transpose ? -s : s) * A.mscale);
+    const int e = p % PP;  // place of the pair in its unit
+    const int at_cs = PP == 1 ? p : ((e >> 1) * A.rot_units + p / PP) * 2 + (e & 1);
+    s_cs[t * half + at_cs] = make_float2(c * A.mscale, (A.transpose ? -s : s) * A.mscale);
   }
   __syncthreads();
   store();
@@ -271,13 +288,15 @@ sta_status launch_rope(RopeArgs& a, const RopeTable& tab, bool interleaved, cuda
   a.rot_units = interleaved ? a.rot / wi : a.rot / 2 / wi;
   a.units = a.rot_units + (a.d - a.rot + wi - 1) / wi;
   a.H = a.heads[0] + a.heads[1] + a.heads[2];
-  // Tokens of a CTA: the number whose units fill rounds of 4 a thread best, the larger of two as good,
-  // while two CTAs are left to every SM.
-  const int64_t per_token = (int64_t)a.H * a.units, round = 4 * kThreads;
+  // Tokens of a CTA: the number whose units fill rounds of 2 a thread best, the larger of two as good,
+  // while two CTAs are left to every SM; two rounds only where six are.
+  const int64_t per_token = (int64_t)a.H * a.units, round = 2 * kThreads;
   int tokens = 1;
   double best = 0;
-  for (int t = 1; t <= kMaxTokens && t * per_token <= 2 * round && (t == 1 || a.n_tokens >= (int64_t)t * 152 * 2); ++t) {
-    const double fill = (double)(t * per_token) / (double)(cdiv(t * per_token, round) * round);
+  for (int t = 1; t <= kMaxTokens; ++t) {
+    const int64_t rounds = cdiv(t * per_token, round);
+    if (t > 1 && (rounds > 2 || a.n_tokens < (int64_t)t * 152 * (rounds > 1 ? 6 : 2))) break;
+    const double fill = (double)(t * per_token) / (double)(rounds * round);
     if (fill >= best) {
       best = fill;
       tokens = t;
