@@ -54,7 +54,7 @@ struct ChunkArgs {
   const int32_t* kv_indptr;
   float* part_o;     // [partial rows, d]
   float* part_lse;   // [partial rows]
-  int N, Hq, Hkv, G, TQ;  // TQ tokens a query tile
+  int N, Hq, Hkv, d, G, TQ;  // TQ tokens a query tile
   int page_size, n_pages;
   int box;                // tokens of a TMA box, or 0: cp.async
   float scale_log2;
@@ -63,15 +63,16 @@ struct ChunkArgs {
   int* err;
 };
 
-// What the host planned: requests in launch order (heaviest first). Rank k has the items base[k] ..
-// base[k+1]-1: ((u, from the last pair of query tiles down) * Hkv + KV head) * ns + chunk.
+// What the host planned: ranges of a request's pairs of query tiles, longest key lists first. Rank k
+// has the items base[k] .. base[k+1]-1: ((u, from its last pair down) * Hkv + KV head) * ns + chunk.
 template <int CAP>
 struct Plan {
-  int n;                // requests
+  int n;                // ranks
   int32_t base[CAP + 1];
   int32_t rows[CAP];    // merged rows up to and with the rank's (those of requests that are cut)
   int32_t part[CAP];    // first partial row
-  int32_t qn[CAP];      // new tokens on the host
+  int32_t qn[CAP];      // new tokens of the request on the host
+  int32_t u0[CAP];      // first pair
   uint16_t req[CAP];    // request, from the launch's first
   uint16_t ns[CAP];     // chunks
 };
@@ -140,7 +141,7 @@ __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP>& P,
   it.rank = lo;
   it.ns = P.ns[lo];
   const int x = item - P.base[lo], per_u = A.Hkv * it.ns, units = (P.base[lo + 1] - P.base[lo]) / per_u;
-  const int u = units - 1 - x / per_u, y = x - (x / per_u) * per_u;
+  const int u = P.u0[lo] + units - 1 - x / per_u, y = x - (x / per_u) * per_u;
   it.hk = y / it.ns;
   it.c = y - it.hk * it.ns;
   it.r = req0 + P.req[lo];
@@ -879,63 +880,120 @@ bool make_map(CUtensorMap* m, const void* base, int d, int heads, int64_t rows, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Requests [r0, r1) as one launch: launch order, chunks, items and partial rows.
+// Requests from r0 on as one launch: its ranks, and how much scratch they need.
 struct Group {
-  int r0 = 0, n = 0;
+  int r0 = 0;
   int64_t items = 0, rows = 0, parts = 0;  // items; merged rows; partial rows
-  std::vector<int> req, qn, ns;
-  std::vector<int64_t> base, row1, part0;
+  struct Rank {
+    int req, qn, ns, u0;
+    int64_t base, row1, part;
+  };
+  std::vector<Rank> ranks;
 };
 
 constexpr int kSmallPlan = 64, kLargePlan = 1024;
 
 sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, int r0, int r1, int num_splits, int sms,
                       Group& g) {
-  // Chunks. A CTA an SM, items heaviest first: an item longer than a third of an SM's share of the
-  // key tiles would show in the tail, so it is cut into pieces of about that; pieces below kMinTiles
-  // tiles cost more in prologue and merge than they gain.
-  constexpr int kMinTiles = 8, kMaxAuto = 256;
+  constexpr int kMaxAuto = 256, kMaxRanges = 16;
+  constexpr double kItem = 2.0;    // an item's prologue and epilogue, in key tiles
+  constexpr double kMerge = 4.0;   // the merge launch
+  struct Req {
+    int req, n, units, first, last, ns;  // new tokens, pairs of query tiles, key tiles of the first and last pair
+  };
+  std::vector<Req> reqs;
   g.r0 = r0;
-  std::vector<int> tiles(r1 - r0), units(r1 - r0), idx;
-  double work = 0;
+  auto tiles_of = [&](int n, int64_t len, int u) {  // key tiles of pair u
+    int gt, wl;
+    const int64_t t0 = (int64_t)2 * u * a.TQ, te = std::min<int64_t>(n, t0 + 2 * a.TQ), p0 = len - n;
+    return tile_list(seen(a, p0 + t0, p0 + te - 1, len), gt, wl);
+  };
+  int most = 0, several = 0;
   for (int r = r0; r < r1; ++r) {
     const int n = qi[r + 1] - qi[r];
-    const int64_t len = (int64_t)ki[r + 1] - ki[r];
     if (n == 0) continue;
-    const int nt = (n + a.TQ - 1) / a.TQ, u = (nt + 1) / 2;
-    const int64_t p0 = len - n;
-    auto count = [&](int v) {  // key tiles of pair v
-      int gt, wl;
-      const int64_t t0 = (int64_t)2 * v * a.TQ, te = std::min<int64_t>(n, t0 + 2 * a.TQ);
-      return tile_list(seen(a, p0 + t0, p0 + te - 1, len), gt, wl);
+    const int64_t len = (int64_t)ki[r + 1] - ki[r];
+    const int units = ((n + a.TQ - 1) / a.TQ + 1) / 2;
+    reqs.push_back(Req{r - r0, n, units, tiles_of(n, len, 0), tiles_of(n, len, units - 1), std::max(num_splits, 1)});
+    most = std::max(most, std::max(reqs.back().first, reqs.back().last));
+    several += units > 1;
+  }
+  // Chunks. The launch ends when the SM with the most to do does: with the items sorted by length and
+  // handed out one by one that is about the largest of an SM's share, the longest item, and k times the
+  // item number (k - 1) * SMs + 1 (some SM has k items of at least that length). Cutting shortens items
+  // and adds to the share: a prologue each, fp32 partials written and read, and a merge. Lengths of
+  // pieces from the longest list down are tried and the best estimate is kept. (64 single tokens over
+  // 549,646 cached ones: 459 us whole, 355 in pieces of an SM's third, 482 in 16 pieces each; a
+  // 2048-token prompt: 85 us in pieces of 8 tiles, 40 whole.)
+  if (num_splits == 0 && most > 2) {
+    auto chunks = [&](int tiles, int piece) { return std::min(kMaxAuto, std::max(1, (tiles + piece - 1) / piece)); };
+    auto estimate = [&](int piece) {
+      constexpr int kBins = 32;
+      double work = 0, longest = 0;
+      int64_t bins[kBins] = {0};  // items by length, in steps of the longest possible one / 32
+      const double step = (std::min(piece, most) + kItem) / kBins;
+      bool cut = false;
+      for (const Req& q : reqs) {
+        const int tiles = std::max(q.first, q.last), ns = chunks(tiles, piece);
+        const int64_t items = (int64_t)q.units * a.Hkv * ns;
+        const double len = 0.5 * (q.first + q.last) / ns + kItem;
+        work += len * (double)items;
+        longest = std::max(longest, (double)tiles / ns + kItem);
+        bins[std::min(kBins - 1, (int)(len / step))] += items;
+        if (ns > 1) {
+          cut = true;
+          work += (double)q.n * a.Hq * ns * 8.0 * (a.d + 1) / 65536.0;  // (a tile of K and V is 64 KB at most)
+        }
+      }
+      double end = std::max(work / sms, longest);
+      int64_t before = 0, k = 1;
+      for (int b = kBins - 1; b >= 0 && k <= 8; --b) {
+        for (; k <= 8 && (k - 1) * sms < before + bins[b]; ++k) end = std::max(end, (double)k * (b + 0.5) * step);
+        before += bins[b];
+      }
+      return end + (cut ? kMerge : 0.0);
     };
-    tiles[r - r0] = std::max(count(u - 1), count(0));
-    units[r - r0] = u;
-    work += (double)a.Hkv * u * (count(0) + count(u - 1)) / 2.0;
-    idx.push_back(r - r0);
-  }
-  const int piece = std::max(kMinTiles, (int)std::ceil(work / sms / 3.0));
-  std::vector<int> chunks(r1 - r0);
-  for (int i : idx) chunks[i] = num_splits > 0 ? num_splits : std::min(kMaxAuto, std::max(1, (tiles[i] + piece - 1) / piece));
-  // longest pieces first
-  std::stable_sort(idx.begin(), idx.end(), [&](int x, int y) {
-    return (int64_t)tiles[x] * chunks[y] > (int64_t)tiles[y] * chunks[x];
-  });
-  for (int i : idx) {
-    const int n = qi[r0 + i + 1] - qi[r0 + i], ns = chunks[i];
-    g.req.push_back(i);
-    g.qn.push_back(n);
-    g.ns.push_back(ns);
-    g.base.push_back(g.items);
-    g.part0.push_back(g.parts);
-    g.items += (int64_t)units[i] * a.Hkv * ns;
-    if (ns > 1) {
-      g.rows += (int64_t)n * a.Hq;
-      g.parts += (int64_t)n * a.Hq * ns;
+    int best = most;
+    double best_end = estimate(most);
+    for (int piece = most; piece > 2;) {
+      piece = std::max(2, piece * 2 / 3);
+      const double end = estimate(piece);
+      if (end < 0.97 * best_end) {
+        best = piece;
+        best_end = end;
+      }
     }
-    g.row1.push_back(g.rows);
+    for (Req& q : reqs) q.ns = chunks(std::max(q.first, q.last), best);
   }
-  g.n = (int)g.req.size();
+  // ranks: with several prompts each is cut into ranges of pairs, so that long and short lists of all
+  // of them sort together
+  const int ranges = several > 1 ? std::max(1, std::min(kMaxRanges, kLargePlan / (int)reqs.size())) : 1;
+  struct Key {
+    double len;
+    int q, u0, u1;
+  };
+  std::vector<Key> keys;
+  for (int i = 0; i < (int)reqs.size(); ++i) {
+    const Req& q = reqs[i];
+    const int per = (q.units + ranges - 1) / ranges;
+    for (int u0 = 0; u0 < q.units; u0 += per) {
+      const int u1 = std::min(q.units, u0 + per);
+      const double last = q.units > 1 ? q.first + (double)(q.last - q.first) * (u1 - 1) / (q.units - 1) : q.last;
+      keys.push_back(Key{last / q.ns, i, u0, u1});
+    }
+  }
+  std::stable_sort(keys.begin(), keys.end(), [](const Key& x, const Key& y) { return x.len > y.len; });
+  std::vector<int64_t> part(reqs.size(), -1);
+  for (const Key& k : keys) {
+    const Req& q = reqs[k.q];
+    if (q.ns > 1 && part[k.q] < 0) {  // the request's first rank stands for its merged rows
+      part[k.q] = g.parts;
+      g.rows += (int64_t)q.n * a.Hq;
+      g.parts += (int64_t)q.n * a.Hq * q.ns;
+    }
+    g.ranks.push_back(Group::Rank{q.req, q.n, q.ns, k.u0, g.items, g.rows, std::max<int64_t>(part[k.q], 0)});
+    g.items += (int64_t)(k.u1 - k.u0) * a.Hkv * q.ns;
+  }
   if (g.items > INT32_MAX || g.parts > INT32_MAX / 2) return STA_ERR_UNSUPPORTED;
   return STA_OK;
 }
@@ -945,17 +1003,19 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 template <int D, int CAP>
 sta_status launch_group(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a,
                         const Group& g, cudaStream_t st) {
-  Plan<CAP> p{};
-  p.n = g.n;
-  for (int i = 0; i < g.n; ++i) {
-    p.base[i] = (int32_t)g.base[i];
-    p.rows[i] = (int32_t)g.row1[i];
-    p.part[i] = (int32_t)g.part0[i];
-    p.qn[i] = g.qn[i];
-    p.req[i] = (uint16_t)g.req[i];
-    p.ns[i] = (uint16_t)g.ns[i];
+  Plan<CAP> p;
+  p.n = (int)g.ranks.size();
+  for (int i = 0; i < p.n; ++i) {
+    const Group::Rank& k = g.ranks[i];
+    p.base[i] = (int32_t)k.base;
+    p.rows[i] = (int32_t)k.row1;
+    p.part[i] = (int32_t)k.part;
+    p.qn[i] = k.qn;
+    p.u0[i] = k.u0;
+    p.req[i] = (uint16_t)k.req;
+    p.ns[i] = (uint16_t)k.ns;
   }
-  p.base[g.n] = (int32_t)g.items;
+  p.base[p.n] = (int32_t)g.items;
   auto kern = chunk_kernel<D, CAP>;
   STA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM));
   kern<<<(unsigned)g.items, kThreads, Cfg<D>::SMEM, st>>>(tq, tk, tv, a, p, g.r0);
@@ -1007,6 +1067,7 @@ extern "C" sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const
   a.N = q_indptr_host[n_req];
   a.Hq = Hq;
   a.Hkv = Hkv;
+  a.d = d;
   a.G = Hq / Hkv;
   a.TQ = kBM / a.G;
   a.page_size = page_size;
@@ -1066,7 +1127,7 @@ extern "C" sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const
   const cudaStream_t s = (cudaStream_t)stream;
   for (const Group& g : groups) {
     if (g.items == 0) continue;
-    const sta_status st = g.n <= kSmallPlan ? (d == 64 ? launch_group<64, kSmallPlan>(tq, tk, tv, a, g, s)
+    const sta_status st = g.ranks.size() <= kSmallPlan ? (d == 64 ? launch_group<64, kSmallPlan>(tq, tk, tv, a, g, s)
                                                        : launch_group<128, kSmallPlan>(tq, tk, tv, a, g, s))
                                             : (d == 64 ? launch_group<64, kLargePlan>(tq, tk, tv, a, g, s)
                                                        : launch_group<128, kLargePlan>(tq, tk, tv, a, g, s));
