@@ -100,10 +100,10 @@ __global__ void __launch_bounds__(kThreads) pages_copy_kernel(const __grid_const
     uint4 v[kSlice / 16 / kThreads];
 #pragma unroll
     for (int u = 0; u < kSlice / 16 / kThreads; ++u)
-      if (threadIdx.x + u * kThreads < nv) v[u] = __ldcs(from + threadIdx.x + u * kThreads);
+      if (threadIdx.x + u * kThreads < nv) v[u] = __ldg(from + threadIdx.x + u * kThreads);
 #pragma unroll
     for (int u = 0; u < kSlice / 16 / kThreads; ++u)
-      if (threadIdx.x + u * kThreads < nv) __stcs(to + threadIdx.x + u * kThreads, v[u]);
+      if (threadIdx.x + u * kThreads < nv) to[threadIdx.x + u * kThreads] = v[u];
   }
 }
 
@@ -387,13 +387,13 @@ sta_status launch_copy(void* const* bufs, int n_bufs, size_t page_bytes, int n_p
                        const int32_t* dst, int n, const int32_t* n_dev, const Lists& L, const int32_t* page_map, int* err,
                        cudaStream_t st) {
   const int64_t slices = cdiv((int64_t)page_bytes, kSlice);
-  const unsigned remap = page_map ? (unsigned)std::min<int64_t>(cdiv(L.n_req, kThreads / 32), 152 * 8) : 0;
+  const unsigned remap = page_map ? (unsigned)std::min<int64_t>(cdiv(L.n_req, kThreads / 32), 152 * 6) : 0;
   for (int b0 = 0; b0 == 0 || b0 < n_bufs; b0 += kMaxBufs) {
     PageBufs pb;
     const int nb = std::min(kMaxBufs, n_bufs - b0);
     for (int b = 0; b < nb; ++b) pb.p[b] = static_cast<uint8_t*>(bufs[b0 + b]);
     const int64_t items = (int64_t)n * nb * slices;
-    const unsigned grid = std::max((unsigned)std::min<int64_t>(items, 152 * 8), b0 == 0 ? remap : 0u);
+    const unsigned grid = std::max((unsigned)std::min<int64_t>(items, 152 * 6), b0 == 0 ? remap : 0u);
     if (grid == 0) continue;
     pages_copy_kernel<<<grid, kThreads, 0, st>>>(pb, nb, (int64_t)page_bytes, n_pages, src, dst, n, n_dev, L,
                                                  b0 == 0 ? page_map : nullptr, err);
