@@ -305,6 +305,18 @@ __device__ __forceinline__ int clc_answer(const void* answer) {
   return got ? (int)x : -1;
 }
 
+// 32 bytes to one place, a whole sector at once (both halves of it where p is not 32-byte aligned).
+__device__ __forceinline__ void store32(void* p, const uint32_t* r) {
+  if (((uintptr_t)p & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+  }
+}
+
 // Bits of keys k0 .. k0 + 31 that lie in [lo, hi].
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int k0) {
   const int a = lo - k0, b = hi - k0;
@@ -797,14 +809,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (live) {
             if (it.ns > 1) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(A.part_o + prow * D + c0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            } else {
-#pragma unroll
               for (int e = 0; e < 32; e += 8)
-                *reinterpret_cast<uint4*>(A.o + row * D + c0 + e) =
-                    make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]), pack_bf16x2(o[e + 4], o[e + 5]),
-                               pack_bf16x2(o[e + 6], o[e + 7]));
+                store32(A.part_o + prow * D + c0 + e, reinterpret_cast<const uint32_t*>(o) + e);
+            } else {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+              store32(A.o + row * D + c0, w);
+              store32(A.o + row * D + c0 + 16, w + 8);
             }
           }
         }
