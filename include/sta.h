@@ -537,7 +537,8 @@ sta_status sta_rope_append_paged(const void* q, const void* k, const void* v, in
  *              computed (0x606 in the device error word)
  *   page_indptr / page_indices  as for sta_decode_splitkv_paged; a page number outside
  *              [0, n_pages), or a list shorter than its sequence, reads page 0 and sets
- *              the device error word to 0x110
+ *              the device error word to 0x110. page_indices may be NULL when every
+ *              sequence is empty
  *   pattern    NULL: causal; else a STA_MASK_PATTERN source (host) over positions:
  *              token at position i sees key j when (!causal || j <= i) && ((win_lo <=
  *              j - i && j - i <= win_hi) || j < n_global_cols). A token that sees no key

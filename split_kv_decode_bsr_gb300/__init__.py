@@ -820,7 +820,7 @@ def sta_chunk_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
         _need(o.shape == q.shape and o.dtype == q.dtype and o.is_contiguous(), "o: contiguous, q's shape and dtype")
         _need(lse.shape == (n, Hq) and lse.dtype == torch.float32 and lse.is_contiguous(), "lse: contiguous float32 [n, Hq]")
         args = (q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), page_size, n_pages, page_indptr_dev.data_ptr(),
-                page_indices_dev.data_ptr(), q_indptr_dev.data_ptr(), qh, kv_indptr_dev.data_ptr(), kh, n_req, Hq, Hkv, d,
+                page_indices_dev.data_ptr() or None, q_indptr_dev.data_ptr(), qh, kv_indptr_dev.data_ptr(), kh, n_req, Hq, Hkv, d,
                 _dtype_code(q.dtype), scale, pat, num_splits, o.data_ptr(), lse.data_ptr())
         # most calls cut nothing and need the least scratch there is: one that needs more says how much
         ws = _workspace(256, workspace, dev)
@@ -845,7 +845,7 @@ def chunk_workspace_bytes(q_indptr, kv_indptr, n_req: int, Hq: int, Hkv: int, d:
     return int(n.value)
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=1024)
 def _pages_ws(fn: str, n_pages: int, n_req: int, n_forks: int) -> int:
     """Workspace size of a page call (it depends on these alone)."""
     n = C.c_size_t(0)

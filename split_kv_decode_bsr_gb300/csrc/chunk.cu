@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int pb = 0, pe = 0;
     auto page_at = [&](int tok) -> int {  // list entry of a token, unchecked; -1 behind the list
       const int o = pb + tok / P0;
-      return o >= 0 && o < pe ? __ldg(A.page_indices + o) : -1;
+      return o >= 0 && o < pe && A.page_indices ? __ldg(A.page_indices + o) : -1;
     };
     auto row_at = [&](int page, int tok) -> int {  // cache row; a page outside the cache reads page 0
       if (page < 0 || page >= A.n_pages) {
@@ -1111,8 +1111,8 @@ extern "C" sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const
   }
   if ((uintptr_t)workspace & 255) return STA_ERR_UNSUPPORTED;
   if (a.N == 0) return STA_OK;
-  if (!q || !k_pages || !v_pages || !page_indptr_dev || !page_indices_dev || !q_indptr_dev || !kv_indptr_dev || !o)
-    return STA_ERR_INVALID_ARG;
+  if (!q || !k_pages || !v_pages || !page_indptr_dev || !q_indptr_dev || !kv_indptr_dev || !o) return STA_ERR_INVALID_ARG;
+  if (!page_indices_dev && kv_indptr_host[n_req] > 0) return STA_ERR_INVALID_ARG;  // (no sequence holds a page)
   if (((uintptr_t)q | (uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)o) & 15) return STA_ERR_UNSUPPORTED;
   if (((uintptr_t)page_indptr_dev | (uintptr_t)page_indices_dev | (uintptr_t)q_indptr_dev | (uintptr_t)kv_indptr_dev |
        (uintptr_t)lse) & 3)

@@ -98,7 +98,7 @@ __device__ __forceinline__ bool token_place(const RopeArgs& A, int64_t t, int& p
   }
   pos = (int)p;
   const int64_t e = (int64_t)__ldg(A.page_indptr + lo) + p / A.page_size;
-  if (e >= __ldg(A.page_indptr + lo + 1)) {
+  if (e < 0 || e >= __ldg(A.page_indptr + lo + 1)) {
     record_error(A.err, 0x604);
     return true;
   }

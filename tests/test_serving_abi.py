@@ -139,6 +139,17 @@ def test_chunk_workspace_grows_with_the_splits(lib):
     assert _chunk(lib, splits=1)[1] == 256
 
 
+def test_chunk_workspace_of_many_requests(lib):
+    # planned 1024 requests at a time, over one workspace: that of the largest part
+    def need(n_req, kv, splits):
+        return sta.chunk_workspace_bytes(np.arange(n_req + 1), np.arange(n_req + 1) * kv, n_req, 8, 2, 64, num_splits=splits)
+
+    assert need(1024, 300, 2) == need(2048, 300, 2) == need(3000, 300, 2) > need(1000, 300, 2)
+    assert need(3000, 300, 1) == 256
+    assert need(1, 1, 0) == 256  # one key: nothing to cut
+    assert need(1, 1 << 20, 0) > 256  # one long sequence: cut over the SMs
+
+
 def _bufs(n=2, at=P):
     return (C.c_void_p * max(n, 1))(*[at + 4096 * i for i in range(n)])
 

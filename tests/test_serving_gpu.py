@@ -317,6 +317,115 @@ def test_chunk_single_tokens_equal_the_paged_decode(dev):
     check_chunk(o2, lse2, ref, 5)
 
 
+def test_chunk_many_requests(dev):
+    # more requests than one launch plans, single tokens and short chunks, all lengths from 0 on
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    g = np.random.default_rng(23)
+    R = 1300
+    new = g.integers(0, 3, R)
+    kv = np.maximum(new, g.integers(0, 60, R))
+    c = PagedCase(23, new, kv, 2, 1, 64, 16)
+    ref = c.ref(1 / 8)
+    for splits in (0, 2):
+        o, lse = sta.sta_chunk_fwd_paged(**c.dev(dev), num_splits=splits)
+        check_chunk(o, lse, ref, int(c.q_indptr[-1]), f"{splits}")
+    # the lists' numbers and lengths of an empty batch
+    x = c.dev(dev)
+    zero = torch.zeros(R + 1, dtype=torch.int32, device=dev)
+    x.update(kv_indptr_dev=zero, kv_indptr_host=np.zeros(R + 1, np.int32), page_indptr_dev=zero,
+             page_indices_dev=torch.empty(0, dtype=torch.int32, device=dev))
+    o, lse = sta.sta_chunk_fwd_paged(**x)
+    assert (o == 0).all() and lse.isneginf().all()
+
+
+def test_chunk_several_prompts(dev):
+    # query tiles of several prompts in one launch order
+    _chunk_case(dev, PagedCase(24, [700, 1, 333, 500, 2, 64], [700, 900, 800, 510, 3, 64], 6, 2, 64, 32))
+
+
+def test_chunk_group_of_128_heads(dev):
+    _chunk_case(dev, PagedCase(25, [3, 1, 2], [40, 500, 2], 128, 1, 128, 16))
+
+
+def test_chunk_output_at_odd_places(dev):
+    # o on a 16-byte boundary that is not a 32-byte one; lse on a 4-byte one
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = PagedCase(26, [5, 40], [300, 50], 4, 2, 64, 16)
+    room = torch.full((45 * 4 * 64 + 8 + 8,), 3.0, device=dev, dtype=torch.bfloat16)
+    o = room[8:-8].view(45, 4, 64)
+    lroom = torch.full((45 * 4 + 2,), 3.0, device=dev)
+    lse = lroom[1:-1].view(45, 4)
+    sta.sta_chunk_fwd_paged(**c.dev(dev), o=o, lse=lse)
+    check_chunk(o, lse, c.ref(1 / 8), 45)
+    assert (room[:8] == 3.0).all() and (room[-8:] == 3.0).all() and lroom[0] == 3.0 and lroom[-1] == 3.0
+
+
+def test_chunk_cache_past_32_bits(dev):
+    # pages at the end of a cache of more than 4 GiB a tensor: byte offsets past 2^32
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    n_pages, P, Hkv, d = 40000, 64, 8, 128
+    kc = torch.zeros(n_pages, P, Hkv, d, device=dev, dtype=torch.bfloat16)
+    vc = torch.zeros_like(kc)
+    assert kc.numel() * 2 > 1 << 32
+    for P_case in (64, 100):
+        c = PagedCase(27, [3, 20], [200, 150], 16, 8, 128, P_case)
+        x = c.dev(dev)
+        at = n_pages * P // P_case - c.n_pages  # the case's pages, at the end of the cache
+        k, v = (t.flatten()[: (n_pages * P // P_case) * P_case * Hkv * d].view(-1, P_case, Hkv, d) for t in (kc, vc))
+        k[at:].copy_(x["k_pages"]), v[at:].copy_(x["v_pages"])
+        x["page_indices_dev"] += at
+        x.update(k_pages=k, v_pages=v)
+        o, lse = sta.sta_chunk_fwd_paged(**x)
+        check_chunk(o, lse, c.ref(1 / math.sqrt(128)), 23, f"{P_case}")
+        new = torch.randn(23, 8, 128, device=dev).to(torch.bfloat16)
+        sta.sta_rope_append_paged(None, new, new, k, v, x["page_indptr_dev"], x["page_indices_dev"], x["q_indptr_dev"],
+                                  x["kv_indptr_dev"])
+        rows = np.r_[c.rows(0, np.arange(197, 200)), c.rows(1, np.arange(130, 150))] + at * P_case
+        assert torch.equal(k.reshape(-1, 8, 128)[torch.from_numpy(rows).to(dev)], new)
+
+
+def test_chunk_is_bitwise_repeatable(dev):
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = PagedCase(28, [200, 1, 1, 77], [900, 3000, 20, 77], 8, 2, 128, 16)
+    x = c.dev(dev)
+    first = sta.sta_chunk_fwd_paged(**x)
+    for _ in range(5):
+        again = sta.sta_chunk_fwd_paged(**x)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_chunk_two_calls_at_once(dev):
+    # two streams, two workspaces, one cache
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    a, b = PagedCase(29, [300, 1], [900, 4000], 8, 2, 128, 16), PagedCase(30, [1, 9, 64], [2500, 30, 640], 8, 2, 128, 16)
+    xa, xb = a.dev(dev), b.dev(dev)
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(4):
+        outs.append((sta.sta_chunk_fwd_paged(**xa, stream=s), sta.sta_chunk_fwd_paged(**xb, stream=t)))
+    torch.cuda.synchronize()
+    ra, rb = a.ref(1 / math.sqrt(128)), b.ref(1 / math.sqrt(128))
+    for (oa, la), (ob, lb) in outs:
+        check_chunk(oa, la, ra, 301)
+        check_chunk(ob, lb, rb, 74)
+
+
 def test_chunk_bad_pages_are_reported(dev):
     import split_kv_decode_bsr_gb300 as sta
 
@@ -481,6 +590,70 @@ def test_pages_compact(dev, P, lens, elems, room, n_pages):
         page_map, status = sta.sta_pages_compact(bufs, ref, ptr, idx, kv, P)
         goes, want = pool.compact(host)
         assert status.tolist() == want and page_map.tolist() == goes
+        _same(pool, ref, idx, host, bufs)
+
+
+def test_pages_counts_at_an_odd_place(dev):
+    # ref on a 4-byte boundary, and a pool that ends inside a run of 16 pages
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    pool = Pool(77, [int(x) for x in np.random.default_rng(9).integers(0, 60, 90)], 7, 12, 1237)
+    ref, ptr, idx, kv = _pool_dev(pool, dev)
+    room = torch.full((pool.n_pages + 6,), 9, dtype=torch.int32, device=dev)
+    room[3:-3] = ref
+    ref = room[3:-3]
+    host, bufs = _buffers(pool, dev, 1, 16)
+    _, status = sta.sta_pages_compact(bufs, ref, ptr, idx, kv, 7)
+    assert status.tolist() == pool.compact(host)[1]
+    _same(pool, ref, idx, host, bufs)
+    new = [min(x + 9, 84) for x in pool.kv]
+    grown = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device=dev)
+    assert sta.sta_pages_grow(ref, ptr, idx, kv, grown, 7).tolist() == pool.grow(new)
+    _same(pool, ref, idx)
+    assert (room[:3] == 9).all() and (room[-3:] == 9).all()
+
+
+def test_pages_calls_captured_together(dev):
+    # one graph holds a step's bookkeeping; replayed on other lists and counts it does other work
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    i32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device=dev)  # noqa: E731
+    lens = [[40, 0, 16, 1, 100, 33, 0, 7], [9, 64, 0, 80, 16, 0, 3, 50]]
+    forks = [([0, 4], [1, 6]), ([3, 1], [2, 5])]
+    leave = [[2, 7], [0, 6]]
+    pools = [Pool(50 + i, n, 16, 9, 60) for i, n in enumerate(lens)]
+    state = [t.clone() for t in _pool_dev(pools[0], dev)]
+    ref, ptr, idx, kv = state
+    _, bufs = _buffers(pools[0], dev, 2, 64)
+    par, ch, out = i32(forks[0][0]), i32(forks[0][1]), i32(leave[0])
+
+    def step():
+        a = sta.sta_pages_fork(bufs, ref, ptr, idx, kv, par, ch, 16)
+        sta.sta_pages_free(ref, ptr, idx, kv, out, 16)
+        return a
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        status = step()
+    for i, pool in enumerate(pools):
+        host, fresh = _buffers(pool, dev, 2, 64, seed=i)
+        for t, n in zip(state, _pool_dev(pool, dev)):
+            t.copy_(n)
+        for b, f in zip(bufs, fresh):
+            b.copy_(f)
+        par.copy_(i32(forks[i][0])), ch.copy_(i32(forks[i][1])), out.copy_(i32(leave[i]))
+        g.replay()
+        assert status.tolist() == pool.fork(host, *forks[i])
+        pool.free(leave[i])
         _same(pool, ref, idx, host, bufs)
 
 
