@@ -551,7 +551,8 @@ sta_status sta_rope_append_paged(const void* q, const void* k, const void* v, in
  *              be NULL)
  *   workspace  device scratch for the chunks' partials, 256-byte aligned; NULL sets
  *              *workspace_bytes and returns, and so does one that is too small, with
- *              STA_ERR_WORKSPACE
+ *              STA_ERR_WORKSPACE. A call that needs 256 bytes cuts nothing and does not
+ *              touch them
  * Keys and values of a sequence's tokens must be finite; what pages hold behind the
  * sequence is never used. Asynchronous on `stream`. */
 sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages, int page_size,

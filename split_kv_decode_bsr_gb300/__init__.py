@@ -21,6 +21,7 @@ Operations (sources):
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import functools
 import math
@@ -29,6 +30,7 @@ import threading
 from dataclasses import dataclass
 from typing import List, Optional, Sequence
 
+import numpy as np
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -635,32 +637,32 @@ def _addr(t: Optional[torch.Tensor]):
 
 class _Launch:
     """The device a call launches on, made current, and its stream, made torch's current one so that
-    what the call allocates belongs to that stream. Entering gives the stream's handle."""
-    __slots__ = ("_dev", "_stream", "_outer")
+    what the call allocates belongs to that stream; leave() puts back what was current."""
 
     def __init__(self, dev: torch.device, stream):
-        self._dev, self._stream, self._outer = dev, stream, ()
+        self._outer = contextlib.ExitStack()
+        with contextlib.ExitStack() as outer:
+            outer.enter_context(torch.cuda.device(dev))
+            if stream is None:
+                stream = torch.cuda.current_stream(dev)
+            else:
+                if not isinstance(stream, torch.cuda.Stream):
+                    stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
+                outer.enter_context(torch.cuda.stream(stream))
+            self.handle = stream.cuda_stream
+            self._outer = outer.pop_all()
 
-    def __enter__(self):
-        dev, s = self._dev, self._stream
-        if s is None and dev.index == torch._C._cuda_getDevice():
-            return torch._C._cuda_getCurrentRawStream(dev.index)
-        outer = [torch.cuda.device(dev)]
-        outer[0].__enter__()
-        if s is None:
-            s = torch.cuda.current_stream(dev)
-        else:
-            if not isinstance(s, torch.cuda.Stream):
-                s = torch.cuda.ExternalStream(int(s), device=dev) if int(s) else torch.cuda.default_stream(dev)
-            outer.append(torch.cuda.stream(s))
-            outer[1].__enter__()
-        self._outer = outer
-        return s.cuda_stream
+    def leave(self):
+        self._outer.close()
 
-    def __exit__(self, *exc):
-        for c in reversed(self._outer):
-            c.__exit__(*exc)
-        return False
+
+def _enter(dev: torch.device, stream):
+    """The handle of the stream to launch on, and the _Launch to leave afterwards (None: the current
+    device and stream, which the calls of a decoding loop use, need nothing changed)."""
+    if stream is None and dev.index == torch._C._cuda_getDevice():
+        return torch._C._cuda_getCurrentRawStream(dev.index), None
+    ctx = _Launch(dev, stream)
+    return ctx.handle, ctx
 
 
 def _workspace(need: int, workspace: Optional[torch.Tensor], dev: torch.device) -> torch.Tensor:
@@ -674,14 +676,15 @@ def _workspace(need: int, workspace: Optional[torch.Tensor], dev: torch.device) 
 
 
 def _host_i32(x, n: int, what: str):
-    """Host int32 values: their address, and the array that keeps them alive."""
-    import numpy as np
-
-    a = x.numpy() if isinstance(x, torch.Tensor) else x
-    if not (isinstance(a, np.ndarray) and a.dtype == np.int32 and a.flags.c_contiguous):
-        a = np.ascontiguousarray(a, dtype=np.int32)
-    _need(a.shape == (n,), f"{what}: {n} values")
-    return a.__array_interface__["data"][0], a
+    """Host int32 values: their address, the last one, and the object that keeps them alive."""
+    if isinstance(x, torch.Tensor) and x.dtype is torch.int32 and x.device.type == "cpu" and x.is_contiguous():
+        at, shape = x.data_ptr(), x.shape
+    else:
+        x = np.ascontiguousarray(x, dtype=np.int32)
+        at, shape = x.__array_interface__["data"][0], x.shape
+    if n < 1 or len(shape) != 1 or shape[0] != n:
+        raise ValueError(f"{what}: {n} values, at least one")
+    return at, C.c_int32.from_address(at + 4 * (n - 1)).value, x
 
 
 class Rope:
@@ -711,10 +714,11 @@ class Rope:
 
 def _heads_view(t: torch.Tensor, what: str):
     """[n, H, d] with contiguous heads: the token stride."""
-    _need(t.dim() == 3, f"{what}: [tokens, heads, d]")
+    if t.dim() != 3:
+        raise ValueError(f"{what}: [tokens, heads, d]")
     n, H, d = t.shape
-    _need(n == 0 or ((d == 1 or t.stride(2) == 1) and (H == 1 or t.stride(1) == d)),
-          f"{what}: a token's heads must be contiguous")
+    if not (n == 0 or ((d == 1 or t.stride(2) == 1) and (H == 1 or t.stride(1) == d))):
+        raise ValueError(f"{what}: a token's heads must be contiguous")
     return t.stride(0) if n > 1 else H * d
 
 
@@ -730,13 +734,20 @@ def sta_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope, transpose: bo
     dev = x.device
     _on(dev, y)
     _i32(dev, positions=positions)
-    _need(positions.shape == (n,), "positions: one a token")
+    if positions.shape != (n,):
+        raise ValueError("positions: one a token")
     code = _dtype_code(x.dtype)
-    with _Launch(dev, stream) as st:
+    st, ctx = _enter(dev, stream)
+    try:
         y = torch.empty((n, H, d), dtype=x.dtype, device=dev) if y is None else y
-        _need(y.shape == x.shape and y.dtype == x.dtype, "y: x's shape and dtype")
-        _check("sta_rope", lib().sta_rope(_addr(x), _addr(y), _addr(positions), C.byref(rope.struct), n, H, d, xs,
-                                          _heads_view(y, "y"), int(bool(transpose)), code, st))
+        if not (y.shape == x.shape and y.dtype == x.dtype):
+            raise ValueError("y: x's shape and dtype")
+        _check("sta_rope", (_lib_handle or lib()).sta_rope(
+            _addr(x), _addr(y), _addr(positions), C.byref(rope.struct), n, H, d, xs, _heads_view(y, "y"), int(bool(transpose)),
+            code, st))
+    finally:
+        if ctx is not None:
+            ctx.leave()
     return y
 
 
@@ -755,32 +766,42 @@ def sta_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
     _on(dev, q, v, k_pages, v_pages, q_out)
     n_pages, page_size, Hkv, d = k_pages.shape
     n = k.shape[0]
-    _need(v_pages.shape == k_pages.shape and k_pages.is_contiguous() and v_pages.is_contiguous(),
-          "k_pages, v_pages: contiguous [n_pages, page_size, Hkv, d]")
-    _need(k.shape == (n, Hkv, d) and v.shape == k.shape, "k, v: [n, Hkv, d]")
+    if not (v_pages.shape == k_pages.shape and k_pages.is_contiguous() and v_pages.is_contiguous()):
+        raise ValueError("k_pages, v_pages: contiguous [n_pages, page_size, Hkv, d]")
+    if not (k.shape == (n, Hkv, d) and v.shape == k.shape):
+        raise ValueError("k, v: [n, Hkv, d]")
     ks, vs = _heads_view(k, "k"), _heads_view(v, "v")
     Hq, qs = 0, 0
     if q is not None:
         qs = _heads_view(q, "q")
         Hq = q.shape[1]
-        _need(q.shape == (n, Hq, d), "q: [n, Hq, d]")
+        if not (q.shape == (n, Hq, d)):
+            raise ValueError("q: [n, Hq, d]")
     for t in (q, k, v, k_pages, v_pages, q_out):
-        _need(t is None or t.dtype == torch.bfloat16, "bf16 only")
+        if not (t is None or t.dtype == torch.bfloat16):
+            raise ValueError("bf16 only")
     _i32(dev, page_indptr=page_indptr_dev, page_indices=page_indices_dev, q_indptr=q_indptr_dev, kv_indptr=kv_indptr_dev)
     n_req = q_indptr_dev.numel() - 1
-    _need(kv_indptr_dev.numel() == n_req + 1 and page_indptr_dev.numel() == n_req + 1, "indptr: n_req + 1 values each")
+    if not (kv_indptr_dev.numel() == n_req + 1 and page_indptr_dev.numel() == n_req + 1):
+        raise ValueError("indptr: n_req + 1 values each")
     if positions is not None:
         _i32(dev, positions=positions)
-        _need(positions.shape == (n,), "positions: one a token")
-    with _Launch(dev, stream) as st:
+        if positions.shape != (n,):
+            raise ValueError("positions: one a token")
+    st, ctx = _enter(dev, stream)
+    try:
         if q is not None and q_out is None:
             q_out = torch.empty((n, Hq, d), dtype=q.dtype, device=dev)
         if q_out is not None:
-            _need(q is not None and q_out.shape == q.shape and q_out.is_contiguous(), "q_out: contiguous, q's shape")
-        _check("sta_rope_append_paged", lib().sta_rope_append_paged(
+            if not (q is not None and q_out.shape == q.shape and q_out.is_contiguous()):
+                raise ValueError("q_out: contiguous, q's shape")
+        _check("sta_rope_append_paged", (_lib_handle or lib()).sta_rope_append_paged(
             _addr(q), _addr(k), _addr(v), qs, ks, vs, _addr(q_out), _addr(k_pages), _addr(v_pages), page_size, n_pages,
             _addr(page_indptr_dev), _addr(page_indices_dev), _addr(q_indptr_dev), _addr(kv_indptr_dev), _addr(positions),
             C.byref(rope.struct) if rope is not None else None, n, n_req, Hq, Hkv, d, STA_BF16, st))
+    finally:
+        if ctx is not None:
+            ctx.leave()
     return q_out
 
 
@@ -802,34 +823,42 @@ def sta_chunk_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
     dev = q.device
     _on(dev, k_pages, v_pages, o, lse)
     n_pages, page_size, Hkv, dk = k_pages.shape
-    _need(dk == d and v_pages.shape == k_pages.shape and k_pages.is_contiguous() and v_pages.is_contiguous(),
-          "k_pages, v_pages: contiguous [n_pages, page_size, Hkv, d]")
-    _need(q.dtype == k_pages.dtype == v_pages.dtype, "q, k_pages, v_pages: one dtype")
+    if not (dk == d and v_pages.shape == k_pages.shape and k_pages.is_contiguous() and v_pages.is_contiguous()):
+        raise ValueError("k_pages, v_pages: contiguous [n_pages, page_size, Hkv, d]")
+    if not (q.dtype == k_pages.dtype == v_pages.dtype):
+        raise ValueError("q, k_pages, v_pages: one dtype")
     _i32(dev, page_indptr=page_indptr_dev, page_indices=page_indices_dev, q_indptr=q_indptr_dev, kv_indptr=kv_indptr_dev)
     n_req = q_indptr_dev.numel() - 1
-    _need(kv_indptr_dev.numel() == n_req + 1 and page_indptr_dev.numel() == n_req + 1, "indptr: n_req + 1 values each")
-    qh, keep_q = _host_i32(q_indptr_host, n_req + 1, "q_indptr_host")
-    kh, keep_k = _host_i32(kv_indptr_host, n_req + 1, "kv_indptr_host")
-    _need(0 <= int(keep_q[-1]) <= n, "q_indptr: past q's rows")
+    if not (kv_indptr_dev.numel() == n_req + 1 and page_indptr_dev.numel() == n_req + 1):
+        raise ValueError("indptr: n_req + 1 values each")
+    qh, rows, keep_q = _host_i32(q_indptr_host, n_req + 1, "q_indptr_host")
+    kh, _, keep_k = _host_i32(kv_indptr_host, n_req + 1, "kv_indptr_host")
+    if not 0 <= rows <= n:
+        raise ValueError("q_indptr: past q's rows")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     pat = None if pattern is None else _src_array([pattern])
-    h = lib()
-    with _Launch(dev, stream) as st:
+    h = _lib_handle or lib()
+    st, ctx = _enter(dev, stream)
+    try:
         o = torch.empty((n, Hq, d), dtype=q.dtype, device=dev) if o is None else o
         lse = torch.empty((n, Hq), dtype=torch.float32, device=dev) if lse is None else lse
-        _need(o.shape == q.shape and o.dtype == q.dtype and o.is_contiguous(), "o: contiguous, q's shape and dtype")
-        _need(lse.shape == (n, Hq) and lse.dtype == torch.float32 and lse.is_contiguous(), "lse: contiguous float32 [n, Hq]")
+        if not (o.shape == q.shape and o.dtype == q.dtype and o.is_contiguous()):
+            raise ValueError("o: contiguous, q's shape and dtype")
+        if not (lse.shape == (n, Hq) and lse.dtype == torch.float32 and lse.is_contiguous()):
+            raise ValueError("lse: contiguous float32 [n, Hq]")
         args = (q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), page_size, n_pages, page_indptr_dev.data_ptr(),
                 page_indices_dev.data_ptr() or None, q_indptr_dev.data_ptr(), qh, kv_indptr_dev.data_ptr(), kh, n_req, Hq, Hkv, d,
                 _dtype_code(q.dtype), scale, pat, num_splits, o.data_ptr(), lse.data_ptr())
-        # most calls cut nothing and need the least scratch there is: one that needs more says how much
-        ws = _workspace(256, workspace, dev)
-        size = C.c_size_t(ws.numel())
-        status = h.sta_chunk_fwd_paged(*args, ws.data_ptr(), C.byref(size), st)
+        # most calls cut nothing: they need the least size there is and use none of it; one that cuts says how much
+        size = C.c_size_t(256 if workspace is None else _workspace(256, workspace, dev).numel())
+        status = h.sta_chunk_fwd_paged(*args, 256 if workspace is None else workspace.data_ptr(), C.byref(size), st)
         if status == STA_ERR_WORKSPACE:
             ws = _workspace(size.value, workspace, dev)
             status = h.sta_chunk_fwd_paged(*args, ws.data_ptr(), C.byref(size), st)
         _check("sta_chunk_fwd_paged", status)
+    finally:
+        if ctx is not None:
+            ctx.leave()
     return o, lse
 
 
@@ -837,9 +866,9 @@ def chunk_workspace_bytes(q_indptr, kv_indptr, n_req: int, Hq: int, Hkv: int, d:
                           pattern: Optional[MaskSource] = None, num_splits: int = 0) -> int:
     """Workspace size sta_chunk_fwd_paged needs for these requests (host only, never 0)."""
     n = C.c_size_t(0)
-    qh, keep_q = _host_i32(q_indptr, n_req + 1, "q_indptr")
-    kh, keep_k = _host_i32(kv_indptr, n_req + 1, "kv_indptr")
-    _check("sta_chunk_fwd_paged", lib().sta_chunk_fwd_paged(
+    qh, _, keep_q = _host_i32(q_indptr, n_req + 1, "q_indptr")
+    kh, _, keep_k = _host_i32(kv_indptr, n_req + 1, "kv_indptr")
+    _check("sta_chunk_fwd_paged", (_lib_handle or lib()).sta_chunk_fwd_paged(
         None, 0, None, None, page_size, 1, None, None, None, qh, None, kh, n_req, Hq, Hkv, d, STA_BF16, 1.0,
         None if pattern is None else _src_array([pattern]), num_splits, None, None, None, C.byref(n), None))
     return int(n.value)
@@ -862,15 +891,21 @@ def _pages_ws(fn: str, n_pages: int, n_req: int, n_forks: int) -> int:
 
 
 def _buf_array(bufs: Sequence[torch.Tensor], dev: torch.device, n_pages: Optional[int] = None):
-    """The buffers' device pointers (host array), their number, bytes a page and pages."""
+    """[n_pages, ...] buffers of one page size: their addresses, number, bytes a page and n_pages."""
     bufs = list(bufs)
-    page_bytes = 0
+    page_bytes, shape, dtype = 0, None, None
     for b in bufs:
-        _need(b.device == dev and b.is_contiguous() and b.dim() >= 1, f"buffers: contiguous on {dev}")
-        n_pages = b.shape[0] if n_pages is None else n_pages
-        _need(b.shape[0] == n_pages and n_pages > 0, "buffers: [n_pages, ...] each")
+        if not (b.is_contiguous() and b.device == dev and b.dim() >= 1):
+            raise ValueError(f"buffers: contiguous on {dev}")
+        if b.dtype is dtype and b.shape == shape:
+            continue  # as the one before: a cache's buffers are alike
+        shape, dtype = b.shape, b.dtype
+        n_pages = shape[0] if n_pages is None else n_pages
+        if not (shape[0] == n_pages and n_pages > 0):
+            raise ValueError("buffers: [n_pages, ...] each")
         nb = b.numel() // n_pages * b.element_size()
-        _need(page_bytes in (0, nb), "buffers: the same bytes a page")
+        if page_bytes not in (0, nb):
+            raise ValueError("buffers: the same bytes a page")
         page_bytes = nb
     return (C.c_void_p * max(len(bufs), 1))(*[b.data_ptr() for b in bufs]), len(bufs), page_bytes, n_pages
 
@@ -880,7 +915,8 @@ def _lists(ref, page_indptr, page_indices, kv_indptr):
     _on(dev)
     _i32(dev, ref=ref, page_indptr=page_indptr, page_indices=page_indices, kv_indptr=kv_indptr)
     n_req = kv_indptr.numel() - 1
-    _need(page_indptr.numel() == n_req + 1, "page_indptr, kv_indptr: n_req + 1 values each")
+    if not (page_indptr.numel() == n_req + 1):
+        raise ValueError("page_indptr, kv_indptr: n_req + 1 values each")
     return dev, n_req
 
 
@@ -888,14 +924,21 @@ def sta_pages_copy(bufs: Sequence[torch.Tensor], src: torch.Tensor, dst: torch.T
     """Page src[i] onto page dst[i] of every buffer [n_pages, ...] (int32, device; negative: no copy).
     Pages of dst must be distinct and not among src."""
     bufs = list(bufs)
-    _need(bufs, "at least one buffer")
+    if not bufs:
+        raise ValueError("at least one buffer")
     dev = bufs[0].device
     _on(dev)
     _i32(dev, src=src, dst=dst)
-    _need(src.dim() == 1 and src.shape == dst.shape, "src, dst: [n] each")
+    if not (src.dim() == 1 and src.shape == dst.shape):
+        raise ValueError("src, dst: [n] each")
     arr, nb, page_bytes, n_pages = _buf_array(bufs, dev)
-    with _Launch(dev, stream) as st:
-        _check("sta_pages_copy", lib().sta_pages_copy(arr, nb, page_bytes, n_pages, _addr(src), _addr(dst), src.numel(), st))
+    st, ctx = _enter(dev, stream)
+    try:
+        _check("sta_pages_copy", (_lib_handle or lib()).sta_pages_copy(
+            arr, nb, page_bytes, n_pages, _addr(src), _addr(dst), src.numel(), st))
+    finally:
+        if ctx is not None:
+            ctx.leave()
 
 
 def sta_pages_grow(ref: torch.Tensor, page_indptr: torch.Tensor, page_indices: torch.Tensor, kv_indptr: torch.Tensor,
@@ -904,13 +947,19 @@ def sta_pages_grow(ref: torch.Tensor, page_indptr: torch.Tensor, page_indices: t
     new_kv_indptr's; updates ref and page_indices, returns status int32 [2] {taken, missing}."""
     dev, n_req = _lists(ref, page_indptr, page_indices, kv_indptr)
     _i32(dev, new_kv_indptr=new_kv_indptr)
-    _need(new_kv_indptr.numel() == n_req + 1, "new_kv_indptr: n_req + 1 values")
-    with _Launch(dev, stream) as st:
+    if not (new_kv_indptr.numel() == n_req + 1):
+        raise ValueError("new_kv_indptr: n_req + 1 values")
+    st, ctx = _enter(dev, stream)
+    try:
         status = torch.empty(2, dtype=torch.int32, device=dev)
         args = (_addr(ref), ref.numel(), _addr(page_indptr), _addr(page_indices), _addr(kv_indptr), _addr(new_kv_indptr), n_req,
                 page_size, _addr(status))
         ws = torch.empty(_pages_ws("sta_pages_grow", ref.numel(), n_req, 0), dtype=torch.uint8, device=dev)
-        _check("sta_pages_grow", lib().sta_pages_grow(*args, ws.data_ptr(), C.byref(C.c_size_t(ws.numel())), st))
+        _check("sta_pages_grow", (_lib_handle or lib()).sta_pages_grow(
+            *args, ws.data_ptr(), C.byref(C.c_size_t(ws.numel())), st))
+    finally:
+        if ctx is not None:
+            ctx.leave()
     return status
 
 
@@ -922,14 +971,20 @@ def sta_pages_fork(bufs: Sequence[torch.Tensor], ref: torch.Tensor, page_indptr:
     page_indices, returns status int32 [2] {pages taken, missing}."""
     dev, n_req = _lists(ref, page_indptr, page_indices, kv_indptr)
     _i32(dev, parent=parent, child=child)
-    _need(parent.dim() == 1 and parent.shape == child.shape, "parent, child: [n_forks] each")
+    if not (parent.dim() == 1 and parent.shape == child.shape):
+        raise ValueError("parent, child: [n_forks] each")
     arr, nb, page_bytes, _ = _buf_array(bufs, dev, ref.numel())
-    with _Launch(dev, stream) as st:
+    st, ctx = _enter(dev, stream)
+    try:
         status = torch.empty(2, dtype=torch.int32, device=dev)
         args = (arr, nb, page_bytes, _addr(ref), ref.numel(), _addr(page_indptr), _addr(page_indices), _addr(kv_indptr), n_req,
                 page_size, _addr(parent), _addr(child), parent.numel(), _addr(status))
         ws = torch.empty(_pages_ws("sta_pages_fork", ref.numel(), n_req, parent.numel()), dtype=torch.uint8, device=dev)
-        _check("sta_pages_fork", lib().sta_pages_fork(*args, ws.data_ptr(), C.byref(C.c_size_t(ws.numel())), st))
+        _check("sta_pages_fork", (_lib_handle or lib()).sta_pages_fork(
+            *args, ws.data_ptr(), C.byref(C.c_size_t(ws.numel())), st))
+    finally:
+        if ctx is not None:
+            ctx.leave()
     return status
 
 
@@ -938,9 +993,14 @@ def sta_pages_free(ref: torch.Tensor, page_indptr: torch.Tensor, page_indices: t
     """The listed requests (int32, device) let go of the pages they hold; their entries become -1."""
     dev, n_req = _lists(ref, page_indptr, page_indices, kv_indptr)
     _i32(dev, reqs=reqs)
-    with _Launch(dev, stream) as st:
-        _check("sta_pages_free", lib().sta_pages_free(_addr(ref), ref.numel(), _addr(page_indptr), _addr(page_indices),
-                                                      _addr(kv_indptr), n_req, page_size, _addr(reqs), reqs.numel(), st))
+    st, ctx = _enter(dev, stream)
+    try:
+        _check("sta_pages_free", (_lib_handle or lib()).sta_pages_free(
+            _addr(ref), ref.numel(), _addr(page_indptr), _addr(page_indices), _addr(kv_indptr), n_req, page_size, _addr(reqs),
+            reqs.numel(), st))
+    finally:
+        if ctx is not None:
+            ctx.leave()
 
 
 def sta_pages_compact(bufs: Sequence[torch.Tensor], ref: torch.Tensor, page_indptr: torch.Tensor,
@@ -950,13 +1010,18 @@ def sta_pages_compact(bufs: Sequence[torch.Tensor], ref: torch.Tensor, page_indp
     {pages in use, pages moved}."""
     dev, n_req = _lists(ref, page_indptr, page_indices, kv_indptr)
     arr, nb, page_bytes, _ = _buf_array(bufs, dev, ref.numel())
-    with _Launch(dev, stream) as st:
+    st, ctx = _enter(dev, stream)
+    try:
         page_map = torch.empty(ref.numel(), dtype=torch.int32, device=dev)
         status = torch.empty(2, dtype=torch.int32, device=dev)
         args = (arr, nb, page_bytes, _addr(ref), ref.numel(), _addr(page_indptr), _addr(page_indices), _addr(kv_indptr), n_req,
                 page_size, _addr(page_map), _addr(status))
         ws = torch.empty(_pages_ws("sta_pages_compact", ref.numel(), n_req, 0), dtype=torch.uint8, device=dev)
-        _check("sta_pages_compact", lib().sta_pages_compact(*args, ws.data_ptr(), C.byref(C.c_size_t(ws.numel())), st))
+        _check("sta_pages_compact", (_lib_handle or lib()).sta_pages_compact(
+            *args, ws.data_ptr(), C.byref(C.c_size_t(ws.numel())), st))
+    finally:
+        if ctx is not None:
+            ctx.leave()
     return page_map, status
 
 
