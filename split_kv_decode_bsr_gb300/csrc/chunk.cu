@@ -840,8 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (warp_live && (dual || x == 0)) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const float row_lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+        const float inv = l != 0.f ? 1.f / l : 0.f;  // a NaN among the scores stays one
+        const float row_lse = l != 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
         w0 *= inv;
         w1 *= inv;
         const int h = it.hk * A.G + (m - tt * A.G);

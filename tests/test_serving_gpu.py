@@ -593,6 +593,39 @@ def test_pages_compact(dev, P, lens, elems, room, n_pages):
         _same(pool, ref, idx, host, bufs)
 
 
+@pytest.mark.parametrize("P", [1, 16])
+def test_pages_of_long_sequences(dev, P):
+    """Lists of thousands of pages, shared by many warps: freed, grown, forked, compacted."""
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    lens, room = [9000, 0, 20011, 0, 0, 5], 22000
+    pool = Pool(70, lens, P, room, 110000 // P + 6)
+    ref, ptr, idx, kv = _pool_dev(pool, dev)
+    host, bufs = _buffers(pool, dev, 1, 8)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+    cum = lambda a: i32([0] + np.cumsum(a).tolist())  # noqa: E731
+    assert sta.sta_pages_fork(bufs, ref, ptr, idx, kv, i32([2, 5]), i32([1, 3]), P).tolist() == pool.fork(host, [2, 5], [1, 3])
+    _same(pool, ref, idx, host, bufs)
+    pool.kv[1], pool.kv[3] = lens[2], lens[5]
+    sta.sta_pages_free(ref, ptr, idx, cum(pool.kv), i32([0, 2]), P)
+    pool.free([0, 2])
+    _same(pool, ref, idx)
+    pool.kv[0] = pool.kv[2] = 0
+    new = [0, 20500, 0, 5, 21999, 18000]
+    assert sta.sta_pages_grow(ref, ptr, idx, cum(pool.kv), cum(new), P).tolist() == pool.grow(new)
+    _same(pool, ref, idx)
+    pool.kv = new
+    sta.sta_pages_free(ref, ptr, idx, cum(new), i32([4]), P)
+    pool.free([4])
+    pool.kv[4] = 0
+    page_map, status = sta.sta_pages_compact(bufs, ref, ptr, idx, cum(pool.kv), P)
+    goes, want = pool.compact(host)
+    assert status.tolist() == want and page_map.tolist() == goes
+    _same(pool, ref, idx, host, bufs)
+
+
 def test_pages_counts_at_an_odd_place(dev):
     # ref on a 4-byte boundary, and a pool that ends inside a run of 16 pages
     import torch
