@@ -571,7 +571,8 @@ sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const void* k_pa
  * device) may be NULL. Codes in the device error word: 0x601 a page number outside
  * [0, n_pages), 0x602 a request number outside [0, n_req) (or a parent that is its own
  * child), 0x603 a free page freed, 0x604 a list too short, 0x605 a child that holds pages
- * or is named twice; the entry, fork or request concerned is then left as it was. All are
+ * or is named twice; the entry, fork or request concerned is then left as it was (a shared
+ * entry without a valid page is -1 in the child). All are
  * asynchronous on `stream` and synchronise nothing; workspace (256-byte aligned) follows
  * the usual protocol: NULL sets *workspace_bytes and returns. n_pages <= 2^30. */
 
@@ -585,7 +586,10 @@ sta_status sta_pages_copy(void* const* bufs_host, int n_bufs, size_t page_bytes,
 /* sta_pages_grow -- gives each request the free pages that it needs to go from the lengths
  * of kv_indptr to those of new_kv_indptr (a shorter new length gives and takes nothing).
  * status: {pages taken, pages that were wanted but not there}; an entry without a page is
- * -1. A request whose list has no room for the new length gets nothing (0x604). */
+ * -1. A request whose list has no room for the new length gets nothing (0x604). When pages
+ * run out the last requests lack them: sta_pages_free with new_kv_indptr's lengths gives
+ * back all that such a request holds (entries of -1 are passed over); calling this again
+ * with the old lengths would overwrite entries whose pages are taken already. */
 sta_status sta_pages_grow(int32_t* ref_dev, int n_pages, const int32_t* page_indptr_dev, int32_t* page_indices_dev,
                           const int32_t* kv_indptr_dev, const int32_t* new_kv_indptr_dev, int n_req, int page_size,
                           int32_t* status_dev, void* workspace, size_t* workspace_bytes, sta_stream stream);
