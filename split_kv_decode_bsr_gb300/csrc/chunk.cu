@@ -879,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (live) {
-          if (it.ns > 1) A.part_lse[prow] = row_lse;
+          if (it.ns > 1) A.part_lse[prow] = row_lse == row_lse ? row_lse : INFINITY;  // the merge makes a NaN of it again
           else if (A.lse) A.lse[row] = row_lse;
         }
       }

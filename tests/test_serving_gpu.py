@@ -288,6 +288,27 @@ def test_chunk_large_scores(dev):
     _chunk_case(dev, PagedCase(15, [50, 1], [300, 500], 4, 2, 64, 16, value=4.0), scale=3.0)
 
 
+@pytest.mark.parametrize("splits", [1, 3])
+def test_chunk_nan_query_stays_nan(dev, splits):
+    """A NaN in one head's query shows in that row's output and LSE, and nowhere else. (The second of
+    them is at position 5 - 40 + 19 of its sequence: it sees no key, and has no score to be NaN.)"""
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = PagedCase(15, [1, 40, 200], [700, 5, 300], 8, 2, 64, 16)
+    x = c.dev(dev)
+    clean, clean_lse = sta.sta_chunk_fwd_paged(**x, num_splits=splits)
+    bad = [(0, 3), (20, 0), (240, 7)]
+    for t, h in bad:
+        x["q"][t, h, 5] = float("nan")
+    o, lse = sta.sta_chunk_fwd_paged(**x, num_splits=splits)
+    for t, h in bad[::2]:
+        assert torch.isnan(o[t, h]).all() and torch.isnan(lse[t, h])
+        o[t, h], lse[t, h] = clean[t, h], clean_lse[t, h]
+    assert torch.equal(o, clean) and torch.equal(lse, clean_lse)
+
+
 def test_chunk_strided_queries(dev):
     import torch
 
