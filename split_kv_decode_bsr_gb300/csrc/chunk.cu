@@ -69,8 +69,8 @@ struct ChunkArgs {
   int* err;
 };
 
-// What the host planned: ranges of a request's pairs of query tiles, longest key lists first. Rank k
-// has the items base[k] .. base[k+1]-1: ((u, from its last pair down) * Hkv + KV head) * ns + chunk.
+// What the host planned: the requests with new tokens, longest key lists first. Rank k has the items
+// base[k] .. base[k+1]-1: ((pair of query tiles, from the last down) * Hkv + KV head) * ns + chunk.
 template <int CAP>
 struct Plan {
   int n;                // ranks
@@ -78,7 +78,6 @@ struct Plan {
   int32_t rows[CAP];    // merged rows up to and with the rank's (those of requests that are cut)
   int32_t part[CAP];    // first partial row
   int32_t qn[CAP];      // new tokens of the request on the host
-  int32_t u0[CAP];      // first pair
   uint16_t req[CAP];    // request, from the launch's first
   uint16_t ns[CAP];     // chunks
 };
@@ -147,7 +146,7 @@ __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP>& P,
   it.rank = lo;
   it.ns = P.ns[lo];
   const int x = item - P.base[lo], per_u = A.Hkv * it.ns, units = (P.base[lo + 1] - P.base[lo]) / per_u;
-  const int u = P.u0[lo] + units - 1 - x / per_u, y = x - (x / per_u) * per_u;
+  const int u = units - 1 - x / per_u, y = x - (x / per_u) * per_u;
   it.hk = y / it.ns;
   it.c = y - it.hk * it.ns;
   it.r = req0 + P.req[lo];
@@ -974,7 +973,7 @@ struct Group {
   int r0 = 0;
   int64_t items = 0, rows = 0, parts = 0;  // items; merged rows; partial rows
   struct Rank {
-    int req, qn, ns, u0;
+    int req, qn, ns;
     int64_t base, row1, part;
   };
   std::vector<Rank> ranks;
@@ -984,7 +983,7 @@ constexpr int kSmallPlan = 64, kLargePlan = 1024;
 
 sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, int r0, int r1, int num_splits, int sms,
                       Group& g) {
-  constexpr int kMaxAuto = 256, kMaxRanges = 16;
+  constexpr int kMaxAuto = 256;
   constexpr double kItem = 2.0;    // an item's prologue and epilogue, in key tiles
   constexpr double kMerge = 4.0;   // the merge launch
   struct Req {
@@ -997,7 +996,7 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
     const int64_t t0 = (int64_t)2 * u * a.TQ, te = std::min<int64_t>(n, t0 + 2 * a.TQ), p0 = len - n;
     return tile_list(seen(a, p0 + t0, p0 + te - 1, len), gt, wl);
   };
-  int most = 0, several = 0;
+  int most = 0;
   for (int r = r0; r < r1; ++r) {
     const int n = qi[r + 1] - qi[r];
     if (n == 0) continue;
@@ -1005,7 +1004,6 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
     const int units = ((n + a.TQ - 1) / a.TQ + 1) / 2;
     reqs.push_back(Req{r - r0, n, units, tiles_of(n, len, 0), tiles_of(n, len, units - 1), std::max(num_splits, 1)});
     most = std::max(most, std::max(reqs.back().first, reqs.back().last));
-    several += units > 1;
   }
   // Chunks. The launch ends when the SM with the most to do does: with the items sorted by length and
   // handed out one by one that is about the largest of an SM's share, the longest item, and k times the
@@ -1054,34 +1052,16 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
     }
     for (Req& q : reqs) q.ns = chunks(std::max(q.first, q.last), best);
   }
-  // ranks: with several prompts each is cut into ranges of pairs, so that long and short lists of all
-  // of them sort together
-  const int ranges = several > 1 ? std::max(1, std::min(kMaxRanges, kLargePlan / (int)reqs.size())) : 1;
-  struct Key {
-    double len;
-    int q, u0, u1;
-  };
-  std::vector<Key> keys;
-  for (int i = 0; i < (int)reqs.size(); ++i) {
-    const Req& q = reqs[i];
-    const int per = (q.units + ranges - 1) / ranges;
-    for (int u0 = 0; u0 < q.units; u0 += per) {
-      const int u1 = std::min(q.units, u0 + per);
-      const double last = q.units > 1 ? q.first + (double)(q.last - q.first) * (u1 - 1) / (q.units - 1) : q.last;
-      keys.push_back(Key{last / q.ns, i, u0, u1});
-    }
-  }
-  std::stable_sort(keys.begin(), keys.end(), [](const Key& x, const Key& y) { return x.len > y.len; });
-  std::vector<int64_t> part(reqs.size(), -1);
-  for (const Key& k : keys) {
-    const Req& q = reqs[k.q];
-    if (q.ns > 1 && part[k.q] < 0) {  // the request's first rank stands for its merged rows
-      part[k.q] = g.parts;
+  auto longest = [](const Req& q) { return (double)std::max(q.first, q.last) / q.ns; };
+  std::stable_sort(reqs.begin(), reqs.end(), [&](const Req& x, const Req& y) { return longest(x) > longest(y); });
+  for (const Req& q : reqs) {
+    const int64_t part = g.parts;
+    if (q.ns > 1) {
       g.rows += (int64_t)q.n * a.Hq;
       g.parts += (int64_t)q.n * a.Hq * q.ns;
     }
-    g.ranks.push_back(Group::Rank{q.req, q.n, q.ns, k.u0, g.items, g.rows, std::max<int64_t>(part[k.q], 0)});
-    g.items += (int64_t)(k.u1 - k.u0) * a.Hkv * q.ns;
+    g.ranks.push_back(Group::Rank{q.req, q.n, q.ns, g.items, g.rows, part});
+    g.items += (int64_t)q.units * a.Hkv * q.ns;
   }
   if (g.items > INT32_MAX || g.parts > INT32_MAX / 2) return STA_ERR_UNSUPPORTED;
   return STA_OK;
@@ -1103,7 +1083,6 @@ sta_status launch_group(const Maps& m, const ChunkArgs& a, const Group& g, cudaS
     p.rows[i] = (int32_t)k.row1;
     p.part[i] = (int32_t)k.part;
     p.qn[i] = k.qn;
-    p.u0[i] = k.u0;
     p.req[i] = (uint16_t)k.req;
     p.ns[i] = (uint16_t)k.ns;
   }
