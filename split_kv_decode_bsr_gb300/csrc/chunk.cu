@@ -23,10 +23,18 @@
 // multiple of 8 (whole swizzle atoms). For other P of 8 or more, runs of 32 and of 8 tokens that a
 // page holds whole go by TMA, and the groups of 8 that a page's end cuts by 16-byte copies
 // (cp.async) to the same swizzled places; pages of fewer than 8 tokens by such copies alone. (Copies
-// alone keep the load queue full, which the other warps' barriers share: 530 us against 357 for 64
-// single tokens over pages of 100, 543 against 334 for an 8192-token prompt.) Rows of V behind the
+// alone keep the load queue full, which the other warps' barriers share: 530 us against 349 for 64
+// single tokens over pages of 100, 543 against 325 for an 8192-token prompt; 413 for the prompt with
+// runs of 8 alone.) Rows of V behind the
 // sequence are set to zero, since what a page holds there may be NaN; rows of K there only reach
 // masked scores.
+//
+// What bounds it (32 query and 8 KV heads of 128). An 8192-token prompt: 316 us, 1.74 PFLOP/s where
+// cuBLAS reaches 1.90; the tensor cores, with the softmax just below them. 64 single tokens over 549,646
+// cached ones: 343 us, 6.2 TB/s where a copy reaches 6.77; HBM. Chunks with a window of 256 keys: 59 us
+// for 700 items of some 4 tiles; each item's fixed part (the wait for its Q, the first product and
+// softmax, its result) is a third of that. Heads of 64: a prompt takes 276 us for half the products,
+// bound by the instructions of the softmax, which are as many as for heads of 128.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -916,7 +924,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// One warp per (new token, query head) of the requests that were cut.
+// One warp per (new token, query head) of the requests that were cut. It reads ns fp32 partials of d + 1
+// a row, which stay in L2 (one 30,000-token sequence, 32 rows in 19 pieces: 44 us with the attention, of
+// which 18 are the cache at copy speed).
 template <int D, int CAP>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant__ ChunkArgs A,
                                                           const __grid_constant__ Plan<CAP> P, int req0, int n_rows) {
@@ -979,6 +989,8 @@ struct Group {
   std::vector<Rank> ranks;
 };
 
+// Ranks of a launch: the plan travels in the launch's parameters, 1.2 KB of them for up to 64 requests,
+// 18 KB for more (copied at each launch: 58 us of host time a call of 64 requests, 88 with the large one).
 constexpr int kSmallPlan = 64, kLargePlan = 1024;
 
 sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, int r0, int r1, int num_splits, int sms,
