@@ -350,6 +350,7 @@ __global__ void __launch_bounds__(kScanThreads) pages_plan_compact_kernel(const 
                                                                           int32_t* dst, int32_t* n_moves,
                                                                           int32_t* status) {
   __shared__ int s_warp[32];
+  __shared__ uint32_t s_live[kScanThreads];  // a thread's 16 pages, for the coalesced writes of the map
   int used = 0;
   for (int64_t p0 = 16 * threadIdx.x; p0 < L.n_pages; p0 += 16 * kScanThreads) used += __popc(page_bits(L, (int)p0, true));
   int all;
@@ -370,7 +371,13 @@ __global__ void __launch_bounds__(kScanThreads) pages_plan_compact_kernel(const 
     for (; mover; mover &= mover - 1) *m++ = p + __ffs(mover) - 1;
     holes += total & 0xffff;
     movers += total >> 16;
-    for (int e = 0; e < 16 && p + e < L.n_pages; ++e) page_map[p + e] = (live >> e) & 1 ? p + e : -1;
+    s_live[threadIdx.x] = live;
+    __syncthreads();  // (the next round's scan separates these reads from its writes)
+    const int here = (int)min((int64_t)16 * kScanThreads, L.n_pages - r0);
+    for (int i = threadIdx.x; i < here; i += kScanThreads) {
+      const int page = (int)r0 + i;
+      page_map[page] = (s_live[i >> 4] >> (i & 15)) & 1 ? page : -1;
+    }
   }
   __syncthreads();
   for (int k = threadIdx.x; k < movers; k += kScanThreads) {
