@@ -282,20 +282,25 @@ __global__ void __launch_bounds__(kScanThreads) pages_fork_kernel(const Lists L,
     }
     return part;
   };
-  int want = 0;
+  // then what the first look found is still there for the second (4 forks: 15.5 us, 17.5 looking twice)
+  const bool once = n <= kScanThreads;
+  int want = 0, w = 0, k = 0;
   for (int i0 = 0; i0 < n; i0 += kScanThreads) {
     int total;
-    block_scan(own_page(i0 + threadIdx.x), total, s_warp);
+    w = own_page(i0 + threadIdx.x);
+    k = block_scan(w, total, s_warp);
     want += total;
   }
   const int got = take_free(L, want, taken, s_warp);
   int base = 0;
   for (int i0 = 0; i0 < n; i0 += kScanThreads) {
     const int i = i0 + threadIdx.x;
-    int total;
-    const int w = own_page(i);
-    const int k = base + block_scan(w, total, s_warp);
-    base += total;
+    if (!once) {
+      int total;
+      w = own_page(i);
+      k = base + block_scan(w, total, s_warp);
+      base += total;
+    }
     if (i >= n) continue;
     src[i] = dst[i] = -1;
     if (!w) continue;

@@ -614,6 +614,23 @@ def test_pages_compact(dev, P, lens, elems, room, n_pages):
         _same(pool, ref, idx, host, bufs)
 
 
+def test_pages_more_forks_than_one_round(dev):
+    """1,300 forks of three parents, whose partly filled last pages are copied until no page is left."""
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    lens = [7, 4, 10] + [0] * 1300
+    pool = Pool(80, lens, 4, 3, 6 + 1000)
+    ref, ptr, idx, kv = _pool_dev(pool, dev)
+    host, bufs = _buffers(pool, dev, 1, 8)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+    parent, child = [k % 7 % 3 for k in range(1300)], list(np.random.default_rng(4).permutation(1300) + 3)
+    status = sta.sta_pages_fork(bufs, ref, ptr, idx, kv, i32(parent), i32(child), 4)
+    assert status.tolist() == pool.fork(host, parent, [int(c) for c in child])
+    _same(pool, ref, idx, host, bufs)
+
+
 @pytest.mark.parametrize("P", [1, 16])
 def test_pages_of_long_sequences(dev, P):
     """Lists of thousands of pages, shared by many warps: freed, grown, forked, compacted."""
