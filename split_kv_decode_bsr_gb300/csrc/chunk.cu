@@ -435,9 +435,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kKWarp || warp == kVWarp) {
     // ------------------------------------------------------------ K or V: ring stages 2i and 2i + 1
     const bool is_v = warp == kVWarp;
-    // (One lane waits and arms, under a name of its own, and __all_sync gathers the result: with lane == 0 spelt
-    // out and the result broadcast by a shuffle, 64 single tokens took 349 us against 339.)
-    const bool lead = lane == 0;
     const int P0 = A.page_size;
     int pb = 0, pe = 0;
     auto page_no = [&](int tok) -> int {  // tok / P0
@@ -482,12 +479,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int in = min(boxes, (it.len - tok0 + A.box - 1) >> box_shift);  // boxes with tokens
           const bool tail_v = is_v && tok0 + kBN > it.len;                 // rows behind the sequence
           if (i > 0 && i == ask && lane == 0) mbar_arrive(&sh.want);
-          if (lead) ok = mbar_wait(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
+          // every lane waits: with one that waits and broadcasts the result 64 single tokens took 349 us against 338
+          ok = mbar_wait(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           uint8_t* dst = smem + C::OFF_KV + s * C::TILE;
           uint64_t* bar = tail_v ? &sh.tail : &sh.full[s];
-          if (lead) mbar_arrive_expect_tx(bar, (uint32_t)(in * A.box * 128 * C::KH));
+          if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(in * A.box * 128 * C::KH));
           __syncwarp();
           if (b < in)
             tma_load_3d(dst + kh * (kBN * 128) + off * 128, is_v ? &tm_v : &tm_k, kh * 64, it.hk, row_at(page, tok0 + off), bar);
