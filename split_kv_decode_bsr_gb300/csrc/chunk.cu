@@ -20,20 +20,19 @@
 // online one with a lazy maximum: O is rescaled only when a row's maximum grows by more than 2^8.
 //
 // Pages. A page of P tokens is copied by TMA in boxes of gcd(P, 128) tokens when that is a
-// multiple of 8 (whole swizzle atoms). For other P of 8 or more, runs of 32 and of 8 tokens that a
+// multiple of 8 (whole swizzle atoms). For other P of 40 or more, runs of 32 and of 8 tokens that a
 // page holds whole go by TMA, and the groups of 8 that a page's end cuts by 16-byte copies
-// (cp.async) to the same swizzled places; pages of fewer than 8 tokens by such copies alone. (Copies
-// alone keep the load queue full, which the other warps' barriers share: 530 us against 349 for 64
-// single tokens over pages of 100, 543 against 325 for an 8192-token prompt; 413 for the prompt with
-// runs of 8 alone.) Rows of V behind the
-// sequence are set to zero, since what a page holds there may be NaN; rows of K there only reach
-// masked scores.
+// (cp.async) to the same swizzled places; smaller pages by such copies alone. (64 single tokens over
+// pages of 33: 353 us by copies, 368 by runs; of 60: 351 and 327; of 100: 384 and 329. An 8192-token
+// prompt over pages of 33: 433 and 437, of 60: 443 and 341, of 100: 433 and 323, by runs of 8 alone
+// 413.) Rows of V behind the sequence are set to zero, since what a page holds there may be NaN; rows
+// of K there only reach masked scores.
 //
 // What bounds it (32 query and 8 KV heads of 128). An 8192-token prompt: 312 us, 1.76 PFLOP/s where
 // cuBLAS reaches 1.90; the tensor cores, with the softmax just below them. 64 single tokens over 549,646
 // cached ones: 338 us, 6.3 TB/s where a copy reaches 6.77; HBM. Chunks with a window of 256 keys: 59 us
 // for 700 items of some 4 tiles; each item's fixed part (the wait for its Q, the first product and
-// softmax, its result) is a third of that. Heads of 64: a prompt takes 276 us for half the products,
+// softmax, its result) is a third of that. Heads of 64: a prompt takes 270 to 306 us for half the products,
 // bound by the instructions of the softmax, which are as many as for heads of 128.
 #include <cudaTypedefs.h>
 
@@ -52,6 +51,7 @@ constexpr int kBM = 128;  // rows of a query tile
 constexpr int kBN = 128;  // keys of a tile
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kVWarp = 9, kKWarp = 10, kQWarp = 11;
+constexpr int kRunPage = 40;  // tokens of a page, no multiple of 8, from which its runs are copied by TMA
 constexpr int kAhead = 4;  // K tiles of an item that are still to load when the next item is taken
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&sh.full[s], A.box > 0 ? 1 : (A.page_size >= 8 ? 33 : 32));  // TMA bytes, the copying lanes
+      mbar_init(&sh.full[s], A.box > 0 ? 1 : (A.page_size >= kRunPage ? 33 : 32));  // TMA bytes, the copying lanes
       mbar_init(&sh.empty[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -479,7 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int in = min(boxes, (it.len - tok0 + A.box - 1) >> box_shift);  // boxes with tokens
           const bool tail_v = is_v && tok0 + kBN > it.len;                 // rows behind the sequence
           if (i > 0 && i == ask && lane == 0) mbar_arrive(&sh.want);
-          // every lane waits: with one that waits and broadcasts the result 64 single tokens took 349 us against 338
+          // every lane waits, for one that waits alone leaves the warp diverged (349 us against 338 for 64 single
+          // tokens; over pages of one token, below, 625 against 439)
           ok = mbar_wait(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -499,10 +500,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&sh.full[s]);
           }
         }
-      } else if (P0 >= 8) {
+      } else if (P0 >= kRunPage) {
         // Groups of 8 tokens: lane b (of 16) looks up the cache row of group b's first token, lane 16 + b
         // that of its last. Rows that follow one another go by TMA, a lane per column block; groups that
-        // a page's end cuts (once at most, at 8 tokens a page) or the sequence's end go row by row in
+        // a page's end cuts (once at most) or the sequence's end go row by row in
         // 16-byte copies of all lanes.
         constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an instruction
         const int ch = lane % LPR, hi = lane / LPR, b = lane & 15, far = lane >> 4;
@@ -517,14 +518,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = live ? row_at(page, token(tok0)) : -1;
           const int first = __shfl_sync(0xffffffffu, row, b), last = __shfl_sync(0xffffffffu, row, b + 16);
           const bool whole = tok0 + 8 * b + 7 < it.len && last == first + 7;
-          // four groups in one run of rows (a page of 32 tokens or more ends once among them) in one box
+          // four groups in one run of rows (a page ends once among them at most) in one box
           const int first4 = __shfl_sync(0xffffffffu, row, b & 12), last4 = __shfl_sync(0xffffffffu, row, (b | 3) + 16);
-          const bool whole4 = P0 >= 32 && tok0 + 8 * (b | 3) + 7 < it.len && last4 == first4 + 31;
+          const bool whole4 = tok0 + 8 * (b | 3) + 7 < it.len && last4 == first4 + 31;
           const uint32_t boxes = __ballot_sync(0xffffffffu, whole) & 0xffffu;
           const uint32_t rest = __ballot_sync(0xffffffffu, !whole && (is_v || live)) & 0xffffu;
           if (i > 0 && i == ask && lane == 0) mbar_arrive(&sh.want);
-          if (lane == 0) ok = mbar_wait(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+          ok = mbar_wait(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           uint8_t* tile = smem + C::OFF_KV + s * C::TILE;
           if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(__popc(boxes) * 1024 * C::KH));
@@ -547,8 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         // Small pages: 16-byte copies alone. Lane l looks up the rows of tokens l, l + 32, .. of the tile,
-        // which the copies take from it by shuffles. No more than three quarters of a tile wait to land:
-        // a full load queue would hold up the other warps' barriers as well.
+        // which the copies take from it by shuffles.
         constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an instruction
         const int ch = lane % LPR;
         const __nv_bfloat16* src = (is_v ? A.v : A.k) + (int64_t)it.hk * D + ch * 8;
@@ -570,13 +570,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             pg[g] = next < it.len ? page_at(next) : -1;
           }
           if (i > 0 && i == ask && lane == 0) mbar_arrive(&sh.want);
-          if (lane == 0) ok = mbar_wait(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+          ok = mbar_wait(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint32_t dst = smem_u32(smem + C::OFF_KV + s * C::TILE) + (ch >> 3) * (kBN * 128);
 #pragma unroll
           for (int g = 0; g < kBN / 32; ++g) {
-            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 2;" ::: "memory");
             int at[32 / RPI];
 #pragma unroll
             for (int r = 0; r < 32 / RPI; ++r) at[r] = __shfl_sync(0xffffffffu, row[g], r * RPI + lane / LPR);

@@ -243,6 +243,13 @@ def test_chunk_long(dev, P, d):
     _chunk_case(dev, PagedCase(P, [300, 77, 129], [300, 1000, 1111], 4, 2, d, P))
 
 
+@pytest.mark.parametrize("P", [3, 9, 31, 33, 39, 41, 60, 127, 129, 300])
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunk_pages_off_the_swizzle(dev, P, d):
+    """Pages that no box of whole 8-row groups tiles, on both sides of the size where their runs go by TMA."""
+    _chunk_case(dev, PagedCase(P + d, [1, 70, 0, 40], [1 + 3 * P, 70 + 2 * P, 5, 40], 6, 2, d, P, spare_entries=1))
+
+
 @pytest.mark.parametrize("pattern", [dict(causal=True, win_lo=0), dict(causal=True, win_lo=-63), dict(causal=True, win_lo=-200, n_global_cols=5),
                                      dict(causal=True, win_lo=-30, n_global_cols=300), dict(causal=False),
                                      dict(causal=False, win_lo=-40, win_hi=40), dict(causal=False, win_lo=3, win_hi=9),
