@@ -745,16 +745,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = true;
     uint32_t ns = 0, no = 0, nx = 0;  // tiles, results and merges of this slot so far
-    for (int k = 0; ok; ++k) {
-      if (!mbar_wait(&sh.item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
+    const int tt = m / A.G;
+    // this row's part of item k, if there is one
+    struct Part {
+      int cnt, dual, t, some;
+      bool live;
+      Seen sn;
+    };
+    auto look = [&](int k, Part& p) {
+      const Item& it = sh.item[k & 1];
+      p.some = mbar_wait(&sh.item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d) && !it.end;
+      if (!p.some) return;
+      p.cnt = it.count(x);
+      p.dual = it.dual;
+      p.t = it.t0 + (p.dual ? x * A.TQ : 0) + tt;
+      p.live = tt < A.TQ && p.t < it.n;
+      p.sn = seen(A, it.pos0 + p.t, it.pos0 + p.t, it.len);
+    };
+    Part part;
+    look(0, part);
+    for (int k = 0; ok && part.some; ++k) {
       const Item& it = sh.item[k & 1];  // given back at the end: few registers are left beside S
-      if (it.end) break;
-      const int cnt = it.count(x), dual = it.dual;
-      const int tt = m / A.G, t = it.t0 + (dual ? x * A.TQ : 0) + tt;
-      const bool live = tt < A.TQ && t < it.n;
-      const bool warp_live = __any_sync(0xffffffffu, live);
-      const int pos = it.pos0 + t;
-      const Seen sn = seen(A, pos, pos, it.len);
+      const int cnt = part.cnt, dual = part.dual, t = part.t;
+      const bool live = part.live, warp_live = __any_sync(0xffffffffu, live);
+      const Seen sn = part.sn;
       float m_ref = -INFINITY, l = 0.f;
       for (int n = 0; ok && n < cnt; ++n) {
         const int k0 = it.tile(it.j0 + (dual ? n : 2 * n + x)) * kBN;
@@ -826,6 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sh.p_full[x]);
         }
       }
+      look(k + 1, part);  // under the last PV (eight 1024-token prompts: 74.9 us, 76.9 when looked up afterwards)
       // ---- result
       if (ok && cnt > 0) ok = mbar_wait(&sh.o_full[x], no++ & 1u, A.err, 0x62a);
       tc_fence_after();
