@@ -687,6 +687,9 @@ def _host_i32(x, n: int, what: str):
     return at, C.c_int32.from_address(at + 4 * (n - 1)).value, x
 
 
+_ROPE_SCALINGS = {"none": STA_ROPE_SCALE_NONE, "linear": STA_ROPE_SCALE_LINEAR, "blend": STA_ROPE_SCALE_BLEND}
+
+
 class Rope:
     """Rotary positions of a model's heads (sta_rope_params).
 
@@ -700,14 +703,16 @@ class Rope:
     def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
                  factor: float = 1.0, orig_len: float = 0.0, low_turns: float = 1.0, high_turns: float = 32.0,
                  mscale: float = 1.0, freqs: Optional[Sequence[float]] = None):
-        kinds = {"none": STA_ROPE_SCALE_NONE, "linear": STA_ROPE_SCALE_LINEAR, "blend": STA_ROPE_SCALE_BLEND}
-        _need(scaling in kinds, f"scaling: one of {sorted(kinds)}")
+        kind = _ROPE_SCALINGS.get(scaling)
+        if kind is None:
+            raise ValueError(f"scaling: one of {sorted(_ROPE_SCALINGS)}")
         self._freqs = None
         if freqs is not None:
-            _need(len(freqs) == rot_dim // 2, "freqs: rot_dim / 2 values")
+            if len(freqs) != rot_dim // 2:
+                raise ValueError("freqs: rot_dim / 2 values")
             self._freqs = (C.c_double * len(freqs))(*[float(f) for f in freqs])
         self.rot_dim = int(rot_dim)
-        self.struct = _RopeParams(int(rot_dim), STA_ROPE_INTERLEAVED if interleaved else STA_ROPE_HALF, kinds[scaling],
+        self.struct = _RopeParams(int(rot_dim), STA_ROPE_INTERLEAVED if interleaved else STA_ROPE_HALF, kind,
                                   float(mscale), float(base), float(factor), float(orig_len), float(low_turns),
                                   float(high_turns), C.cast(self._freqs, C.c_void_p) if self._freqs else None)
 
@@ -717,6 +722,8 @@ def _heads_view(t: torch.Tensor, what: str):
     if t.dim() != 3:
         raise ValueError(f"{what}: [tokens, heads, d]")
     n, H, d = t.shape
+    if t.is_contiguous():
+        return H * d
     if not (n == 0 or ((d == 1 or t.stride(2) == 1) and (H == 1 or t.stride(1) == d))):
         raise ValueError(f"{what}: a token's heads must be contiguous")
     return t.stride(0) if n > 1 else H * d
@@ -739,11 +746,14 @@ def sta_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope, transpose: bo
     code = _dtype_code(x.dtype)
     st, ctx = _enter(dev, stream)
     try:
-        y = torch.empty((n, H, d), dtype=x.dtype, device=dev) if y is None else y
-        if not (y.shape == x.shape and y.dtype == x.dtype):
-            raise ValueError("y: x's shape and dtype")
+        if y is None:
+            y, ys = torch.empty((n, H, d), dtype=x.dtype, device=dev), H * d
+        else:
+            if not (y.shape == x.shape and y.dtype == x.dtype):
+                raise ValueError("y: x's shape and dtype")
+            ys = _heads_view(y, "y")
         _check("sta_rope", (_lib_handle or lib()).sta_rope(
-            _addr(x), _addr(y), _addr(positions), C.byref(rope.struct), n, H, d, xs, _heads_view(y, "y"), int(bool(transpose)),
+            _addr(x), _addr(y), _addr(positions), C.byref(rope.struct), n, H, d, xs, ys, int(bool(transpose)),
             code, st))
     finally:
         if ctx is not None:
@@ -790,11 +800,10 @@ def sta_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
             raise ValueError("positions: one a token")
     st, ctx = _enter(dev, stream)
     try:
-        if q is not None and q_out is None:
-            q_out = torch.empty((n, Hq, d), dtype=q.dtype, device=dev)
-        if q_out is not None:
-            if not (q is not None and q_out.shape == q.shape and q_out.is_contiguous()):
-                raise ValueError("q_out: contiguous, q's shape")
+        if q_out is None:
+            q_out = None if q is None else torch.empty((n, Hq, d), dtype=q.dtype, device=dev)
+        elif not (q is not None and q_out.shape == q.shape and q_out.is_contiguous()):
+            raise ValueError("q_out: contiguous, q's shape")
         _check("sta_rope_append_paged", (_lib_handle or lib()).sta_rope_append_paged(
             _addr(q), _addr(k), _addr(v), qs, ks, vs, _addr(q_out), _addr(k_pages), _addr(v_pages), page_size, n_pages,
             _addr(page_indptr_dev), _addr(page_indices_dev), _addr(q_indptr_dev), _addr(kv_indptr_dev), _addr(positions),
@@ -840,11 +849,13 @@ def sta_chunk_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
     h = _lib_handle or lib()
     st, ctx = _enter(dev, stream)
     try:
-        o = torch.empty((n, Hq, d), dtype=q.dtype, device=dev) if o is None else o
-        lse = torch.empty((n, Hq), dtype=torch.float32, device=dev) if lse is None else lse
-        if not (o.shape == q.shape and o.dtype == q.dtype and o.is_contiguous()):
+        if o is None:
+            o = torch.empty((n, Hq, d), dtype=q.dtype, device=dev)
+        elif not (o.shape == q.shape and o.dtype == q.dtype and o.is_contiguous()):
             raise ValueError("o: contiguous, q's shape and dtype")
-        if not (lse.shape == (n, Hq) and lse.dtype == torch.float32 and lse.is_contiguous()):
+        if lse is None:
+            lse = torch.empty((n, Hq), dtype=torch.float32, device=dev)
+        elif not (lse.shape == (n, Hq) and lse.dtype == torch.float32 and lse.is_contiguous()):
             raise ValueError("lse: contiguous float32 [n, Hq]")
         args = (q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), page_size, n_pages, page_indptr_dev.data_ptr(),
                 page_indices_dev.data_ptr() or None, q_indptr_dev.data_ptr(), qh, kv_indptr_dev.data_ptr(), kh, n_req, Hq, Hkv, d,
