@@ -30,7 +30,7 @@
 //
 // What bounds it (32 query and 8 KV heads of 128). An 8192-token prompt: 312 us, 1.76 PFLOP/s where
 // cuBLAS reaches 1.90; the tensor cores, with the softmax just below them. 64 single tokens over 549,646
-// cached ones: 338 us, 6.3 TB/s where a copy reaches 6.77; HBM. Chunks with a window of 256 keys: 59 us
+// cached ones: 333 us, 6.4 TB/s where a copy reaches 6.77; HBM. Chunks with a window of 256 keys: 59 us
 // for 700 items of some 4 tiles; each item's fixed part (the wait for its Q, the first product and
 // softmax, its result) is a third of that. Heads of 64: a prompt takes 270 to 306 us for half the products,
 // bound by the instructions of the softmax, which are as many as for heads of 128.
@@ -392,7 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The CTA starts with its own item and takes over those of CTAs that have not started yet, in
     // the grid's order (heaviest first): the next one when the last K tiles of this one are being
     // loaded. (Taken as early as there is room for them, items lie waiting in CTAs that are busy with
-    // long ones while others run out of work: 370 us against 349 for 64 single tokens.)
+    // long ones while others run out of work: 366 us against 333 for 64 single tokens, 52 against 40 for a
+    // 2048-token prompt.)
     if (lane == 0) {
       bool ok = true;
       int item = blockIdx.x, k = 0, nq = 0;
@@ -1037,8 +1038,8 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
   // item number (k - 1) * SMs + 1 (some SM has k items of at least that length). Cutting shortens items
   // and adds to the share: a prologue each, fp32 partials written and read, and a merge. Lengths of
   // pieces from the longest list down are tried and the best estimate is kept. (64 single tokens over
-  // 549,646 cached ones: 459 us whole, 355 in pieces of an SM's third, 482 in 16 pieces each; a
-  // 2048-token prompt: 85 us in pieces of 8 tiles, 40 whole.)
+  // 549,646 cached ones: 345 us whole, 333 in the pieces found, 421 in 16 pieces each; a 2048-token
+  // prompt: 79 us in pieces of 8 tiles, 40 whole.)
   if (num_splits == 0 && most > 2) {
     auto chunks = [&](int tiles, int piece) { return std::min(kMaxAuto, std::max(1, (tiles + piece - 1) / piece)); };
     auto estimate = [&](int piece) {
