@@ -28,7 +28,7 @@
 // 413.) Rows of V behind the sequence are set to zero, since what a page holds there may be NaN; rows
 // of K there only reach masked scores.
 //
-// What bounds it (32 query and 8 KV heads of 128). An 8192-token prompt: 312 us, 1.76 PFLOP/s where
+// What bounds it (32 query and 8 KV heads of 128). An 8192-token prompt: 309 us, 1.78 PFLOP/s where
 // cuBLAS reaches 1.90; the tensor cores, with the softmax just below them. 64 single tokens over 549,646
 // cached ones: 333 us, 6.4 TB/s where a copy reaches 6.77; HBM. Chunks with a window of 256 keys: 59 us
 // for 700 items of some 4 tiles; each item's fixed part (the wait for its Q, the first product and

@@ -92,15 +92,17 @@ __device__ __forceinline__ bool token_place(const RopeArgs& A, int64_t t, int& p
     if (__ldg(A.q_indptr + mid) <= t) lo = mid;
     else hi = mid - 1;
   }
+  // (all at once: each of these is a round trip to memory at first)
   const int64_t q1 = __ldg(A.q_indptr + lo + 1), len = (int64_t)__ldg(A.kv_indptr + lo + 1) - __ldg(A.kv_indptr + lo);
+  const int64_t list = __ldg(A.page_indptr + lo), list_end = __ldg(A.page_indptr + lo + 1);
   const int64_t p = len - (q1 - t);
   if (p < 0 || t >= q1) {  // the sequence is shorter than its chunk: this token is not in it
     pos = (int)(p < INT32_MIN ? INT32_MIN : p);
     return true;
   }
   pos = (int)p;
-  const int64_t e = (int64_t)__ldg(A.page_indptr + lo) + p / A.page_size;
-  if (e < 0 || e >= __ldg(A.page_indptr + lo + 1)) {
+  const int64_t e = list + p / A.page_size;
+  if (e < 0 || e >= list_end) {
     record_error(A.err, 0x604);
     return true;
   }
