@@ -615,8 +615,9 @@ sta_status sta_pages_free(int32_t* ref_dev, int n_pages, const int32_t* page_ind
 
 /* sta_pages_compact -- with U pages in use, moves those numbered U or more onto the free
  * pages below U (both ascending): page data in every buffer, ref, and the held list
- * entries of every request. page_map (int32 [n_pages], device, written): each used page's
- * new number, -1 for a free one, for lists kept elsewhere. status: {U, pages moved}. */
+ * entries of every request (negative ones, which hold no page, are passed over). page_map
+ * (int32 [n_pages], device, written): each used page's new number, -1 for a free one, for
+ * lists kept elsewhere. status: {U, pages moved}. */
 sta_status sta_pages_compact(void* const* bufs_host, int n_bufs, size_t page_bytes, int32_t* ref_dev, int n_pages,
                              const int32_t* page_indptr_dev, int32_t* page_indices_dev, const int32_t* kv_indptr_dev,
                              int n_req, int page_size, int32_t* page_map_dev, int32_t* status_dev, void* workspace,

@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kThreads) pages_copy_kernel(const __grid_const
       const int held = min(pages_of(tokens_of(L.kv_indptr, r), L.page_size), __ldg(L.indptr + r + 1) - b);
       for (int k = (int)(w % runs) * 32 + lane; k < held; k += 32 * runs) {
         const int page = L.indices[b + k];
-        if (page < 0 || page >= n_pages) record_error(err, 0x601);
+        if (page < 0) continue;  // no page: there was none left when the request grew
+        if (page >= n_pages) record_error(err, 0x601);
         else L.indices[b + k] = __ldg(page_map + page);
       }
     }
