@@ -571,8 +571,8 @@ sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const void* k_pa
  * device) may be NULL. Codes in the device error word: 0x601 a page number outside
  * [0, n_pages), 0x602 a request number outside [0, n_req) (or a parent that is its own
  * child), 0x603 a free page freed, 0x604 a list too short, 0x605 a child that holds pages
- * or is named twice; the entry, fork or request concerned is then left as it was (a shared
- * entry without a valid page is -1 in the child). All are
+ * or is named twice; the entry, fork or request concerned is then left as it was (a forked
+ * entry without a valid page is -1 in the child, and no page is taken for it). All are
  * asynchronous on `stream` and synchronise nothing; workspace (256-byte aligned) follows
  * the usual protocol: NULL sets *workspace_bytes and returns. n_pages <= 2^30. */
 

@@ -274,14 +274,21 @@ __global__ void __launch_bounds__(kScanThreads) pages_fork_kernel(const Lists L,
     if (c >= 0 && c < L.n_req) atomicMin(owner + c, i);
   }
   __syncthreads();
-  // the page that fork i needs for a last, partly filled one
+  // the page that fork i needs for a last, partly filled one (old: the parent's; without it there is
+  // nothing to copy, so the child's entry holds no page either and none is taken)
+  int old = -1;
   auto own_page = [&](int i) -> int {
     if (i >= n || !fork_of(L, parent, child, i, p, c, whole, part)) return 0;
     if (*(volatile int32_t*)(owner + c) != i) {
       record_error(L.err, 0x605);
       return 0;
     }
-    return part;
+    if (!part) return 0;
+    old = L.indices[__ldg(L.indptr + p) + whole];
+    if (old >= 0 && old < L.n_pages) return 1;
+    record_error(L.err, 0x601);
+    L.indices[__ldg(L.indptr + c) + whole] = -1;
+    return 0;
   };
   // then what the first look found is still there for the second (4 forks: 15.5 us, 17.5 looking twice)
   const bool once = n <= kScanThreads;
@@ -306,14 +313,9 @@ __global__ void __launch_bounds__(kScanThreads) pages_fork_kernel(const Lists L,
     src[i] = dst[i] = -1;
     if (!w) continue;
     const int page = k < got ? taken[k] : -1;
-    const int old = L.indices[__ldg(L.indptr + p) + whole];
     L.indices[__ldg(L.indptr + c) + whole] = page;
     if (page < 0) continue;
     L.ref[page] = 1;
-    if (old < 0 || old >= L.n_pages) {
-      record_error(L.err, 0x601);
-      continue;
-    }
     src[i] = old;
     dst[i] = page;
   }

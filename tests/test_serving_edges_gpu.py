@@ -86,3 +86,66 @@ def test_pages_compact_reports_entries_past_the_pool(dev):
     got = idx.tolist()
     assert got[2] == 12 and got[12] == -9  # left as they were
     assert sta.sta_device_error(reset=True) == 0x601
+
+
+def _fork(pool, bufs, parent, child):
+    """Pool.fork for parents with entries that hold no page: the child's is -1, and no page is taken for it."""
+    free = iter([p for p in range(pool.n_pages) if pool.ref[p] == 0])
+    got = missing = 0
+    for a, c in zip(parent, child):
+        for e in range(pool.need(pool.kv[a])):
+            old = pool.idx[pool.ptr[a] + e]
+            at = pool.ptr[c] + e
+            if not 0 <= old < pool.n_pages:
+                pool.idx[at] = -1
+            elif (e + 1) * pool.P <= pool.kv[a]:
+                pool.idx[at] = old
+                pool.ref[old] += 1
+            else:
+                p = pool.idx[at] = next(free, -1)
+                if p < 0:
+                    missing += 1
+                    continue
+                pool.ref[p], got = 1, got + 1
+                for b in bufs:
+                    b[p] = b[old]
+    return [got, missing]
+
+
+@pytest.mark.parametrize("n_forks", [2, 1300])  # forks that are looked at once, and twice
+@pytest.mark.parametrize("entry", [0, 2])       # a whole page; the last, partly filled one
+@pytest.mark.parametrize("bad", [-1, -(1 << 31), 0, (1 << 31) - 1])
+def test_pages_fork_of_a_parent_without_a_page(dev, bad, entry, n_forks):
+    import split_kv_decode_bsr_gb300 as sta
+
+    pool = Pool(92, [20, 30] + [0] * n_forks, 8, 5, 7 + n_forks)
+    pool.idx[entry] = bad + pool.n_pages if bad == 0 else bad  # (0: the first number past the pool)
+    pool.idx[10:] = [5] * (len(pool.idx) - 10)  # what a child's list held before
+    ref, ptr, idx, kv = _state(pool, dev)
+    host, bufs = _buffers(pool, dev, 2, 16)
+    parent, child = [i % 2 for i in range(n_forks)], [2 + i for i in range(n_forks)]
+    status = sta.sta_pages_fork(bufs, ref, ptr, idx, kv, _i32(dev, parent), _i32(dev, child), 8)
+    want = _fork(pool, host, parent, child)
+    assert want == [n_forks // 2 if entry == 2 else n_forks, 0]
+    assert status.tolist() == want
+    _same(pool, ref, idx, host, bufs)
+    assert sta.sta_device_error(reset=True) == 0x601
+
+
+def test_pages_fork_after_pages_ran_out(dev):
+    """A parent that grew into a shortage is forked under its grown length: its child lacks the same pages."""
+    import split_kv_decode_bsr_gb300 as sta
+
+    pool = Pool(93, [20, 9, 0, 0], 8, 8, 7)
+    ref, ptr, idx, kv = _state(pool, dev)
+    host, bufs = _buffers(pool, dev, 1, 16)
+    new = [20, 60, 0, 0]
+    assert sta.sta_pages_grow(ref, ptr, idx, kv, _indptr(dev, new), 8).tolist() == pool.grow(new) == [2, 4]
+    pool.kv = new
+    sta.sta_pages_free(ref, ptr, idx, _indptr(dev, new), _i32(dev, [0]), 8)
+    pool.free([0])
+    pool.kv[0] = 0
+    status = sta.sta_pages_fork(bufs, ref, ptr, idx, _indptr(dev, pool.kv), _i32(dev, [1]), _i32(dev, [2]), 8)
+    assert status.tolist() == _fork(pool, host, [1], [2]) == [0, 0]
+    _same(pool, ref, idx, host, bufs)
+    assert sta.sta_device_error(reset=True) == 0x601
