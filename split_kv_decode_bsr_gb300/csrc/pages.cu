@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kScanThreads) pages_fork_kernel(const Lists L,
 }
 
 // `runs` warps per listed request: its held entries become -1, their pages lose a holder. The entry
-// is taken by an exchange, so a request listed twice is freed once.
+// is taken by an exchange, so a request listed twice is freed once; one that is reported is put back.
 __global__ void __launch_bounds__(kThreads) pages_free_kernel(const Lists L, const int32_t* reqs, int n,
                                                               int runs) {
   const int64_t w = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
@@ -342,11 +342,13 @@ __global__ void __launch_bounds__(kThreads) pages_free_kernel(const Lists L, con
     const int page = atomicExch(L.indices + b + k, -1);
     if (page < 0) continue;
     if (page >= L.n_pages) {
+      atomicExch(L.indices + b + k, page);
       record_error(L.err, 0x601);
       continue;
     }
     if (atomicSub(L.ref + page, 1) <= 0) {  // the page was free already: its count stays 0
       atomicAdd(L.ref + page, 1);
+      atomicExch(L.indices + b + k, page);
       record_error(L.err, 0x603);
     }
   }

@@ -149,3 +149,24 @@ def test_pages_fork_after_pages_ran_out(dev):
     assert status.tolist() == _fork(pool, host, [1], [2]) == [0, 0]
     _same(pool, ref, idx, host, bufs)
     assert sta.sta_device_error(reset=True) == 0x601
+
+
+def test_pages_free_leaves_entries_that_it_reports(dev):
+    """An entry past the pool, and one whose page is free already, are reported and stay as they were."""
+    import split_kv_decode_bsr_gb300 as sta
+
+    for what, code in (("past", 0x601), ("free", 0x603)):
+        pool = Pool(94, [30, 20, 40], 8, 6, 20)
+        page = pool.idx[1]
+        if what == "past":
+            pool.idx[1] = 20
+        else:
+            pool.ref[page] = 0
+        ref, ptr, idx, kv = _state(pool, dev)
+        sta.sta_pages_free(ref, ptr, idx, kv, _i32(dev, [0, 2, 0]), 8)  # (one named twice)
+        stays = pool.idx[1]
+        pool.idx[1] = -1
+        pool.free([0, 2])
+        pool.idx[1] = stays
+        _same(pool, ref, idx)
+        assert sta.sta_device_error(reset=True) == code
