@@ -862,6 +862,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           w1 = exp2f(ml.x - M);
           l = l * w0 + ml.y * w1;
           m_ref = M;
+        } else {
+          l += ml.y;  // 0, or NaN where the query is one: maxima pass over NaN
         }
       }
       if (warp_live && (dual || x == 0)) {

@@ -1,9 +1,10 @@
-"""Serving over a paged KV cache in the states that follow a shortage or bad input."""
+"""Serving over a paged KV cache in the states that follow a shortage or bad input: lists with entries
+that hold no page, and queries that are no numbers."""
 
 import numpy as np
 import pytest
 
-from _serving import Pool
+from _serving import PagedCase, Pool, check_chunk
 
 pytestmark = pytest.mark.gpu
 
@@ -170,3 +171,26 @@ def test_pages_free_leaves_entries_that_it_reports(dev):
         pool.idx[1] = stays
         _same(pool, ref, idx)
         assert sta.sta_device_error(reset=True) == code
+
+
+# ---- queries that are no numbers
+
+
+@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,kv,Hq,Hkv,win,sinks", [(128, 328, 2, 2, 64, 0), (32, 300, 8, 2, 32, 0), (128, 584, 1, 1, 64, 256)])
+def test_chunk_nan_query_under_a_window(dev, new, kv, Hq, Hkv, win, sinks, d, splits):
+    """A NaN query of a token whose window begins in a later key tile than that of its query tile's first
+    token: the LSE is NaN, not that of a token without a key, and the other rows do not change."""
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = PagedCase(95, [new, 1], [kv, 40], Hq, Hkv, d, 16)
+    x = c.dev(dev)
+    kw = dict(pattern=sta.MaskSource.pattern(causal=True, win_lo=1 - win, n_global_cols=sinks), num_splits=splits)
+    clean, clean_lse = sta.sta_chunk_fwd_paged(**x, **kw)
+    check_chunk(clean, clean_lse, c.ref(d ** -0.5, causal=True, win_lo=1 - win, n_global=sinks), new + 1)
+    x["q"][new - 1, 0, 3] = float("nan")
+    o, lse = sta.sta_chunk_fwd_paged(**x, **kw)
+    assert o[new - 1, 0].isnan().all() and lse[new - 1, 0].isnan()
+    o[new - 1, 0], lse[new - 1, 0] = clean[new - 1, 0], clean_lse[new - 1, 0]
+    assert o.equal(clean) and lse.equal(clean_lse)
