@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int T = 0, n_tail = 0;  // tiles of earlier items; tail tiles so far
     for (int k = 0; ok; ++k) {
-      if (!mbar_wait(&sh.item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
+      if (!mbar_wait_warp(&sh.item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
       const Item it = read_item(&sh.item[k & 1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.item_empty[k & 1]);
@@ -483,8 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i > 0 && i == ask && lane == 0) mbar_arrive(&sh.want);
           // every lane waits, for one that waits alone leaves the warp diverged (349 us against 338 for 64 single
           // tokens; over pages of one token, below, 625 against 439)
-          ok = mbar_wait(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = mbar_wait_warp(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
           if (!ok) break;
           uint8_t* dst = smem + C::OFF_KV + s * C::TILE;
           uint64_t* bar = tail_v ? &sh.tail : &sh.full[s];
@@ -526,8 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t boxes = __ballot_sync(0xffffffffu, whole) & 0xffffu;
           const uint32_t rest = __ballot_sync(0xffffffffu, !whole && (is_v || live)) & 0xffffu;
           if (i > 0 && i == ask && lane == 0) mbar_arrive(&sh.want);
-          ok = mbar_wait(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = mbar_wait_warp(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
           if (!ok) break;
           uint8_t* tile = smem + C::OFF_KV + s * C::TILE;
           if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(__popc(boxes) * 1024 * C::KH));
@@ -572,8 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             pg[g] = next < it.len ? page_at(next) : -1;
           }
           if (i > 0 && i == ask && lane == 0) mbar_arrive(&sh.want);
-          ok = mbar_wait(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = mbar_wait_warp(&sh.empty[s], ((y / ST) & 1u) ^ 1u, A.err, 0x621);
           if (!ok) break;
           const uint32_t dst = smem_u32(smem + C::OFF_KV + s * C::TILE) + (ch >> 3) * (kBN * 128);
 #pragma unroll
@@ -612,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int np0 = 0, np1 = 0, nf0 = 0, nf1 = 0;  // tiles, and items with tiles, of each slot so far
     const bool by_lanes = A.box == 0;
     for (int k = 0; ok; ++k) {
-      if (!mbar_wait(&sh.item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
+      if (!mbar_wait_warp(&sh.item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d)) break;
       const Item it = read_item(&sh.item[k & 1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.item_empty[k & 1]);
@@ -756,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto look = [&](int k, Part& p) {
       const Item& it = sh.item[k & 1];
-      p.some = mbar_wait(&sh.item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d) && !it.end;
+      p.some = mbar_wait_warp(&sh.item_full[k & 1], (k >> 1) & 1u, A.err, 0x62d) && !it.end;
       if (!p.some) return;
       p.cnt = it.count(x);
       p.dual = it.dual;
@@ -774,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_ref = -INFINITY, l = 0.f;
       for (int n = 0; ok && n < cnt; ++n) {
         const int k0 = it.tile(it.j0 + (dual ? n : 2 * n + x)) * kBN;
-        if (!(ok = mbar_wait(&sh.s_full[x], ns++ & 1u, A.err, 0x629))) break;
+        if (!(ok = mbar_wait_warp(&sh.s_full[x], ns++ & 1u, A.err, 0x629))) break;
         tc_fence_after();
         if (warp_live) {
           float s[128];
@@ -844,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       look(k + 1, part);  // under the last PV (eight 1024-token prompts: 74.9 us, 76.9 when looked up afterwards)
       // ---- result
-      if (ok && cnt > 0) ok = mbar_wait(&sh.o_full[x], no++ & 1u, A.err, 0x62a);
+      if (ok && cnt > 0) ok = mbar_wait_warp(&sh.o_full[x], no++ & 1u, A.err, 0x62a);
       tc_fence_after();
       float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and, for a single tile, of slot 1's
       const bool other = !dual && x == 0 && it.count(1) > 0;
@@ -853,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive(&sh.x_full);
       }
       if (other) {
-        if (ok) ok = mbar_wait(&sh.x_full, nx++ & 1u, A.err, 0x62f);
+        if (ok) ok = mbar_wait_warp(&sh.x_full, nx++ & 1u, A.err, 0x62f);
         tc_fence_after();
         const float2 ml = sh.row[m];
         const float M = fmaxf(m_ref, ml.x);
