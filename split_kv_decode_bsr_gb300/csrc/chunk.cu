@@ -492,7 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (b < in)
             tma_load_3d(dst + kh * (kBN * 128) + off * 128, is_v ? &tm_v : &tm_k, kh * 64, it.hk, row_at(page, tok0 + off), bar);
           if (tail_v) {  // (the last tile of a list at most)
-            mbar_wait(&sh.tail, n_tail++ & 1u, A.err, 0x622);
+            if (!(ok = mbar_wait_warp(&sh.tail, n_tail & 1u, A.err, 0x622))) {
+              mbar_wait_warp(&sh.tail, n_tail & 1u, A.err, 0x622);  // shared memory is not released under a copy
+              break;
+            }
+            ++n_tail;
             for (int z = (it.len - tok0) * 8 + lane; z < kBN * 8; z += 32)
 #pragma unroll
               for (int k = 0; k < C::KH; ++k) *reinterpret_cast<uint4*>(dst + k * (kBN * 128) + z * 16) = make_uint4(0, 0, 0, 0);

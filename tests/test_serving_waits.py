@@ -29,3 +29,12 @@ def test_whole_warps_vote_where_they_wait():
     conditions = re.findall(r"if \((.*)\) (?:return true;|\{)", body)  # every way on or out is a vote
     assert len(conditions) == body.count("return") == 3
     assert all(re.match(r"__(all|any)_sync\(0xffffffffu, ", c) for c in conditions)
+
+
+def test_a_wait_that_gives_up_is_heeded():
+    """Nothing is written over a copy in flight, nor a stage passed on, after a wait that ran out. The outcome is
+    dropped only where a role ends and its last copies or products are waited for, at most once more."""
+    text = _source("chunk.cu")
+    dropped = re.findall(r"(?:[;{}]|\bif \([^;{}]*\))\s*mbar_wait(?:_warp)?\(&sh\.(\w+)[^;]*;\s*([^;]*);", text)
+    assert {name for name, _ in dropped} <= {"q_full", "full", "drain", "tail"}
+    assert [after for name, after in dropped if name == "tail"] == ["break"]
