@@ -456,8 +456,10 @@ sta_status sta_merge_lse(const float* part_o, const float* part_lse, int n_rows,
  * q_indptr[r+1]-1, and they are the LAST tokens of its sequence, whose length
  * kv_indptr[r+1] - kv_indptr[r] counts them: row q_indptr[r] + i has position
  * length - (number of new tokens) + i. Rows at or past q_indptr[n_req] (a padded
- * batch) are neither read nor written. (The pages have no counterpart for these
- * calls: they are what a serving step needs around the paged decode.) */
+ * batch) are not written, and nothing depends on what they hold (they may be
+ * loaded: they are memory of the tensor that is passed). (The pages have no
+ * counterpart for these calls: they are what a serving step needs around the paged
+ * decode.) */
 
 /* Which elements of a head form pair p of the rot_dim / 2 pairs that turn. */
 #define STA_ROPE_HALF 0        /* p and p + rot_dim / 2 */
