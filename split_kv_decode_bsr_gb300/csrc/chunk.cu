@@ -28,12 +28,16 @@
 // 413.) Rows of V behind the sequence are set to zero, since what a page holds there may be NaN; rows
 // of K there only reach masked scores.
 //
-// What bounds it (32 query and 8 KV heads of 128). An 8192-token prompt: 309 us, 1.78 PFLOP/s where
-// cuBLAS reaches 1.90; the tensor cores, with the softmax just below them. 64 single tokens over 549,646
-// cached ones: 333 us, 6.4 TB/s where a copy reaches 6.77; HBM. Chunks with a window of 256 keys: 59 us
-// for 700 items of some 4 tiles; each item's fixed part (the wait for its Q, the first product and
-// softmax, its result) is a third of that. Heads of 64: a prompt takes 270 to 306 us for half the products,
-// bound by the instructions of the softmax, which are as many as for heads of 128.
+// What bounds it (32 query and 8 KV heads of 128; here and below, unless it says otherwise, times of a
+// CUDA graph replayed from a cold L2, some 4 to 5 us of events and graph launch included). An 8192-token
+// prompt: 310 to 315 us, 1.75 to 1.77 PFLOP/s where cuBLAS reaches 1.90 in a burst (back to back, at the
+// lower clocks of a card at its power limit, 336 to 345 us, 1.6 PFLOP/s; cuBLAS 1.68); the tensor cores,
+// with the softmax just below them. 64 single tokens over 522,892 cached ones: 333 to 339 us, 6.3 to 6.4
+// TB/s where a copy reaches 6.77 (back to back 325 us, 6.6 TB/s); HBM. Chunks with a window of 256 keys:
+// 58.5 us for 700 items of some 4 tiles; each item's fixed part (the wait for its Q, the first product and
+// softmax, its result) is a third of that. Heads of 64: a prompt takes 272 to 318 us for half the products,
+// bound by the instructions of the softmax, which are as many as for heads of 128, and the latency between
+// them.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -829,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               f32x2_unpack(f32x2_fma(f32x2_pack(s[64 * half + 2 * e], s[64 * half + 2 * e + 1]), c2, nm2), a0, a1);
               const float p0 = ex2(a0), p1 = ex2(a1);
               l2[e & 3] = f32x2_add(l2[e & 3], f32x2_pack(p0, p1));
-              pk[e] = pack_bf16x2(p0, p1);  // rounded for the MMA; the sum takes the fp32 values
+              pk[e] = pack_bf16x2(p0, p1);  // bf16 for the MMA, off by 2^-8 at most; the sum takes the fp32 values
             }
             tmem_st32_sync(tS + 32 * half, pk);
             arrive(half ? &sh.p_full[x] : &sh.p_half[x]);
@@ -1042,7 +1046,7 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
   // item number (k - 1) * SMs + 1 (some SM has k items of at least that length). Cutting shortens items
   // and adds to the share: a prologue each, fp32 partials written and read, and a merge. Lengths of
   // pieces from the longest list down are tried and the best estimate is kept. (64 single tokens over
-  // 549,646 cached ones: 345 us whole, 333 in the pieces found, 421 in 16 pieces each; a 2048-token
+  // 522,892 cached ones: 345 us whole, 333 in the pieces found, 421 in 16 pieces each; a 2048-token
   // prompt: 79 us in pieces of 8 tiles, 40 whole.)
   if (num_splits == 0 && most > 2) {
     auto chunks = [&](int tiles, int piece) { return std::min(kMaxAuto, std::max(1, (tiles + piece - 1) / piece)); };

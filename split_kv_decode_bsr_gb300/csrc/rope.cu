@@ -12,8 +12,12 @@
 // vector (half layout: the two vectors half a rotation apart) that one thread turns. All
 // loads of a thread's first two units are issued before the table is computed. Every element
 // is read and written once, so HBM bounds it: 16384 tokens x 40 heads x 128 bf16 (336 MB moved)
-// take 53 us of which 49.6 are the copy at the measured 6.77 TB/s; 64 new tokens of 48 heads are
-// bound by the chain of lookups (request, lengths, page list, page) and the launch, about 6 us.
+// take 55.3 us back to back, 90 % of the copy rate (all of it: 49.6 us at the measured 6.77 TB/s). A few new
+// tokens are bound by latency: one thread a token finds its place by dependent loads while the CTA waits
+// for it (whether it is padding, a binary search for the request, which is six steps for 64, then lengths and
+// list together, then the page), before the table, the turn and the stores. 64 tokens of 48 heads with their
+// cache write take 11.4 us. (That and the times below are of a CUDA graph replayed from a cold L2, some 4 to 5
+// us of events and graph launch included; so taken, the 16384 tokens are 58.5 us.)
 #include <cmath>
 
 #include "common.cuh"
@@ -120,7 +124,7 @@ __device__ __forceinline__ bool token_place(const RopeArgs& A, int64_t t, int& p
 template <typename T, int W, bool IL, bool APPEND>
 __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const RopeArgs A, const __grid_constant__ RopeTable tab) {
   constexpr int WI = IL && W == 1 ? 2 : W;  // elements of a vector: whole pairs when interleaved
-  // units of a thread in flight: 2, and 6 CTAs an SM (16384 x 40 x 128 in bf16: 58 us; 4 with 3 CTAs 67)
+  // units of a thread in flight: 2, and 6 CTAs an SM (16384 x 40 x 128 in bf16: 58.5 us; 4 with 3 CTAs 67)
   constexpr int U = 2;
   constexpr int PP = IL ? WI / 2 : WI;      // pairs of a unit
   // cosine and sine, two pairs in 16 bytes: [tokens][PP / 2][units][2], so that neighbouring threads
@@ -282,7 +286,7 @@ template <typename T, bool APPEND>
 sta_status launch_rope(RopeArgs& a, const RopeTable& tab, bool interleaved, cudaStream_t st) {
   constexpr int W = 16 / (int)sizeof(T);
   // 16-byte vectors when every vector lies whole on one side of each border and starts on a
-  // 16-byte boundary; else element by element (16384 x 40 x 128 bf16: 58 us, 201 element by element)
+  // 16-byte boundary; else element by element (16384 x 40 x 128 bf16: 58.5 us, 201 element by element)
   bool wide = a.d % W == 0 && (interleaved ? a.rot % W == 0 : (a.rot / 2) % W == 0);
   for (int g = 0; g < 3; ++g)
     if (a.heads[g])
