@@ -82,24 +82,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
   }
 }
 
-// The same wait by all lanes of a converged warp, which vote on each try and on the time: one outcome
-// for all of them. (Each by its own tries and its own reading of the timer, some could go on and others
-// leave when the phase completes as the time runs out, and the votes, shuffles and .aligned instructions
-// that follow would wait for lanes that never come. A vote on the outcome of mbar_wait would do too, but
-// a try that has to leave its loop first costs more: an 8192-token prompt of the chunk attention 310 us,
-// 308 as here, 306 with lanes on their own; back to back 333 both ways.)
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, int* err, int err_code) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  const unsigned long long t0 = globaltimer_ns();
-  for (;;) {
-    if (__all_sync(0xffffffffu, mbar_try_wait_suspend(bar, parity, kSuspendHintNs))) return true;
-    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) {
-      record_error(err, err_code);
-      return false;
-    }
-  }
-}
-
 // ------------------------------------------------------- bulk / TMA copies
 // 1-D bulk copy global -> shared, completion counted on `bar` (bytes % 16 == 0,
 // both addresses 16-byte aligned).

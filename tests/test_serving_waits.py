@@ -25,7 +25,7 @@ def test_whole_warps_vote_where_they_wait():
     by_warps = {"item_full", "empty", "s_full", "o_full", "x_full"}
     assert by_warps <= _barriers(text, "mbar_wait_warp")
     assert not by_warps & _barriers(text, "mbar_wait")
-    body = re.search(r"bool mbar_wait_warp\(.*?\{(.*?)\n\}", _source("ptx.cuh"), re.S).group(1)
+    body = re.search(r"bool mbar_wait_warp\(.*?\{(.*?)\n\}", text, re.S).group(1)
     conditions = re.findall(r"if \((.*)\) (?:return true;|\{)", body)  # every way on or out is a vote
     assert len(conditions) == body.count("return") == 3
     assert all(re.match(r"__(all|any)_sync\(0xffffffffu, ", c) for c in conditions)
