@@ -30,7 +30,7 @@
 //
 // What bounds it (32 query and 8 KV heads of 128; here and below, unless it says otherwise, times of a
 // CUDA graph replayed from a cold L2, some 4 to 5 us of events and graph launch included). An 8192-token
-// prompt: 310 to 315 us, 1.75 to 1.77 PFLOP/s where cuBLAS reaches 1.90 in a burst (back to back, at the
+// prompt: 306 to 316 us, 1.74 to 1.79 PFLOP/s where cuBLAS reaches 1.90 in a burst (back to back, at the
 // lower clocks of a card at its power limit, 333 to 354 us, 1.55 to 1.65 PFLOP/s; cuBLAS 1.68); the tensor cores,
 // with the softmax just below them. 64 single tokens over 522,892 cached ones: 333 to 339 us, 6.3 to 6.4
 // TB/s where a copy reaches 6.77 (back to back 319 to 326 us, 6.6 to 6.7 TB/s); HBM. Chunks with a window of 256 keys:
