@@ -500,6 +500,51 @@ sta_status sta_rope(const void* x, void* y, const int32_t* positions_dev, const 
                     int64_t n_tokens, int H, int d, int64_t x_stride, int64_t y_stride, int transpose,
                     sta_dtype dtype, sta_stream stream);
 
+/* sta_norm_rope -- root-mean-square norm of each query and key head, and the rotary
+ * positions in the same pass:
+ *   y = R_t (x r w),  r = 1 / sqrt(mean(x^2) + eps),
+ * the mean over the d elements of the head, R_t the turn of sta_rope at the token's
+ * position (the leading rot_dim elements; the rest is normed alone). Arithmetic in fp32
+ * (squares are summed there: finite up to |x| of 8e17), one rounding to dtype.
+ *
+ *   q, k       [n_tokens, Hq | Hk, d] dtype (device), q_stride / k_stride >= H d elements
+ *              between tokens, heads d apart. Hk == 0 with k == k_out == NULL: one tensor
+ *              alone (Hq == 0 likewise); its strides and weight are then ignored
+ *   q_out, k_out  likewise with strides of their own (written; may be q and k with equal
+ *              strides; other overlap is not allowed). What lies between tokens is not touched
+ *   q_weight, k_weight  [d] f32 (device), shared by a tensor's heads, or NULL (1)
+ *   eps        > 0 and finite
+ *   positions  int32 [n_tokens] (device), any values; rope NULL: nothing turns, positions
+ *              may be NULL
+ *   d          2 .. 512; Hq, Hk 0 .. 65536; dtype STA_BF16 or STA_F32
+ * Any d, rot_dim and stride is taken; 16-byte vectors are used as in sta_rope. n_tokens
+ * == 0 launches nothing. One launch, asynchronous on `stream`. */
+sta_status sta_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, void* q_out, void* k_out,
+                         int64_t q_out_stride, int64_t k_out_stride, const float* q_weight, const float* k_weight,
+                         float eps, const int32_t* positions_dev, const sta_rope_params* rope, int64_t n_tokens, int Hq,
+                         int Hk, int d, sta_dtype dtype, sta_stream stream);
+
+/* sta_norm_rope_bwd -- the gradients of sta_norm_rope: with g = R_t' dy (the turn back),
+ *   dx = r (g w - x r^2 mean(g w x)),  dw = sum over tokens and heads of g x r.
+ *
+ *   dq_out, dk_out  gradients of the results, [n_tokens, H, d] dtype (device), strides of
+ *              their own; q, k, weights, eps, positions, rope: as given to sta_norm_rope
+ *   dq, dk     gradients of q and k (written; may be dq_out and dk_out, or q and k, with
+ *              equal strides)
+ *   dq_weight, dk_weight  [d] f32 (device, written: not added to) or NULL. Sums in fp32, in
+ *              the same order in every call of the same sizes and pointers' alignment
+ *   workspace  device scratch, 256-byte aligned; NULL sets *workspace_bytes (it depends on
+ *              d alone) and returns, and so does one that is too small, with
+ *              STA_ERR_WORKSPACE. Calls that may run at once need one each
+ * n_tokens == 0 sets dq_weight and dk_weight to 0. Two launches at most, asynchronous on
+ * `stream`. */
+sta_status sta_norm_rope_bwd(const void* dq_out, const void* dk_out, int64_t dq_out_stride, int64_t dk_out_stride,
+                             const void* q, const void* k, int64_t q_stride, int64_t k_stride, void* dq, void* dk,
+                             int64_t dq_stride, int64_t dk_stride, const float* q_weight, const float* k_weight,
+                             float* dq_weight, float* dk_weight, float eps, const int32_t* positions_dev,
+                             const sta_rope_params* rope, int64_t n_tokens, int Hq, int Hk, int d, sta_dtype dtype,
+                             void* workspace, size_t* workspace_bytes, sta_stream stream);
+
 /* sta_rope_append_paged -- turns the queries and keys of a step's new tokens and
  * writes the keys and values to their places in the paged cache.
  *
@@ -524,6 +569,19 @@ sta_status sta_rope_append_paged(const void* q, const void* k, const void* v, in
                                  const int32_t* q_indptr_dev, const int32_t* kv_indptr_dev,
                                  const int32_t* positions_dev, const sta_rope_params* rope, int64_t n_tokens, int n_req,
                                  int Hq, int Hkv, int d, sta_dtype dtype, sta_stream stream);
+
+/* sta_norm_rope_append_paged -- sta_rope_append_paged for a model that norms its query
+ * and key heads: q and k are normed (q_weight, k_weight [d] f32 or NULL, eps, as in
+ * sta_norm_rope), turned, and k and v written to their places in the paged cache. rope
+ * NULL: normed alone. Every other argument, and what happens to padding, to tokens
+ * without a place and on bad pages, is as there. One launch, asynchronous on `stream`. */
+sta_status sta_norm_rope_append_paged(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                                      int64_t v_stride, void* q_out, void* k_pages, void* v_pages, int page_size,
+                                      int n_pages, const int32_t* page_indptr_dev, const int32_t* page_indices_dev,
+                                      const int32_t* q_indptr_dev, const int32_t* kv_indptr_dev,
+                                      const int32_t* positions_dev, const float* q_weight, const float* k_weight,
+                                      float eps, const sta_rope_params* rope, int64_t n_tokens, int n_req, int Hq,
+                                      int Hkv, int d, sta_dtype dtype, sta_stream stream);
 
 /* sta_chunk_fwd_paged -- attention of each request's new tokens (one, a few, or a
  * whole prompt) over its sequence in the paged cache, whose last tokens they are:

@@ -49,7 +49,8 @@ EXPORTED = ("sta_encode_mask", "sta_tile_lists_bytes", "sta_mha_fwd", "sta_mha_f
             "sta_bias_residual_layernorm", "sta_validate_mask", "sta_mla_decode", "sta_mha_select_kernel", "sta_decode_splitkv",
             "sta_decode_splitkv_noalloc", "sta_decode_splitkv_paged", "sta_merge_lse", "sta_status_string", "sta_device_error",
             "sta_check_bounded_wait", "sta_last_cuda_error", "sta_last_cuda_error_string", "sta_rope",
-            "sta_rope_append_paged", "sta_chunk_fwd_paged", "sta_pages_copy", "sta_pages_grow", "sta_pages_fork",
+            "sta_norm_rope", "sta_norm_rope_bwd", "sta_rope_append_paged", "sta_norm_rope_append_paged",
+            "sta_chunk_fwd_paged", "sta_pages_copy", "sta_pages_grow", "sta_pages_fork",
             "sta_pages_free", "sta_pages_compact")
 
 BIG = 1 << 40
@@ -116,6 +117,11 @@ def lib():
             h.sta_merge_lse.argtypes = [P, P, i32, i32, i32, P, i32, P, P]
             i64, R = C.c_int64, C.POINTER(_RopeParams)
             h.sta_rope.argtypes = [P, P, P, R, i64, i32, i32, i64, i64, i32, i32, P]
+            h.sta_norm_rope.argtypes = [P, P, i64, i64, P, P, i64, i64, P, P, f32, P, R, i64, i32, i32, i32, i32, P]
+            h.sta_norm_rope_bwd.argtypes = [P, P, i64, i64, P, P, i64, i64, P, P, i64, i64, P, P, P, P, f32, P, R, i64,
+                                            i32, i32, i32, i32, P, sz, P]
+            h.sta_norm_rope_append_paged.argtypes = [P, P, P, i64, i64, i64, P, P, P, i32, i32, P, P, P, P, P, P, P, f32,
+                                                     R, i64, i32, i32, i32, i32, i32, P]
             h.sta_rope_append_paged.argtypes = [P, P, P, i64, i64, i64, P, P, P, i32, i32, P, P, P, P, P, R, i64, i32,
                                                 i32, i32, i32, i32, P]
             h.sta_chunk_fwd_paged.argtypes = [P, i64, P, P, i32, i32, P, P, P, P, P, P, i32, i32, i32, i32, i32, f32,
@@ -761,6 +767,127 @@ def sta_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope, transpose: bo
     return y
 
 
+def _heads(x: Optional[torch.Tensor], what: str, dev: torch.device, n: int, d: int, dtype: torch.dtype):
+    """An optional [n, H, d] tensor of heads: its address, H and token stride."""
+    if x is None:
+        return None, 0, 0
+    stride = _heads_view(x, what)
+    if not (x.shape[0] == n and x.shape[2] == d and x.dtype is dtype and x.device == dev):
+        raise ValueError(f"{what}: [{n}, heads, {d}] {dtype} on {dev}")
+    return x.data_ptr(), x.shape[1], stride
+
+
+def _norm_weight(w: Optional[torch.Tensor], what: str, dev: torch.device, d: int):
+    if w is None:
+        return None
+    if not (w.dtype is torch.float32 and w.shape == (d,) and w.is_contiguous() and w.device == dev):
+        raise ValueError(f"{what}: contiguous float32 [{d}] on {dev}")
+    return w.data_ptr()
+
+
+def _norm_of(q, k, positions, rope):
+    """What the calls with a norm share: device, tokens, head size, dtype, and the positions' address."""
+    x = q if q is not None else k
+    if x is None or x.dim() != 3:
+        raise ValueError("q or k: [tokens, heads, d]")
+    n, _, d = x.shape
+    dev = x.device
+    _on(dev)
+    if rope is not None:
+        if positions is None:
+            raise ValueError("positions: one a token")
+        _i32(dev, positions=positions)
+        if positions.shape != (n,):
+            raise ValueError("positions: one a token")
+    return dev, n, d, x.dtype, _dtype_code(x.dtype), None if rope is None else positions.data_ptr()
+
+
+def _result(given: Optional[torch.Tensor], x: Optional[torch.Tensor], what: str):
+    """Where a result shaped like x goes: `given`, or a new contiguous tensor. Its token stride too."""
+    if x is None:
+        if given is not None:
+            raise ValueError(f"{what}: nothing to write there")
+        return None, None, 0
+    if given is None:
+        given = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return given, given.data_ptr(), x.shape[1] * x.shape[2]
+    if not (given.shape == x.shape and given.dtype is x.dtype and given.device == x.device):
+        raise ValueError(f"{what}: the shape, dtype and device of what it is for")
+    return given, given.data_ptr(), _heads_view(given, what)
+
+
+def sta_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                  rope: Optional[Rope], q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                  eps: float = 1e-6, q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Root-mean-square norm of each head of q [n, Hq, d] and k [n, Hk, d], and the rotary positions in one pass.
+
+    bf16 or float32, any token strides; positions int32 [n]; weights float32 [d] or None (1). k (or q)
+    None: the other alone. rope None: normed alone. q_out / k_out may be q / k (in place). Returns
+    (q_out, k_out), new [n, H, d] tensors where none are given.
+    """
+    dev, n, d, dtype, code, pos = _norm_of(q, k, positions, rope)
+    qa, Hq, qs = _heads(q, "q", dev, n, d, dtype)
+    ka, Hk, ks = _heads(k, "k", dev, n, d, dtype)
+    qw, kw = _norm_weight(q_weight, "q_weight", dev, d), _norm_weight(k_weight, "k_weight", dev, d)
+    st, ctx = _enter(dev, stream)
+    try:
+        q_out, qo, qos = _result(q_out, q, "q_out")
+        k_out, ko, kos = _result(k_out, k, "k_out")
+        _check("sta_norm_rope", (_lib_handle or lib()).sta_norm_rope(
+            qa, ka, qs, ks, qo, ko, qos, kos, qw, kw, eps, pos, C.byref(rope.struct) if rope is not None else None, n, Hq,
+            Hk, d, code, st))
+    finally:
+        if ctx is not None:
+            ctx.leave()
+    return q_out, k_out
+
+
+def sta_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tensor], q: Optional[torch.Tensor],
+                      k: Optional[torch.Tensor], positions: Optional[torch.Tensor], rope: Optional[Rope],
+                      q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of sta_norm_rope from those of its results: (dq, dk, dq_weight, dk_weight).
+
+    dq_out, dk_out [n, H, d] as q, k (any token strides); dq / dk may be dq_out / dk_out, or q / k, or
+    views of one packed gradient. The weights' gradients are new float32 [d] tensors, also where a weight is None
+    (that of a factor of 1); None where q or k is.
+    """
+    dev, n, d, dtype, code, pos = _norm_of(q, k, positions, rope)
+    qa, Hq, qs = _heads(q, "q", dev, n, d, dtype)
+    ka, Hk, ks = _heads(k, "k", dev, n, d, dtype)
+    ya, Hy, ys = _heads(dq_out, "dq_out", dev, n, d, dtype)
+    za, Hz, zs = _heads(dk_out, "dk_out", dev, n, d, dtype)
+    if not (Hy == Hq and Hz == Hk):
+        raise ValueError("dq_out, dk_out: the shapes of q and k")
+    qw, kw = _norm_weight(q_weight, "q_weight", dev, d), _norm_weight(k_weight, "k_weight", dev, d)
+    st, ctx = _enter(dev, stream)
+    try:
+        dq, dqa, dqs = _result(dq, q, "dq")
+        dk, dka, dks = _result(dk, k, "dk")
+        dqw = torch.empty(d, dtype=torch.float32, device=dev) if q is not None else None
+        dkw = torch.empty(d, dtype=torch.float32, device=dev) if k is not None else None
+        ws = _workspace(_norm_bwd_ws(d), workspace, dev)
+        _check("sta_norm_rope_bwd", (_lib_handle or lib()).sta_norm_rope_bwd(
+            ya, za, ys, zs, qa, ka, qs, ks, dqa, dka, dqs, dks, qw, kw, _addr(dqw), _addr(dkw), eps, pos,
+            C.byref(rope.struct) if rope is not None else None, n, Hq, Hk, d, code, ws.data_ptr(),
+            C.byref(C.c_size_t(ws.numel())), st))
+    finally:
+        if ctx is not None:
+            ctx.leave()
+    return dq, dk, dqw, dkw
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_bwd_ws(d: int) -> int:
+    """Workspace size of sta_norm_rope_bwd (it depends on d alone)."""
+    n = C.c_size_t(0)
+    _check("sta_norm_rope_bwd", lib().sta_norm_rope_bwd(
+        None, None, d, 0, None, None, d, 0, None, None, d, 0, None, None, None, None, 1.0, None, None, 0, 1, 0, d, STA_BF16,
+        None, C.byref(n), None))
+    return int(n.value)
+
+
 def sta_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
                           v_pages: torch.Tensor, page_indptr_dev: torch.Tensor, page_indices_dev: torch.Tensor,
                           q_indptr_dev: torch.Tensor, kv_indptr_dev: torch.Tensor, rope: Optional[Rope] = None,
@@ -772,6 +899,27 @@ def sta_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
     kv_indptr[r+1] - kv_indptr[r] tokens (both int32, device). rope None: nothing turns. q None: keys
     and values only. Returns the turned q [n, Hq, d] (rows of a padded batch's padding unwritten).
     """
+    return _append_paged(None, q, k, v, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev, kv_indptr_dev, rope,
+                         positions, q_out, stream)
+
+
+def sta_norm_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
+                               v_pages: torch.Tensor, page_indptr_dev: torch.Tensor, page_indices_dev: torch.Tensor,
+                               q_indptr_dev: torch.Tensor, kv_indptr_dev: torch.Tensor, rope: Optional[Rope] = None,
+                               q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                               eps: float = 1e-6, positions: Optional[torch.Tensor] = None,
+                               q_out: Optional[torch.Tensor] = None, stream=None):
+    """sta_rope_append_paged with each head of q and k normed first (as in sta_norm_rope: weights float32
+    [d] or None, eps). rope None: normed alone. Returns the normed and turned q."""
+    d, dev = k.shape[-1], k.device
+    norm = (_norm_weight(q_weight, "q_weight", dev, d), _norm_weight(k_weight, "k_weight", dev, d), eps)
+    return _append_paged(norm, q, k, v, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev, kv_indptr_dev, rope,
+                         positions, q_out, stream)
+
+
+def _append_paged(norm, q, k, v, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev, kv_indptr_dev, rope,
+                  positions, q_out, stream):
+    """sta_rope_append_paged, or with norm (the weights' addresses and eps) sta_norm_rope_append_paged."""
     dev = k.device
     _on(dev, q, v, k_pages, v_pages, q_out)
     n_pages, page_size, Hkv, d = k_pages.shape
@@ -804,10 +952,14 @@ def sta_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
             q_out = None if q is None else torch.empty((n, Hq, d), dtype=q.dtype, device=dev)
         elif not (q is not None and q_out.shape == q.shape and q_out.is_contiguous()):
             raise ValueError("q_out: contiguous, q's shape")
-        _check("sta_rope_append_paged", (_lib_handle or lib()).sta_rope_append_paged(
-            _addr(q), _addr(k), _addr(v), qs, ks, vs, _addr(q_out), _addr(k_pages), _addr(v_pages), page_size, n_pages,
-            _addr(page_indptr_dev), _addr(page_indices_dev), _addr(q_indptr_dev), _addr(kv_indptr_dev), _addr(positions),
-            C.byref(rope.struct) if rope is not None else None, n, n_req, Hq, Hkv, d, STA_BF16, st))
+        h = _lib_handle or lib()
+        args = (_addr(q), _addr(k), _addr(v), qs, ks, vs, _addr(q_out), _addr(k_pages), _addr(v_pages), page_size, n_pages,
+                _addr(page_indptr_dev), _addr(page_indices_dev), _addr(q_indptr_dev), _addr(kv_indptr_dev), _addr(positions))
+        end = (C.byref(rope.struct) if rope is not None else None, n, n_req, Hq, Hkv, d, STA_BF16, st)
+        if norm is None:
+            _check("sta_rope_append_paged", h.sta_rope_append_paged(*args, *end))
+        else:
+            _check("sta_norm_rope_append_paged", h.sta_norm_rope_append_paged(*args, *norm, *end))
     finally:
         if ctx is not None:
             ctx.leave()
