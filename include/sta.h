@@ -622,6 +622,33 @@ sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const void* k_pa
                                float scale, const sta_mask_src* pattern, int num_splits, void* o, float* lse,
                                void* workspace, size_t* workspace_bytes, sta_stream stream);
 
+/* sta_prefix_fwd_paged -- sta_chunk_fwd_paged (causal) for requests that share their
+ * first pages, as forks do: what a group shares is read and attended once for all of its
+ * new tokens, each request's own part by itself, and the two are merged by LSE.
+ *
+ *   group_indptr  int32 [n_groups+1] (host), non-decreasing from 0 to n_req: the requests
+ *              of group i are group_indptr[i] .. group_indptr[i+1]-1
+ *   prefix     int32 [n_groups] (host): tokens that the group's requests share, a multiple
+ *              of page_size, 0 for none. Their page lists start with the same prefix /
+ *              page_size pages, and every new token lies behind them (length - new tokens
+ *              >= prefix, for each request with new tokens)
+ * Every other argument and the results are those of sta_chunk_fwd_paged with pattern NULL,
+ * up to the rounding of the merge. Whether a group's prefix is taken apart is the library's
+ * choice (it is not where the new tokens fill the tensor cores anyway). A captured call may be
+ * replayed as there, with the same groups and prefixes: the prefix's pages are read from the
+ * list of the group's first request that has new tokens in the host copy, which must keep them
+ * there. A request whose new tokens no longer lie behind its prefix sets the device error word
+ * to 0x608, one whose list has another last shared page to 0x609; its results are then
+ * undefined.
+ * Asynchronous on `stream`. */
+sta_status sta_prefix_fwd_paged(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages, int page_size,
+                                int n_pages, const int32_t* page_indptr_dev, const int32_t* page_indices_dev,
+                                const int32_t* q_indptr_dev, const int32_t* q_indptr_host, const int32_t* kv_indptr_dev,
+                                const int32_t* kv_indptr_host, int n_req, const int32_t* group_indptr_host,
+                                const int32_t* prefix_host, int n_groups, int Hq, int Hkv, int d, sta_dtype dtype,
+                                float scale, int num_splits, void* o, float* lse, void* workspace,
+                                size_t* workspace_bytes, sta_stream stream);
+
 /* Page bookkeeping on the device. ref is int32 [n_pages] (device): how many lists hold
  * each page, 0 for a free one; page_indptr, page_indices and kv_indptr (the sequences'
  * lengths) as above, all on the device. Buffers (K and V of every layer, say) are a

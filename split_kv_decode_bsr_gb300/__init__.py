@@ -50,7 +50,7 @@ EXPORTED = ("sta_encode_mask", "sta_tile_lists_bytes", "sta_mha_fwd", "sta_mha_f
             "sta_decode_splitkv_noalloc", "sta_decode_splitkv_paged", "sta_merge_lse", "sta_status_string", "sta_device_error",
             "sta_check_bounded_wait", "sta_last_cuda_error", "sta_last_cuda_error_string", "sta_rope",
             "sta_norm_rope", "sta_norm_rope_bwd", "sta_rope_append_paged", "sta_norm_rope_append_paged",
-            "sta_chunk_fwd_paged", "sta_pages_copy", "sta_pages_grow", "sta_pages_fork",
+            "sta_chunk_fwd_paged", "sta_prefix_fwd_paged", "sta_pages_copy", "sta_pages_grow", "sta_pages_fork",
             "sta_pages_free", "sta_pages_compact")
 
 BIG = 1 << 40
@@ -126,6 +126,8 @@ def lib():
                                                 i32, i32, i32, i32, P]
             h.sta_chunk_fwd_paged.argtypes = [P, i64, P, P, i32, i32, P, P, P, P, P, P, i32, i32, i32, i32, i32, f32,
                                               C.POINTER(_MaskSrc), i32, P, P, P, sz, P]
+            h.sta_prefix_fwd_paged.argtypes = [P, i64, P, P, i32, i32, P, P, P, P, P, P, i32, P, P, i32, i32, i32, i32, i32,
+                                               f32, i32, P, P, P, sz, P]
             h.sta_pages_copy.argtypes = [P, i32, C.c_size_t, i32, P, P, i32, P]
             h.sta_pages_grow.argtypes = [P, i32, P, P, P, P, i32, i32, P, P, sz, P]
             h.sta_pages_fork.argtypes = [P, i32, C.c_size_t, P, i32, P, P, P, i32, i32, P, P, i32, P, P, sz, P]
@@ -979,6 +981,32 @@ def sta_chunk_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
     positions. Rows past q_indptr[n_req] are left as they are. Returns O [n, Hq, d] and LSE
     [n, Hq] float32 (-inf for a token that sees no key).
     """
+    return _chunk_fwd(None, q, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev, q_indptr_host, kv_indptr_dev,
+                      kv_indptr_host, scale, pattern, num_splits, o, lse, workspace, stream)
+
+
+def sta_prefix_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_indptr_dev: torch.Tensor,
+                         page_indices_dev: torch.Tensor, q_indptr_dev: torch.Tensor, q_indptr_host, kv_indptr_dev: torch.Tensor,
+                         kv_indptr_host, group_indptr_host, prefix_host, scale=None, num_splits: int = 0,
+                         o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """sta_chunk_fwd_paged (causal) for requests that share their first pages, which are read and attended once
+    for all of a group.
+
+    Requests group_indptr[i] .. group_indptr[i+1]-1 share their first prefix[i] tokens (int32, host; whole pages,
+    0: none): their page lists start with the same prefix[i] / page_size pages, as sta_pages_fork leaves them, and
+    all of their new tokens lie behind them. Results are those of sta_chunk_fwd_paged up to rounding.
+    """
+    gh, last, keep_g = _host_i32(group_indptr_host, len(group_indptr_host), "group_indptr_host")
+    n_groups = len(group_indptr_host) - 1
+    ph, _, keep_p = _host_i32(prefix_host, n_groups, "prefix_host")
+    return _chunk_fwd((gh, ph, n_groups), q, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev, q_indptr_host,
+                      kv_indptr_dev, kv_indptr_host, scale, None, num_splits, o, lse, workspace, stream)
+
+
+def _chunk_fwd(groups, q, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev, q_indptr_host, kv_indptr_dev,
+               kv_indptr_host, scale, pattern, num_splits, o, lse, workspace, stream):
+    """sta_chunk_fwd_paged, or with groups (addresses of their requests and prefixes, their number) sta_prefix_fwd_paged."""
     qs = _heads_view(q, "q")
     n, Hq, d = q.shape
     dev = q.device
@@ -1010,21 +1038,26 @@ def sta_chunk_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
         elif not (lse.shape == (n, Hq) and lse.dtype == torch.float32 and lse.is_contiguous()):
             raise ValueError("lse: contiguous float32 [n, Hq]")
         args = (q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), page_size, n_pages, page_indptr_dev.data_ptr(),
-                page_indices_dev.data_ptr() or None, q_indptr_dev.data_ptr(), qh, kv_indptr_dev.data_ptr(), kh, n_req, Hq, Hkv, d,
-                _dtype_code(q.dtype), scale, pat, num_splits, o.data_ptr(), lse.data_ptr())
+                page_indices_dev.data_ptr() or None, q_indptr_dev.data_ptr(), qh, kv_indptr_dev.data_ptr(), kh, n_req)
+        if groups is None:
+            name, call = "sta_chunk_fwd_paged", h.sta_chunk_fwd_paged
+            args += (Hq, Hkv, d, _dtype_code(q.dtype), scale, pat, num_splits, o.data_ptr(), lse.data_ptr())
+        else:
+            name, call = "sta_prefix_fwd_paged", h.sta_prefix_fwd_paged
+            args += (*groups, Hq, Hkv, d, _dtype_code(q.dtype), scale, num_splits, o.data_ptr(), lse.data_ptr())
         # Most calls cut nothing: they need the least size there is and use none of it. Few new tokens over many
         # cached ones are mostly cut, into no more than 32 pieces (64 single tokens: 48 us of host time a call,
         # 56 when it first asks). A call that needs more says how much.
         at, size = 256, C.c_size_t(256)
-        if workspace is not None or (rows <= 8 * n_req and keys >= 8192):
+        if workspace is not None or groups is not None or (rows <= 8 * n_req and keys >= 8192):
             guess = 256 if workspace is not None else max(256, min(32 * rows * Hq * (d + 2) * 4, 1 << 26))
             ws = _workspace(guess, workspace, dev)
             at, size.value = ws.data_ptr(), ws.numel()
-        status = h.sta_chunk_fwd_paged(*args, at, C.byref(size), st)
+        status = call(*args, at, C.byref(size), st)
         if status == STA_ERR_WORKSPACE:
             ws = _workspace(size.value, workspace, dev)
-            status = h.sta_chunk_fwd_paged(*args, ws.data_ptr(), C.byref(size), st)
-        _check("sta_chunk_fwd_paged", status)
+            status = call(*args, ws.data_ptr(), C.byref(size), st)
+        _check(name, status)
     finally:
         if ctx is not None:
             ctx.leave()
@@ -1040,6 +1073,20 @@ def chunk_workspace_bytes(q_indptr, kv_indptr, n_req: int, Hq: int, Hkv: int, d:
     _check("sta_chunk_fwd_paged", (_lib_handle or lib()).sta_chunk_fwd_paged(
         None, 0, None, None, page_size, 1, None, None, None, qh, None, kh, n_req, Hq, Hkv, d, STA_BF16, 1.0,
         None if pattern is None else _src_array([pattern]), num_splits, None, None, None, C.byref(n), None))
+    return int(n.value)
+
+
+def prefix_workspace_bytes(q_indptr, kv_indptr, n_req: int, group_indptr, prefix, Hq: int, Hkv: int, d: int,
+                           page_size: int = 16, num_splits: int = 0) -> int:
+    """Workspace size sta_prefix_fwd_paged needs for these requests (host only, never 0)."""
+    n = C.c_size_t(0)
+    qh, _, keep_q = _host_i32(q_indptr, n_req + 1, "q_indptr")
+    kh, _, keep_k = _host_i32(kv_indptr, n_req + 1, "kv_indptr")
+    gh, _, keep_g = _host_i32(group_indptr, len(group_indptr), "group_indptr")
+    ph, _, keep_p = _host_i32(prefix, len(group_indptr) - 1, "prefix")
+    _check("sta_prefix_fwd_paged", (_lib_handle or lib()).sta_prefix_fwd_paged(
+        None, 0, None, None, page_size, 1, None, None, None, qh, None, kh, n_req, gh, ph, len(group_indptr) - 1, Hq, Hkv, d,
+        STA_BF16, 1.0, num_splits, None, None, None, C.byref(n), None))
     return int(n.value)
 
 

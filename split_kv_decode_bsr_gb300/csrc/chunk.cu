@@ -83,8 +83,20 @@ struct ChunkArgs {
 
 // What the host planned: the requests with new tokens, longest key lists first. Rank k has the items
 // base[k] .. base[k+1]-1: ((pair of query tiles, from the last down) * Hkv + KV head) * ns + chunk.
+//
+// With shared prefixes a rank is a request of its own (skip 0), what a request has behind its group's prefix
+// of `skip` tokens (pre: the prefix's rank), or that prefix itself (pre -2), whose rows are those of all the group's
+// requests req .. end - 1 and whose pages are those of request `lead`.
+template <int CAP, bool SHARED>
+struct Groups {};
 template <int CAP>
-struct Plan {
+struct Groups<CAP, true> {
+  int32_t skip[CAP];
+  int16_t pre[CAP];  // -1: neither
+  uint16_t end[CAP], lead[CAP];
+};
+template <int CAP, bool SHARED>
+struct Plan : Groups<CAP, SHARED> {
   int n;                // ranks
   int32_t base[CAP + 1];
   int32_t rows[CAP];    // merged rows up to and with the rank's (those of requests that are cut)
@@ -147,8 +159,8 @@ __host__ __device__ inline int tile_list(const Seen& s, int& gt, int& wl) {
   return gt + (wh >= wl ? wh - wl + 1 : 0);
 }
 
-template <int CAP>
-__device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP>& P, int req0, int item, Item& it) {
+template <int CAP, bool SHARED>
+__device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP, SHARED>& P, int req0, int item, Item& it) {
   int lo = 0, hi = P.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -163,11 +175,29 @@ __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP>& P,
   it.hk = y / it.ns;
   it.c = y - it.hk * it.ns;
   it.r = req0 + P.req[lo];
-  const int q0 = __ldg(A.q_indptr + it.r), q1 = __ldg(A.q_indptr + it.r + 1);
-  const int64_t len = (int64_t)__ldg(A.kv_indptr + it.r + 1) - __ldg(A.kv_indptr + it.r);
-  it.pb = __ldg(A.page_indptr + it.r);  // (with the lengths, not later by the loaders: a 2048-token prompt 36 us, 39)
-  it.pe = __ldg(A.page_indptr + it.r + 1);
+  int kr = it.r, q_end = it.r + 1;  // whose keys, whose last row
+  if constexpr (SHARED) {
+    q_end = req0 + P.end[lo];
+    if (P.pre[lo] == -2) kr = req0 + P.lead[lo];
+  }
+  const int q0 = __ldg(A.q_indptr + it.r), q1 = __ldg(A.q_indptr + q_end);
+  int64_t len = (int64_t)__ldg(A.kv_indptr + kr + 1) - __ldg(A.kv_indptr + kr);
+  it.pb = __ldg(A.page_indptr + kr);  // (with the lengths, not later by the loaders: a 2048-token prompt 36 us, 39)
+  it.pe = __ldg(A.page_indptr + kr + 1);
   int n = q1 - q0;
+  int64_t pos0 = len - n;
+  if constexpr (SHARED) {
+    const int skip = P.skip[lo], pre = P.pre[lo];
+    if (pre >= 0 && n > 0 && pos0 < skip) record_error(A.err, 0x608);  // new tokens that are not behind the prefix
+    if (pre == -2) {  // every row is behind all of its keys
+      len = skip;
+      pos0 = skip;
+    } else if (pre >= 0) {  // keys and positions counted from the prefix's end
+      pos0 -= skip;
+      len = len > skip ? len - skip : 0;
+      it.pb += skip / A.page_size;
+    }
+  }
   if (n > P.qn[lo]) {
     record_error(A.err, 0x606);
     n = P.qn[lo];
@@ -182,7 +212,7 @@ __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP>& P,
   if (it.t0 >= n) return false;
   it.dual = it.t0 + A.TQ < n;
   it.len = (int)len;
-  it.pos0 = (int)(len - (q1 - q0));
+  it.pos0 = (int)pos0;
   const int te = min(n, it.t0 + (it.dual ? 2 : 1) * A.TQ);
   const Seen s = seen(A, it.pos0 + it.t0, it.pos0 + te - 1, len);
   const int nt = tile_list(s, it.gt, it.wl);
@@ -196,6 +226,9 @@ __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP>& P,
     const int lt = last >= 0 ? last / kBN : -1;  // last tile of slot 0
     const int na = lt < 0 ? 0 : (lt < it.gt ? lt + 1 : it.gt + max(0, lt - it.wl + 1));
     it.j1a = max(it.j0, min(it.j1, na));
+  }
+  if constexpr (SHARED) {
+    if (P.pre[lo] != -1) it.ns = 2;  // a partial result, whether it is cut or not
   }
   return true;
 }
@@ -363,12 +396,12 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int k0) {
   return (a <= 0 ? ~0u : ~0u << a) & (b >= 31 ? ~0u : (2u << b) - 1u);
 }
 
-template <int D, int CAP>
+template <int D, int CAP, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k4,
                  const __grid_constant__ CUtensorMap tm_v4, const __grid_constant__ ChunkArgs A,
-                 const __grid_constant__ Plan<CAP> P, int req0) {
+                 const __grid_constant__ Plan<CAP, SHARED> P, int req0) {
   using C = Cfg<D>;
   constexpr int ST = C::STAGES;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -966,12 +999,48 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// merge_row over two lists of partials: na of them at row a, `astride` rows apart, then nb at row b.
+template <int E>
+__device__ __forceinline__ float merge_two(const float* po, const float* pl, int d, int64_t a, size_t astride, int na, int64_t b,
+                                           size_t bstride, int nb, int lane, float* out) {
+  const int s = na + nb;
+  auto at = [&](int i) { return i < na ? a + (int64_t)(i * astride) : b + (int64_t)((i - na) * bstride); };
+  float M = -INFINITY;
+  for (int i = lane; i < s; i += 32) M = fmaxf(M, __ldg(pl + at(i)));
+  M = warp_max(M);
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = 0.f;
+  if (M == -INFINITY) return -INFINITY;
+  constexpr int U = 4;  // partials in flight
+  float wsum = 0.f;
+  for (int i0 = 0; i0 < s; i0 += U) {
+    float v[U][E], w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      w[u] = i0 + u < s ? __ldg(pl + at(i0 + u)) : -INFINITY;
+      if (i0 + u < s) load_dims<E>(po + at(i0 + u) * d + lane * E, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u < s) {
+        const float x = exp2f((w[u] - M) * kLog2e);
+        wsum += x;
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[e] = fmaf(x, v[u][e], out[e]);
+      }
+  }
+  const float inv = 1.f / wsum;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] *= inv;
+  return M + logf(wsum);
+}
+
 // One warp per (new token, query head) of the requests that were cut. It reads ns fp32 partials of d + 1
 // a row, which stay in L2 (one 30,000-token sequence, 32 rows in 19 pieces: 44 us with the attention, of
 // which 18 are the cache at copy speed).
-template <int D, int CAP>
+template <int D, int CAP, bool SHARED>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant__ ChunkArgs A,
-                                                          const __grid_constant__ Plan<CAP> P, int req0, int n_rows) {
+                                                          const __grid_constant__ Plan<CAP, SHARED> P, int req0, int n_rows) {
   constexpr int E = D / 32;
   const int64_t mr = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -988,7 +1057,28 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
   const int64_t pr = (int64_t)P.part[lo] + y;
   const size_t stride = (size_t)P.qn[lo] * A.Hq;
   float out[E];
-  const float L = merge_row<E>(A.part_o + pr * D, stride * D, A.part_lse + pr, stride, P.ns[lo], lane, out);
+  float L;
+  if constexpr (SHARED) {
+    const int pre = P.pre[lo];
+    if (pre >= 0) {  // the prefix's partials of this row, then the request's own
+      const int64_t tg = (int64_t)q0 + t - __ldg(A.q_indptr + req0 + P.req[pre]);  // its row of the group's
+      if (tg < 0 || tg >= P.qn[pre]) return;
+      const int64_t pp = (int64_t)P.part[pre] + tg * A.Hq + y % A.Hq;
+      const size_t pstride = (size_t)P.qn[pre] * A.Hq;
+      L = merge_two<E>(A.part_o, A.part_lse, D, pp, pstride, P.ns[pre], pr, stride, P.ns[lo], lane, out);
+      if (y == 0 && lane == 0) {  // the request's list holds the pages that were read for it
+        const int e = P.skip[lo] / A.page_size - 1, lead = req0 + P.lead[lo];
+        const int a = __ldg(A.page_indptr + r) + e, b = __ldg(A.page_indptr + lead) + e;
+        if (a < 0 || a >= __ldg(A.page_indptr + r + 1) || b < 0 || b >= __ldg(A.page_indptr + lead + 1) ||
+            __ldg(A.page_indices + a) != __ldg(A.page_indices + b))
+          record_error(A.err, 0x609);
+      }
+    } else {
+      L = merge_row<E>(A.part_o + pr * D, stride * D, A.part_lse + pr, stride, P.ns[lo], lane, out);
+    }
+  } else {
+    L = merge_row<E>(A.part_o + pr * D, stride * D, A.part_lse + pr, stride, P.ns[lo], lane, out);
+  }
   const int64_t row = (int64_t)(q0 + t) * A.Hq + y % A.Hq;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
@@ -1027,7 +1117,9 @@ struct Group {
   struct Rank {
     int req, qn, ns;
     int64_t base, row1, part;
+    int skip, pre, end, lead;  // with shared prefixes
   };
+  bool shared = false;  // some prefix is computed once for its group
   std::vector<Rank> ranks;
 };
 
@@ -1035,29 +1127,71 @@ struct Group {
 // 18 KB for more (copied at each launch: 58 us of host time a call of 64 requests, 88 with the large one).
 constexpr int kSmallPlan = 64, kLargePlan = 1024;
 
-sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, int r0, int r1, int num_splits, int sms,
-                      Group& g) {
+// Requests that share their first tokens, on the host: requests indptr[i] .. indptr[i + 1] - 1 the first prefix[i].
+struct Prefixes {
+  int n = 0;
+  const int32_t* indptr = nullptr;
+  const int32_t* prefix = nullptr;
+};
+
+sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, const Prefixes& pf, int r0, int r1,
+                      int num_splits, int sms, Group& g) {
   constexpr int kMaxAuto = 256;
   constexpr double kItem = 2.0;    // an item's prologue and epilogue, in key tiles
   constexpr double kMerge = 4.0;   // the merge launch
   struct Req {
     int req, n, units, first, last, ns;  // new tokens, pairs of query tiles, key tiles of the first and last pair
+    int skip, pre, end, lead;            // as in Plan; pre: number of the prefix among reqs, -1 none, -2 itself one
   };
   std::vector<Req> reqs;
   g.r0 = r0;
+  // A prefix is computed once where that is less work than with each of its requests, in the time of key tiles of
+  // pairs of query tiles: it takes an item more a request, and fp32 partials of all rows twice.
+  auto shares = [&](int r, int end, int64_t skip) {
+    int some = 0, n = 0, units = 0;
+    for (int x = r; x < end; ++x) {
+      const int m = qi[x + 1] - qi[x];
+      some += m > 0;
+      n += m;
+      units += ((m + a.TQ - 1) / a.TQ + 1) / 2;
+    }
+    if (some < 2 || skip == 0) return false;
+    const double tiles = (double)((skip + kBN - 1) / kBN), all = ((n + a.TQ - 1) / a.TQ + 1) / 2;
+    return (units - all) * tiles * a.Hkv > all * a.Hkv * kItem + 2.0 * n * a.Hq * 8.0 * (a.d + 1) / 65536.0 + kMerge;
+  };
   auto tiles_of = [&](int n, int64_t len, int u) {  // key tiles of pair u
     int gt, wl;
     const int64_t t0 = (int64_t)2 * u * a.TQ, te = std::min<int64_t>(n, t0 + 2 * a.TQ), p0 = len - n;
     return tile_list(seen(a, p0 + t0, p0 + te - 1, len), gt, wl);
   };
   int most = 0;
-  for (int r = r0; r < r1; ++r) {
-    const int n = qi[r + 1] - qi[r];
-    if (n == 0) continue;
-    const int64_t len = (int64_t)ki[r + 1] - ki[r];
-    const int units = ((n + a.TQ - 1) / a.TQ + 1) / 2;
-    reqs.push_back(Req{r - r0, n, units, tiles_of(n, len, 0), tiles_of(n, len, units - 1), std::max(num_splits, 1)});
+  auto units_of = [&](int n) { return ((n + a.TQ - 1) / a.TQ + 1) / 2; };
+  auto add = [&](int r, int64_t skip, int pre, int lead) {  // request r's keys from token `skip` on
+    const int n = qi[r + 1] - qi[r], units = units_of(n);
+    const int64_t len = (int64_t)ki[r + 1] - ki[r] - skip;
+    reqs.push_back(Req{r - r0, n, units, tiles_of(n, len, 0), tiles_of(n, len, units - 1), std::max(num_splits, 1), (int)skip, pre,
+                       r - r0 + 1, lead});
     most = std::max(most, std::max(reqs.back().first, reqs.back().last));
+  };
+  for (int r = r0, i = 0; r < r1;) {
+    int end = r + 1;
+    if (pf.n > 0) {
+      while (pf.indptr[i + 1] <= r) ++i;
+      end = std::min(r1, (int)pf.indptr[i + 1]);  // (a group that two launches meet in is two groups)
+      if (shares(r, end, pf.prefix[i])) {
+        int lead = r;
+        while (qi[lead + 1] == qi[lead]) ++lead;
+        const int n = qi[end] - qi[r], tiles = (pf.prefix[i] + kBN - 1) / kBN, me = (int)reqs.size();
+        reqs.push_back(Req{r - r0, n, units_of(n), tiles, tiles, std::max(num_splits, 1), pf.prefix[i], -2, end - r0, lead - r0});
+        most = std::max(most, tiles);
+        g.shared = true;
+        for (; r < end; ++r)
+          if (qi[r + 1] > qi[r]) add(r, pf.prefix[i], me, lead - r0);
+        continue;
+      }
+    }
+    for (; r < end; ++r)
+      if (qi[r + 1] > qi[r]) add(r, 0, -1, 0);
   }
   // Chunks. The launch ends when the SM with the most to do does: with the items sorted by length and
   // handed out one by one that is about the largest of an SM's share, the longest item, and k times the
@@ -1081,7 +1215,7 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
         work += len * (double)items;
         longest = std::max(longest, (double)tiles / ns + kItem);
         bins[std::min(kBins - 1, (int)(len / step))] += items;
-        if (ns > 1) {
+        if (ns > 1 || q.pre != -1) {
           cut = true;
           work += (double)q.n * a.Hq * ns * 8.0 * (a.d + 1) / 65536.0;  // (a tile of K and V is 64 KB at most)
         }
@@ -1107,16 +1241,22 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
     for (Req& q : reqs) q.ns = chunks(std::max(q.first, q.last), best);
   }
   auto longest = [](const Req& q) { return (double)std::max(q.first, q.last) / q.ns; };
-  std::stable_sort(reqs.begin(), reqs.end(), [&](const Req& x, const Req& y) { return longest(x) > longest(y); });
-  for (const Req& q : reqs) {
+  std::vector<int> order(reqs.size()), rank(reqs.size());
+  std::iota(order.begin(), order.end(), 0);
+  std::stable_sort(order.begin(), order.end(), [&](int x, int y) { return longest(reqs[x]) > longest(reqs[y]); });
+  for (int i : order) {
+    const Req& q = reqs[i];
     const int64_t part = g.parts;
-    if (q.ns > 1) {
-      g.rows += (int64_t)q.n * a.Hq;
+    if (q.ns > 1 || q.pre != -1) {
+      if (q.pre != -2) g.rows += (int64_t)q.n * a.Hq;
       g.parts += (int64_t)q.n * a.Hq * q.ns;
     }
-    g.ranks.push_back(Group::Rank{q.req, q.n, q.ns, g.items, g.rows, part});
+    rank[i] = (int)g.ranks.size();
+    g.ranks.push_back(Group::Rank{q.req, q.n, q.ns, g.items, g.rows, part, q.skip, q.pre, q.end, q.lead});
     g.items += (int64_t)q.units * a.Hkv * q.ns;
   }
+  for (Group::Rank& k : g.ranks)
+    if (k.pre >= 0) k.pre = rank[k.pre];
   if (g.items > INT32_MAX || g.parts > INT32_MAX / 2) return STA_ERR_UNSUPPORTED;
   return STA_OK;
 }
@@ -1127,9 +1267,9 @@ struct Maps {
   CUtensorMap q, k, v, k4, v4;  // k4, v4: boxes of 32 tokens, beside those of 8
 };
 
-template <int D, int CAP>
+template <int D, int CAP, bool SHARED>
 sta_status launch_group(const Maps& m, const ChunkArgs& a, const Group& g, cudaStream_t st) {
-  Plan<CAP> p;
+  Plan<CAP, SHARED> p;
   p.n = (int)g.ranks.size();
   for (int i = 0; i < p.n; ++i) {
     const Group::Rank& k = g.ranks[i];
@@ -1139,32 +1279,38 @@ sta_status launch_group(const Maps& m, const ChunkArgs& a, const Group& g, cudaS
     p.qn[i] = k.qn;
     p.req[i] = (uint16_t)k.req;
     p.ns[i] = (uint16_t)k.ns;
+    if constexpr (SHARED) {
+      p.skip[i] = k.skip;
+      p.pre[i] = (int16_t)k.pre;
+      p.end[i] = (uint16_t)k.end;
+      p.lead[i] = (uint16_t)k.lead;
+    }
   }
   p.base[p.n] = (int32_t)g.items;
-  auto kern = chunk_kernel<D, CAP>;
+  auto kern = chunk_kernel<D, CAP, SHARED>;
   STA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM));
   kern<<<(unsigned)g.items, kThreads, Cfg<D>::SMEM, st>>>(m.q, m.k, m.v, m.k4, m.v4, a, p, g.r0);
   STA_LAUNCH_CHECK();
   if (g.rows > 0) {
-    chunk_merge_kernel<D, CAP><<<(unsigned)cdiv(g.rows, 8), 256, 0, st>>>(a, p, g.r0, (int)g.rows);
+    chunk_merge_kernel<D, CAP, SHARED><<<(unsigned)cdiv(g.rows, 8), 256, 0, st>>>(a, p, g.r0, (int)g.rows);
     STA_LAUNCH_CHECK();
   }
   return STA_OK;
 }
 
-}  // namespace
-}  // namespace sta
+template <int D>
+sta_status launch_any(const Maps& m, const ChunkArgs& a, const Group& g, cudaStream_t st) {
+  const bool small = g.ranks.size() <= kSmallPlan;
+  if (g.shared) return small ? launch_group<D, kSmallPlan, true>(m, a, g, st) : launch_group<D, kLargePlan, true>(m, a, g, st);
+  return small ? launch_group<D, kSmallPlan, false>(m, a, g, st) : launch_group<D, kLargePlan, false>(m, a, g, st);
+}
 
-using namespace sta;
-
-extern "C" sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages,
-                                          int page_size, int n_pages, const int32_t* page_indptr_dev,
-                                          const int32_t* page_indices_dev, const int32_t* q_indptr_dev,
-                                          const int32_t* q_indptr_host, const int32_t* kv_indptr_dev,
-                                          const int32_t* kv_indptr_host, int n_req, int Hq, int Hkv, int d,
-                                          sta_dtype dtype, float scale, const sta_mask_src* pattern, int num_splits,
-                                          void* o, float* lse, void* workspace, size_t* workspace_bytes,
-                                          sta_stream stream) try {
+// The two calls: with groups of requests that share their first tokens, or none of them.
+sta_status chunk_fwd(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages, int page_size, int n_pages,
+                     const int32_t* page_indptr_dev, const int32_t* page_indices_dev, const int32_t* q_indptr_dev,
+                     const int32_t* q_indptr_host, const int32_t* kv_indptr_dev, const int32_t* kv_indptr_host, int n_req,
+                     int Hq, int Hkv, int d, sta_dtype dtype, float scale, const sta_mask_src* pattern, const Prefixes& pf,
+                     int num_splits, void* o, float* lse, void* workspace, size_t* workspace_bytes, sta_stream stream) {
   constexpr int64_t kFar = (int64_t)1 << 31;  // beyond any distance between two tokens
   if (!workspace_bytes || !q_indptr_host || !kv_indptr_host || n_req < 1 || Hq < 1 || Hkv < 1 || page_size < 1 ||
       n_pages < 1 || num_splits < 0 || num_splits > 1024)
@@ -1176,6 +1322,13 @@ extern "C" sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const
   for (int r = 0; r < n_req; ++r)
     if (q_indptr_host[r + 1] < q_indptr_host[r] || kv_indptr_host[r + 1] < kv_indptr_host[r]) return STA_ERR_INVALID_ARG;
   if (kv_indptr_host[n_req] > INT32_MAX - 2 * kBN) return STA_ERR_UNSUPPORTED;
+  for (int i = 0; i < pf.n; ++i) {  // every new token lies behind its group's prefix
+    if (pf.prefix[i] < 0 || pf.prefix[i] % page_size != 0) return STA_ERR_INVALID_ARG;
+    for (int r = pf.indptr[i]; r < pf.indptr[i + 1]; ++r) {
+      const int n = q_indptr_host[r + 1] - q_indptr_host[r];
+      if (n > 0 && (int64_t)kv_indptr_host[r + 1] - kv_indptr_host[r] - n < pf.prefix[i]) return STA_ERR_INVALID_ARG;
+    }
+  }
   ChunkArgs a{};
   a.causal = 1;
   a.win_lo = -kFar;
@@ -1211,9 +1364,10 @@ extern "C" sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const
   cudaGetLastError();  // a size query also works where there is no device
   std::vector<Group> groups;
   int64_t parts = 0;
-  for (int r0 = 0; r0 < n_req; r0 += kLargePlan) {
+  const int batch = pf.n > 0 ? kLargePlan * 2 / 3 : kLargePlan;  // (a prefix has two requests at least)
+  for (int r0 = 0; r0 < n_req; r0 += batch) {
     Group g;
-    const sta_status st = plan_group(a, q_indptr_host, kv_indptr_host, r0, std::min(n_req, r0 + kLargePlan), num_splits, sms, g);
+    const sta_status st = plan_group(a, q_indptr_host, kv_indptr_host, pf, r0, std::min(n_req, r0 + batch), num_splits, sms, g);
     if (st != STA_OK) return st;
     parts = std::max(parts, g.parts);
     groups.push_back(std::move(g));
@@ -1265,13 +1419,47 @@ extern "C" sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const
   const cudaStream_t s = (cudaStream_t)stream;
   for (const Group& g : groups) {
     if (g.items == 0) continue;
-    const sta_status st = g.ranks.size() <= kSmallPlan ? (d == 64 ? launch_group<64, kSmallPlan>(m, a, g, s)
-                                                       : launch_group<128, kSmallPlan>(m, a, g, s))
-                                            : (d == 64 ? launch_group<64, kLargePlan>(m, a, g, s)
-                                                       : launch_group<128, kLargePlan>(m, a, g, s));
+    const sta_status st = d == 64 ? launch_any<64>(m, a, g, s) : launch_any<128>(m, a, g, s);
     if (st != STA_OK) return st;
   }
   return STA_OK;
+}
+
+}  // namespace
+}  // namespace sta
+
+using namespace sta;
+
+extern "C" sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages,
+                                          int page_size, int n_pages, const int32_t* page_indptr_dev,
+                                          const int32_t* page_indices_dev, const int32_t* q_indptr_dev,
+                                          const int32_t* q_indptr_host, const int32_t* kv_indptr_dev,
+                                          const int32_t* kv_indptr_host, int n_req, int Hq, int Hkv, int d,
+                                          sta_dtype dtype, float scale, const sta_mask_src* pattern, int num_splits,
+                                          void* o, float* lse, void* workspace, size_t* workspace_bytes,
+                                          sta_stream stream) try {
+  return chunk_fwd(q, q_stride, k_pages, v_pages, page_size, n_pages, page_indptr_dev, page_indices_dev, q_indptr_dev,
+                   q_indptr_host, kv_indptr_dev, kv_indptr_host, n_req, Hq, Hkv, d, dtype, scale, pattern, Prefixes{},
+                   num_splits, o, lse, workspace, workspace_bytes, stream);
+} catch (...) {  // no memory for the plan
+  return STA_ERR_INVALID_ARG;
+}
+
+extern "C" sta_status sta_prefix_fwd_paged(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages,
+                                           int page_size, int n_pages, const int32_t* page_indptr_dev,
+                                           const int32_t* page_indices_dev, const int32_t* q_indptr_dev,
+                                           const int32_t* q_indptr_host, const int32_t* kv_indptr_dev,
+                                           const int32_t* kv_indptr_host, int n_req, const int32_t* group_indptr_host,
+                                           const int32_t* prefix_host, int n_groups, int Hq, int Hkv, int d,
+                                           sta_dtype dtype, float scale, int num_splits, void* o, float* lse,
+                                           void* workspace, size_t* workspace_bytes, sta_stream stream) try {
+  if (n_req < 1 || n_groups < 1 || !group_indptr_host || !prefix_host) return STA_ERR_INVALID_ARG;
+  if (group_indptr_host[0] != 0 || group_indptr_host[n_groups] != n_req) return STA_ERR_INVALID_ARG;
+  for (int i = 0; i < n_groups; ++i)
+    if (group_indptr_host[i + 1] < group_indptr_host[i]) return STA_ERR_INVALID_ARG;
+  return chunk_fwd(q, q_stride, k_pages, v_pages, page_size, n_pages, page_indptr_dev, page_indices_dev, q_indptr_dev,
+                   q_indptr_host, kv_indptr_dev, kv_indptr_host, n_req, Hq, Hkv, d, dtype, scale, nullptr,
+                   Prefixes{n_groups, group_indptr_host, prefix_host}, num_splits, o, lse, workspace, workspace_bytes, stream);
 } catch (...) {  // no memory for the plan
   return STA_ERR_INVALID_ARG;
 }
