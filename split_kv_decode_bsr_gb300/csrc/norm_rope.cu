@@ -7,18 +7,26 @@
 //
 // L lanes of a warp (a power of two) share a head: each holds the 16-byte vectors (half layout: pairs
 // of them, half a rotation apart) that the rotary kernel calls units, so that the turn needs no exchange
-// and the sums over a head are log2 L shuffles. A head is read once and written once; the products in
-// between stay in fp32 and are rounded once. The cosines and sines of a CTA's tokens go through
-// shared memory, and the turns are exact at any position, as in the rotary kernel.
+// and the sums over a head are log2 L shuffles; the warp's 32 / L neighbouring heads of one tensor and token are
+// a piece of work. Warps work on their own: each takes an equal run of the pieces (tokens, then the heads of q,
+// k and v), copies its next pieces to shared memory ahead of its work (16-byte copies that the same lane reads
+// again), and puts the cosines and sines of the token that it has come to into a table of its own. A head is read once
+// and written once; the products in between stay in fp32 and are rounded once. The turns are exact at any position, as
+// in the rotary kernel.
 #include "rope.inl"
 
 namespace sta {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokens = 16;  // tokens of a CTA (backward: of one of its steps)
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 template <typename T> constexpr int kMany = sizeof(T) == 2 ? 2 : 4;  // units of a lane where a head has more than 32 (at most 64, 128)
-constexpr int kMaxGrid = 152 * 4;  // CTAs of a backward pass, each with a row of partial sums for dw
+constexpr int kMaxGrid = 152 * 2;  // CTAs of a backward pass, each with a row of partial sums for dw
+template <int NU> constexpr int kSlots = NU <= 2 ? 3 : 2;  // pieces that a warp has on their way
+template <int W, bool IL, int NU>
+constexpr int ctas_an_sm(bool backward) {
+  return W == 1 || NU * (IL ? 1 : 2) > 2 ? 1 : (backward ? 2 : 3);
+}
+enum Mode { kForward, kAppend, kBackward };
 
 struct NormArgs {
   const uint8_t* src[3];  // q, k, v (v: to pages alone)
@@ -27,15 +35,12 @@ struct NormArgs {
   int64_t src_stride[3], dst_stride[3], dy_stride[2];  // bytes between tokens (k, v pages: of a page)
   const float* weight[2];
   int heads[3];
-  int H;                  // their sum
-  uint32_t h_mul;         // n / H for n < 2^31: high word of n h_mul, shifted right by h_shift (-1: H is 1)
-  int h_shift;
+  int pieces[3];          // of a token: 32 / L heads of q, k or v each
   int64_t n_tokens;
   int d, rot;
-  int tokens;             // tokens of a CTA (or step)
   int units, rot_units;   // units of a head; the first rot_units turn
   int log_l;              // lanes of a head
-  int w_at;               // byte offset of the weights in shared memory
+  int warp_bytes;         // shared memory of a warp
   float eps, inv_d, mscale;
   const int32_t* positions;
   // paged destination of k and v
@@ -45,62 +50,127 @@ struct NormArgs {
   const int32_t* page_indices;
   int n_req, page_size, n_pages;
   int* err;
-  float* part;            // backward: [CTAs, 2, d]
+  int ctas_q;             // backward: the CTAs of q, then those of k
+  float* part;            // backward: [CTAs, d]
 };
 
-// Where a new token goes, found by a whole warp: its position and its cache row, -1 when it goes
-// nowhere. False for padding. 128 requests are looked at at once, where one thread's binary search would
-// take a round trip to memory for each of its steps.
-__device__ __forceinline__ bool token_place_warp(const NormArgs& A, int64_t t, int lane, int& pos, int64_t& row) {
-  pos = 0;
-  row = -1;
-  const int first = __ldg(A.q_indptr), end = __ldg(A.q_indptr + A.n_req);
-  int lo = 0, n = A.n_req;  // the last request that starts at or before t is among lo .. lo + n - 1
-  while (n > 1) {
-    const int step = (n + 127) >> 7;
-    int c = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int at = (lane + 32 * k) * step;
-      c += __popc(__ballot_sync(0xffffffffu, at < n && __ldg(A.q_indptr + lo + at) <= t));
+// Where new tokens go, found by a whole warp. The next token of a request is looked for only where a page ends.
+struct Place {
+  int pos = 0;        // the token's position
+  int64_t row = -1;   // its cache row, -1 when it goes nowhere
+  bool live = false;  // false: padding
+  int64_t end = -1;   // tokens of the request end here
+  int64_t list = 0, list_end = 0;
+  int left = 0;       // rows of the page behind this one
+
+  __device__ __forceinline__ void find_page(const NormArgs& A, int lane) {
+    const int64_t e = list + pos / A.page_size;
+    const int in = pos % A.page_size;
+    row = -1;
+    left = A.page_size - 1 - in;
+    if (e < 0 || e >= list_end) {
+      if (lane == 0) record_error(A.err, 0x604);
+      return;
     }
-    c = max(c - 1, 0) * step;
-    lo += c;
-    n = min(step, n - c);
+    const int page = __ldg(A.page_indices + e);
+    if (page < 0 || page >= A.n_pages) {
+      if (lane == 0) record_error(A.err, 0x110);
+      return;
+    }
+    row = (int64_t)page * A.page_size + in;
   }
-  if (t < first || t >= end) return false;
-  const int64_t q1 = __ldg(A.q_indptr + lo + 1), len = (int64_t)__ldg(A.kv_indptr + lo + 1) - __ldg(A.kv_indptr + lo);
-  const int64_t list = __ldg(A.page_indptr + lo), list_end = __ldg(A.page_indptr + lo + 1);
-  const int64_t p = len - (q1 - t);
-  if (p < 0 || t >= q1) {  // the sequence is shorter than its chunk: this token is not in it
-    pos = (int)(p < INT32_MIN ? INT32_MIN : p);
-    return true;
+  // 128 requests are looked at at once, where one thread's binary search would take a round trip to memory for
+  // each of its steps
+  __device__ __forceinline__ void find(const NormArgs& A, int64_t t, int lane) {
+    pos = 0;
+    row = -1;
+    left = 0;
+    const int first = __ldg(A.q_indptr), all = __ldg(A.q_indptr + A.n_req);
+    int lo = 0, n = A.n_req;  // the last request that starts at or before t is among lo .. lo + n - 1
+    while (n > 1) {
+      const int step = (n + 127) >> 7;
+      int c = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int at = (lane + 32 * k) * step;
+        c += __popc(__ballot_sync(0xffffffffu, at < n && __ldg(A.q_indptr + lo + at) <= t));
+      }
+      c = max(c - 1, 0) * step;
+      lo += c;
+      n = min(step, n - c);
+    }
+    live = t >= first && t < all;
+    end = -1;
+    if (!live) return;
+    const int64_t q1 = __ldg(A.q_indptr + lo + 1), len = (int64_t)__ldg(A.kv_indptr + lo + 1) - __ldg(A.kv_indptr + lo);
+    list = __ldg(A.page_indptr + lo);
+    list_end = __ldg(A.page_indptr + lo + 1);
+    const int64_t p = len - (q1 - t);
+    if (p < 0 || t >= q1) {  // the sequence is shorter than its chunk: this token is not in it
+      pos = (int)(p < INT32_MIN ? INT32_MIN : p);
+      return;
+    }
+    end = q1;
+    pos = (int)p;
+    find_page(A, lane);
   }
-  pos = (int)p;
-  const int64_t e = list + p / A.page_size;
-  if (e < 0 || e >= list_end) {
-    if (lane == 0) record_error(A.err, 0x604);
-    return true;
+  __device__ __forceinline__ void next(const NormArgs& A, int64_t t, int lane) {  // t - 1 was the last one
+    if (t >= end) {
+      find(A, t, lane);
+      return;
+    }
+    ++pos;
+    if (left == 0) {
+      find_page(A, lane);
+    } else {
+      --left;
+      row += row >= 0;
+    }
   }
-  const int page = __ldg(A.page_indices + e);
-  if (page < 0 || page >= A.n_pages) {
-    if (lane == 0) record_error(A.err, 0x110);
-    return true;
-  }
-  row = (int64_t)page * A.page_size + p % A.page_size;
-  return true;
+};
+
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2_both(float x) { return f32x2_pack(x, x); }
+__device__ __forceinline__ float f32x2_sum(uint64_t x) {
+  float a, b;
+  f32x2_unpack(x, a, b);
+  return a + b;
 }
 
-// A thread's units of its heads: the same elements of every head it works on.
+// 16 bytes to shared memory, or 16 zero bytes where `some` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A thread's units of its heads: the same elements of every head it works on. In fp32 a unit is NP
+// couples of pairs, first elements in A and second ones in B, for the packed instructions (twice the
+// products of an issue slot, which is what bounds these kernels first: 8192 tokens x 40 heads of 128 in
+// bf16 took 36.9 us with scalar ones). A unit that does not turn has its elements there just so (half layout: in A).
 template <typename T, int W, bool IL, int NU>
 struct Units {
   static constexpr int WI = IL && W == 1 ? 2 : W;  // elements of a vector: whole pairs when interleaved
   static constexpr int PP = IL ? WI / 2 : WI;      // pairs of a unit
-  static constexpr int E = IL ? WI : 2 * WI;       // elements of a unit that turns
+  static constexpr int NP = (PP + 1) / 2;
   int unit[NU];  // -1: none
   int off[NU];   // first element
   bool turn[NU];
   int half, d;
+  static constexpr int V = NU * (IL ? 1 : 2);      // vectors of a head that a lane holds
+  struct Row {  // elements that are not there are 0
+    Vec<T, WI> a[NU], b[IL ? 1 : NU];
+  };
+  struct Half2 {
+    uint64_t a[NP], b[NP];
+  };
   __device__ __forceinline__ void set(const NormArgs& A) {
     const int l = threadIdx.x & ((1 << A.log_l) - 1);
     half = A.rot >> 1;
@@ -110,24 +180,46 @@ struct Units {
       const int u = l + (j << A.log_l);
       turn[j] = u < A.rot_units;
       unit[j] = u < A.units ? u : -1;
-      off[j] = turn[j] ? u * WI : A.rot + (u - A.rot_units) * WI;
+      off[j] = turn[j] ? u * WI : (u < A.units ? A.rot + (u - A.rot_units) * WI : 0);
     }
   }
-  struct Row {
-    Vec<T, WI> a[NU], b[IL ? 1 : NU];
+  // places in the head of a unit's couple m: first and second element of its pairs (-1: there is none)
+  struct Places {
+    int a0, a1, b0, b1;
   };
-  // elements that are not there stay as they are
-  __device__ __forceinline__ void load(const T* src, Row& r) const {
+  static __device__ __forceinline__ Places places(int off, bool turn, int m, int half, int d) {
+    Places p;
+    if (IL) p = Places{off + 4 * m, PP == 1 ? -1 : off + 4 * m + 2, off + 4 * m + 1, PP == 1 ? -1 : off + 4 * m + 3};
+    else p = Places{off + 2 * m, PP == 1 ? -1 : off + 2 * m + 1, turn ? off + half + 2 * m : -1,
+                    turn && PP > 1 ? off + half + 2 * m + 1 : -1};
+    if (p.b0 >= d) p.b0 = -1;
+    return p;
+  }
+  // a head's vectors to this lane's places in shared memory, 32 lanes of 16 bytes a vector; zeros where there are none
+  __device__ __forceinline__ void copy(uint32_t to, const uint8_t* head, bool some) const {
+    const T* src = reinterpret_cast<const T*>(head);  // (not read where some is false)
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-      if (unit[j] < 0) continue;
-      if (W == 1 && IL && !turn[j]) {  // the last element of an odd rest is alone
-        r.a[j].v[0] = src[off[j]];
-        if (off[j] + 1 < d) r.a[j].v[1] = src[off[j] + 1];
-      } else {
-        r.a[j].load(src + off[j]);
-      }
-      if (!IL && turn[j]) r.b[j].load(src + off[j] + half);
+      copy16(to + j * 512, src + off[j], some && unit[j] >= 0);
+      if (!IL) copy16(to + (NU + j) * 512, src + off[j] + half, some && turn[j]);
+    }
+  }
+  static __device__ __forceinline__ void take(const uint8_t* from, Row& r) {
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      *reinterpret_cast<uint4*>(r.a[j].v) = *reinterpret_cast<const uint4*>(from + j * 512);
+      if (!IL) *reinterpret_cast<uint4*>(r.b[IL ? 0 : j].v) = *reinterpret_cast<const uint4*>(from + (NU + j) * 512);
+    }
+  }
+  // element by element, straight from memory
+  __device__ __forceinline__ void load(const T* src, bool some, Row& r) const {
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      const Places p = places(off[j], turn[j], 0, half, d);
+      auto at = [&](int x) { return some && unit[j] >= 0 && x >= 0 ? src[x] : from_f<T>(0.f); };
+      r.a[j].v[0] = at(p.a0);
+      if (IL) r.a[j].v[WI - 1] = at(p.b0);
+      else r.b[IL ? 0 : j].v[0] = at(p.b0);
     }
   }
   __device__ __forceinline__ void store(T* dst, const Row& r) const {
@@ -143,344 +235,362 @@ struct Units {
       if (!IL && turn[j]) r.b[j].store(dst + off[j] + half);
     }
   }
-  // element e of unit j: its place in the head, -1 when there is none
-  __device__ __forceinline__ int place(int j, int e) const {
-    if (unit[j] < 0 || (!turn[j] && e >= WI)) return -1;
-    const int p = off[j] + (e < WI ? e : half + e - WI);
-    return p < d ? p : -1;
-  }
-  // the E elements of unit j in fp32, 0 where there is none
-  __device__ __forceinline__ void get(const Row& r, int j, float* x) const {
+  static __device__ __forceinline__ Half2 get(const Row& r, int j) {
+    Half2 x;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const bool some = unit[j] >= 0 && (e < WI || turn[j]) && (W > 1 || !IL || e == 0 || off[j] + e < d);
-      x[e] = some ? to_f(e < WI ? r.a[j].v[e] : r.b[IL ? 0 : j].v[e - WI]) : 0.f;
+    for (int m = 0; m < NP; ++m) {
+      if constexpr (PP == 1) {
+        x.a[m] = f32x2_pack(to_f(r.a[j].v[0]), 0.f);
+        x.b[m] = f32x2_pack(to_f(IL ? r.a[j].v[WI - 1] : r.b[IL ? 0 : j].v[0]), 0.f);
+      } else if constexpr (sizeof(T) == 2) {  // (by words: an element at a time costs an instruction more each)
+        const uint32_t *a = reinterpret_cast<const uint32_t*>(r.a[j].v), *b = reinterpret_cast<const uint32_t*>(r.b[IL ? 0 : j].v);
+        if constexpr (IL) {
+          x.a[m] = f32x2_pack(bf16lo(a[2 * m]), bf16lo(a[2 * m + 1]));
+          x.b[m] = f32x2_pack(bf16hi(a[2 * m]), bf16hi(a[2 * m + 1]));
+        } else {
+          x.a[m] = f32x2_pack(bf16lo(a[m]), bf16hi(a[m]));
+          x.b[m] = f32x2_pack(bf16lo(b[m]), bf16hi(b[m]));
+        }
+      } else if constexpr (IL) {
+        x.a[m] = f32x2_pack(to_f(r.a[j].v[4 * m]), to_f(r.a[j].v[4 * m + 2]));
+        x.b[m] = f32x2_pack(to_f(r.a[j].v[4 * m + 1]), to_f(r.a[j].v[4 * m + 3]));
+      } else {
+        x.a[m] = f32x2_pack(to_f(r.a[j].v[2 * m]), to_f(r.a[j].v[2 * m + 1]));
+        x.b[m] = f32x2_pack(to_f(r.b[j].v[2 * m]), to_f(r.b[j].v[2 * m + 1]));
+      }
     }
+    return x;
   }
-  __device__ __forceinline__ void put(Row& r, int j, const float* x) const {
+  static __device__ __forceinline__ void put(Row& r, int j, const Half2& x) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (e < WI) r.a[j].v[e] = from_f<T>(x[e]);
-      else r.b[IL ? 0 : j].v[e - WI] = from_f<T>(x[e]);
-    }
-  }
-  // The weights of unit j. In shared memory four at a time, [q, k][E / 4][units], so that neighbouring
-  // lanes read neighbouring words; straight from memory where heads go element by element.
-  static __device__ __forceinline__ void stage(const NormArgs& A, float4* s_w) {
-    if constexpr (W > 1) {
-      float* s = reinterpret_cast<float*>(s_w);
-      const int each = A.units * E;
-      for (int i = threadIdx.x; i < 2 * each; i += kThreads) {
-        const int g = i >= each, x = i - g * each, u = (x >> 2) % A.units, e = (x >> 2) / A.units * 4 + (x & 3);
-        const bool turns = u < A.rot_units;
-        const int o = turns ? u * WI : A.rot + (u - A.rot_units) * WI, p = e < WI ? o + e : o + (A.rot >> 1) + e - WI;
-        s[i] = A.weight[g] && (e < WI || turns) ? __ldg(A.weight[g] + p) : 1.f;
+    for (int m = 0; m < NP; ++m) {
+      float a0, a1, b0, b1;
+      f32x2_unpack(x.a[m], a0, a1);
+      f32x2_unpack(x.b[m], b0, b1);
+      if constexpr (PP == 1) {
+        r.a[j].v[0] = from_f<T>(a0);
+        if (IL) r.a[j].v[WI - 1] = from_f<T>(b0);
+        else r.b[IL ? 0 : j].v[0] = from_f<T>(b0);
+      } else if constexpr (sizeof(T) == 2) {
+        if constexpr (IL) {
+          reinterpret_cast<uint32_t*>(r.a[j].v)[2 * m] = pack_bf16x2(a0, b0);
+          reinterpret_cast<uint32_t*>(r.a[j].v)[2 * m + 1] = pack_bf16x2(a1, b1);
+        } else {
+          reinterpret_cast<uint32_t*>(r.a[j].v)[m] = pack_bf16x2(a0, a1);
+          reinterpret_cast<uint32_t*>(r.b[j].v)[m] = pack_bf16x2(b0, b1);
+        }
+      } else if constexpr (IL) {
+        r.a[j].v[4 * m] = a0;
+        r.a[j].v[4 * m + 1] = b0;
+        r.a[j].v[4 * m + 2] = a1;
+        r.a[j].v[4 * m + 3] = b1;
+      } else {
+        r.a[j].v[2 * m] = a0;
+        r.a[j].v[2 * m + 1] = a1;
+        r.b[j].v[2 * m] = b0;
+        r.b[j].v[2 * m + 1] = b1;
       }
     }
   }
-  __device__ __forceinline__ void weights(const NormArgs& A, const float4* s_w, int g, int j, float* w) const {
-    if constexpr (W > 1) {
+  // the weights of this lane's elements (1 where there is none)
+  __device__ __forceinline__ void weights(const float* w, Half2* to) const {
 #pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        const float4 v = s_w[(g * (E / 4) + e / 4) * A.units + max(unit[j], 0)];
-        w[e] = v.x;
-        w[e + 1] = v.y;
-        w[e + 2] = v.z;
-        w[e + 3] = v.w;
-      }
-    } else {
+    for (int j = 0; j < NU; ++j)
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int p = place(j, e);
-        w[e] = A.weight[g] && p >= 0 ? __ldg(A.weight[g] + p) : 1.f;
+      for (int m = 0; m < NP; ++m) {
+        const Places p = places(off[j], turn[j], m, half, d);
+        auto at = [&](int x) { return w && unit[j] >= 0 && x >= 0 ? __ldg(w + x) : 1.f; };
+        to[j].a[m] = f32x2_pack(at(p.a0), at(p.a1));
+        to[j].b[m] = f32x2_pack(at(p.b0), at(p.b1));
       }
+  }
+  // x turned by the token's angles, or back. Of a couple of pairs the two cosines and the two sines lie in 16
+  // bytes, [NP][units that turn].
+  __device__ __forceinline__ void rotate(const NormArgs& A, const float2* s_cs, int j, Half2& x, bool back) const {
+#pragma unroll
+    for (int m = 0; m < NP; ++m) {
+      uint64_t c, s, n;
+      if constexpr (PP == 1) {
+        const float2 v = s_cs[IL ? off[j] >> 1 : off[j]];
+        c = f32x2_pack(v.x, 0.f);
+        s = f32x2_pack(v.y, 0.f);
+        n = f32x2_pack(-v.y, 0.f);
+      } else {
+        const float4 v = reinterpret_cast<const float4*>(s_cs)[m * A.rot_units + unit[j]];
+        c = f32x2_pack(v.x, v.y);
+        s = f32x2_pack(v.z, v.w);
+        n = f32x2_pack(-v.z, -v.w);
+      }
+      const uint64_t t = f32x2_fma(x.b[m], back ? s : n, f32x2_mul(x.a[m], c));
+      x.b[m] = f32x2_fma(x.a[m], back ? n : s, f32x2_mul(x.b[m], c));
+      x.a[m] = t;
     }
   }
-  // cosine and sine of unit j's pairs, two pairs in 16 bytes: [PP / 2][units that turn][2]
-  __device__ __forceinline__ void angles(const NormArgs& A, const float2* s_cs, int j, float2* cs) const {
-    if constexpr (PP == 1) {
-      cs[0] = s_cs[IL ? off[j] >> 1 : off[j]];
-    } else {
-      const float4* c4 = reinterpret_cast<const float4*>(s_cs) + unit[j];
-#pragma unroll
-      for (int i = 0; i < PP / 2; ++i) {
-        const float4 v = c4[i * A.rot_units];
-        cs[2 * i] = make_float2(v.x, v.y);
-        cs[2 * i + 1] = make_float2(v.z, v.w);
-      }
-    }
-  }
-  // pairs (a, b) of x turned: (a cos - b sin, b cos + a sin), or back
-  static __device__ __forceinline__ void turn_pairs(float* x, const float2* cs, bool back) {
-#pragma unroll
-    for (int p = 0; p < PP; ++p) {
-      float &a = x[IL ? 2 * p : p], &b = x[IL ? 2 * p + 1 : WI + p];
-      const float c = cs[p].x, s = back ? -cs[p].y : cs[p].y, t = a;
-      a = t * c - b * s;
-      b = t * s + b * c;
-    }
-  }
-  // The cosines and sines (times the magnitude) of nt tokens.
-  static __device__ __forceinline__ void table(const NormArgs& A, const RopeTable& tab, const int* s_pos, int nt, float2* s_cs) {
-    const int half = A.rot >> 1;
-    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-      const int t = i / half, p = i - t * half;
-      const uint64_t phase = (uint64_t)(int64_t)s_pos[t] * tab.turn[p];
+  // The cosines and sines (times the magnitude) of a position, by a warp.
+  static __device__ __forceinline__ void table(const NormArgs& A, const RopeTable& tab, int pos, float2* s_cs) {
+    for (int p = threadIdx.x & 31; p < A.rot >> 1; p += 32) {
+      const uint64_t phase = (uint64_t)(int64_t)pos * tab.turn[p];
       float s, c;
       sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-      const int e = p % PP;  // place of the pair in its unit
-      const int at = PP == 1 ? p : ((e >> 1) * A.rot_units + p / PP) * 2 + (e & 1);
-      s_cs[t * half + at] = make_float2(c * A.mscale, s * A.mscale);
+      if constexpr (PP == 1) {
+        s_cs[p] = make_float2(c * A.mscale, s * A.mscale);
+      } else {
+        const int e = p % PP;  // place of the pair in its unit
+        float* to = reinterpret_cast<float*>(s_cs) + ((e >> 1) * A.rot_units + p / PP) * 4 + (e & 1);
+        to[0] = c * A.mscale;
+        to[2] = s * A.mscale;
+      }
     }
   }
 };
 
-__device__ __forceinline__ float lanes_sum(float x, int log_l) {
-  for (int o = 1 << log_l >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+// Sums over the lanes of a head.
+template <int N>
+__device__ __forceinline__ void lanes_sum(float* x, int log_l) {
+#pragma unroll
+  for (int o = 4; o >= 0; --o)
+    if (log_l > o) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 1 << o);
+    }
 }
 
-__device__ __forceinline__ int token_of(const NormArgs& A, int row) {
-  return A.h_shift < 0 ? row : (int)(__umulhi((uint32_t)row, A.h_mul) >> A.h_shift);
-}
-
-// W: elements of a vector (1: unaligned data, element by element); IL: interleaved pairs; NU: units of a
-// lane; APPEND: q, k, v with k and v going to pages.
-template <typename T, int W, bool IL, int NU, bool APPEND>
-__global__ void __launch_bounds__(kThreads, NU == 1 ? 5 : 2)
+// W: elements of a vector (1: unaligned data, element by element); IL: interleaved pairs; NU: units of a lane.
+// Backward: a thread's part of dw stays in registers throughout.
+template <typename T, int W, bool IL, int NU, int MODE>
+__global__ void __launch_bounds__(kThreads, ctas_an_sm<W, IL, NU>(MODE == kBackward))
     norm_rope_kernel(const __grid_constant__ NormArgs A, const __grid_constant__ RopeTable tab) {
   using U = Units<T, W, IL, NU>;
-  constexpr int R = NU == 1 ? 2 : 1;  // heads of a lane in flight
+  constexpr bool BWD = MODE == kBackward;
+  constexpr int S = W == 1 ? 0 : kSlots<NU>, SLOT = U::V * 512 * (BWD ? 2 : 1);
   extern __shared__ __align__(16) uint8_t smem[];
-  float2* s_cs = reinterpret_cast<float2*>(smem);
-  float4* s_w = reinterpret_cast<float4*>(smem + A.w_at);
-  __shared__ int64_t s_row[kMaxTokens];
-  __shared__ int s_pos[kMaxTokens];
-  __shared__ int s_live[kMaxTokens];
-  const int half = A.rot >> 1, each = kThreads >> A.log_l;  // heads of a round
-  const int64_t t0 = (int64_t)blockIdx.x * A.tokens;
-  const int nt = (int)min((int64_t)A.tokens, A.n_tokens - t0), total = nt * A.H;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint8_t* mine = smem + warp * A.warp_bytes;  // S slots, then the table
+  const uint32_t ring = smem_u32(mine) + lane * 16;
+  float2* s_cs = reinterpret_cast<float2*>(mine + S * SLOT);
   U u;
   u.set(A);
-  typename U::Row x[R];
-  int tok[R], hd[R];  // token, -1: none; head of q, k and v together
-  auto group = [&](int h) { return h < A.heads[0] ? 0 : (!APPEND || h < A.heads[0] + A.heads[1] ? 1 : 2); };
-  auto in_group = [&](int h, int g) { return h - (g > 0 ? A.heads[0] : 0) - (g > 1 ? A.heads[1] : 0); };
-  auto load = [&](int i0) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int i = i0 + r * each + (threadIdx.x >> A.log_l);
-      tok[r] = -1;
-      if (i >= total) continue;
-      const int t = token_of(A, i), h = i - t * A.H, g = group(h);
-      tok[r] = t;
-      hd[r] = h;
-      u.load(reinterpret_cast<const T*>(A.src[g] + (t0 + t) * A.src_stride[g]) + (int64_t)in_group(h, g) * A.d, x[r]);
-    }
+  const int role = BWD && (int)blockIdx.x >= A.ctas_q;  // backward: the tensor of this CTA
+  const int n_pieces = BWD ? A.pieces[role] : A.pieces[0] + A.pieces[1] + (MODE == kAppend ? A.pieces[2] : 0);
+  const int64_t total = A.n_tokens * n_pieces;
+  const int64_t nw = (int64_t)kWarps * (BWD ? (role ? (int)gridDim.x - A.ctas_q : A.ctas_q) : (int)gridDim.x);
+  const int64_t w0 = (int64_t)kWarps * (blockIdx.x - (role ? A.ctas_q : 0)) + warp;
+  const int64_t each = total / nw, over = total - each * nw, begin = w0 * each + min(w0, over);
+  const int count = (int)(each + (w0 < over));
+  // A place in the run: its token, piece, tensor, this lane's head, and the piece at which the next tensor begins.
+  struct At {
+    int64_t t;
+    int piece, g, h, edge;
   };
-  auto finish = [&]() {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int g = tok[r] < 0 ? 2 : group(hd[r]);
-      float ss = 0.f;
-      if (g < 2) {
-#pragma unroll
-        for (int j = 0; j < NU; ++j) {
-          float v[U::E], s4[4] = {0.f, 0.f, 0.f, 0.f};
-          u.get(x[r], j, v);
-#pragma unroll
-          for (int e = 0; e < U::E; ++e) s4[e & 3] = fmaf(v[e], v[e], s4[e & 3]);
-          ss += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-        }
-      }
-      ss = lanes_sum(ss, A.log_l);  // (of a whole warp: lanes without a head take part)
-      if (tok[r] < 0) continue;
-      const int t = tok[r];
-      if (APPEND && (!s_live[t] || (g > 0 && s_row[t] < 0))) continue;
-      if (g < 2) {
-        const float rms = rsqrtf(fmaf(ss, A.inv_d, A.eps));
-#pragma unroll
-        for (int j = 0; j < NU; ++j) {
-          float v[U::E], w[U::E];
-          u.get(x[r], j, v);
-          u.weights(A, s_w, g, j, w);
-#pragma unroll
-          for (int e = 0; e < U::E; ++e) v[e] = v[e] * rms * w[e];
-          if (u.turn[j]) {
-            float2 cs[U::PP];
-            u.angles(A, s_cs + t * half, j, cs);
-            U::turn_pairs(v, cs, false);
-          }
-          u.put(x[r], j, v);
-        }
-      }
-      const int64_t at = APPEND && g > 0 ? s_row[t] : t0 + t;
-      u.store(reinterpret_cast<T*>(A.dst[g] + at * A.dst_stride[g]) + (int64_t)in_group(hd[r], g) * A.d, x[r]);
-    }
+  const int heads = 32 >> A.log_l, stride = heads * A.d * (int)sizeof(T);  // heads of a piece, their bytes
+  auto settle = [&](At& a) {
+    a.g = BWD ? role : (a.piece < A.pieces[0] ? 0 : (MODE != kAppend || a.piece < A.pieces[0] + A.pieces[1] ? 1 : 2));
+    const int from = BWD ? 0 : (a.g > 0 ? A.pieces[0] : 0) + (a.g > 1 ? A.pieces[1] : 0);
+    a.h = (a.piece - from) * heads + (lane >> A.log_l);
+    a.edge = from + A.pieces[a.g];
   };
-  load(0);  // under the table's latency
-  if constexpr (APPEND) {
-    const int lane = threadIdx.x & 31;
-    for (int t = threadIdx.x >> 5; t < nt; t += kThreads / 32) {
-      int pos;
-      int64_t row;
-      const bool live = token_place_warp(A, t0 + t, lane, pos, row);
-      if (lane == 0) {
-        s_pos[t] = A.positions ? __ldg(A.positions + t0 + t) : pos;
-        s_row[t] = row;
-        s_live[t] = live;
+  auto head = [&](const uint8_t* base, int64_t token_stride, const At& a) {
+    return base + a.t * token_stride + (int64_t)a.h * A.d * (int)sizeof(T);
+  };
+  At at;  // where the work is
+  at.t = begin / n_pieces;
+  at.piece = (int)(begin - at.t * n_pieces);
+  settle(at);
+  At ahead = at;  // where the copies are, and from where
+  const uint8_t *from = head(A.src[at.g], A.src_stride[at.g], at), *from_dy = BWD ? head(A.dy[role], A.dy_stride[role], at) : nullptr;
+  int to_copy = count;
+  uint32_t slot = 0;
+  auto copy = [&](uint32_t to) {
+    if (to_copy > 0) {
+      --to_copy;
+      const bool some = ahead.h < A.heads[ahead.g];
+      u.copy(ring + to * SLOT, from, some);
+      if (BWD) u.copy(ring + to * SLOT + U::V * 512, from_dy, some);
+      ahead.h += heads;
+      from += stride;
+      if (BWD) from_dy += stride;
+      if (++ahead.piece == ahead.edge) {
+        if (ahead.piece == n_pieces) {
+          ahead.piece = 0;
+          ++ahead.t;
+        }
+        settle(ahead);
+        from = head(A.src[ahead.g], A.src_stride[ahead.g], ahead);
+        if (BWD) from_dy = head(A.dy[role], A.dy_stride[role], ahead);
       }
     }
-  } else if ((int)threadIdx.x < nt) {
-    s_pos[threadIdx.x] = A.positions ? __ldg(A.positions + t0 + threadIdx.x) : 0;
+    copy_commit();  // (an empty one at the end, so that the waits count the same)
+  };
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) copy(i);
   }
-  U::stage(A, s_w);
-  __syncthreads();
-  U::table(A, tab, s_pos, nt, s_cs);
-  __syncthreads();
-  finish();
-  for (int i0 = R * each; i0 < total; i0 += R * each) {
-    load(i0);
-    finish();
-  }
-}
-
-// Persistent CTAs over steps of A.tokens tokens; a thread's part of dw stays in registers throughout.
-template <typename T, int W, bool IL, int NU>
-__global__ void __launch_bounds__(kThreads, NU == 1 ? 2 : 1)
-    norm_rope_bwd_kernel(const __grid_constant__ NormArgs A, const __grid_constant__ RopeTable tab) {
-  using U = Units<T, W, IL, NU>;
-  extern __shared__ __align__(16) uint8_t smem[];
-  float2* s_cs = reinterpret_cast<float2*>(smem);
-  float4* s_w = reinterpret_cast<float4*>(smem + A.w_at);
-  __shared__ int s_pos[kMaxTokens];
-  const int half = A.rot >> 1, each = kThreads >> A.log_l;
-  U u;
-  u.set(A);
-  float dw[2][NU][U::E] = {};
-  U::stage(A, s_w);
-  for (int64_t t0 = (int64_t)blockIdx.x * A.tokens; t0 < A.n_tokens; t0 += (int64_t)gridDim.x * A.tokens) {
-    const int nt = (int)min((int64_t)A.tokens, A.n_tokens - t0), total = nt * A.H;
+  typename U::Half2 w[NU], dw[BWD ? NU : 1] = {};
+  if (BWD) u.weights(A.weight[role], w);
+  Place place;
+  uint8_t* out = nullptr;  // where this lane's head goes
+  // a token, or a tensor of it, begins
+  auto enter = [&](bool token) {
+    if (token) {
+      int pos = 0;
+      if constexpr (MODE == kAppend) {
+        place.next(A, at.t, lane);
+        pos = place.pos;
+      }
+      if (A.positions) pos = __ldg(A.positions + at.t);
+      __syncwarp();  // the last token's angles have been read
+      U::table(A, tab, pos, s_cs);
+      __syncwarp();
+    }
+    if (!BWD && at.g < 2) u.weights(A.weight[at.g], w);
+    out = A.dst[at.g] + (MODE == kAppend && at.g > 0 ? place.row : at.t) * A.dst_stride[at.g] + (int64_t)at.h * A.d * (int)sizeof(T);
+  };
+  if (count > 0) enter(true);
+  for (int k = 0; k < count; ++k) {
+    const int g = at.g;
+    const bool some = at.h < A.heads[g];
     typename U::Row x, dy;
-    int tok, hd;
-    auto load = [&](int i0) {
-      const int i = i0 + (threadIdx.x >> A.log_l);
-      tok = -1;
-      if (i >= total) return;
-      tok = token_of(A, i);
-      hd = i - tok * A.H;
-      const int g = hd >= A.heads[0], h = hd - (g ? A.heads[0] : 0);
-      u.load(reinterpret_cast<const T*>(A.src[g] + (t0 + tok) * A.src_stride[g]) + (int64_t)h * A.d, x);
-      u.load(reinterpret_cast<const T*>(A.dy[g] + (t0 + tok) * A.dy_stride[g]) + (int64_t)h * A.d, dy);
-    };
-    auto finish = [&]() {
-      const bool some = tok >= 0;
-      const int g = some && hd >= A.heads[0];
-      float ss = 0.f, sg = 0.f;
-      float gr[NU][U::E];  // R' dy
-      if (some) {
+    if constexpr (W > 1) {
+      copy_wait<S - 1>();
+      U::take(mine + lane * 16 + slot * SLOT, x);
+      if (BWD) U::take(mine + lane * 16 + slot * SLOT + U::V * 512, dy);
+    } else {
+      u.load(reinterpret_cast<const T*>(head(A.src[g], A.src_stride[g], at)), some, x);
+      if (BWD) u.load(reinterpret_cast<const T*>(head(A.dy[g], A.dy_stride[g], at)), some, dy);
+    }
+    uint64_t sa = 0, sb = 0, ga = 0, gb = 0;
+    typename U::Half2 gr[BWD ? NU : 1];  // R' dy
 #pragma unroll
-        for (int j = 0; j < NU; ++j) {
-          float v[U::E], w[U::E];
-          u.get(x, j, v);
-          u.get(dy, j, gr[j]);
-          if (u.turn[j]) {
-            float2 cs[U::PP];
-            u.angles(A, s_cs + tok * half, j, cs);
-            U::turn_pairs(gr[j], cs, true);
-          }
-          u.weights(A, s_w, g, j, w);
-          float s2[2] = {0.f, 0.f}, g2[2] = {0.f, 0.f};
+    for (int j = 0; j < NU; ++j) {
+      const typename U::Half2 v = U::get(x, j);
+      if (BWD) {
+        gr[j] = U::get(dy, j);
+        if (u.turn[j]) u.rotate(A, s_cs, j, gr[j], true);
+      }
 #pragma unroll
-          for (int e = 0; e < U::E; ++e) {
-            s2[e & 1] = fmaf(v[e], v[e], s2[e & 1]);
-            g2[e & 1] = fmaf(gr[j][e] * w[e], v[e], g2[e & 1]);
-          }
-          ss += s2[0] + s2[1];
-          sg += g2[0] + g2[1];
+      for (int m = 0; m < U::NP; ++m) {
+        sa = f32x2_fma(v.a[m], v.a[m], sa);
+        sb = f32x2_fma(v.b[m], v.b[m], sb);
+        if (BWD) {
+          ga = f32x2_fma(f32x2_mul(gr[j].a[m], w[j].a[m]), v.a[m], ga);
+          gb = f32x2_fma(f32x2_mul(gr[j].b[m], w[j].b[m]), v.b[m], gb);
         }
       }
-      ss = lanes_sum(ss, A.log_l);
-      sg = lanes_sum(sg, A.log_l);
-      if (!some) return;
-      const float rms = rsqrtf(fmaf(ss, A.inv_d, A.eps)), mean = rms * (sg * A.inv_d);
+    }
+    float sums[2] = {f32x2_sum(f32x2_add(sa, sb)), BWD ? f32x2_sum(f32x2_add(ga, gb)) : 0.f};
+    lanes_sum<BWD ? 2 : 1>(sums, A.log_l);
+    if constexpr (W > 1) {  // x and dy have been read
+      copy(slot);
+      slot = slot + 1 == S ? 0 : slot + 1;
+    }
+    const float r = rsqrtf(fmaf(sums[0], A.inv_d, A.eps));
+    const uint64_t rms = f32x2_both(r);
+    if (BWD) {
+      const uint64_t mean = f32x2_both(-(r * (sums[1] * A.inv_d)));
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
-        float v[U::E], w[U::E];
-        u.get(x, j, v);
-        u.weights(A, s_w, g, j, w);
+        typename U::Half2 v = U::get(x, j);
+        auto one = [&](uint64_t& x2, uint64_t g2, uint64_t w2, uint64_t& dw2) {
+          const uint64_t xh = f32x2_mul(x2, rms);
+          if (some) dw2 = f32x2_fma(g2, xh, dw2);
+          x2 = f32x2_mul(f32x2_fma(xh, mean, f32x2_mul(g2, w2)), rms);
+        };
 #pragma unroll
-        for (int e = 0; e < U::E; ++e) {
-          const float xh = v[e] * rms, add = gr[j][e] * xh;
-          if (g) dw[1][j][e] += add;
-          else dw[0][j][e] += add;
-          v[e] = rms * (gr[j][e] * w[e] - xh * mean);
+        for (int m = 0; m < U::NP; ++m) {
+          one(v.a[m], gr[j].a[m], w[j].a[m], dw[j].a[m]);
+          one(v.b[m], gr[j].b[m], w[j].b[m], dw[j].b[m]);
         }
-        u.put(dy, j, v);
+        U::put(x, j, v);
       }
-      u.store(reinterpret_cast<T*>(A.dst[g] + (t0 + tok) * A.dst_stride[g]) + (int64_t)(hd - (g ? A.heads[0] : 0)) * A.d, dy);
-    };
-    load(0);
-    if ((int)threadIdx.x < nt) s_pos[threadIdx.x] = A.positions ? __ldg(A.positions + t0 + threadIdx.x) : 0;
-    __syncthreads();
-    U::table(A, tab, s_pos, nt, s_cs);
-    __syncthreads();
-    finish();
-    for (int i0 = each; i0 < total; i0 += each) {
-      load(i0);
-      finish();
-    }
-    __syncthreads();  // the next step's positions and table
-  }
-  // the CTA's sums: over the heads of a warp by shuffles, then over the warps in order
-  float* s_red = reinterpret_cast<float*>(smem);  // [warps][2][d]
-  __syncthreads();
+      if (some) u.store(reinterpret_cast<T*>(out), x);
+    } else {
+      if (g < 2) {
 #pragma unroll
-  for (int g = 0; g < 2; ++g)
+        for (int j = 0; j < NU; ++j) {
+          typename U::Half2 v = U::get(x, j);
+#pragma unroll
+          for (int m = 0; m < U::NP; ++m) {
+            v.a[m] = f32x2_mul(f32x2_mul(v.a[m], rms), w[j].a[m]);
+            v.b[m] = f32x2_mul(f32x2_mul(v.b[m], rms), w[j].b[m]);
+          }
+          if (u.turn[j]) u.rotate(A, s_cs, j, v, false);
+          U::put(x, j, v);
+        }
+      }
+      const bool there = MODE != kAppend || (place.live && (g == 0 || place.row >= 0));
+      if (some && there) u.store(reinterpret_cast<T*>(out), x);
+    }
+    at.h += heads;
+    out += stride;
+    if (++at.piece == at.edge && k + 1 < count) {
+      const bool token = at.piece == n_pieces;
+      if (token) {
+        at.piece = 0;
+        ++at.t;
+      }
+      settle(at);
+      enter(token);
+    }
+  }
+  if constexpr (W > 1) copy_wait<0>();
+  if constexpr (BWD) {
+    // the CTA's sums: over the heads of a warp by shuffles, then over the warps in order
+    float* s_red = reinterpret_cast<float*>(smem);  // [warps][d]
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < NU; ++j)
 #pragma unroll
-      for (int e = 0; e < U::E; ++e) {
-        float v = dw[g][j][e];
-        for (int o = 1 << A.log_l; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        const int p = u.place(j, e);
-        if (p >= 0 && (threadIdx.x & 31) < (1 << A.log_l)) s_red[((threadIdx.x >> 5) * 2 + g) * A.d + p] = v;
-      }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * A.d; i += kThreads) {
-    float v = 0.f;
+      for (int m = 0; m < U::NP; ++m) {
+        float v[4];
+        f32x2_unpack(dw[j].a[m], v[0], v[1]);
+        f32x2_unpack(dw[j].b[m], v[2], v[3]);
+        const typename U::Places p = U::places(u.off[j], u.turn[j], m, u.half, A.d);
+        const int to[4] = {p.a0, p.a1, p.b0, p.b1};
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) v += s_red[w * 2 * A.d + i];
-    A.part[(int64_t)blockIdx.x * 2 * A.d + i] = v;
+        for (int e = 0; e < 4; ++e) {
+          for (int o = 1 << A.log_l; o < 32; o <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
+          if (u.unit[j] >= 0 && to[e] >= 0 && lane < (1 << A.log_l)) s_red[warp * A.d + to[e]] = v[e];
+        }
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < A.d; i += kThreads) {
+      float v = 0.f;
+#pragma unroll
+      for (int y = 0; y < kWarps; ++y) v += s_red[y * A.d + i];
+      A.part[(int64_t)blockIdx.x * A.d + i] = v;
+    }
   }
 }
 
-// dw from the CTAs' sums, always in the same order: 32 columns a block, 32 slices of the CTAs.
-__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int n, int d, float* dqw, float* dkw) {
+// dw from the CTAs' sums, always in the same order: 32 columns a block, 32 slices of the CTAs; q, then k.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int nq, int nk, int d, float* dqw, float* dkw) {
   __shared__ float s[32][33];
   const int c = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
+  float* out = blockIdx.y ? dkw : dqw;
+  if (!out) return;
+  const int n = blockIdx.y ? nk : nq;
+  if (blockIdx.y) part += (int64_t)nq * d;
   float v = 0.f;
-  if (col < 2 * d) {
+  if (col < d) {
 #pragma unroll 4
-    for (int i = y; i < n; i += 32) v += __ldg(part + (int64_t)i * 2 * d + col);
+    for (int i = y; i < n; i += 32) v += __ldg(part + (int64_t)i * d + col);
   }
   s[y][c] = v;
   __syncthreads();
-  if (y == 0 && col < 2 * d) {
+  if (y == 0 && col < d) {
     v = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) v += s[i][c];
-    float* out = col < d ? dqw : dkw;
-    if (out) out[col < d ? col : col - d] = v;
+    out[col] = v;
   }
 }
 
-// Shape of a launch: vectors, units, lanes and tokens of a CTA. False: more heads than a CTA can number.
-bool set_shape(NormArgs& a, int size, bool interleaved, bool backward, bool& wide, int& nu, size_t& smem) {
+// Shape of a launch: vectors, units and lanes, the pieces of a token, and the shared memory of a warp.
+void set_shape(NormArgs& a, int size, bool interleaved, bool backward, int& nu) {
   const int W = 16 / size;
   // 16-byte vectors when every vector lies whole on one side of each border and starts on a 16-byte
   // boundary; else element by element
-  wide = a.d % W == 0 && (interleaved ? a.rot % W == 0 : (a.rot / 2) % W == 0);
+  bool wide = a.d % W == 0 && (interleaved ? a.rot % W == 0 : (a.rot / 2) % W == 0);
   for (int g = 0; g < 3; ++g)
     if (a.heads[g]) {
       wide = wide && !(((uintptr_t)a.src[g] | (uintptr_t)a.dst[g] | (uint64_t)a.src_stride[g] | (uint64_t)a.dst_stride[g]) & 15);
@@ -491,67 +601,64 @@ bool set_shape(NormArgs& a, int size, bool interleaved, bool backward, bool& wid
   a.units = a.rot_units + (a.d - a.rot + wi - 1) / wi;
   a.log_l = 0;
   while (a.log_l < 5 && (1 << a.log_l) < a.units) ++a.log_l;
-  nu = wide ? (a.units <= 32 ? 1 : 4) : 16;
-  if (nu == 16) a.log_l = 5;
-  a.H = a.heads[0] + a.heads[1] + a.heads[2];
-  int l = 0;
-  while (((int64_t)1 << l) < a.H) ++l;
-  a.h_mul = (uint32_t)((((uint64_t)1 << (31 + l)) + a.H - 1) / a.H);  // exact for rows below 2^31
-  a.h_shift = l - 1;
-  a.inv_d = 1.f / (float)a.d;
-  // Tokens of a CTA (or step): the number whose heads fill its rounds best, the larger of two as good, while
-  // two CTAs are left to every SM; more than one round only where six are.
-  const int64_t round = (int64_t)(kThreads >> a.log_l) * (!backward && nu == 1 ? 2 : 1);
-  int tokens = 1;
-  double best = 0;
-  const int most = backward ? 8 : 2;  // rounds
-  for (int t = 1; t <= kMaxTokens; ++t) {
-    const int64_t rounds = cdiv((int64_t)t * a.H, round);
-    if (t > 1 && (rounds > most || a.n_tokens < (int64_t)t * 152 * (rounds > 1 ? 6 : 2))) break;
-    const double fill = (double)((int64_t)t * a.H) / (double)(rounds * round);
-    if (fill >= best) {
-      best = fill;
-      tokens = t;
-    }
+  nu = !wide ? 16 : (a.units <= 32 ? 1 : (size == 2 ? kMany<__nv_bfloat16> : kMany<float>));
+  if (wide && interleaved && size == 2 && a.units > 8 && a.log_l > 0) {
+    nu = 2;
+    a.log_l -= a.units <= 32;
   }
-  a.tokens = tokens;
-  a.w_at = (tokens * (a.rot / 2) * (int)sizeof(float2) + 15) & ~15;
-  smem = a.w_at + (wide ? (size_t)2 * a.units * wi * (interleaved ? 1 : 2) * sizeof(float) : 0);
-  if (backward) smem = std::max(smem, (size_t)(kThreads / 32) * 2 * a.d * sizeof(float));
-  return cdiv(a.n_tokens, tokens) <= INT32_MAX && (int64_t)tokens * a.H <= INT32_MAX / 2;
+  if (!wide) a.log_l = 5;
+  for (int g = 0; g < 3; ++g) a.pieces[g] = (int)cdiv(a.heads[g], 32 >> a.log_l);
+  a.inv_d = 1.f / (float)a.d;
+  const int slots = !wide ? 0 : (nu <= 2 ? kSlots<1> : kSlots<4>);
+  a.warp_bytes = slots * nu * (interleaved ? 1 : 2) * 512 * (backward ? 2 : 1) + ((a.rot / 2 * (int)sizeof(float2) + 15) & ~15);
 }
 
-template <typename T, bool APPEND>
-sta_status launch_norm(NormArgs& a, const RopeTable& tab, bool il, cudaStream_t st) {
+template <typename T, int MODE>
+sta_status launch_norm(NormArgs& a, const RopeTable& tab, bool il, cudaStream_t st, int* ctas = nullptr) {
   constexpr int W = 16 / (int)sizeof(T);
-  bool wide;
   int nu;
-  size_t smem;
-  if (!set_shape(a, (int)sizeof(T), il, false, wide, nu, smem)) return STA_ERR_INVALID_ARG;
-  const unsigned blocks = (unsigned)cdiv(a.n_tokens, a.tokens);
-  auto go = [&](auto kern) { kern<<<blocks, kThreads, smem, st>>>(a, tab); };
-  if (nu == 1) il ? go(norm_rope_kernel<T, W, true, 1, APPEND>) : go(norm_rope_kernel<T, W, false, 1, APPEND>);
-  else if (nu == 4) il ? go(norm_rope_kernel<T, W, true, kMany<T>, APPEND>) : go(norm_rope_kernel<T, W, false, kMany<T>, APPEND>);
-  else il ? go(norm_rope_kernel<T, 1, true, 16, APPEND>) : go(norm_rope_kernel<T, 1, false, 16, APPEND>);
-  STA_LAUNCH_CHECK();
-  return STA_OK;
+  set_shape(a, (int)sizeof(T), il, MODE == kBackward, nu);
+  const int64_t H = MODE == kAppend ? 3 : 2;
+  int64_t pieces = 0;
+  for (int g = 0; g < H; ++g) pieces += a.pieces[g];
+  size_t smem = (size_t)kWarps * a.warp_bytes;
+  unsigned grid;
+  if (MODE == kBackward) {
+    // CTAs by the heads of q and k, one a tensor at least, and none without a piece for each of its warps
+    const int most = nu * (il ? 1 : 2) <= 2 ? kMaxGrid : kMaxGrid / 2;
+    int n[2];
+    for (int g = 0; g < 2; ++g) {
+      int64_t share = (int64_t)(most * (double)a.pieces[g] / (double)pieces + 0.5);
+      share = std::max<int64_t>(1, a.pieces[1 - g] ? std::min<int64_t>(share, most - 1) : share);
+      n[g] = a.pieces[g] ? (int)std::min(share, cdiv(a.n_tokens * a.pieces[g], kWarps)) : 0;
+    }
+    a.ctas_q = n[0];
+    ctas[0] = n[0];
+    ctas[1] = n[1];
+    grid = (unsigned)(n[0] + n[1]);
+    smem = std::max(smem, (size_t)kWarps * a.d * sizeof(float));
+  } else {
+    grid = (unsigned)std::min<int64_t>(152 * (nu * (il ? 1 : 2) <= 2 ? 3 : 1), cdiv(a.n_tokens * pieces, kWarps));
+  }
+  if (a.n_tokens * pieces / ((int64_t)grid * kWarps) >= INT32_MAX) return STA_ERR_INVALID_ARG;
+  auto go = [&](auto kern) -> sta_status {
+    if (smem > 48 * 1024) STA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    kern<<<grid, kThreads, smem, st>>>(a, tab);
+    STA_LAUNCH_CHECK();
+    return STA_OK;
+  };
+  if (nu == 1) return il ? go(norm_rope_kernel<T, W, true, 1, MODE>) : go(norm_rope_kernel<T, W, false, 1, MODE>);
+  if (nu == 16) return il ? go(norm_rope_kernel<T, 1, true, 16, MODE>) : go(norm_rope_kernel<T, 1, false, 16, MODE>);
+  return il ? go(norm_rope_kernel<T, W, true, kMany<T>, MODE>) : go(norm_rope_kernel<T, W, false, kMany<T>, MODE>);
 }
 
 template <typename T>
 sta_status launch_bwd(NormArgs& a, const RopeTable& tab, bool il, float* dqw, float* dkw, cudaStream_t st) {
-  constexpr int W = 16 / (int)sizeof(T);
-  bool wide;
-  int nu;
-  size_t smem;
-  if (!set_shape(a, (int)sizeof(T), il, true, wide, nu, smem)) return STA_ERR_INVALID_ARG;
-  const unsigned blocks = (unsigned)std::min<int64_t>(kMaxGrid, cdiv(a.n_tokens, a.tokens));
-  auto go = [&](auto kern) { kern<<<blocks, kThreads, smem, st>>>(a, tab); };
-  if (nu == 1) il ? go(norm_rope_bwd_kernel<T, W, true, 1>) : go(norm_rope_bwd_kernel<T, W, false, 1>);
-  else if (nu == 4) il ? go(norm_rope_bwd_kernel<T, W, true, kMany<T>>) : go(norm_rope_bwd_kernel<T, W, false, kMany<T>>);
-  else il ? go(norm_rope_bwd_kernel<T, 1, true, 16>) : go(norm_rope_bwd_kernel<T, 1, false, 16>);
-  STA_LAUNCH_CHECK();
+  int ctas[2];
+  const sta_status status = launch_norm<T, kBackward>(a, tab, il, st, ctas);
+  if (status != STA_OK) return status;
   if (dqw || dkw) {
-    norm_dw_kernel<<<(unsigned)cdiv(2 * a.d, 32), 1024, 0, st>>>(a.part, (int)blocks, a.d, dqw, dkw);
+    norm_dw_kernel<<<dim3((unsigned)cdiv(a.d, 32), 2), 1024, 0, st>>>(a.part, ctas[0], ctas[1], a.d, dqw, dkw);
     STA_LAUNCH_CHECK();
   }
   return STA_OK;
@@ -610,8 +717,8 @@ extern "C" sta_status sta_norm_rope(const void* q, const void* k, int64_t q_stri
   a.eps = eps;
   a.positions = rope ? positions_dev : nullptr;
   const bool il = rope && rope->layout == STA_ROPE_INTERLEAVED;
-  return dtype == STA_BF16 ? launch_norm<__nv_bfloat16, false>(a, tab, il, (cudaStream_t)stream)
-                           : launch_norm<float, false>(a, tab, il, (cudaStream_t)stream);
+  return dtype == STA_BF16 ? launch_norm<__nv_bfloat16, kForward>(a, tab, il, (cudaStream_t)stream)
+                           : launch_norm<float, kForward>(a, tab, il, (cudaStream_t)stream);
 }
 
 extern "C" sta_status sta_norm_rope_bwd(const void* dq_out, const void* dk_out, int64_t dq_out_stride,
@@ -638,7 +745,7 @@ extern "C" sta_status sta_norm_rope_bwd(const void* dq_out, const void* dk_out, 
     if (heads[g] == 0 && (src[g] || dst[g] || dy[g] || dw[g])) return STA_ERR_INVALID_ARG;
     if (heads[g] && (ss[g] < row || ds[g] < row || ys[g] < row)) return STA_ERR_INVALID_ARG;
   }
-  const size_t need = (size_t)kMaxGrid * 2 * d * sizeof(float);
+  const size_t need = (size_t)kMaxGrid * d * sizeof(float);
   if (!workspace) {
     *workspace_bytes = need;
     return STA_OK;
@@ -673,7 +780,7 @@ extern "C" sta_status sta_norm_rope_bwd(const void* dq_out, const void* dk_out, 
   const cudaStream_t s = (cudaStream_t)stream;
   if (n_tokens == 0) {  // no rows: the weights' gradients are 0
     if (dq_weight || dk_weight) {
-      norm_dw_kernel<<<(unsigned)cdiv(2 * d, 32), 1024, 0, s>>>(a.part, 0, d, dq_weight, dk_weight);
+      norm_dw_kernel<<<dim3((unsigned)cdiv(d, 32), 2), 1024, 0, s>>>(a.part, 0, 0, d, dq_weight, dk_weight);
       STA_LAUNCH_CHECK();
     }
     return STA_OK;
@@ -742,5 +849,5 @@ extern "C" sta_status sta_norm_rope_append_paged(const void* q, const void* k, c
   a.page_size = page_size;
   a.n_pages = n_pages;
   a.err = device_error_word();
-  return launch_norm<__nv_bfloat16, true>(a, tab, rope && rope->layout == STA_ROPE_INTERLEAVED, (cudaStream_t)stream);
+  return launch_norm<__nv_bfloat16, kAppend>(a, tab, rope && rope->layout == STA_ROPE_INTERLEAVED, (cudaStream_t)stream);
 }
