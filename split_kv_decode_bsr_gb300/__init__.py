@@ -24,6 +24,7 @@ from __future__ import annotations
 import contextlib
 import ctypes as C
 import functools
+import importlib
 import math
 import os
 import threading
@@ -87,6 +88,7 @@ class _RopeParams(C.Structure):
 
 _lock = threading.Lock()
 _lib_handle = None
+_bound_calls = None  # csrc/bind.cpp, once a call of it is made
 
 
 def lib():
@@ -723,6 +725,7 @@ class Rope:
         self.struct = _RopeParams(int(rot_dim), STA_ROPE_INTERLEAVED if interleaved else STA_ROPE_HALF, kind,
                                   float(mscale), float(base), float(factor), float(orig_len), float(low_turns),
                                   float(high_turns), C.cast(self._freqs, C.c_void_p) if self._freqs else None)
+        self.at = C.addressof(self.struct)
 
 
 def _heads_view(t: torch.Tensor, what: str):
@@ -769,53 +772,21 @@ def sta_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope, transpose: bo
     return y
 
 
-def _heads(x: Optional[torch.Tensor], what: str, dev: torch.device, n: int, d: int, dtype: torch.dtype):
-    """An optional [n, H, d] tensor of heads: its address, H and token stride."""
-    if x is None:
-        return None, 0, 0
-    stride = _heads_view(x, what)
-    if not (x.shape[0] == n and x.shape[2] == d and x.dtype is dtype and x.device == dev):
-        raise ValueError(f"{what}: [{n}, heads, {d}] {dtype} on {dev}")
-    return x.data_ptr(), x.shape[1], stride
-
-
-def _norm_weight(w: Optional[torch.Tensor], what: str, dev: torch.device, d: int):
-    if w is None:
-        return None
-    if not (w.dtype is torch.float32 and w.shape == (d,) and w.is_contiguous() and w.device == dev):
-        raise ValueError(f"{what}: contiguous float32 [{d}] on {dev}")
-    return w.data_ptr()
-
-
-def _norm_of(q, k, positions, rope):
-    """What the calls with a norm share: device, tokens, head size, dtype, and the positions' address."""
-    x = q if q is not None else k
-    if x is None or x.dim() != 3:
-        raise ValueError("q or k: [tokens, heads, d]")
-    n, _, d = x.shape
-    dev = x.device
-    _on(dev)
-    if rope is not None:
-        if positions is None:
-            raise ValueError("positions: one a token")
-        _i32(dev, positions=positions)
-        if positions.shape != (n,):
-            raise ValueError("positions: one a token")
-    return dev, n, d, x.dtype, _dtype_code(x.dtype), None if rope is None else positions.data_ptr()
-
-
-def _result(given: Optional[torch.Tensor], x: Optional[torch.Tensor], what: str):
-    """Where a result shaped like x goes: `given`, or a new contiguous tensor. Its token stride too."""
-    if x is None:
-        if given is not None:
-            raise ValueError(f"{what}: nothing to write there")
-        return None, None, 0
-    if given is None:
-        given = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        return given, given.data_ptr(), x.shape[1] * x.shape[2]
-    if not (given.shape == x.shape and given.dtype is x.dtype and given.device == x.device):
-        raise ValueError(f"{what}: the shape, dtype and device of what it is for")
-    return given, given.data_ptr(), _heads_view(given, what)
+def _bound(call: str, stream, tensor, *args):
+    """A call of csrc/bind.cpp, which checks, allocates and launches on the tensors' device and the current stream."""
+    global _bound_calls
+    if _bound_calls is None:
+        if not os.path.exists(os.path.join(_HERE, "_bind.so")):
+            raise RuntimeError("_bind.so not built; run split_kv_decode_bsr_gb300.build.build()")
+        _bound_calls = importlib.import_module("._bind", __name__)
+    call = getattr(_bound_calls, call)
+    if stream is None or tensor is None or not tensor.is_cuda:
+        return call(*args)
+    ctx = _Launch(tensor.device, stream)
+    try:
+        return call(*args)
+    finally:
+        ctx.leave()
 
 
 def sta_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
@@ -827,21 +798,8 @@ def sta_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], position
     None: the other alone. rope None: normed alone. q_out / k_out may be q / k (in place). Returns
     (q_out, k_out), new [n, H, d] tensors where none are given.
     """
-    dev, n, d, dtype, code, pos = _norm_of(q, k, positions, rope)
-    qa, Hq, qs = _heads(q, "q", dev, n, d, dtype)
-    ka, Hk, ks = _heads(k, "k", dev, n, d, dtype)
-    qw, kw = _norm_weight(q_weight, "q_weight", dev, d), _norm_weight(k_weight, "k_weight", dev, d)
-    st, ctx = _enter(dev, stream)
-    try:
-        q_out, qo, qos = _result(q_out, q, "q_out")
-        k_out, ko, kos = _result(k_out, k, "k_out")
-        _check("sta_norm_rope", (_lib_handle or lib()).sta_norm_rope(
-            qa, ka, qs, ks, qo, ko, qos, kos, qw, kw, eps, pos, C.byref(rope.struct) if rope is not None else None, n, Hq,
-            Hk, d, code, st))
-    finally:
-        if ctx is not None:
-            ctx.leave()
-    return q_out, k_out
+    return _bound("norm_rope", stream, q if q is not None else k, q, k, positions, 0 if rope is None else rope.at, q_weight,
+                  k_weight, eps, q_out, k_out)
 
 
 def sta_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tensor], q: Optional[torch.Tensor],
@@ -855,39 +813,8 @@ def sta_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Ten
     views of one packed gradient. The weights' gradients are new float32 [d] tensors, also where a weight is None
     (that of a factor of 1); None where q or k is.
     """
-    dev, n, d, dtype, code, pos = _norm_of(q, k, positions, rope)
-    qa, Hq, qs = _heads(q, "q", dev, n, d, dtype)
-    ka, Hk, ks = _heads(k, "k", dev, n, d, dtype)
-    ya, Hy, ys = _heads(dq_out, "dq_out", dev, n, d, dtype)
-    za, Hz, zs = _heads(dk_out, "dk_out", dev, n, d, dtype)
-    if not (Hy == Hq and Hz == Hk):
-        raise ValueError("dq_out, dk_out: the shapes of q and k")
-    qw, kw = _norm_weight(q_weight, "q_weight", dev, d), _norm_weight(k_weight, "k_weight", dev, d)
-    st, ctx = _enter(dev, stream)
-    try:
-        dq, dqa, dqs = _result(dq, q, "dq")
-        dk, dka, dks = _result(dk, k, "dk")
-        dqw = torch.empty(d, dtype=torch.float32, device=dev) if q is not None else None
-        dkw = torch.empty(d, dtype=torch.float32, device=dev) if k is not None else None
-        ws = _workspace(_norm_bwd_ws(d), workspace, dev)
-        _check("sta_norm_rope_bwd", (_lib_handle or lib()).sta_norm_rope_bwd(
-            ya, za, ys, zs, qa, ka, qs, ks, dqa, dka, dqs, dks, qw, kw, _addr(dqw), _addr(dkw), eps, pos,
-            C.byref(rope.struct) if rope is not None else None, n, Hq, Hk, d, code, ws.data_ptr(),
-            C.byref(C.c_size_t(ws.numel())), st))
-    finally:
-        if ctx is not None:
-            ctx.leave()
-    return dq, dk, dqw, dkw
-
-
-@functools.lru_cache(maxsize=1024)
-def _norm_bwd_ws(d: int) -> int:
-    """Workspace size of sta_norm_rope_bwd (it depends on d alone)."""
-    n = C.c_size_t(0)
-    _check("sta_norm_rope_bwd", lib().sta_norm_rope_bwd(
-        None, None, d, 0, None, None, d, 0, None, None, d, 0, None, None, None, None, 1.0, None, None, 0, 1, 0, d, STA_BF16,
-        None, C.byref(n), None))
-    return int(n.value)
+    return _bound("norm_rope_bwd", stream, q if q is not None else k, dq_out, dk_out, q, k, positions,
+                  0 if rope is None else rope.at, q_weight, k_weight, eps, dq, dk, workspace)
 
 
 def sta_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
@@ -901,27 +828,6 @@ def sta_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
     kv_indptr[r+1] - kv_indptr[r] tokens (both int32, device). rope None: nothing turns. q None: keys
     and values only. Returns the turned q [n, Hq, d] (rows of a padded batch's padding unwritten).
     """
-    return _append_paged(None, q, k, v, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev, kv_indptr_dev, rope,
-                         positions, q_out, stream)
-
-
-def sta_norm_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
-                               v_pages: torch.Tensor, page_indptr_dev: torch.Tensor, page_indices_dev: torch.Tensor,
-                               q_indptr_dev: torch.Tensor, kv_indptr_dev: torch.Tensor, rope: Optional[Rope] = None,
-                               q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
-                               eps: float = 1e-6, positions: Optional[torch.Tensor] = None,
-                               q_out: Optional[torch.Tensor] = None, stream=None):
-    """sta_rope_append_paged with each head of q and k normed first (as in sta_norm_rope: weights float32
-    [d] or None, eps). rope None: normed alone. Returns the normed and turned q."""
-    d, dev = k.shape[-1], k.device
-    norm = (_norm_weight(q_weight, "q_weight", dev, d), _norm_weight(k_weight, "k_weight", dev, d), eps)
-    return _append_paged(norm, q, k, v, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev, kv_indptr_dev, rope,
-                         positions, q_out, stream)
-
-
-def _append_paged(norm, q, k, v, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev, kv_indptr_dev, rope,
-                  positions, q_out, stream):
-    """sta_rope_append_paged, or with norm (the weights' addresses and eps) sta_norm_rope_append_paged."""
     dev = k.device
     _on(dev, q, v, k_pages, v_pages, q_out)
     n_pages, page_size, Hkv, d = k_pages.shape
@@ -954,18 +860,26 @@ def _append_paged(norm, q, k, v, k_pages, v_pages, page_indptr_dev, page_indices
             q_out = None if q is None else torch.empty((n, Hq, d), dtype=q.dtype, device=dev)
         elif not (q is not None and q_out.shape == q.shape and q_out.is_contiguous()):
             raise ValueError("q_out: contiguous, q's shape")
-        h = _lib_handle or lib()
-        args = (_addr(q), _addr(k), _addr(v), qs, ks, vs, _addr(q_out), _addr(k_pages), _addr(v_pages), page_size, n_pages,
-                _addr(page_indptr_dev), _addr(page_indices_dev), _addr(q_indptr_dev), _addr(kv_indptr_dev), _addr(positions))
-        end = (C.byref(rope.struct) if rope is not None else None, n, n_req, Hq, Hkv, d, STA_BF16, st)
-        if norm is None:
-            _check("sta_rope_append_paged", h.sta_rope_append_paged(*args, *end))
-        else:
-            _check("sta_norm_rope_append_paged", h.sta_norm_rope_append_paged(*args, *norm, *end))
+        _check("sta_rope_append_paged", (_lib_handle or lib()).sta_rope_append_paged(
+            _addr(q), _addr(k), _addr(v), qs, ks, vs, _addr(q_out), _addr(k_pages), _addr(v_pages), page_size, n_pages,
+            _addr(page_indptr_dev), _addr(page_indices_dev), _addr(q_indptr_dev), _addr(kv_indptr_dev), _addr(positions),
+            C.byref(rope.struct) if rope is not None else None, n, n_req, Hq, Hkv, d, STA_BF16, st))
     finally:
         if ctx is not None:
             ctx.leave()
     return q_out
+
+
+def sta_norm_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
+                               v_pages: torch.Tensor, page_indptr_dev: torch.Tensor, page_indices_dev: torch.Tensor,
+                               q_indptr_dev: torch.Tensor, kv_indptr_dev: torch.Tensor, rope: Optional[Rope] = None,
+                               q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                               eps: float = 1e-6, positions: Optional[torch.Tensor] = None,
+                               q_out: Optional[torch.Tensor] = None, stream=None):
+    """sta_rope_append_paged with each head of q and k normed first (as in sta_norm_rope: weights float32
+    [d] or None, eps). rope None: normed alone. Returns the normed and turned q."""
+    return _bound("norm_rope_append_paged", stream, k, q, k, v, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev,
+                  kv_indptr_dev, 0 if rope is None else rope.at, q_weight, k_weight, eps, positions, q_out)
 
 
 def sta_chunk_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_indptr_dev: torch.Tensor,
@@ -981,32 +895,6 @@ def sta_chunk_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
     positions. Rows past q_indptr[n_req] are left as they are. Returns O [n, Hq, d] and LSE
     [n, Hq] float32 (-inf for a token that sees no key).
     """
-    return _chunk_fwd(None, q, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev, q_indptr_host, kv_indptr_dev,
-                      kv_indptr_host, scale, pattern, num_splits, o, lse, workspace, stream)
-
-
-def sta_prefix_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_indptr_dev: torch.Tensor,
-                         page_indices_dev: torch.Tensor, q_indptr_dev: torch.Tensor, q_indptr_host, kv_indptr_dev: torch.Tensor,
-                         kv_indptr_host, group_indptr_host, prefix_host, scale=None, num_splits: int = 0,
-                         o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                         workspace: Optional[torch.Tensor] = None, stream=None):
-    """sta_chunk_fwd_paged (causal) for requests that share their first pages, which are read and attended once
-    for all of a group.
-
-    Requests group_indptr[i] .. group_indptr[i+1]-1 share their first prefix[i] tokens (int32, host; whole pages,
-    0: none): their page lists start with the same prefix[i] / page_size pages, as sta_pages_fork leaves them, and
-    all of their new tokens lie behind them. Results are those of sta_chunk_fwd_paged up to rounding.
-    """
-    gh, last, keep_g = _host_i32(group_indptr_host, len(group_indptr_host), "group_indptr_host")
-    n_groups = len(group_indptr_host) - 1
-    ph, _, keep_p = _host_i32(prefix_host, n_groups, "prefix_host")
-    return _chunk_fwd((gh, ph, n_groups), q, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev, q_indptr_host,
-                      kv_indptr_dev, kv_indptr_host, scale, None, num_splits, o, lse, workspace, stream)
-
-
-def _chunk_fwd(groups, q, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev, q_indptr_host, kv_indptr_dev,
-               kv_indptr_host, scale, pattern, num_splits, o, lse, workspace, stream):
-    """sta_chunk_fwd_paged, or with groups (addresses of their requests and prefixes, their number) sta_prefix_fwd_paged."""
     qs = _heads_view(q, "q")
     n, Hq, d = q.shape
     dev = q.device
@@ -1038,30 +926,41 @@ def _chunk_fwd(groups, q, k_pages, v_pages, page_indptr_dev, page_indices_dev, q
         elif not (lse.shape == (n, Hq) and lse.dtype == torch.float32 and lse.is_contiguous()):
             raise ValueError("lse: contiguous float32 [n, Hq]")
         args = (q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), page_size, n_pages, page_indptr_dev.data_ptr(),
-                page_indices_dev.data_ptr() or None, q_indptr_dev.data_ptr(), qh, kv_indptr_dev.data_ptr(), kh, n_req)
-        if groups is None:
-            name, call = "sta_chunk_fwd_paged", h.sta_chunk_fwd_paged
-            args += (Hq, Hkv, d, _dtype_code(q.dtype), scale, pat, num_splits, o.data_ptr(), lse.data_ptr())
-        else:
-            name, call = "sta_prefix_fwd_paged", h.sta_prefix_fwd_paged
-            args += (*groups, Hq, Hkv, d, _dtype_code(q.dtype), scale, num_splits, o.data_ptr(), lse.data_ptr())
+                page_indices_dev.data_ptr() or None, q_indptr_dev.data_ptr(), qh, kv_indptr_dev.data_ptr(), kh, n_req, Hq, Hkv, d,
+                _dtype_code(q.dtype), scale, pat, num_splits, o.data_ptr(), lse.data_ptr())
         # Most calls cut nothing: they need the least size there is and use none of it. Few new tokens over many
         # cached ones are mostly cut, into no more than 32 pieces (64 single tokens: 48 us of host time a call,
         # 56 when it first asks). A call that needs more says how much.
         at, size = 256, C.c_size_t(256)
-        if workspace is not None or groups is not None or (rows <= 8 * n_req and keys >= 8192):
+        if workspace is not None or (rows <= 8 * n_req and keys >= 8192):
             guess = 256 if workspace is not None else max(256, min(32 * rows * Hq * (d + 2) * 4, 1 << 26))
             ws = _workspace(guess, workspace, dev)
             at, size.value = ws.data_ptr(), ws.numel()
-        status = call(*args, at, C.byref(size), st)
+        status = h.sta_chunk_fwd_paged(*args, at, C.byref(size), st)
         if status == STA_ERR_WORKSPACE:
             ws = _workspace(size.value, workspace, dev)
-            status = call(*args, ws.data_ptr(), C.byref(size), st)
-        _check(name, status)
+            status = h.sta_chunk_fwd_paged(*args, ws.data_ptr(), C.byref(size), st)
+        _check("sta_chunk_fwd_paged", status)
     finally:
         if ctx is not None:
             ctx.leave()
     return o, lse
+
+
+def sta_prefix_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_indptr_dev: torch.Tensor,
+                         page_indices_dev: torch.Tensor, q_indptr_dev: torch.Tensor, q_indptr_host, kv_indptr_dev: torch.Tensor,
+                         kv_indptr_host, group_indptr_host, prefix_host, scale=None, num_splits: int = 0,
+                         o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """sta_chunk_fwd_paged (causal) for requests that share their first pages, which are read and attended once
+    for all of a group.
+
+    Requests group_indptr[i] .. group_indptr[i+1]-1 share their first prefix[i] tokens (int32, host; whole pages,
+    0: none): their page lists start with the same prefix[i] / page_size pages, as sta_pages_fork leaves them, and
+    all of their new tokens lie behind them. Results are those of sta_chunk_fwd_paged up to rounding.
+    """
+    return _bound("prefix_fwd_paged", stream, q, q, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev,
+                  q_indptr_host, kv_indptr_dev, kv_indptr_host, group_indptr_host, prefix_host, scale, num_splits, o, lse, workspace)
 
 
 def chunk_workspace_bytes(q_indptr, kv_indptr, n_req: int, Hq: int, Hkv: int, d: int, page_size: int = 16,

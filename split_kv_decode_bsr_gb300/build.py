@@ -17,6 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsta.so")
+BIND = os.path.join(HERE, "_bind.so")  # some of the Python calls
 SOURCES = ["api.cu", "encode.cu", "mha_row.cu", "mha_block.cu", "decode.cu", "decode_noalloc.cu", "epilogue.cu", "validate.cu", "mla.cu",
            "diag.cu", "rope.cu", "norm_rope.cu", "chunk.cu", "pages.cu"]
 HEADERS = ["common.cuh", "internal.h", "ptx.cuh", "rope.inl"]
@@ -42,6 +43,23 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _bind_commands(obj: str, out: str):
+    """g++ commands for csrc/bind.cpp, against the installed torch and libsta.so beside it."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+           os.path.join(ROOT, "include")]
+    cc = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *[f"-I{i}" for i in inc], "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj]
+    ld = ["g++", "-shared", "-o", out, obj, f"-L{os.path.join(root, 'lib')}", f"-L{HERE}", "-l:libsta.so", "-lc10", "-lc10_cuda",
+          "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    return cc, ld
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "sta.h")]
@@ -51,6 +69,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         o = os.path.join(BUILD, src.replace(".cu", ".o"))
         if force or _stale(o, [s] + hdrs):
             jobs.append([nvcc(), *_flags(extra_flags), "-c", s, "-o", o])
+    bind_obj, bind_tmp = os.path.join(BUILD, "bind.o"), BIND + f".tmp{os.getpid()}"
+    cc, ld = _bind_commands(bind_obj, bind_tmp)
+    if force or _stale(bind_obj, [os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "sta.h")]):
+        jobs.append(cc)
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             res = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
@@ -58,7 +80,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             if verbose or r.returncode:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode:
-                raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
+                raise RuntimeError(f"compilation failed: {' '.join(cmd)}")
     objs = [os.path.join(BUILD, s.replace(".cu", ".o")) for s in SOURCES]
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
@@ -68,6 +90,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link of libsta.so failed")
         os.replace(tmp, LIB)
+    if force or cc in jobs or _stale(BIND, [bind_obj]):
+        r = subprocess.run(ld, capture_output=True, text=True)
+        if r.returncode:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("link of _bind.so failed")
+        os.replace(bind_tmp, BIND)
     return LIB
 
 

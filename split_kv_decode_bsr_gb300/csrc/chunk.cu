@@ -62,6 +62,8 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 struct ChunkArgs {
   __nv_bfloat16* o;  // [N, Hq, d]
   float* lse;        // [N, Hq] or null
+  const __nv_bfloat16* q;
+  int64_t q_stride;
   const __nv_bfloat16* k;
   const __nv_bfloat16* v;
   const int32_t* page_indptr;
@@ -91,6 +93,7 @@ template <int CAP, bool SHARED>
 struct Groups {};
 template <int CAP>
 struct Groups<CAP, true> {
+  int n_rows, row_ctas;  // the first ranks, of few rows, and the CTAs that do them, the grid's first
   int32_t skip[CAP];
   int16_t pre[CAP];  // -1: neither
   uint16_t end[CAP], lead[CAP];
@@ -396,6 +399,345 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int k0) {
   return (a <= 0 ? ~0u : ~0u << a) & (b >= 31 ? ~0u : (2u << b) - 1u);
 }
 
+// Few rows: the (at most 16) rows of a request's new tokens and a KV head, over a piece of its keys, by one warp and
+// mma.sync. Beside a shared prefix, whose rows fill the tensor cores' tiles, what a request has of its own is a short
+// list for each KV head: an item of it would take a CTA's 128-row tiles for 4 rows or so, and some 6 us between its
+// lookups, its loads, its one product and its result. Twelve warps a CTA hide that behind one another; each looks the
+// next piece up and begins to load it while it works on the present one. The first CTAs of the grid do nothing else,
+// beside those of the prefix.
+template <int D>
+struct RowCfg {
+  static constexpr int KEYS = 16;                  // of a tile
+  static constexpr int TILE = KEYS * D * 2;        // its K or its V, 16-byte blocks of a row swizzled by the row
+  static constexpr int STAGES = D == 128 ? 2 : 4;  // tiles of a warp
+  static constexpr int WARP = STAGES * 2 * TILE;
+  static constexpr int WARPS = kThreads / 32;
+  static_assert(WARPS * WARP + 16 <= Cfg<D>::SMEM, "beside the other CTAs' shared memory");
+};
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A piece: the rank's rows of a KV head, chunk c of its tiles (j0 .. j1 - 1).
+struct Piece {
+  int rank, hk, c;      // rank -1: none
+  int q0, n, pos0, len; // first row in q, new tokens, position of the first one, keys
+  int pb, pe;           // page list
+  int j0, j1;
+};
+
+template <int D, int CAP>
+__device__ __forceinline__ void few_rows(const ChunkArgs& A, const Plan<CAP, true>& P, int req0, uint8_t* smem) {
+  using C = RowCfg<D>;
+  constexpr int ST = C::STAGES, LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an instruction
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* counter = reinterpret_cast<int*>(smem + C::WARPS * C::WARP);
+  if (threadIdx.x == 0) *counter = 0;
+  __syncthreads();
+  const uint32_t mine = smem_u32(smem) + warp * C::WARP;
+  const int P0 = A.page_size, n_items = P.base[P.n_rows];
+  const int64_t row_elems = (int64_t)A.Hkv * D;
+  const bool one_page = P0 % C::KEYS == 0;  // (a prefix is whole pages, so that the rest starts with one)
+  auto page_no = [&](int tok) -> int { return A.page_shift < 0 ? tok : (int)(__umulhi((uint32_t)tok, A.page_mul) >> A.page_shift); };
+  const float c = A.scale_log2;
+
+  // The next piece's rank, head and chunk; a lane loads one of the six numbers that it goes by.
+  auto take = [&](Piece& p) -> int {
+    int x = 0;
+    if (lane == 0) x = atomicAdd(counter, 1);
+    x = __shfl_sync(0xffffffffu, x, 0);
+    const int64_t number = blockIdx.x + (int64_t)x * P.row_ctas;
+    p.rank = -1;
+    if (number >= n_items) return 0;
+    int lo = 0, hi = P.n_rows;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (P.base[mid] <= number) lo = mid;
+      else hi = mid;
+    }
+    const int y = (int)number - P.base[lo], ns = P.ns[lo], r = req0 + P.req[lo];
+    p.rank = lo;
+    p.hk = y / ns;
+    p.c = y - p.hk * ns;
+    const int32_t* from = lane < 2 ? A.q_indptr : (lane < 4 ? A.kv_indptr : A.page_indptr);
+    return lane < 6 ? __ldg(from + r + (lane & 1)) : 0;
+  };
+  auto settle = [&](Piece& p, int loaded) {
+    const int q0 = __shfl_sync(0xffffffffu, loaded, 0), q1 = __shfl_sync(0xffffffffu, loaded, 1);
+    int64_t len = (int64_t)__shfl_sync(0xffffffffu, loaded, 3) - __shfl_sync(0xffffffffu, loaded, 2);
+    p.pb = __shfl_sync(0xffffffffu, loaded, 4);
+    p.pe = __shfl_sync(0xffffffffu, loaded, 5);
+    p.n = p.j0 = p.j1 = 0;
+    if (p.rank < 0) return;
+    int n = q1 - q0;
+    int64_t pos0 = len - n;
+    if (n > P.qn[p.rank]) {
+      record_error(A.err, 0x606);
+      n = P.qn[p.rank];
+    }
+    if (q0 < 0 || n < 0 || q0 > A.N - n || len < 0 || len > INT32_MAX - 2 * kBN) {
+      record_error(A.err, 0x111);
+      return;
+    }
+    if (P.pre[p.rank] >= 0) {  // keys and positions counted from the prefix's end
+      const int skip = P.skip[p.rank];
+      if (n > 0 && pos0 < skip) record_error(A.err, 0x608);  // new tokens that are not behind the prefix
+      pos0 -= skip;
+      len = len > skip ? len - skip : 0;
+      p.pb += skip / P0;
+    }
+    p.q0 = q0;
+    p.n = n;
+    p.pos0 = (int)pos0;
+    p.len = (int)len;
+    if (n == 0) return;
+    const int nt = (p.len + C::KEYS - 1) / C::KEYS, ns = P.ns[p.rank];
+    p.j0 = (int)((int64_t)p.c * nt / ns);
+    p.j1 = (int)((int64_t)(p.c + 1) * nt / ns);
+  };
+
+  // What is being loaded: tile `at` up to `end` of a piece. A lane holds one entry of its page list, and one of the 32
+  // after them; -1 behind the list.
+  int at = 0, end = 0, l_len = 0, l_pb = 0, l_pe = 0, l_hk = 0, window = 0, pages = -1, later = -1;
+  auto entry = [&](int e) -> int {
+    const int o = l_pb + e;
+    return o >= 0 && o < l_pe && (int64_t)e * P0 < l_len && A.page_indices ? __ldg(A.page_indices + o) : -1;
+  };
+  auto begin = [&](const Piece& p) {
+    at = p.j0;
+    end = p.j1;
+    l_len = p.len;
+    l_pb = p.pb;
+    l_pe = p.pe;
+    l_hk = p.hk;
+    window = page_no(at * C::KEYS);
+    pages = at < end ? entry(window + lane) : -1;
+    later = at < end ? entry(window + 32 + lane) : -1;
+  };
+  uint32_t done = 0;  // tiles that have been worked on
+  int ahead = 0;      // tiles that are loaded or on their way
+  auto fill = [&]() {
+    while (ahead < ST && at < end) {
+      const uint32_t to = mine + (done + ahead) % ST * (2 * C::TILE);
+      const int first = page_no(at * C::KEYS);
+      if (first >= window + 32) {
+        window += 32;
+        pages = later;
+        later = entry(window + 32 + lane);
+      }
+      if (one_page) {  // the tile's rows follow one another
+        int page = __shfl_sync(0xffffffffu, pages, first - window);
+        if (page < 0 || page >= A.n_pages) {
+          record_error(A.err, 0x110);
+          page = 0;
+        }
+        const int m0 = lane / LPR, in = l_len - at * C::KEYS;
+        const int64_t off = ((int64_t)page * P0 + (at * C::KEYS - first * P0) + m0) * row_elems + l_hk * D + (lane % LPR) * 8;
+        const __nv_bfloat16 *k = A.k + off, *v = A.v + off;
+#pragma unroll
+        for (int i = 0; i < C::KEYS / RPI; ++i) {
+          const int m = i * RPI + m0;
+          const uint32_t dst = to + m * (D * 2) + (((lane % LPR) ^ (m & 7)) << 4);
+          cp_async16(dst, k, m < in);
+          cp_async16(dst + C::TILE, v, m < in);
+          k += RPI * row_elems;
+          v += RPI * row_elems;
+        }
+        cp_async_commit();
+        ++at;
+        ++ahead;
+        continue;
+      }
+      const int tok = at * C::KEYS + (lane & 15), no = page_no(tok);
+      const int near = __shfl_sync(0xffffffffu, pages, no - window), far = __shfl_sync(0xffffffffu, later, no - window - 32);
+      int page = no < window + 32 ? near : far, row = -1;  // behind the sequence: zeros
+      if (tok < l_len) {
+        if (page < 0 || page >= A.n_pages) {
+          record_error(A.err, 0x110);
+          page = 0;
+        }
+        row = page * P0 + tok - no * P0;
+      }
+#pragma unroll
+      for (int i = 0; i < C::KEYS / RPI; ++i) {
+        const int m = i * RPI + lane / LPR, ch = lane % LPR, from = __shfl_sync(0xffffffffu, row, m);
+        const int64_t off = (int64_t)max(from, 0) * row_elems + l_hk * D + ch * 8;
+        const uint32_t dst = to + m * (D * 2) + ((ch ^ (m & 7)) << 4);
+        cp_async16(dst, A.k + off, from >= 0);
+        cp_async16(dst + C::TILE, A.v + off, from >= 0);
+      }
+      cp_async_commit();
+      ++at;
+      ++ahead;
+    }
+  };
+
+  Piece p;
+  {
+    const int loaded = take(p);
+    settle(p, loaded);
+  }
+  begin(p);
+  fill();
+  while (p.rank >= 0) {
+    Piece q;
+    const int loaded = take(q);
+    bool looked_up = false;  // q has its places, and is what is being loaded
+    auto look_up = [&]() {
+      settle(q, loaded);
+      begin(q);
+      looked_up = true;
+    };
+    if (p.n > 0) {
+      // Q: this lane's rows lane / 4 and that + 8 (token, head of the group), zeros past the last
+      const int R = p.n * A.G, r0 = lane >> 2, r1 = r0 + 8, t0 = r0 / A.G, t1 = r1 / A.G;
+      const bool live0 = r0 < R, live1 = r1 < R;
+      uint32_t qa[D / 16][4];
+      {
+        auto q_row = [&](int r, int t) { return A.q + (int64_t)(p.q0 + t) * A.q_stride + (p.hk * A.G + r - t * A.G) * D; };
+        const __nv_bfloat16 *a0 = q_row(live0 ? r0 : 0, live0 ? t0 : 0), *a1 = q_row(live1 ? r1 : 0, live1 ? t1 : 0);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const int e = k * 16 + (lane & 3) * 2;
+          qa[k][0] = live0 ? __ldg(reinterpret_cast<const uint32_t*>(a0 + e)) : 0u;
+          qa[k][1] = live1 ? __ldg(reinterpret_cast<const uint32_t*>(a1 + e)) : 0u;
+          qa[k][2] = live0 ? __ldg(reinterpret_cast<const uint32_t*>(a0 + e + 8)) : 0u;
+          qa[k][3] = live1 ? __ldg(reinterpret_cast<const uint32_t*>(a1 + e + 8)) : 0u;
+        }
+      }
+      float o[D / 8][4];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+      const int mi = lane >> 3, mr = lane & 7;
+      for (int j = p.j0; j < p.j1; ++j) {
+        if (ahead == ST) cp_async_wait<ST - 1>();
+        else cp_async_wait<0>();
+        __syncwarp();
+        const uint32_t kt = mine + done % ST * (2 * C::TILE), vt = kt + C::TILE;
+        float s[2][4] = {}, s2[2][4] = {};  // (two short chains of products rather than one long)
+        {
+          const int row = mr + (mi >> 1) * 8;
+#pragma unroll
+          for (int k = 0; k < D / 16; k += 2) {
+            uint32_t b[4], b2[4];
+            ldsm_x4(kt + row * (D * 2) + (((2 * k + (mi & 1)) ^ (row & 7)) << 4), b);
+            ldsm_x4(kt + row * (D * 2) + (((2 * k + 2 + (mi & 1)) ^ (row & 7)) << 4), b2);
+            mma_bf16_16816(s[0], qa[k], b[0], b[1]);
+            mma_bf16_16816(s[1], qa[k], b[2], b[3]);
+            mma_bf16_16816(s2[0], qa[k + 1], b2[0], b2[1]);
+            mma_bf16_16816(s2[1], qa[k + 1], b2[2], b2[3]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[0][e] += s2[0][e];
+            s[1][e] += s2[1][e];
+          }
+        }
+        if (j * C::KEYS + C::KEYS - 1 > p.pos0) {  // keys that some row does not see
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = j * C::KEYS + b * 8 + (lane & 3) * 2 + (e & 1);
+              if (key > p.pos0 + (e < 2 ? t0 : t1)) s[b][e] = -INFINITY;
+            }
+        }
+        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])), x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
+          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
+        }
+        x0 *= c;
+        x1 *= c;
+        float a0 = 1.f, a1 = 1.f;
+        if (x0 > m0 + kRescaleThreshold) {
+          if (m0 != -INFINITY) a0 = ex2(m0 - x0);
+          m0 = x0;
+        }
+        if (x1 > m1 + kRescaleThreshold) {
+          if (m1 != -INFINITY) a1 = ex2(m1 - x1);
+          m1 = x1;
+        }
+        if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {
+          l0 *= a0;
+          l1 *= a1;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][0] *= a0;
+            o[i][1] *= a0;
+            o[i][2] *= a1;
+            o[i][3] *= a1;
+          }
+        }
+        const float n0 = m0 == -INFINITY ? 0.f : m0, n1 = m1 == -INFINITY ? 0.f : m1;
+        float w[2][4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          w[b][0] = ex2(fmaf(s[b][0], c, -n0));
+          w[b][1] = ex2(fmaf(s[b][1], c, -n0));
+          w[b][2] = ex2(fmaf(s[b][2], c, -n1));
+          w[b][3] = ex2(fmaf(s[b][3], c, -n1));
+          l0 += w[b][0] + w[b][1];
+          l1 += w[b][2] + w[b][3];
+        }
+        // P in bf16 for the product, off by 2^-8 at most; the sums take the fp32 values
+        const uint32_t pa[4] = {pack_bf16x2(w[0][0], w[0][1]), pack_bf16x2(w[0][2], w[0][3]), pack_bf16x2(w[1][0], w[1][1]),
+                                pack_bf16x2(w[1][2], w[1][3])};
+        {
+          const int row = mr + (mi & 1) * 8;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t b[4];
+            ldsm_x4_t(vt + row * (D * 2) + (((2 * i + (mi >> 1)) ^ (row & 7)) << 4), b);
+            mma_bf16_16816(o[2 * i], pa, b[0], b[1]);
+            mma_bf16_16816(o[2 * i + 1], pa, b[2], b[3]);
+          }
+        }
+        __syncwarp();  // the tile has been read by all lanes
+        ++done;
+        --ahead;
+        if (at == end && !looked_up) look_up();
+        fill();
+      }
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+      }
+      const bool part = P.ns[p.rank] > 1 || P.pre[p.rank] != -1;
+      auto result = [&](bool live, int r, int t, float m, float l, int e) {
+        if (!live) return;
+        const float inv = l != 0.f ? 1.f / l : 0.f;  // a NaN among the scores stays one
+        const float lse = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        const int h = p.hk * A.G + r - t * A.G;
+        if (part) {
+          const int64_t prow = P.part[p.rank] + ((int64_t)p.c * P.qn[p.rank] + t) * A.Hq + h;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<float2*>(A.part_o + prow * D + i * 8 + (lane & 3) * 2) = make_float2(o[i][e] * inv, o[i][e + 1] * inv);
+          if ((lane & 3) == 0) A.part_lse[prow] = lse == lse ? lse : INFINITY;  // the merge makes a NaN of it again
+        } else {
+          const int64_t row = (int64_t)(p.q0 + t) * A.Hq + h;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<uint32_t*>(A.o + row * D + i * 8 + (lane & 3) * 2) = pack_bf16x2(o[i][e] * inv, o[i][e + 1] * inv);
+          if ((lane & 3) == 0 && A.lse) A.lse[row] = lse;
+        }
+      };
+      result(live0, r0, t0, m0, l0, 0);
+      result(live1, r1, t1, m1, l1, 2);
+    }
+    if (!looked_up) look_up();
+    fill();
+    p = q;
+  }
+  cp_async_wait<0>();
+}
+
 template <int D, int CAP, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -410,6 +752,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (smem_u32(smem) & 1023) {  // swizzle atoms start on 1024-byte boundaries
     record_error(A.err, 0x607);
     return;
+  }
+  if constexpr (SHARED) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    if ((int)blockIdx.x < P.row_ctas) {
+      few_rows<D, CAP>(A, P, req0, smem);
+      return;
+    }
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
@@ -455,8 +804,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       bool ok = true;
       int item = blockIdx.x, k = 0, nq = 0;
+      int row = -1;  // the next of several items of a CTA of few rows that was taken over (it starts first: hardly ever)
+      if constexpr (SHARED) item += P.base[P.n_rows] - P.row_ctas;
       Item it;
-      for (int n = 0; ok && item >= 0; ++n) {
+      for (int n = 0; ok && item >= 0;) {
         if (get_item(A, P, req0, item, it)) {
           if (k >= 2) ok = mbar_wait(&sh.item_empty[k & 1], ((k >> 1) & 1u) ^ 1u, A.err, 0x62b);
           if (ok) {
@@ -480,9 +831,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = ok && mbar_wait(&sh.want, (k - 1) & 1u, A.err, 0x632);
         }
         if (!ok) break;
+        if constexpr (SHARED) {
+          if (row >= 0) {
+            item = row;
+            row += P.row_ctas;
+            if (row >= P.base[P.n_rows]) row = -1;
+            continue;
+          }
+        }
         clc_request(&sh.clc, &sh.clc_full);
         item = mbar_wait(&sh.clc_full, n & 1u, A.err, 0x62c) ? clc_answer(&sh.clc) : -1;
         fence_proxy_async_smem();  // the answer has been read before the next one is written
+        ++n;
+        if constexpr (SHARED) {
+          if (item >= P.row_ctas) item += P.base[P.n_rows] - P.row_ctas;
+          else if (item >= 0 && item + P.row_ctas < P.base[P.n_rows]) row = item + P.row_ctas;
+        }
       }
       if (ok && k >= 2) ok = mbar_wait(&sh.item_empty[k & 1], ((k >> 1) & 1u) ^ 1u, A.err, 0x62b);
       if (ok) {
@@ -529,10 +893,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         // while this tile's stage is waited for
         const int b = lane / C::KH, kh = lane % C::KH, off = b * A.box;
         const int boxes = kBN / A.box, box_shift = __ffs(A.box) - 1;  // (a power of 2)
-        int pg = nj > 0 && b < boxes ? page_at(it.tile(it.j0) * kBN + off) : -1;
+        // With a shared prefix, whose tiles come from memory rather than from L2, page numbers one tile ahead are a round
+        // trip to memory for each tile: there a lane holds one page number of the next 32 / boxes tiles, and the 32 after
+        // them are on their way (2.5 us a tile over pages of 16 otherwise, 1.5 so).
+        const int in_window = 32 / boxes;
+        auto window = [&](int i0) -> int {
+          const int t = i0 + lane / boxes;
+          return t < nj ? page_at(it.tile(it.j0 + t) * kBN + (lane & (boxes - 1)) * A.box) : -1;
+        };
+        int pg = -1, later = -1;
+        if constexpr (SHARED) {
+          pg = window(0);
+          later = window(in_window);
+        } else {
+          pg = nj > 0 && b < boxes ? page_at(it.tile(it.j0) * kBN + off) : -1;
+        }
         for (; i < nj; ++i) {
-          const int y = 2 * (T + i) + is_v, s = y % ST, tok0 = it.tile(it.j0 + i) * kBN, page = pg;
-          if (i + 1 < nj && b < boxes) pg = page_at(it.tile(it.j0 + i + 1) * kBN + off);
+          const int y = 2 * (T + i) + is_v, s = y % ST, tok0 = it.tile(it.j0 + i) * kBN;
+          int page = pg;
+          if constexpr (SHARED) {
+            const int at = i & (in_window - 1);
+            if (i > 0 && at == 0) {
+              pg = later;
+              later = window(i + in_window);
+            }
+            page = __shfl_sync(0xffffffffu, pg, at * boxes + min(b, boxes - 1));
+          } else {
+            if (i + 1 < nj && b < boxes) pg = page_at(it.tile(it.j0 + i + 1) * kBN + off);
+          }
           const int in = min(boxes, (it.len - tok0 + A.box - 1) >> box_shift);  // boxes with tokens
           const bool tail_v = is_v && tok0 + kBN > it.len;                 // rows behind the sequence
           if (i > 0 && i == ask && lane == 0) mbar_arrive(&sh.want);
@@ -999,35 +1387,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// merge_row over two lists of partials: na of them at row a, `astride` rows apart, then nb at row b.
+// merge_row over two lists of partials: na of them at row a, `astride` rows apart, then nb at row b. The LSEs of 32 and the
+// values of 8 are on their way at once, the first of both before the maximum is known.
 template <int E>
 __device__ __forceinline__ float merge_two(const float* po, const float* pl, int d, int64_t a, size_t astride, int na, int64_t b,
                                            size_t bstride, int nb, int lane, float* out) {
+  constexpr int U = 8;
   const int s = na + nb;
   auto at = [&](int i) { return i < na ? a + (int64_t)(i * astride) : b + (int64_t)((i - na) * bstride); };
-  float M = -INFINITY;
-  for (int i = lane; i < s; i += 32) M = fmaxf(M, __ldg(pl + at(i)));
+  const float first = lane < s ? __ldg(pl + at(lane)) : -INFINITY;
+  float v[U][E];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < s) load_dims<E>(po + at(u) * d + lane * E, v[u]);
+  float M = first;
+  for (int i = lane + 32; i < s; i += 32) M = fmaxf(M, __ldg(pl + at(i)));
   M = warp_max(M);
 #pragma unroll
   for (int e = 0; e < E; ++e) out[e] = 0.f;
   if (M == -INFINITY) return -INFINITY;
-  constexpr int U = 4;  // partials in flight
   float wsum = 0.f;
-  for (int i0 = 0; i0 < s; i0 += U) {
-    float v[U][E], w[U];
+  for (int i0 = 0; i0 < s; i0 += 32) {
+    const float x = i0 == 0 ? first : (i0 + lane < s ? __ldg(pl + at(i0 + lane)) : -INFINITY);
+    const float w = exp2f((x - M) * kLog2e);  // 0 past the last
+    for (int j = i0; j < min(s, i0 + 32); j += U) {
+      if (j > 0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      w[u] = i0 + u < s ? __ldg(pl + at(i0 + u)) : -INFINITY;
-      if (i0 + u < s) load_dims<E>(po + at(i0 + u) * d + lane * E, v[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + u < s) {
-        const float x = exp2f((w[u] - M) * kLog2e);
-        wsum += x;
-#pragma unroll
-        for (int e = 0; e < E; ++e) out[e] = fmaf(x, v[u][e], out[e]);
+        for (int u = 0; u < U; ++u)
+          if (j + u < s) load_dims<E>(po + at(j + u) * d + lane * E, v[u]);
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float wu = __shfl_sync(0xffffffffu, w, j - i0 + u);
+        if (j + u < s) {
+          wsum += wu;
+#pragma unroll
+          for (int e = 0; e < E; ++e) out[e] = fmaf(wu, v[u][e], out[e]);
+        }
+      }
+    }
   }
   const float inv = 1.f / wsum;
 #pragma unroll
@@ -1060,11 +1458,13 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
   float L;
   if constexpr (SHARED) {
     const int pre = P.pre[lo];
+    if (pre < 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (pre >= 0) {  // the prefix's partials of this row, then the request's own
       const int64_t tg = (int64_t)q0 + t - __ldg(A.q_indptr + req0 + P.req[pre]);  // its row of the group's
       if (tg < 0 || tg >= P.qn[pre]) return;
       const int64_t pp = (int64_t)P.part[pre] + tg * A.Hq + y % A.Hq;
       const size_t pstride = (size_t)P.qn[pre] * A.Hq;
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials
       L = merge_two<E>(A.part_o, A.part_lse, D, pp, pstride, P.ns[pre], pr, stride, P.ns[lo], lane, out);
       if (y == 0 && lane == 0) {  // the request's list holds the pages that were read for it
         const int e = P.skip[lo] / A.page_size - 1, lead = req0 + P.lead[lo];
@@ -1120,12 +1520,15 @@ struct Group {
     int skip, pre, end, lead;  // with shared prefixes
   };
   bool shared = false;  // some prefix is computed once for its group
+  int n_rows = 0, row_ctas = 0;
+  int64_t row_items = 0;
   std::vector<Rank> ranks;
 };
 
 // Ranks of a launch: the plan travels in the launch's parameters, 1.2 KB of them for up to 64 requests,
 // 18 KB for more (copied at each launch: 58 us of host time a call of 64 requests, 88 with the large one).
 constexpr int kSmallPlan = 64, kLargePlan = 1024;
+constexpr int kSmallShared = 96;  // (64 requests and their prefixes)
 
 // Requests that share their first tokens, on the host: requests indptr[i] .. indptr[i + 1] - 1 the first prefix[i].
 struct Prefixes {
@@ -1134,16 +1537,103 @@ struct Prefixes {
   const int32_t* prefix = nullptr;
 };
 
+// What the host plans with: a request, what it has behind its group's prefix, or a prefix.
+struct Req {
+  int req, n, units, first, last, ns;  // new tokens, pairs of query tiles, key tiles of the first and last pair
+  int skip, pre, end, lead;            // as in Plan; pre: number of the prefix among reqs, -1 none, -2 itself one
+  int few;                             // few rows: their own keys, else 0
+};
+constexpr int kMaxAuto = 256;    // chunks that the plan cuts a list into at most
+constexpr double kItem = 2.0;    // an item's prologue and epilogue, in key tiles
+constexpr double kMerge = 4.0;   // the merge launch
+
+// Chunks of a launch with shared prefixes, and the CTAs of few rows. The launch ends when its bytes have come, when the
+// last of the prefixes' items is done or the last of the warps of few rows. Measured: a warp's piece takes 5 us (lookups,
+// the first tiles and Q, one after the other) and 0.8 a tile of 16 keys; an item of query tiles 7.5 us and 1.5 a key tile
+// (heads of 64: 1.0), 3 of them again for each further one of its CTA. The lengths of both kinds of pieces that end
+// soonest are taken for each share of the SMs, and the best share.
+void plan_shared(const ChunkArgs& a, std::vector<Req>& reqs, int num_splits, int sms, Group& g) {
+  constexpr int kWarps = kThreads / 32, kPieces = 8, kTiles = 14;
+  static const int pieces[kPieces] = {32, 64, 96, 128, 192, 256, 384, 512};
+  const double tile_us = a.d == 128 ? 1.5 : 1.0, key_bytes = 4.0 * a.d;
+  int64_t row_items[kPieces] = {0};
+  double bytes = 0, row_bytes = 0;
+  int most = 1, longest_row = 0;
+  for (const Req& q : reqs) {
+    if (q.few) {
+      row_bytes += (double)q.few * a.Hkv * key_bytes;
+      longest_row = std::max(longest_row, q.few);
+      for (int k = 0; k < kPieces; ++k)
+        row_items[k] += (int64_t)a.Hkv * (num_splits ? num_splits : std::min(kMaxAuto, (q.few + pieces[k] - 1) / pieces[k]));
+    } else {
+      bytes += (double)kBN * std::max(q.first, q.last) * a.Hkv * key_bytes;
+      most = std::max(most, std::max(q.first, q.last));
+    }
+  }
+  bytes += row_bytes;
+  struct Tiles {  // the items of pieces of `tiles` key tiles: the longest one's time and that of all, us
+    int tiles;
+    int64_t items;
+    double longest, work;
+  } t[kTiles];
+  int nt = 0;
+  for (int tiles = most; nt < kTiles; tiles = std::max(2, tiles * 3 / 4)) {
+    Tiles x{tiles, 0, 0, 0};
+    for (const Req& q : reqs)
+      if (!q.few) {
+        const int len = std::max(q.first, q.last), ns = num_splits ? num_splits : std::min(kMaxAuto, (len + tiles - 1) / tiles);
+        const int64_t items = (int64_t)q.units * a.Hkv * ns;
+        x.items += items;
+        x.work += (tile_us * 0.5 * (q.first + q.last) / ns + 3.0) * (double)items;
+        x.work += (double)q.n * a.Hq * ns * 8.0 * (a.d + 1) / 45e3;  // partials, 45 KB/us of an SM
+        x.longest = std::max(x.longest, tile_us * len / ns);
+      }
+    t[nt++] = x;
+    if (tiles <= 2 || num_splits) break;
+  }
+  double best = 0;
+  int best_tiles = 0, best_piece = 0;
+  const int shares = row_bytes > 0 ? 16 : 1;
+  for (int c = 0; c < shares; ++c) {
+    const int n = row_bytes > 0 ? std::max(1, std::min(sms - 1, sms * (c + 1) / 17)) : 0, m = sms - n;
+    double t_rows = 0, t_tiles = 0;
+    int bk = 0, bt = 0;
+    for (int k = 0; k < kPieces && n > 0; ++k) {
+      const double one = 5.0 + 0.05 * (num_splits ? longest_row / num_splits : std::min(pieces[k], longest_row));
+      const double rate = kWarps * (double)row_bytes / (double)row_items[k] / one;  // bytes a us of an SM whose warps are busy
+      const double end = row_items[k] <= (int64_t)n * kWarps ? one : row_bytes / (n * rate) + 0.5 * one;
+      if (k == 0 || end < t_rows) {
+        t_rows = end;
+        bk = k;
+      }
+    }
+    for (int i = 0; i < nt; ++i) {
+      const double end = 4.5 + (t[i].items <= m ? t[i].longest + 3.0 : std::max(t[i].longest + 3.0, t[i].work / m + 0.3 * t[i].longest));
+      if (i == 0 || end < t_tiles) {
+        t_tiles = end;
+        bt = i;
+      }
+    }
+    const double end = std::max(bytes / 6.5e6 + 5.0, std::max(t_rows, t_tiles)) + 0.05 * (t_rows + t_tiles);
+    if (c == 0 || end < best) {
+      best = end;
+      best_piece = bk;
+      best_tiles = bt;
+      g.row_ctas = n;
+    }
+  }
+  if (num_splits == 0)
+    for (Req& q : reqs) {
+      const int len = q.few ? q.few : std::max(q.first, q.last), piece = q.few ? pieces[best_piece] : t[best_tiles].tiles;
+      q.ns = std::min(kMaxAuto, std::max(1, (len + piece - 1) / piece));
+    }
+  g.row_ctas = (int)std::min<int64_t>(g.row_ctas, row_items[best_piece]);
+}
+
 sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, const Prefixes& pf, int r0, int r1,
                       int num_splits, int sms, Group& g) {
-  constexpr int kMaxAuto = 256;
-  constexpr double kItem = 2.0;    // an item's prologue and epilogue, in key tiles
-  constexpr double kMerge = 4.0;   // the merge launch
-  struct Req {
-    int req, n, units, first, last, ns;  // new tokens, pairs of query tiles, key tiles of the first and last pair
-    int skip, pre, end, lead;            // as in Plan; pre: number of the prefix among reqs, -1 none, -2 itself one
-  };
   std::vector<Req> reqs;
+  reqs.reserve(pf.n > 0 ? 2 * (size_t)(r1 - r0) : (size_t)(r1 - r0));
   g.r0 = r0;
   // A prefix is computed once where that is less work than with each of its requests, in the time of key tiles of
   // pairs of query tiles: it takes an item more a request, and fp32 partials of all rows twice.
@@ -1170,7 +1660,7 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
     const int n = qi[r + 1] - qi[r], units = units_of(n);
     const int64_t len = (int64_t)ki[r + 1] - ki[r] - skip;
     reqs.push_back(Req{r - r0, n, units, tiles_of(n, len, 0), tiles_of(n, len, units - 1), std::max(num_splits, 1), (int)skip, pre,
-                       r - r0 + 1, lead});
+                       r - r0 + 1, lead, (int64_t)n * a.G <= 16 ? (int)len : 0});
     most = std::max(most, std::max(reqs.back().first, reqs.back().last));
   };
   for (int r = r0, i = 0; r < r1;) {
@@ -1182,7 +1672,7 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
         int lead = r;
         while (qi[lead + 1] == qi[lead]) ++lead;
         const int n = qi[end] - qi[r], tiles = (pf.prefix[i] + kBN - 1) / kBN, me = (int)reqs.size();
-        reqs.push_back(Req{r - r0, n, units_of(n), tiles, tiles, std::max(num_splits, 1), pf.prefix[i], -2, end - r0, lead - r0});
+        reqs.push_back(Req{r - r0, n, units_of(n), tiles, tiles, std::max(num_splits, 1), pf.prefix[i], -2, end - r0, lead - r0, 0});
         most = std::max(most, tiles);
         g.shared = true;
         for (; r < end; ++r)
@@ -1193,6 +1683,9 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
     for (; r < end; ++r)
       if (qi[r + 1] > qi[r]) add(r, 0, -1, 0);
   }
+  if (g.shared) plan_shared(a, reqs, num_splits, sms, g);
+  else
+    for (Req& q : reqs) q.few = 0;
   // Chunks. The launch ends when the SM with the most to do does: with the items sorted by length and
   // handed out one by one that is about the largest of an SM's share, the longest item, and k times the
   // item number (k - 1) * SMs + 1 (some SM has k items of at least that length). Cutting shortens items
@@ -1200,7 +1693,7 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
   // pieces from the longest list down are tried and the best estimate is kept. (64 single tokens over
   // 522,892 cached ones: 345 us whole, 333 in the pieces found, 421 in 16 pieces each; a 2048-token
   // prompt: 79 us in pieces of 8 tiles, 40 whole.)
-  if (num_splits == 0 && most > 2) {
+  if (!g.shared && num_splits == 0 && most > 2) {
     auto chunks = [&](int tiles, int piece) { return std::min(kMaxAuto, std::max(1, (tiles + piece - 1) / piece)); };
     auto estimate = [&](int piece) {
       constexpr int kBins = 32;
@@ -1215,7 +1708,7 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
         work += len * (double)items;
         longest = std::max(longest, (double)tiles / ns + kItem);
         bins[std::min(kBins - 1, (int)(len / step))] += items;
-        if (ns > 1 || q.pre != -1) {
+        if (ns > 1) {
           cut = true;
           work += (double)q.n * a.Hq * ns * 8.0 * (a.d + 1) / 65536.0;  // (a tile of K and V is 64 KB at most)
         }
@@ -1240,7 +1733,7 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
     }
     for (Req& q : reqs) q.ns = chunks(std::max(q.first, q.last), best);
   }
-  auto longest = [](const Req& q) { return (double)std::max(q.first, q.last) / q.ns; };
+  auto longest = [](const Req& q) { return q.few ? 1e9 + (double)q.few / q.ns : (double)std::max(q.first, q.last) / q.ns; };
   std::vector<int> order(reqs.size()), rank(reqs.size());
   std::iota(order.begin(), order.end(), 0);
   std::stable_sort(order.begin(), order.end(), [&](int x, int y) { return longest(reqs[x]) > longest(reqs[y]); });
@@ -1250,6 +1743,10 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
     if (q.ns > 1 || q.pre != -1) {
       if (q.pre != -2) g.rows += (int64_t)q.n * a.Hq;
       g.parts += (int64_t)q.n * a.Hq * q.ns;
+    }
+    if (q.few) {
+      g.n_rows += 1;
+      g.row_items = g.items + (int64_t)a.Hkv * q.ns;
     }
     rank[i] = (int)g.ranks.size();
     g.ranks.push_back(Group::Rank{q.req, q.n, q.ns, g.items, g.rows, part, q.skip, q.pre, q.end, q.lead});
@@ -1287,22 +1784,43 @@ sta_status launch_group(const Maps& m, const ChunkArgs& a, const Group& g, cudaS
     }
   }
   p.base[p.n] = (int32_t)g.items;
+  unsigned grid = (unsigned)g.items;
+  if constexpr (SHARED) {
+    p.n_rows = g.n_rows;
+    p.row_ctas = g.row_ctas;
+    grid = (unsigned)(g.items - g.row_items + g.row_ctas);
+  }
   auto kern = chunk_kernel<D, CAP, SHARED>;
   STA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM));
-  kern<<<(unsigned)g.items, kThreads, Cfg<D>::SMEM, st>>>(m.q, m.k, m.v, m.k4, m.v4, a, p, g.r0);
+  kern<<<grid, kThreads, Cfg<D>::SMEM, st>>>(m.q, m.k, m.v, m.k4, m.v4, a, p, g.r0);
   STA_LAUNCH_CHECK();
   if (g.rows > 0) {
-    chunk_merge_kernel<D, CAP, SHARED><<<(unsigned)cdiv(g.rows, 8), 256, 0, st>>>(a, p, g.r0, (int)g.rows);
-    STA_LAUNCH_CHECK();
+    if constexpr (SHARED) {
+      // started as the first kernel's CTAs end: it finds its rows, then waits for the last of them
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3((unsigned)cdiv(g.rows, 8));
+      cfg.blockDim = dim3(256);
+      cfg.stream = st;
+      cudaLaunchAttribute early{};
+      early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      early.val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = &early;
+      cfg.numAttrs = 1;
+      STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D, CAP, SHARED>, a, p, g.r0, (int)g.rows));
+    } else {
+      chunk_merge_kernel<D, CAP, SHARED><<<(unsigned)cdiv(g.rows, 8), 256, 0, st>>>(a, p, g.r0, (int)g.rows);
+      STA_LAUNCH_CHECK();
+    }
   }
   return STA_OK;
 }
 
 template <int D>
 sta_status launch_any(const Maps& m, const ChunkArgs& a, const Group& g, cudaStream_t st) {
-  const bool small = g.ranks.size() <= kSmallPlan;
-  if (g.shared) return small ? launch_group<D, kSmallPlan, true>(m, a, g, st) : launch_group<D, kLargePlan, true>(m, a, g, st);
-  return small ? launch_group<D, kSmallPlan, false>(m, a, g, st) : launch_group<D, kLargePlan, false>(m, a, g, st);
+  if (g.shared)
+    return g.ranks.size() <= kSmallShared ? launch_group<D, kSmallShared, true>(m, a, g, st)
+                                          : launch_group<D, kLargePlan, true>(m, a, g, st);
+  return g.ranks.size() <= kSmallPlan ? launch_group<D, kSmallPlan, false>(m, a, g, st) : launch_group<D, kLargePlan, false>(m, a, g, st);
 }
 
 // The two calls: with groups of requests that share their first tokens, or none of them.
@@ -1391,6 +1909,8 @@ sta_status chunk_fwd(const void* q, int64_t q_stride, const void* k_pages, const
        (uintptr_t)lse) & 3)
     return STA_ERR_UNSUPPORTED;
   a.o = static_cast<__nv_bfloat16*>(o);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_stride = q_stride;
   a.lse = lse;
   a.k = static_cast<const __nv_bfloat16*>(k_pages);
   a.v = static_cast<const __nv_bfloat16*>(v_pages);
