@@ -632,9 +632,12 @@ sta_status sta_chunk_fwd_paged(const void* q, int64_t q_stride, const void* k_pa
  *              of page_size, 0 for none. Their page lists start with the same prefix /
  *              page_size pages, and every new token lies behind them (length - new tokens
  *              >= prefix, for each request with new tokens)
+ *   num_splits 0: the library chooses whether a prefix is taken apart (it is not where that
+ *              saves less than the merge costs) and how all is cut; 1..1024: every prefix of
+ *              two requests or more with new tokens is, and every list longer than a few
+ *              keys is cut into that many
  * Every other argument and the results are those of sta_chunk_fwd_paged with pattern NULL,
- * up to the rounding of the merge. Whether a group's prefix is taken apart is the library's
- * choice (it is not where the new tokens fill the tensor cores anyway). A captured call may be
+ * up to the rounding of the merge. A captured call may be
  * replayed as there, with the same groups and prefixes: the prefix's pages are read from the
  * list of the group's first request that has new tokens in the host copy, which must keep them
  * there. A request whose new tokens no longer lie behind its prefix sets the device error word

@@ -957,7 +957,8 @@ def sta_prefix_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
 
     Requests group_indptr[i] .. group_indptr[i+1]-1 share their first prefix[i] tokens (int32, host; whole pages,
     0: none): their page lists start with the same prefix[i] / page_size pages, as sta_pages_fork leaves them, and
-    all of their new tokens lie behind them. Results are those of sta_chunk_fwd_paged up to rounding.
+    all of their new tokens lie behind them. num_splits 0: the library chooses which prefixes are taken apart; n > 0:
+    all, in n pieces. Results are those of sta_chunk_fwd_paged up to rounding.
     """
     return _bound("prefix_fwd_paged", stream, q, q, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev,
                   q_indptr_host, kv_indptr_dev, kv_indptr_host, group_indptr_host, prefix_host, scale, num_splits, o, lse, workspace)

@@ -77,6 +77,7 @@ struct ChunkArgs {
   uint32_t page_mul;      // division of a position by page_size: high word of the product with this,
   int page_shift;         // shifted right (by -1: page_size is 1)
   int box;                // tokens of a TMA box, or 0: cp.async
+  int row_box;            // and of one of few_rows: 16 or 8; 0: there are none
   float scale_log2;
   int causal;
   int64_t win_lo, win_hi, n_global;
@@ -88,18 +89,12 @@ struct ChunkArgs {
 //
 // With shared prefixes a rank is a request of its own (skip 0), what a request has behind its group's prefix
 // of `skip` tokens (pre: the prefix's rank), or that prefix itself (pre -2), whose rows are those of all the group's
-// requests req .. end - 1 and whose pages are those of request `lead`.
+// requests req .. end - 1 and whose pages are those of request `lead`. The first ranks, those of few rows, have no
+// items: base counts their tiles of 16 keys, kStart more for each, in one row, of which each CTA of few rows takes an equal
+// run. A rank's numbers lie side by side there: each part of a parameter that a kernel first reads by an index
+// costs it a round trip to memory.
 template <int CAP, bool SHARED>
-struct Groups {};
-template <int CAP>
-struct Groups<CAP, true> {
-  int n_rows, row_ctas;  // the first ranks, of few rows, and the CTAs that do them, the grid's first
-  int32_t skip[CAP];
-  int16_t pre[CAP];  // -1: neither
-  uint16_t end[CAP], lead[CAP];
-};
-template <int CAP, bool SHARED>
-struct Plan : Groups<CAP, SHARED> {
+struct Plan {
   int n;                // ranks
   int32_t base[CAP + 1];
   int32_t rows[CAP];    // merged rows up to and with the rank's (those of requests that are cut)
@@ -108,6 +103,30 @@ struct Plan : Groups<CAP, SHARED> {
   uint16_t req[CAP];    // request, from the launch's first
   uint16_t ns[CAP];     // chunks
 };
+constexpr int kStart = 2;  // what the start and the end of a piece of few rows cost, in tiles
+struct Rank {
+  int32_t part, qn, skip;
+  uint16_t req, ns, end, lead;
+  int16_t pre;  // -1: neither
+  uint16_t pad;
+};
+template <int CAP>
+struct Plan<CAP, true> {
+  int n;
+  int n_rows, row_ctas, ctas;  // ranks of few rows, CTAs that do them (the grid's first), the other CTAs
+  int runs, run;               // CTAs of few rows for each group of KV heads, length of their runs
+  int32_t base[CAP + 1];
+  int32_t rows[CAP];
+  Rank rank[CAP];
+};
+template <int CAP>
+__device__ __forceinline__ Rank rank_of(const Plan<CAP, false>& P, int i) {
+  return Rank{P.part[i], P.qn[i], 0, P.req[i], P.ns[i], 0, 0, -1, 0};
+}
+template <int CAP>
+__device__ __forceinline__ Rank rank_of(const Plan<CAP, true>& P, int i) {
+  return P.rank[i];
+}
 
 struct Item {
   int end;         // no more items
@@ -172,16 +191,17 @@ __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP, SHA
   }
   it.end = 0;
   it.rank = lo;
-  it.ns = P.ns[lo];
+  const Rank k = rank_of(P, lo);
+  it.ns = k.ns;
   const int x = item - P.base[lo], per_u = A.Hkv * it.ns, units = (P.base[lo + 1] - P.base[lo]) / per_u;
   const int u = units - 1 - x / per_u, y = x - (x / per_u) * per_u;
   it.hk = y / it.ns;
   it.c = y - it.hk * it.ns;
-  it.r = req0 + P.req[lo];
+  it.r = req0 + k.req;
   int kr = it.r, q_end = it.r + 1;  // whose keys, whose last row
   if constexpr (SHARED) {
-    q_end = req0 + P.end[lo];
-    if (P.pre[lo] == -2) kr = req0 + P.lead[lo];
+    q_end = req0 + k.end;
+    if (k.pre == -2) kr = req0 + k.lead;
   }
   const int q0 = __ldg(A.q_indptr + it.r), q1 = __ldg(A.q_indptr + q_end);
   int64_t len = (int64_t)__ldg(A.kv_indptr + kr + 1) - __ldg(A.kv_indptr + kr);
@@ -190,7 +210,7 @@ __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP, SHA
   int n = q1 - q0;
   int64_t pos0 = len - n;
   if constexpr (SHARED) {
-    const int skip = P.skip[lo], pre = P.pre[lo];
+    const int skip = k.skip, pre = k.pre;
     if (pre >= 0 && n > 0 && pos0 < skip) record_error(A.err, 0x608);  // new tokens that are not behind the prefix
     if (pre == -2) {  // every row is behind all of its keys
       len = skip;
@@ -201,9 +221,9 @@ __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP, SHA
       it.pb += skip / A.page_size;
     }
   }
-  if (n > P.qn[lo]) {
+  if (n > k.qn) {
     record_error(A.err, 0x606);
-    n = P.qn[lo];
+    n = k.qn;
   }
   if (q0 < 0 || n < 0 || q0 > A.N - n || len < 0 || len > INT32_MAX - 2 * kBN) {
     record_error(A.err, 0x111);
@@ -231,7 +251,7 @@ __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP, SHA
     it.j1a = max(it.j0, min(it.j1, na));
   }
   if constexpr (SHARED) {
-    if (P.pre[lo] != -1) it.ns = 2;  // a partial result, whether it is cut or not
+    if (k.pre != -1) it.ns = 2;  // a partial result, whether it is cut or not
   }
   return true;
 }
@@ -399,351 +419,380 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int k0) {
   return (a <= 0 ? ~0u : ~0u << a) & (b >= 31 ? ~0u : (2u << b) - 1u);
 }
 
-// Few rows: the (at most 16) rows of a request's new tokens and a KV head, over a piece of its keys, by one warp and
-// mma.sync. Beside a shared prefix, whose rows fill the tensor cores' tiles, what a request has of its own is a short
-// list for each KV head: an item of it would take a CTA's 128-row tiles for 4 rows or so, and some 6 us between its
-// lookups, its loads, its one product and its result. Twelve warps a CTA hide that behind one another; each looks the
-// next piece up and begins to load it while it works on the present one. The first CTAs of the grid do nothing else,
-// beside those of the prefix.
+// Few rows: the (at most 16) rows of a request's new tokens for each KV head, over a piece of its keys, on mma.sync. Beside
+// a shared prefix, whose rows fill the tensor cores' tiles, what a request has of its own is a short list for each KV head:
+// an item of it would take a CTA's 128-row tiles for 4 rows or so, and some 6 us between its lookups, its loads, its
+// one product and its result. Here a CTA takes a piece for up to 8 KV heads at once: two warps copy K and V of 16 tokens by
+// TMA, 16-KB boxes of all the heads (a warp that looked up and copied for its own head alone spent more issue slots on that
+// than on the products), and 8 warps compute, one a head, or several a head that take tiles in turn where there are
+// fewer heads. The first CTAs of the grid do nothing else, beside those of the prefix.
 template <int D>
 struct RowCfg {
-  static constexpr int KEYS = 16;                  // of a tile
-  static constexpr int TILE = KEYS * D * 2;        // its K or its V, 16-byte blocks of a row swizzled by the row
-  static constexpr int STAGES = D == 128 ? 2 : 4;  // tiles of a warp
-  static constexpr int WARP = STAGES * 2 * TILE;
-  static constexpr int WARPS = kThreads / 32;
-  static_assert(WARPS * WARP + 16 <= Cfg<D>::SMEM, "beside the other CTAs' shared memory");
+  static constexpr int KEYS = 16;              // of a tile
+  static constexpr int KH = D / 64;            // 128-byte column blocks of a row
+  static constexpr int HEAD = KEYS * 128;      // a head's part of such a block
+  static constexpr int BYTES = 192 * 1024;     // of the ring
+  static constexpr int MAX_STAGES = 16, WARPS = 8, PIECES = 4;
 };
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+constexpr int row_heads(int Hkv) { return Hkv < 8 ? Hkv : 8; }       // KV heads of a CTA
+constexpr int row_turns(int Hkv) { return 8 / row_heads(Hkv); }      // warps of a head
 
-// A piece: the rank's rows of a KV head, chunk c of its tiles (j0 .. j1 - 1).
+// Partials beside shared prefixes: those of chunk c of a rank are [D / 8][rows][8], rows by KV head, token and head of the
+// group, so that the threads of a warp, a row each, write whole lines (a row's 512 bytes by one thread took an item of two
+// query tiles 2 us longer).
+struct SharedPart {
+  int64_t first;  // row of the chunk's first
+  int rows, row;
+  __device__ __forceinline__ SharedPart(const Rank& k, int Hq, int G, int c, int hk, int t, int g)
+      : first(k.part + (int64_t)c * k.qn * Hq), rows(k.qn * Hq), row((hk * k.qn + t) * G + g) {}
+  __device__ __forceinline__ int64_t lse() const { return first + row; }
+  __device__ __forceinline__ int64_t values(int D, int eighth) const { return first * D + ((int64_t)eighth * rows + row) * 8; }
+};
+
+// K and V in boxes of ChunkArgs::row_box tokens.
+template <bool SHARED>
+struct RowMaps {};
+template <>
+struct RowMaps<true> {
+  CUtensorMap k, v;
+};
+
+// A piece: the rank's rows of KV heads h0 .. , chunk c of its 16-key tiles (j0 .. j1 - 1).
 struct Piece {
-  int rank, hk, c;      // rank -1: none
+  int rank, h0, c;      // rank -1: none
   int q0, n, pos0, len; // first row in q, new tokens, position of the first one, keys
   int pb, pe;           // page list
   int j0, j1;
 };
+struct RowShared {  // behind the ring
+  uint64_t full[16], empty[16], piece_full[4], piece_empty[4];
+  Piece piece[4];
+};
 
 template <int D, int CAP>
-__device__ __forceinline__ void few_rows(const ChunkArgs& A, const Plan<CAP, true>& P, int req0, uint8_t* smem) {
+__device__ __forceinline__ void few_rows(const ChunkArgs& A, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                         const Plan<CAP, true>& P, int req0, uint8_t* smem) {
   using C = RowCfg<D>;
-  constexpr int ST = C::STAGES, LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an instruction
+  static_assert(C::BYTES + (int)sizeof(RowShared) <= Cfg<D>::SMEM, "beside the other CTAs' shared memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int* counter = reinterpret_cast<int*>(smem + C::WARPS * C::WARP);
-  if (threadIdx.x == 0) *counter = 0;
+  RowShared& sh = *reinterpret_cast<RowShared*>(smem + C::BYTES);
+  const int HB = row_heads(A.Hkv), turns = row_turns(A.Hkv), half = HB * C::KH * C::HEAD;  // K's or V's part of a stage
+  const int ST = min(C::MAX_STAGES, C::BYTES / (2 * half));
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&sh.full[s], 2);
+      mbar_init(&sh.empty[s], HB);
+    }
+    for (int i = 0; i < C::PIECES; ++i) {
+      mbar_init(&sh.piece_full[i], 1);
+      mbar_init(&sh.piece_empty[i], HB * turns);
+    }
+    fence_mbar_init();
+  }
   __syncthreads();
-  const uint32_t mine = smem_u32(smem) + warp * C::WARP;
-  const int P0 = A.page_size, n_items = P.base[P.n_rows];
-  const int64_t row_elems = (int64_t)A.Hkv * D;
-  const bool one_page = P0 % C::KEYS == 0;  // (a prefix is whole pages, so that the rest starts with one)
+  const int P0 = A.page_size;
   auto page_no = [&](int tok) -> int { return A.page_shift < 0 ? tok : (int)(__umulhi((uint32_t)tok, A.page_mul) >> A.page_shift); };
-  const float c = A.scale_log2;
 
-  // The next piece's rank, head and chunk; a lane loads one of the six numbers that it goes by.
-  auto take = [&](Piece& p) -> int {
-    int x = 0;
-    if (lane == 0) x = atomicAdd(counter, 1);
-    x = __shfl_sync(0xffffffffu, x, 0);
-    const int64_t number = blockIdx.x + (int64_t)x * P.row_ctas;
-    p.rank = -1;
-    if (number >= n_items) return 0;
+  if (warp >= C::WARPS) {
+    // ------------------------------------------------------------ K and the pieces, V
+    const int me = warp - C::WARPS, is_v = me;
+    if (me > 1) return;
+    // This CTA's run, over as many ranks as it touches: a piece of each.
+    const int group = blockIdx.x / P.runs, x0 = (blockIdx.x - group * P.runs) * P.run, x1 = min(x0 + P.run, P.base[P.n_rows]);
     int lo = 0, hi = P.n_rows;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (P.base[mid] <= number) lo = mid;
+      if (P.base[mid] <= x0) lo = mid;
       else hi = mid;
     }
-    const int y = (int)number - P.base[lo], ns = P.ns[lo], r = req0 + P.req[lo];
-    p.rank = lo;
-    p.hk = y / ns;
-    p.c = y - p.hk * ns;
-    const int32_t* from = lane < 2 ? A.q_indptr : (lane < 4 ? A.kv_indptr : A.page_indptr);
-    return lane < 6 ? __ldg(from + r + (lane & 1)) : 0;
-  };
-  auto settle = [&](Piece& p, int loaded) {
-    const int q0 = __shfl_sync(0xffffffffu, loaded, 0), q1 = __shfl_sync(0xffffffffu, loaded, 1);
-    int64_t len = (int64_t)__shfl_sync(0xffffffffu, loaded, 3) - __shfl_sync(0xffffffffu, loaded, 2);
-    p.pb = __shfl_sync(0xffffffffu, loaded, 4);
-    p.pe = __shfl_sync(0xffffffffu, loaded, 5);
-    p.n = p.j0 = p.j1 = 0;
-    if (p.rank < 0) return;
-    int n = q1 - q0;
-    int64_t pos0 = len - n;
-    if (n > P.qn[p.rank]) {
-      record_error(A.err, 0x606);
-      n = P.qn[p.rank];
-    }
-    if (q0 < 0 || n < 0 || q0 > A.N - n || len < 0 || len > INT32_MAX - 2 * kBN) {
-      record_error(A.err, 0x111);
-      return;
-    }
-    if (P.pre[p.rank] >= 0) {  // keys and positions counted from the prefix's end
-      const int skip = P.skip[p.rank];
-      if (n > 0 && pos0 < skip) record_error(A.err, 0x608);  // new tokens that are not behind the prefix
-      pos0 -= skip;
-      len = len > skip ? len - skip : 0;
-      p.pb += skip / P0;
-    }
-    p.q0 = q0;
-    p.n = n;
-    p.pos0 = (int)pos0;
-    p.len = (int)len;
-    if (n == 0) return;
-    const int nt = (p.len + C::KEYS - 1) / C::KEYS, ns = P.ns[p.rank];
-    p.j0 = (int)((int64_t)p.c * nt / ns);
-    p.j1 = (int)((int64_t)(p.c + 1) * nt / ns);
-  };
-
-  // What is being loaded: tile `at` up to `end` of a piece. A lane holds one entry of its page list, and one of the 32
-  // after them; -1 behind the list.
-  int at = 0, end = 0, l_len = 0, l_pb = 0, l_pe = 0, l_hk = 0, window = 0, pages = -1, later = -1;
-  auto entry = [&](int e) -> int {
-    const int o = l_pb + e;
-    return o >= 0 && o < l_pe && (int64_t)e * P0 < l_len && A.page_indices ? __ldg(A.page_indices + o) : -1;
-  };
-  auto begin = [&](const Piece& p) {
-    at = p.j0;
-    end = p.j1;
-    l_len = p.len;
-    l_pb = p.pb;
-    l_pe = p.pe;
-    l_hk = p.hk;
-    window = page_no(at * C::KEYS);
-    pages = at < end ? entry(window + lane) : -1;
-    later = at < end ? entry(window + 32 + lane) : -1;
-  };
-  uint32_t done = 0;  // tiles that have been worked on
-  int ahead = 0;      // tiles that are loaded or on their way
-  auto fill = [&]() {
-    while (ahead < ST && at < end) {
-      const uint32_t to = mine + (done + ahead) % ST * (2 * C::TILE);
-      const int first = page_no(at * C::KEYS);
-      if (first >= window + 32) {
-        window += 32;
-        pages = later;
+    int from = P.base[lo], a = 0, b = 0, tiles = 1;  // the next piece: where its rank begins, its tiles of all there were on the host
+    // The next piece's rank, heads and chunk; a lane loads one of the six numbers that it goes by.
+    auto take = [&](Piece& p) -> int {
+      p.rank = -1;
+      if (lo >= P.n_rows || from >= x1) return 0;
+      const Rank k = rank_of(P, lo);
+      const int to = P.base[lo + 1];
+      p.rank = lo;
+      p.h0 = group * HB;
+      p.c = from < x0 ? x0 / P.run - from / P.run : 0;
+      tiles = to - from - kStart;
+      a = max(max(x0, from) - from - kStart, 0);
+      b = max(min(x1, to) - from - kStart, 0);
+      ++lo;
+      from = to;
+      const int32_t* in = lane < 2 ? A.q_indptr : (lane < 4 ? A.kv_indptr : A.page_indptr);
+      return lane < 6 ? __ldg(in + req0 + k.req + (lane & 1)) : 0;
+    };
+    auto settle = [&](Piece& p, int loaded) {
+      const int q0 = __shfl_sync(0xffffffffu, loaded, 0), q1 = __shfl_sync(0xffffffffu, loaded, 1);
+      int64_t len = (int64_t)__shfl_sync(0xffffffffu, loaded, 3) - __shfl_sync(0xffffffffu, loaded, 2);
+      p.pb = __shfl_sync(0xffffffffu, loaded, 4);
+      p.pe = __shfl_sync(0xffffffffu, loaded, 5);
+      p.n = p.j0 = p.j1 = 0;
+      if (p.rank < 0) return;
+      const Rank k = rank_of(P, p.rank);
+      int n = q1 - q0;
+      int64_t pos0 = len - n;
+      if (n > k.qn) {
+        record_error(A.err, 0x606);
+        n = k.qn;
+      }
+      if (q0 < 0 || n < 0 || q0 > A.N - n || len < 0 || len > INT32_MAX - 2 * kBN) {
+        record_error(A.err, 0x111);
+        return;
+      }
+      if (k.pre >= 0) {  // keys and positions counted from the prefix's end
+        if (n > 0 && pos0 < k.skip) record_error(A.err, 0x608);  // new tokens that are not behind the prefix
+        pos0 -= k.skip;
+        len = len > k.skip ? len - k.skip : 0;
+        p.pb += page_no(k.skip);
+      }
+      p.q0 = q0;
+      p.n = n;
+      p.pos0 = (int)pos0;
+      p.len = (int)len;
+      if (n == 0) return;
+      const int nt = (p.len + C::KEYS - 1) / C::KEYS;
+      p.j0 = nt == tiles ? a : (int)((int64_t)a * nt / tiles);  // (other lengths than the host's: the same parts of them)
+      p.j1 = nt == tiles ? b : (int)((int64_t)b * nt / tiles);
+    };
+    bool ok = true;
+    uint32_t T = 0;  // tiles of earlier pieces
+    Piece next;
+    int loaded = take(next);
+    for (uint32_t k = 0; ok; ++k) {
+      Piece p = next;
+      settle(p, loaded);
+      if (me == 0) {
+        if (k >= C::PIECES) ok = mbar_wait_warp(&sh.piece_empty[k % C::PIECES], ((k / C::PIECES) & 1u) ^ 1u, A.err, 0x635);
+        if (!ok) break;
+        if (lane == 0) {
+          sh.piece[k % C::PIECES] = p;
+          mbar_arrive(&sh.piece_full[k % C::PIECES]);
+        }
+      }
+      if (p.rank < 0) break;
+      loaded = take(next);
+      // A lane holds one entry of the page list, and one of the 32 after them; -1 behind the list.
+      auto entry = [&](int e) -> int {
+        const int o = p.pb + e;
+        return o >= 0 && o < p.pe && (int64_t)e * P0 < p.len && A.page_indices ? __ldg(A.page_indices + o) : -1;
+      };
+      int window = page_no(p.j0 * C::KEYS), pages = -1, later = -1;
+      if (p.j0 < p.j1) {
+        pages = entry(window + lane);
         later = entry(window + 32 + lane);
       }
-      if (one_page) {  // the tile's rows follow one another
-        int page = __shfl_sync(0xffffffffu, pages, first - window);
-        if (page < 0 || page >= A.n_pages) {
-          record_error(A.err, 0x110);
-          page = 0;
+      for (int j = p.j0; j < p.j1; ++j, ++T) {
+        const int tok0 = j * C::KEYS, in = min(C::KEYS, p.len - tok0);
+        if (page_no(tok0) >= window + 32) {
+          window += 32;
+          pages = later;
+          later = entry(window + 32 + lane);
         }
-        const int m0 = lane / LPR, in = l_len - at * C::KEYS;
-        const int64_t off = ((int64_t)page * P0 + (at * C::KEYS - first * P0) + m0) * row_elems + l_hk * D + (lane % LPR) * 8;
-        const __nv_bfloat16 *k = A.k + off, *v = A.v + off;
-#pragma unroll
-        for (int i = 0; i < C::KEYS / RPI; ++i) {
-          const int m = i * RPI + m0;
-          const uint32_t dst = to + m * (D * 2) + (((lane % LPR) ^ (m & 7)) << 4);
-          cp_async16(dst, k, m < in);
-          cp_async16(dst + C::TILE, v, m < in);
-          k += RPI * row_elems;
-          v += RPI * row_elems;
+        const int tok = tok0 + (lane & 15) * A.row_box;  // the first of the tile's box, or of the two of 8
+        const bool some = (lane & 15) * A.row_box < in;
+        const int no = page_no(some ? tok : tok0);
+        const int near = __shfl_sync(0xffffffffu, pages, no - window), far = __shfl_sync(0xffffffffu, later, no - window - 32);
+        int page = no < window + 32 ? near : far, row = -1;
+        if (some) {
+          if (page < 0 || page >= A.n_pages) {
+            record_error(A.err, 0x110);
+            page = 0;
+          }
+          row = page * P0 + tok - no * P0;
         }
-        cp_async_commit();
-        ++at;
-        ++ahead;
-        continue;
-      }
-      const int tok = at * C::KEYS + (lane & 15), no = page_no(tok);
-      const int near = __shfl_sync(0xffffffffu, pages, no - window), far = __shfl_sync(0xffffffffu, later, no - window - 32);
-      int page = no < window + 32 ? near : far, row = -1;  // behind the sequence: zeros
-      if (tok < l_len) {
-        if (page < 0 || page >= A.n_pages) {
-          record_error(A.err, 0x110);
-          page = 0;
+        const int s = T % ST;
+        if (T >= (uint32_t)ST && !(ok = mbar_wait_warp(&sh.empty[s], ((T / ST) & 1u) ^ 1u, A.err, 0x636))) break;
+        uint8_t* to = smem + s * 2 * half + is_v * half;
+        const int nb = A.row_box == C::KEYS ? 1 : (in + 7) >> 3;
+        const int row1 = __shfl_sync(0xffffffffu, row, 1);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(nb * A.row_box * HB * 128 * C::KH));
+#pragma unroll
+          for (int kh = 0; kh < C::KH; ++kh) {
+            // [KH][box][HB][tokens of a box] rows of 128 bytes
+            tma_load_3d(to + kh * (HB * C::HEAD), is_v ? &tm_v : &tm_k, kh * 64, row, p.h0, &sh.full[s]);
+            if (nb > 1) tma_load_3d(to + kh * (HB * C::HEAD) + HB * 1024, is_v ? &tm_v : &tm_k, kh * 64, row1, p.h0, &sh.full[s]);
+          }
         }
-        row = page * P0 + tok - no * P0;
-      }
-#pragma unroll
-      for (int i = 0; i < C::KEYS / RPI; ++i) {
-        const int m = i * RPI + lane / LPR, ch = lane % LPR, from = __shfl_sync(0xffffffffu, row, m);
-        const int64_t off = (int64_t)max(from, 0) * row_elems + l_hk * D + ch * 8;
-        const uint32_t dst = to + m * (D * 2) + ((ch ^ (m & 7)) << 4);
-        cp_async16(dst, A.k + off, from >= 0);
-        cp_async16(dst + C::TILE, A.v + off, from >= 0);
-      }
-      cp_async_commit();
-      ++at;
-      ++ahead;
-    }
-  };
-
-  Piece p;
-  {
-    const int loaded = take(p);
-    settle(p, loaded);
-  }
-  begin(p);
-  fill();
-  while (p.rank >= 0) {
-    Piece q;
-    const int loaded = take(q);
-    bool looked_up = false;  // q has its places, and is what is being loaded
-    auto look_up = [&]() {
-      settle(q, loaded);
-      begin(q);
-      looked_up = true;
-    };
-    if (p.n > 0) {
-      // Q: this lane's rows lane / 4 and that + 8 (token, head of the group), zeros past the last
-      const int R = p.n * A.G, r0 = lane >> 2, r1 = r0 + 8, t0 = r0 / A.G, t1 = r1 / A.G;
-      const bool live0 = r0 < R, live1 = r1 < R;
-      uint32_t qa[D / 16][4];
-      {
-        auto q_row = [&](int r, int t) { return A.q + (int64_t)(p.q0 + t) * A.q_stride + (p.hk * A.G + r - t * A.G) * D; };
-        const __nv_bfloat16 *a0 = q_row(live0 ? r0 : 0, live0 ? t0 : 0), *a1 = q_row(live1 ? r1 : 0, live1 ? t1 : 0);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const int e = k * 16 + (lane & 3) * 2;
-          qa[k][0] = live0 ? __ldg(reinterpret_cast<const uint32_t*>(a0 + e)) : 0u;
-          qa[k][1] = live1 ? __ldg(reinterpret_cast<const uint32_t*>(a1 + e)) : 0u;
-          qa[k][2] = live0 ? __ldg(reinterpret_cast<const uint32_t*>(a0 + e + 8)) : 0u;
-          qa[k][3] = live1 ? __ldg(reinterpret_cast<const uint32_t*>(a1 + e + 8)) : 0u;
-        }
-      }
-      float o[D / 8][4];
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-      const int mi = lane >> 3, mr = lane & 7;
-      for (int j = p.j0; j < p.j1; ++j) {
-        if (ahead == ST) cp_async_wait<ST - 1>();
-        else cp_async_wait<0>();
         __syncwarp();
-        const uint32_t kt = mine + done % ST * (2 * C::TILE), vt = kt + C::TILE;
-        float s[2][4] = {}, s2[2][4] = {};  // (two short chains of products rather than one long)
-        {
-          const int row = mr + (mi >> 1) * 8;
-#pragma unroll
-          for (int k = 0; k < D / 16; k += 2) {
-            uint32_t b[4], b2[4];
-            ldsm_x4(kt + row * (D * 2) + (((2 * k + (mi & 1)) ^ (row & 7)) << 4), b);
-            ldsm_x4(kt + row * (D * 2) + (((2 * k + 2 + (mi & 1)) ^ (row & 7)) << 4), b2);
-            mma_bf16_16816(s[0], qa[k], b[0], b[1]);
-            mma_bf16_16816(s[1], qa[k], b[2], b[3]);
-            mma_bf16_16816(s2[0], qa[k + 1], b2[0], b2[1]);
-            mma_bf16_16816(s2[1], qa[k + 1], b2[2], b2[3]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[0][e] += s2[0][e];
-            s[1][e] += s2[1][e];
-          }
-        }
-        if (j * C::KEYS + C::KEYS - 1 > p.pos0) {  // keys that some row does not see
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = j * C::KEYS + b * 8 + (lane & 3) * 2 + (e & 1);
-              if (key > p.pos0 + (e < 2 ? t0 : t1)) s[b][e] = -INFINITY;
-            }
-        }
-        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])), x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-#pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
-          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
-        }
-        x0 *= c;
-        x1 *= c;
-        float a0 = 1.f, a1 = 1.f;
-        if (x0 > m0 + kRescaleThreshold) {
-          if (m0 != -INFINITY) a0 = ex2(m0 - x0);
-          m0 = x0;
-        }
-        if (x1 > m1 + kRescaleThreshold) {
-          if (m1 != -INFINITY) a1 = ex2(m1 - x1);
-          m1 = x1;
-        }
-        if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {
-          l0 *= a0;
-          l1 *= a1;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[i][0] *= a0;
-            o[i][1] *= a0;
-            o[i][2] *= a1;
-            o[i][3] *= a1;
-          }
-        }
-        const float n0 = m0 == -INFINITY ? 0.f : m0, n1 = m1 == -INFINITY ? 0.f : m1;
-        float w[2][4];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          w[b][0] = ex2(fmaf(s[b][0], c, -n0));
-          w[b][1] = ex2(fmaf(s[b][1], c, -n0));
-          w[b][2] = ex2(fmaf(s[b][2], c, -n1));
-          w[b][3] = ex2(fmaf(s[b][3], c, -n1));
-          l0 += w[b][0] + w[b][1];
-          l1 += w[b][2] + w[b][3];
-        }
-        // P in bf16 for the product, off by 2^-8 at most; the sums take the fp32 values
-        const uint32_t pa[4] = {pack_bf16x2(w[0][0], w[0][1]), pack_bf16x2(w[0][2], w[0][3]), pack_bf16x2(w[1][0], w[1][1]),
-                                pack_bf16x2(w[1][2], w[1][3])};
-        {
-          const int row = mr + (mi & 1) * 8;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            uint32_t b[4];
-            ldsm_x4_t(vt + row * (D * 2) + (((2 * i + (mi >> 1)) ^ (row & 7)) << 4), b);
-            mma_bf16_16816(o[2 * i], pa, b[0], b[1]);
-            mma_bf16_16816(o[2 * i + 1], pa, b[2], b[3]);
-          }
-        }
-        __syncwarp();  // the tile has been read by all lanes
-        ++done;
-        --ahead;
-        if (at == end && !looked_up) look_up();
-        fill();
       }
+    }
+    // shared memory is not released under a copy
+    for (uint32_t t = T > (uint32_t)ST ? T - ST : 0; t < T; ++t)
+      if (!mbar_wait_warp(&sh.full[t % ST], (t / ST) & 1u, A.err, 0x637)) break;
+    return;
+  }
+
+  // -------------------------------------------------------------- products and softmax of a head, by turns
+  constexpr int NB = C::KEYS / 8;
+  const float c = A.scale_log2;
+  const int head = warp % HB, turn = warp / HB;
+  if (turn >= turns) return;
+  // this lane's rows of a piece, lane / 4 and that + 8: their tokens and heads of the group
+  const int r0 = lane >> 2, r1 = r0 + 8, t0 = r0 / A.G, t1 = r1 / A.G, g0 = r0 - t0 * A.G, g1 = r1 - t1 * A.G;
+  const int mi = lane >> 3, mr = lane & 7;
+  // a head's rows 0 .. 7 and 8 .. 15 of a tile: in one box, or in two
+  const int at_head = A.row_box == 8 ? head * 1024 : head * C::HEAD, to_second = A.row_box == 8 ? HB * 1024 : 1024;
+  bool ok = true;
+  uint32_t T = 0;
+  for (uint32_t k = 0; ok; ++k) {
+    if (!(ok = mbar_wait_warp(&sh.piece_full[k % C::PIECES], (k / C::PIECES) & 1u, A.err, 0x638))) break;
+    const Piece p = sh.piece[k % C::PIECES];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.piece_empty[k % C::PIECES]);
+    if (p.rank < 0) break;
+    const int hk = p.h0 + head;
+    const bool mine = hk < A.Hkv, live0 = mine && t0 < p.n, live1 = mine && t1 < p.n;  // (rows past the last: zeros)
+    uint32_t qa[D / 16][4];
+    {
+      auto q_row = [&](int t, int g) { return A.q + (int64_t)(p.q0 + t) * A.q_stride + ((int64_t)hk * A.G + g) * D; };
+      const __nv_bfloat16 *a0 = q_row(t0, g0), *a1 = q_row(t1, g1);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const int e = i * 16 + (lane & 3) * 2;
+        qa[i][0] = live0 ? __ldg(reinterpret_cast<const uint32_t*>(a0 + e)) : 0u;
+        qa[i][1] = live1 ? __ldg(reinterpret_cast<const uint32_t*>(a1 + e)) : 0u;
+        qa[i][2] = live0 ? __ldg(reinterpret_cast<const uint32_t*>(a0 + e + 8)) : 0u;
+        qa[i][3] = live1 ? __ldg(reinterpret_cast<const uint32_t*>(a1 + e + 8)) : 0u;
+      }
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    const int nt = p.j1 - p.j0;
+    for (int i = turn; i < nt; i += turns) {
+      const int j = p.j0 + i, tail = p.len - j * C::KEYS, st = (T + i) % ST;  // tail: keys of this tile
+      if (!(ok = mbar_wait_warp(&sh.full[st], ((T + i) / ST) & 1u, A.err, 0x639))) break;
+      const uint8_t* kt = smem + st * 2 * half + at_head;
+      float s[NB][4], s2[NB][4];  // (two short chains of products rather than one long)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[b][e] = s2[b][e] = 0.f;
+      {
+        const uint32_t base = smem_u32(kt) + (mi >> 1) * to_second + mr * 128;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          uint32_t f[4];
+          ldsm_x4(base + (x >> 2) * (HB * C::HEAD) + ((((2 * x + (mi & 1)) & 7) ^ mr) << 4), f);
+          mma_bf16_16816(x & 1 ? s2[0] : s[0], qa[x], f[0], f[1]);
+          mma_bf16_16816(x & 1 ? s2[1] : s[1], qa[x], f[2], f[3]);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[b][e] += s2[b][e];
+      if (j * C::KEYS + C::KEYS - 1 > p.pos0) {  // keys that some row does not see
+        const int k0 = j * C::KEYS + (lane & 3) * 2, see0 = p.pos0 + t0 - k0, see1 = p.pos0 + t1 - k0;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (b * 8 + (e & 1) > (e < 2 ? see0 : see1) || b * 8 + (e & 1) + (lane & 3) * 2 >= tail) s[b][e] = -INFINITY;
+      }
+      float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])), x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
 #pragma unroll
       for (int d = 1; d < 4; d <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
       }
-      const bool part = P.ns[p.rank] > 1 || P.pre[p.rank] != -1;
-      auto result = [&](bool live, int r, int t, float m, float l, int e) {
-        if (!live) return;
-        const float inv = l != 0.f ? 1.f / l : 0.f;  // a NaN among the scores stays one
-        const float lse = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-        const int h = p.hk * A.G + r - t * A.G;
-        if (part) {
-          const int64_t prow = P.part[p.rank] + ((int64_t)p.c * P.qn[p.rank] + t) * A.Hq + h;
+      x0 *= c;
+      x1 *= c;
+      float a0 = 1.f, a1 = 1.f;
+      if (x0 > m0 + kRescaleThreshold) {
+        if (m0 != -INFINITY) a0 = ex2(m0 - x0);
+        m0 = x0;
+      }
+      if (x1 > m1 + kRescaleThreshold) {
+        if (m1 != -INFINITY) a1 = ex2(m1 - x1);
+        m1 = x1;
+      }
+      if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {
+        l0 *= a0;
+        l1 *= a1;
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(A.part_o + prow * D + i * 8 + (lane & 3) * 2) = make_float2(o[i][e] * inv, o[i][e + 1] * inv);
-          if ((lane & 3) == 0) A.part_lse[prow] = lse == lse ? lse : INFINITY;  // the merge makes a NaN of it again
-        } else {
-          const int64_t row = (int64_t)(p.q0 + t) * A.Hq + h;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<uint32_t*>(A.o + row * D + i * 8 + (lane & 3) * 2) = pack_bf16x2(o[i][e] * inv, o[i][e + 1] * inv);
-          if ((lane & 3) == 0 && A.lse) A.lse[row] = lse;
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][0] *= a0;
+          o[i][1] *= a0;
+          o[i][2] *= a1;
+          o[i][3] *= a1;
         }
-      };
-      result(live0, r0, t0, m0, l0, 0);
-      result(live1, r1, t1, m1, l1, 2);
+      }
+      const float n0 = m0 == -INFINITY ? 0.f : -m0, n1 = m1 == -INFINITY ? 0.f : -m1;
+      uint32_t pa[4];  // P in bf16 for the product, off by 2^-8 at most; the sums take the fp32 values
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float w0 = ex2(fmaf(s[b][0], c, n0)), w1 = ex2(fmaf(s[b][1], c, n0));
+        const float w2 = ex2(fmaf(s[b][2], c, n1)), w3 = ex2(fmaf(s[b][3], c, n1));
+        l0 += w0 + w1;
+        l1 += w2 + w3;
+        pa[b * 2] = pack_bf16x2(w0, w1);
+        pa[b * 2 + 1] = pack_bf16x2(w2, w3);
+      }
+      uint8_t* vt = smem + st * 2 * half + half + at_head;
+      if (tail < C::KEYS) {  // rows behind the sequence: what a page holds there may be NaN
+        for (int z = tail * 8 + lane; z < C::KEYS * 8; z += 32)
+#pragma unroll
+          for (int kh = 0; kh < C::KH; ++kh)
+            *reinterpret_cast<uint4*>(vt + kh * (HB * C::HEAD) + (z >= 64 ? to_second + (z - 64) * 16 : z * 16)) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      {
+        const uint32_t base = smem_u32(vt) + (mi & 1) * to_second + mr * 128;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          uint32_t f[4];
+          ldsm_x4_t(base + (x >> 2) * (HB * C::HEAD) + ((((2 * x + (mi >> 1)) & 7) ^ mr) << 4), f);
+          mma_bf16_16816(o[2 * x], pa, f[0], f[1]);
+          mma_bf16_16816(o[2 * x + 1], pa, f[2], f[3]);
+        }
+      }
+      __syncwarp();  // the tile has been read by all lanes
+      if (lane == 0) mbar_arrive(&sh.empty[st]);
     }
-    if (!looked_up) look_up();
-    fill();
-    p = q;
+    T += nt;
+    if (!ok) break;
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+    }
+    const Rank rk = rank_of(P, p.rank);
+    auto result = [&](bool live, int t, int g, float m, float l, int e) {
+      if (!live) return;
+      const float inv = l != 0.f ? 1.f / l : 0.f;  // a NaN among the scores stays one
+      const float lse = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      const int h = hk * A.G + g;
+      if (rk.ns > 1 || rk.pre != -1) {
+        const SharedPart to(rk, A.Hq, A.G, p.c * turns + turn, hk, t, g);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<float2*>(A.part_o + to.values(D, i) + (lane & 3) * 2) = make_float2(o[i][e] * inv, o[i][e + 1] * inv);
+        if ((lane & 3) == 0) A.part_lse[to.lse()] = lse == lse ? lse : INFINITY;  // the merge makes a NaN of it again
+      } else {
+        const int64_t to = (int64_t)(p.q0 + t) * A.Hq + h;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<uint32_t*>(A.o + to * D + i * 8 + (lane & 3) * 2) = pack_bf16x2(o[i][e] * inv, o[i][e + 1] * inv);
+        if ((lane & 3) == 0 && A.lse) A.lse[to] = lse;
+      }
+    };
+    result(live0, t0, g0, m0, l0, 0);
+    result(live1, t1, g1, m1, l1, 2);
   }
-  cp_async_wait<0>();
 }
 
 template <int D, int CAP, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k4,
-                 const __grid_constant__ CUtensorMap tm_v4, const __grid_constant__ ChunkArgs A,
-                 const __grid_constant__ Plan<CAP, SHARED> P, int req0) {
+                 const __grid_constant__ CUtensorMap tm_v4, const __grid_constant__ RowMaps<SHARED> R,
+                 const __grid_constant__ ChunkArgs A, const __grid_constant__ Plan<CAP, SHARED> P, int req0) {
   using C = Cfg<D>;
   constexpr int ST = C::STAGES;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -756,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (SHARED) {
     asm volatile("griddepcontrol.launch_dependents;");
     if ((int)blockIdx.x < P.row_ctas) {
-      few_rows<D, CAP>(A, P, req0, smem);
+      few_rows<D, CAP>(A, R.k, R.v, P, req0, smem);
       return;
     }
   }
@@ -804,7 +853,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       bool ok = true;
       int item = blockIdx.x, k = 0, nq = 0;
-      int row = -1;  // the next of several items of a CTA of few rows that was taken over (it starts first: hardly ever)
       if constexpr (SHARED) item += P.base[P.n_rows] - P.row_ctas;
       Item it;
       for (int n = 0; ok && item >= 0;) {
@@ -832,10 +880,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         if constexpr (SHARED) {
-          if (row >= 0) {
-            item = row;
-            row += P.row_ctas;
-            if (row >= P.base[P.n_rows]) row = -1;
+          if (P.row_ctas > 0) {  // CTAs of few rows may not be taken over: the others go round by themselves
+            item += P.ctas;
+            if (item >= P.base[P.n]) break;
             continue;
           }
         }
@@ -843,10 +890,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         item = mbar_wait(&sh.clc_full, n & 1u, A.err, 0x62c) ? clc_answer(&sh.clc) : -1;
         fence_proxy_async_smem();  // the answer has been read before the next one is written
         ++n;
-        if constexpr (SHARED) {
-          if (item >= P.row_ctas) item += P.base[P.n_rows] - P.row_ctas;
-          else if (item >= 0 && item + P.row_ctas < P.base[P.n_rows]) row = item + P.row_ctas;
-        }
       }
       if (ok && k >= 2) ok = mbar_wait(&sh.item_empty[k & 1], ((k >> 1) & 1u) ^ 1u, A.err, 0x62b);
       if (ok) {
@@ -1317,7 +1360,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         w1 *= inv;
         const int h = it.hk * A.G + (m - tt * A.G);
         const int64_t row = (int64_t)(it.q0 + t) * A.Hq + h;
-        const int64_t prow = it.ns > 1 ? P.part[it.rank] + ((int64_t)it.c * P.qn[it.rank] + t) * A.Hq + h : 0;
+        int64_t prow = 0, step = 8;  // the row's LSE; elements between eighths of its values
+        float* pvalues = nullptr;
+        if (it.ns > 1) {
+          const Rank rk = rank_of(P, it.rank);
+          if constexpr (SHARED) {
+            const SharedPart to(rk, A.Hq, A.G, it.c, it.hk, t, m - tt * A.G);
+            prow = to.lse();
+            pvalues = A.part_o + to.values(D, 0);
+            step = (int64_t)to.rows * 8;
+          } else {
+            prow = rk.part + ((int64_t)it.c * rk.qn + t) * A.Hq + h;
+            pvalues = A.part_o + prow * D;
+          }
+        }
         // (Short code: a CTA comes here once an item and has to fetch it. With the loops unrolled, windowed
         // chunks took 62.6 us against 59, an 8192-token prompt 318 against 315. Four lanes that exchanged
         // pieces of their rows by shuffles, to store whole 128-byte lines, lost 4 us to the exchange.)
@@ -1356,7 +1412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it.ns > 1) {
 #pragma unroll
               for (int e = 0; e < 32; e += 8)
-                store32(A.part_o + prow * D + c0 + e, reinterpret_cast<const uint32_t*>(o) + e);
+                store32(pvalues + (c0 + e) / 8 * step, reinterpret_cast<const uint32_t*>(o) + e);
             } else {
               uint32_t w[16];
 #pragma unroll
@@ -1387,58 +1443,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// merge_row over two lists of partials: na of them at row a, `astride` rows apart, then nb at row b. The LSEs of 32 and the
-// values of 8 are on their way at once, the first of both before the maximum is known.
-template <int E>
-__device__ __forceinline__ float merge_two(const float* po, const float* pl, int d, int64_t a, size_t astride, int na, int64_t b,
-                                           size_t bstride, int nb, int lane, float* out) {
-  constexpr int U = 8;
-  const int s = na + nb;
-  auto at = [&](int i) { return i < na ? a + (int64_t)(i * astride) : b + (int64_t)((i - na) * bstride); };
-  const float first = lane < s ? __ldg(pl + at(lane)) : -INFINITY;
-  float v[U][E];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (u < s) load_dims<E>(po + at(u) * d + lane * E, v[u]);
-  float M = first;
-  for (int i = lane + 32; i < s; i += 32) M = fmaxf(M, __ldg(pl + at(i)));
-  M = warp_max(M);
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = 0.f;
-  if (M == -INFINITY) return -INFINITY;
-  float wsum = 0.f;
-  for (int i0 = 0; i0 < s; i0 += 32) {
-    const float x = i0 == 0 ? first : (i0 + lane < s ? __ldg(pl + at(i0 + lane)) : -INFINITY);
-    const float w = exp2f((x - M) * kLog2e);  // 0 past the last
-    for (int j = i0; j < min(s, i0 + 32); j += U) {
-      if (j > 0) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (j + u < s) load_dims<E>(po + at(j + u) * d + lane * E, v[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float wu = __shfl_sync(0xffffffffu, w, j - i0 + u);
-        if (j + u < s) {
-          wsum += wu;
-#pragma unroll
-          for (int e = 0; e < E; ++e) out[e] = fmaf(wu, v[u][e], out[e]);
-        }
-      }
-    }
-  }
-  const float inv = 1.f / wsum;
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] *= inv;
-  return M + logf(wsum);
-}
-
 // One warp per (new token, query head) of the requests that were cut. It reads ns fp32 partials of d + 1
 // a row, which stay in L2 (one 30,000-token sequence, 32 rows in 19 pieces: 44 us with the attention, of
 // which 18 are the cache at copy speed).
-template <int D, int CAP, bool SHARED>
+template <int D, int CAP>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant__ ChunkArgs A,
-                                                          const __grid_constant__ Plan<CAP, SHARED> P, int req0, int n_rows) {
+                                                          const __grid_constant__ Plan<CAP, false> P, int req0, int n_rows) {
   constexpr int E = D / 32;
   const int64_t mr = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -1455,35 +1465,104 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
   const int64_t pr = (int64_t)P.part[lo] + y;
   const size_t stride = (size_t)P.qn[lo] * A.Hq;
   float out[E];
-  float L;
-  if constexpr (SHARED) {
-    const int pre = P.pre[lo];
-    if (pre < 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (pre >= 0) {  // the prefix's partials of this row, then the request's own
-      const int64_t tg = (int64_t)q0 + t - __ldg(A.q_indptr + req0 + P.req[pre]);  // its row of the group's
-      if (tg < 0 || tg >= P.qn[pre]) return;
-      const int64_t pp = (int64_t)P.part[pre] + tg * A.Hq + y % A.Hq;
-      const size_t pstride = (size_t)P.qn[pre] * A.Hq;
-      asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials
-      L = merge_two<E>(A.part_o, A.part_lse, D, pp, pstride, P.ns[pre], pr, stride, P.ns[lo], lane, out);
-      if (y == 0 && lane == 0) {  // the request's list holds the pages that were read for it
-        const int e = P.skip[lo] / A.page_size - 1, lead = req0 + P.lead[lo];
-        const int a = __ldg(A.page_indptr + r) + e, b = __ldg(A.page_indptr + lead) + e;
-        if (a < 0 || a >= __ldg(A.page_indptr + r + 1) || b < 0 || b >= __ldg(A.page_indptr + lead + 1) ||
-            __ldg(A.page_indices + a) != __ldg(A.page_indices + b))
-          record_error(A.err, 0x609);
-      }
-    } else {
-      L = merge_row<E>(A.part_o + pr * D, stride * D, A.part_lse + pr, stride, P.ns[lo], lane, out);
-    }
-  } else {
-    L = merge_row<E>(A.part_o + pr * D, stride * D, A.part_lse + pr, stride, P.ns[lo], lane, out);
-  }
+  const float L = merge_row<E>(A.part_o + pr * D, stride * D, A.part_lse + pr, stride, P.ns[lo], lane, out);
   const int64_t row = (int64_t)(q0 + t) * A.Hq + y % A.Hq;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
     *reinterpret_cast<uint32_t*>(A.o + row * D + lane * E + e) = pack_bf16x2(out[e], out[e + 1]);
   if (A.lse && lane == 0) A.lse[row] = L;
+}
+
+// Four merged rows a warp: a rank's own partials, and before them its prefix's. Lane (eighth x of 4, row y of 4, half z):
+// 16 bytes of its row's eighths x, x + 4, .., so that four rows side by side are whole lines. It starts as the first
+// kernel's CTAs end, finds its rows, then waits for the last of them.
+template <int D, int CAP>
+__global__ void __launch_bounds__(128) chunk_merge_shared_kernel(const __grid_constant__ ChunkArgs A,
+                                                                 const __grid_constant__ Plan<CAP, true> P, int req0, int n_rows) {
+  constexpr int NV = D / 32, U = 4;  // 16-byte parts of a lane, partials on their way
+  const int lane = threadIdx.x & 31, z = lane & 1, sub = (lane >> 3) * 2 + z;  // sub: of the 8 lanes of a row
+  const int64_t mr = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * 4 + ((lane >> 1) & 3);
+  bool some = mr < n_rows;
+  int lo = 0, hi = P.n - 1;  // the first rank whose rows end behind this one
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (P.rows[mid] > mr) hi = mid;
+    else lo = mid + 1;
+  }
+  const Rank k = rank_of(P, lo);
+  const int y = some ? (int)mr - (lo > 0 ? P.rows[lo - 1] : 0) : 0, r = req0 + k.req;
+  const int g = y % A.G, ht = y / A.G, hk = ht / k.qn, t = ht - hk * k.qn;
+  const int q0 = __ldg(A.q_indptr + r), n = __ldg(A.q_indptr + r + 1) - q0;
+  some = some && q0 >= 0 && t < n && q0 <= A.N - min(n, k.qn);
+  SharedPart own(k, A.Hq, A.G, 0, hk, t, g), pre = own;
+  int na = 0;  // the prefix's partials
+  if (k.pre >= 0) {
+    const Rank kp = rank_of(P, k.pre);
+    const int64_t tg = (int64_t)q0 + t - __ldg(A.q_indptr + req0 + kp.req);  // its token of the group's
+    some = some && tg >= 0 && tg < kp.qn;
+    if (some) pre = SharedPart(kp, A.Hq, A.G, 0, hk, (int)tg, g);
+    na = kp.ns;
+    if (some && y == 0 && sub == 0) {  // the request's list holds the pages that were read for it
+      const int e = k.skip / A.page_size - 1, lead = req0 + k.lead;
+      const int a = __ldg(A.page_indptr + r) + e, b = __ldg(A.page_indptr + lead) + e;
+      if (a < 0 || a >= __ldg(A.page_indptr + r + 1) || b < 0 || b >= __ldg(A.page_indptr + lead + 1) ||
+          __ldg(A.page_indices + a) != __ldg(A.page_indices + b))
+        record_error(A.err, 0x609);
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials
+  const int s = some ? na + k.ns : 0;
+  int most = s;
+#pragma unroll
+  for (int d = 2; d <= 4; d <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+  auto lse_at = [&](int i) {
+    return i < s ? __ldg(A.part_lse + (i < na ? pre.lse() + (int64_t)i * pre.rows : own.lse() + (int64_t)(i - na) * own.rows)) : -INFINITY;
+  };
+  auto value = [&](int i, int v) {
+    const SharedPart& p = i < na ? pre : own;
+    const int64_t c = (int64_t)(i < na ? i : i - na) * p.rows;  // rows of the chunks before
+    return __ldg(reinterpret_cast<const float4*>(A.part_o + p.values(D, (lane >> 3) + 4 * v) + c * D + z * 4));
+  };
+  float M = -INFINITY;
+  for (int i = sub; i < most; i += 8) M = fmaxf(M, lse_at(i));
+#pragma unroll
+  for (int d : {1, 8, 16}) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  float4 out[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) out[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int i0 = 0; i0 < most; i0 += U) {
+    float4 x[U][NV];
+    float w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      w[u] = lse_at(i0 + u);
+      if (i0 + u < s)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) x[u][v] = value(i0 + u, v);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u < s && M != -INFINITY) {
+        const float e = exp2f((w[u] - M) * kLog2e);
+        sum += e;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          out[v].x = fmaf(e, x[u][v].x, out[v].x);
+          out[v].y = fmaf(e, x[u][v].y, out[v].y);
+          out[v].z = fmaf(e, x[u][v].z, out[v].z);
+          out[v].w = fmaf(e, x[u][v].w, out[v].w);
+        }
+      }
+  }
+  if (!some) return;
+  const float inv = M != -INFINITY ? 1.f / sum : 0.f;
+  const int64_t row = (int64_t)(q0 + t) * A.Hq + hk * A.G + g;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    *reinterpret_cast<uint2*>(A.o + row * D + ((lane >> 3) + 4 * v) * 8 + z * 4) =
+        make_uint2(pack_bf16x2(out[v].x * inv, out[v].y * inv), pack_bf16x2(out[v].z * inv, out[v].w * inv));
+  if (A.lse && sub == 0) A.lse[row] = M != -INFINITY ? M + logf(sum) : -INFINITY;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -1510,6 +1589,18 @@ bool make_map(CUtensorMap* m, const void* base, int d, int heads, int64_t rows, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The cache's [rows, heads, d] as (d, rows, heads), boxes of 64 x br x the heads of a CTA of few rows.
+bool make_row_map(CUtensorMap* m, const void* base, int d, int heads, int64_t rows, int br) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)heads * d * 2, (cuuint64_t)d * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)br, (cuuint32_t)row_heads(heads)}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Requests from r0 on as one launch: its ranks, and how much scratch they need.
 struct Group {
   int r0 = 0;
@@ -1520,15 +1611,14 @@ struct Group {
     int skip, pre, end, lead;  // with shared prefixes
   };
   bool shared = false;  // some prefix is computed once for its group
-  int n_rows = 0, row_ctas = 0;
-  int64_t row_items = 0;
+  int n_rows = 0, row_ctas = 0, ctas = 0, runs = 0, run = 0;
   std::vector<Rank> ranks;
 };
 
 // Ranks of a launch: the plan travels in the launch's parameters, 1.2 KB of them for up to 64 requests,
 // 18 KB for more (copied at each launch: 58 us of host time a call of 64 requests, 88 with the large one).
 constexpr int kSmallPlan = 64, kLargePlan = 1024;
-constexpr int kSmallShared = 96;  // (64 requests and their prefixes)
+constexpr int kSmallShared = 96, kLargeShared = 768;  // (64 requests and their prefixes)
 
 // Requests that share their first tokens, on the host: requests indptr[i] .. indptr[i + 1] - 1 the first prefix[i].
 struct Prefixes {
@@ -1548,29 +1638,22 @@ constexpr double kItem = 2.0;    // an item's prologue and epilogue, in key tile
 constexpr double kMerge = 4.0;   // the merge launch
 
 // Chunks of a launch with shared prefixes, and the CTAs of few rows. The launch ends when its bytes have come, when the
-// last of the prefixes' items is done or the last of the warps of few rows. Measured: a warp's piece takes 5 us (lookups,
-// the first tiles and Q, one after the other) and 0.8 a tile of 16 keys; an item of query tiles 7.5 us and 1.5 a key tile
-// (heads of 64: 1.0), 3 of them again for each further one of its CTA. The lengths of both kinds of pieces that end
-// soonest are taken for each share of the SMs, and the best share.
+// last of the prefixes' items is done or the last CTA of few rows. Measured: a run of few rows takes 3.5 us and 0.6 a tile of 16
+// keys (and a piece 2 of them more); an item of query tiles 7.5 us and 1.5 a key tile (heads of 64: 1.0), 3 again for
+// each further one of its CTA. For each share of the SMs the length of the prefixes' pieces that ends soonest is taken, and
+// the best share.
 void plan_shared(const ChunkArgs& a, std::vector<Req>& reqs, int num_splits, int sms, Group& g) {
-  constexpr int kWarps = kThreads / 32, kPieces = 8, kTiles = 14;
-  static const int pieces[kPieces] = {32, 64, 96, 128, 192, 256, 384, 512};
-  const double tile_us = a.d == 128 ? 1.5 : 1.0, key_bytes = 4.0 * a.d;
-  int64_t row_items[kPieces] = {0};
-  double bytes = 0, row_bytes = 0;
-  int most = 1, longest_row = 0;
-  for (const Req& q : reqs) {
-    if (q.few) {
-      row_bytes += (double)q.few * a.Hkv * key_bytes;
-      longest_row = std::max(longest_row, q.few);
-      for (int k = 0; k < kPieces; ++k)
-        row_items[k] += (int64_t)a.Hkv * (num_splits ? num_splits : std::min(kMaxAuto, (q.few + pieces[k] - 1) / pieces[k]));
-    } else {
-      bytes += (double)kBN * std::max(q.first, q.last) * a.Hkv * key_bytes;
-      most = std::max(most, std::max(q.first, q.last));
-    }
+  constexpr int kTiles = 14, kKeys = 16;
+  const int heads = row_heads(a.Hkv), groups = (a.Hkv + heads - 1) / heads, turns = row_turns(a.Hkv);
+  const double tile_us = a.d == 128 ? 1.5 : 1.0, row_us = 0.6 / turns, key_bytes = 4.0 * a.d;
+  int64_t row = 0;  // the tiles of few rows, one after the other
+  double bytes = 0;
+  int most = 1;
+  for (Req& q : reqs) {
+    bytes += (q.few ? (double)q.few : (double)kBN * std::max(q.first, q.last)) * a.Hkv * key_bytes;
+    if (q.few) row += (q.few + kKeys - 1) / kKeys + kStart;
+    else most = std::max(most, std::max(q.first, q.last));
   }
-  bytes += row_bytes;
   struct Tiles {  // the items of pieces of `tiles` key tiles: the longest one's time and that of all, us
     int tiles;
     int64_t items;
@@ -1592,21 +1675,13 @@ void plan_shared(const ChunkArgs& a, std::vector<Req>& reqs, int num_splits, int
     if (tiles <= 2 || num_splits) break;
   }
   double best = 0;
-  int best_tiles = 0, best_piece = 0;
-  const int shares = row_bytes > 0 ? 16 : 1;
+  int best_tiles = 0, best_runs = 0;
+  const int shares = row > 0 ? 24 : 1;
   for (int c = 0; c < shares; ++c) {
-    const int n = row_bytes > 0 ? std::max(1, std::min(sms - 1, sms * (c + 1) / 17)) : 0, m = sms - n;
-    double t_rows = 0, t_tiles = 0;
-    int bk = 0, bt = 0;
-    for (int k = 0; k < kPieces && n > 0; ++k) {
-      const double one = 5.0 + 0.05 * (num_splits ? longest_row / num_splits : std::min(pieces[k], longest_row));
-      const double rate = kWarps * (double)row_bytes / (double)row_items[k] / one;  // bytes a us of an SM whose warps are busy
-      const double end = row_items[k] <= (int64_t)n * kWarps ? one : row_bytes / (n * rate) + 0.5 * one;
-      if (k == 0 || end < t_rows) {
-        t_rows = end;
-        bk = k;
-      }
-    }
+    const int runs = row > 0 ? std::max(1, std::min(sms - 1, sms * (c + 1) / (shares + 1)) / groups) : 0, m = std::max(1, sms - runs * groups);
+    const double t_rows = row > 0 ? 3.5 + row_us * (double)((row + runs - 1) / runs) : 0.0;
+    double t_tiles = 0;
+    int bt = 0;
     for (int i = 0; i < nt; ++i) {
       const double end = 4.5 + (t[i].items <= m ? t[i].longest + 3.0 : std::max(t[i].longest + 3.0, t[i].work / m + 0.3 * t[i].longest));
       if (i == 0 || end < t_tiles) {
@@ -1617,17 +1692,23 @@ void plan_shared(const ChunkArgs& a, std::vector<Req>& reqs, int num_splits, int
     const double end = std::max(bytes / 6.5e6 + 5.0, std::max(t_rows, t_tiles)) + 0.05 * (t_rows + t_tiles);
     if (c == 0 || end < best) {
       best = end;
-      best_piece = bk;
       best_tiles = bt;
-      g.row_ctas = n;
+      best_runs = runs;
     }
   }
-  if (num_splits == 0)
-    for (Req& q : reqs) {
-      const int len = q.few ? q.few : std::max(q.first, q.last), piece = q.few ? pieces[best_piece] : t[best_tiles].tiles;
-      q.ns = std::min(kMaxAuto, std::max(1, (len + piece - 1) / piece));
-    }
-  g.row_ctas = (int)std::min<int64_t>(g.row_ctas, row_items[best_piece]);
+  for (Req& q : reqs)
+    if (!q.few && num_splits == 0)
+      q.ns = std::min(kMaxAuto, std::max(1, (std::max(q.first, q.last) + t[best_tiles].tiles - 1) / t[best_tiles].tiles));
+  if (row > 0) {
+    // runs of a third of a tile's worth would only cut more; a request is cut into no more than 256 pieces
+    int longest = 1;
+    for (const Req& q : reqs) longest = std::max(longest, q.few);
+    if (num_splits) best_runs = num_splits;
+    g.run = (int)std::max<int64_t>({(row + best_runs - 1) / best_runs, kStart + 1, (longest / kKeys + kStart) / (kMaxAuto - 2) + 1});
+    g.runs = (int)((row + g.run - 1) / g.run);
+    g.row_ctas = g.runs * groups;
+  }
+  g.ctas = (int)std::min<int64_t>(std::max(sms / 8, sms - g.row_ctas), t[best_tiles].items);
 }
 
 sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, const Prefixes& pf, int r0, int r1,
@@ -1635,20 +1716,38 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
   std::vector<Req> reqs;
   reqs.reserve(pf.n > 0 ? 2 * (size_t)(r1 - r0) : (size_t)(r1 - r0));
   g.r0 = r0;
-  // A prefix is computed once where that is less work than with each of its requests, in the time of key tiles of
-  // pairs of query tiles: it takes an item more a request, and fp32 partials of all rows twice.
-  auto shares = [&](int r, int end, int64_t skip) {
-    int some = 0, n = 0, units = 0;
+  // What it saves to compute a group's prefix once, in the time of key tiles of a pair of query tiles; kNot: there is
+  // nothing to share. An item takes 3 more beside its tiles, few rows 0.4 for 16 keys and twice that more a piece.
+  constexpr double kNot = -1e300;
+  auto saves = [&](int r, int end, int64_t skip) -> double {
+    int some = 0, n = 0;
+    double apart = 0, own = 0;
+    auto items = [&](int m, int64_t keys) {  // of m tokens over keys: a single query tile takes half of a pair's time
+      const int q = (m + a.TQ - 1) / a.TQ;
+      return a.Hkv * (0.5 * q * (double)((keys + kBN - 1) / kBN) + 3.0 * ((q + 1) / 2));
+    };
     for (int x = r; x < end; ++x) {
       const int m = qi[x + 1] - qi[x];
-      some += m > 0;
+      if (m == 0) continue;
+      const int64_t len = (int64_t)ki[x + 1] - ki[x];
+      ++some;
       n += m;
-      units += ((m + a.TQ - 1) / a.TQ + 1) / 2;
+      apart += items(m, len);
+      own += (int64_t)m * a.G <= 16 && a.row_box > 0 ? 0.4 * (double)((len - skip + 15) / 16 + kStart) * ((a.Hkv + 7) / 8) : items(m, len - skip);
     }
-    if (some < 2 || skip == 0) return false;
-    const double tiles = (double)((skip + kBN - 1) / kBN), all = ((n + a.TQ - 1) / a.TQ + 1) / 2;
-    return (units - all) * tiles * a.Hkv > all * a.Hkv * kItem + 2.0 * n * a.Hq * 8.0 * (a.d + 1) / 65536.0 + kMerge;
+    if (some < 2 || skip == 0) return kNot;
+    return apart - own - items(n, skip) - 2.0 * n * a.Hq * 8.0 * (a.d + 1) / 65536.0;
   };
+  // It has to save the time of the merge, 4 us, or 2.5 tiles of each SM. (num_splits asks for it.)
+  bool worth = num_splits > 0;
+  if (pf.n > 0 && !worth) {
+    double sum = 0;
+    for (int i = 0; i < pf.n; ++i) {
+      const int from = std::max(r0, (int)pf.indptr[i]), to = std::min(r1, (int)pf.indptr[i + 1]);
+      if (from < to) sum += std::max(0.0, saves(from, to, pf.prefix[i]));
+    }
+    worth = sum > 2.5 * sms;
+  }
   auto tiles_of = [&](int n, int64_t len, int u) {  // key tiles of pair u
     int gt, wl;
     const int64_t t0 = (int64_t)2 * u * a.TQ, te = std::min<int64_t>(n, t0 + 2 * a.TQ), p0 = len - n;
@@ -1668,7 +1767,7 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
     if (pf.n > 0) {
       while (pf.indptr[i + 1] <= r) ++i;
       end = std::min(r1, (int)pf.indptr[i + 1]);  // (a group that two launches meet in is two groups)
-      if (shares(r, end, pf.prefix[i])) {
+      if (const double saved = worth ? saves(r, end, pf.prefix[i]) : kNot; num_splits > 0 ? saved > kNot : saved > 0) {
         int lead = r;
         while (qi[lead + 1] == qi[lead]) ++lead;
         const int n = qi[end] - qi[r], tiles = (pf.prefix[i] + kBN - 1) / kBN, me = (int)reqs.size();
@@ -1683,9 +1782,13 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
     for (; r < end; ++r)
       if (qi[r + 1] > qi[r]) add(r, 0, -1, 0);
   }
-  if (g.shared) plan_shared(a, reqs, num_splits, sms, g);
-  else
-    for (Req& q : reqs) q.few = 0;
+  bool rows = false;
+  for (Req& q : reqs) {
+    // (pages that hold no boxes of 8 tokens, copied token by token: 44 us for a case that takes 33 in items)
+    if (!g.shared || a.row_box == 0) q.few = 0;
+    rows = rows || q.few > 0;
+  }
+  if (rows) plan_shared(a, reqs, num_splits, sms, g);
   // Chunks. The launch ends when the SM with the most to do does: with the items sorted by length and
   // handed out one by one that is about the largest of an SM's share, the longest item, and k times the
   // item number (k - 1) * SMs + 1 (some SM has k items of at least that length). Cutting shortens items
@@ -1693,7 +1796,7 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
   // pieces from the longest list down are tried and the best estimate is kept. (64 single tokens over
   // 522,892 cached ones: 345 us whole, 333 in the pieces found, 421 in 16 pieces each; a 2048-token
   // prompt: 79 us in pieces of 8 tiles, 40 whole.)
-  if (!g.shared && num_splits == 0 && most > 2) {
+  if (!rows && num_splits == 0 && most > 2) {
     auto chunks = [&](int tiles, int piece) { return std::min(kMaxAuto, std::max(1, (tiles + piece - 1) / piece)); };
     auto estimate = [&](int piece) {
       constexpr int kBins = 32;
@@ -1708,7 +1811,7 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
         work += len * (double)items;
         longest = std::max(longest, (double)tiles / ns + kItem);
         bins[std::min(kBins - 1, (int)(len / step))] += items;
-        if (ns > 1) {
+        if (ns > 1 || q.pre != -1) {
           cut = true;
           work += (double)q.n * a.Hq * ns * 8.0 * (a.d + 1) / 65536.0;  // (a tile of K and V is 64 KB at most)
         }
@@ -1733,24 +1836,27 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
     }
     for (Req& q : reqs) q.ns = chunks(std::max(q.first, q.last), best);
   }
-  auto longest = [](const Req& q) { return q.few ? 1e9 + (double)q.few / q.ns : (double)std::max(q.first, q.last) / q.ns; };
+  auto longest = [](const Req& q) { return q.few ? 1e9 : (double)std::max(q.first, q.last) / q.ns; };
   std::vector<int> order(reqs.size()), rank(reqs.size());
   std::iota(order.begin(), order.end(), 0);
   std::stable_sort(order.begin(), order.end(), [&](int x, int y) { return longest(reqs[x]) > longest(reqs[y]); });
   for (int i : order) {
-    const Req& q = reqs[i];
+    Req& q = reqs[i];
     const int64_t part = g.parts;
+    const int64_t tiles = q.few ? (q.few + 15) / 16 + kStart : 0;  // (first in the order: base counts tiles so far)
+    if (q.few) q.ns = (int)((g.items + tiles - 1) / g.run - g.items / g.run + 1) * row_turns(a.Hkv);
     if (q.ns > 1 || q.pre != -1) {
       if (q.pre != -2) g.rows += (int64_t)q.n * a.Hq;
       g.parts += (int64_t)q.n * a.Hq * q.ns;
     }
-    if (q.few) {
-      g.n_rows += 1;
-      g.row_items = g.items + (int64_t)a.Hkv * q.ns;
-    }
     rank[i] = (int)g.ranks.size();
     g.ranks.push_back(Group::Rank{q.req, q.n, q.ns, g.items, g.rows, part, q.skip, q.pre, q.end, q.lead});
-    g.items += (int64_t)q.units * a.Hkv * q.ns;
+    if (q.few) {
+      ++g.n_rows;
+      g.items += tiles;
+    } else {
+      g.items += (int64_t)q.units * a.Hkv * q.ns;
+    }
   }
   for (Group::Rank& k : g.ranks)
     if (k.pre >= 0) k.pre = rank[k.pre];
@@ -1762,6 +1868,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Maps {
   CUtensorMap q, k, v, k4, v4;  // k4, v4: boxes of 32 tokens, beside those of 8
+  RowMaps<true> rows;
 };
 
 template <int D, int CAP, bool SHARED>
@@ -1772,15 +1879,13 @@ sta_status launch_group(const Maps& m, const ChunkArgs& a, const Group& g, cudaS
     const Group::Rank& k = g.ranks[i];
     p.base[i] = (int32_t)k.base;
     p.rows[i] = (int32_t)k.row1;
-    p.part[i] = (int32_t)k.part;
-    p.qn[i] = k.qn;
-    p.req[i] = (uint16_t)k.req;
-    p.ns[i] = (uint16_t)k.ns;
     if constexpr (SHARED) {
-      p.skip[i] = k.skip;
-      p.pre[i] = (int16_t)k.pre;
-      p.end[i] = (uint16_t)k.end;
-      p.lead[i] = (uint16_t)k.lead;
+      p.rank[i] = Rank{(int32_t)k.part, k.qn, k.skip, (uint16_t)k.req, (uint16_t)k.ns, (uint16_t)k.end, (uint16_t)k.lead, (int16_t)k.pre, 0};
+    } else {
+      p.part[i] = (int32_t)k.part;
+      p.qn[i] = k.qn;
+      p.req[i] = (uint16_t)k.req;
+      p.ns[i] = (uint16_t)k.ns;
     }
   }
   p.base[p.n] = (int32_t)g.items;
@@ -1788,27 +1893,31 @@ sta_status launch_group(const Maps& m, const ChunkArgs& a, const Group& g, cudaS
   if constexpr (SHARED) {
     p.n_rows = g.n_rows;
     p.row_ctas = g.row_ctas;
-    grid = (unsigned)(g.items - g.row_items + g.row_ctas);
+    p.ctas = g.ctas;
+    p.runs = g.runs;
+    p.run = g.run;
+    if (g.row_ctas > 0) grid = (unsigned)(g.row_ctas + g.ctas);
   }
   auto kern = chunk_kernel<D, CAP, SHARED>;
   STA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM));
-  kern<<<grid, kThreads, Cfg<D>::SMEM, st>>>(m.q, m.k, m.v, m.k4, m.v4, a, p, g.r0);
+  RowMaps<SHARED> rows;
+  if constexpr (SHARED) rows = m.rows;
+  kern<<<grid, kThreads, Cfg<D>::SMEM, st>>>(m.q, m.k, m.v, m.k4, m.v4, rows, a, p, g.r0);
   STA_LAUNCH_CHECK();
   if (g.rows > 0) {
     if constexpr (SHARED) {
-      // started as the first kernel's CTAs end: it finds its rows, then waits for the last of them
       cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3((unsigned)cdiv(g.rows, 8));
-      cfg.blockDim = dim3(256);
+      cfg.gridDim = dim3((unsigned)cdiv(g.rows, 16));
+      cfg.blockDim = dim3(128);
       cfg.stream = st;
       cudaLaunchAttribute early{};
       early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
       early.val.programmaticStreamSerializationAllowed = 1;
       cfg.attrs = &early;
       cfg.numAttrs = 1;
-      STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D, CAP, SHARED>, a, p, g.r0, (int)g.rows));
+      STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, chunk_merge_shared_kernel<D, CAP>, a, p, g.r0, (int)g.rows));
     } else {
-      chunk_merge_kernel<D, CAP, SHARED><<<(unsigned)cdiv(g.rows, 8), 256, 0, st>>>(a, p, g.r0, (int)g.rows);
+      chunk_merge_kernel<D, CAP><<<(unsigned)cdiv(g.rows, 8), 256, 0, st>>>(a, p, g.r0, (int)g.rows);
       STA_LAUNCH_CHECK();
     }
   }
@@ -1819,7 +1928,7 @@ template <int D>
 sta_status launch_any(const Maps& m, const ChunkArgs& a, const Group& g, cudaStream_t st) {
   if (g.shared)
     return g.ranks.size() <= kSmallShared ? launch_group<D, kSmallShared, true>(m, a, g, st)
-                                          : launch_group<D, kLargePlan, true>(m, a, g, st);
+                                          : launch_group<D, kLargeShared, true>(m, a, g, st);
   return g.ranks.size() <= kSmallPlan ? launch_group<D, kSmallPlan, false>(m, a, g, st) : launch_group<D, kLargePlan, false>(m, a, g, st);
 }
 
@@ -1876,13 +1985,14 @@ sta_status chunk_fwd(const void* q, int64_t q_stride, const void* k_pages, const
   a.page_shift = l - 1;
   const int box = std::gcd(page_size, kBN);
   a.box = box % 8 == 0 ? box : 0;
+  a.row_box = std::min(a.box, 16);
   a.scale_log2 = scale * kLog2e;
   int dev = 0, sms = 152;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaGetLastError();  // a size query also works where there is no device
   std::vector<Group> groups;
   int64_t parts = 0;
-  const int batch = pf.n > 0 ? kLargePlan * 2 / 3 : kLargePlan;  // (a prefix has two requests at least)
+  const int batch = pf.n > 0 ? kLargeShared * 2 / 3 : kLargePlan;  // (a prefix has two requests at least)
   for (int r0 = 0; r0 < n_req; r0 += batch) {
     Group g;
     const sta_status st = plan_group(a, q_indptr_host, kv_indptr_host, pf, r0, std::min(n_req, r0 + batch), num_splits, sms, g);
@@ -1932,6 +2042,10 @@ sta_status chunk_fwd(const void* q, int64_t q_stride, const void* k_pages, const
     m.k4 = m.k;
     m.v4 = m.v;
   }
+  if (pf.n > 0 && a.row_box > 0)
+    maps = maps && make_row_map(&m.rows.k, k_pages, d, Hkv, rows, a.row_box) && make_row_map(&m.rows.v, v_pages, d, Hkv, rows, a.row_box);
+  else
+    m.rows.k = m.rows.v = m.k;  // not used
   if (!maps) {
     note_cuda_error(cudaErrorInvalidValue);  // tensor-map encoding refused
     return STA_ERR_CUDA;

@@ -27,37 +27,31 @@ def no_device_error(cuda_ok):
     assert sta.sta_device_error(reset=True) == 0
 
 
-def _is_shared(c, splits=0):
-    """A prefix is taken apart: partials, also where nothing is cut."""
+def _run(dev, c, scale=None, splits=(0, 1, 3)):
+    """As the library chooses; with every prefix taken apart, in one piece and in three (own parts of few rows then in
+    so many runs)."""
     import split_kv_decode_bsr_gb300 as sta
 
-    return sta.prefix_workspace_bytes(c.q_indptr, c.kv_indptr, len(c.new), c.group_indptr, c.prefix, c.Hq, c.Hkv, c.d, c.P, 1) > 256
-
-
-def _run(dev, c, scale=None, shared=True, **kw):
-    import split_kv_decode_bsr_gb300 as sta
-
-    assert shared is None or _is_shared(c) == shared
     scale = 1 / math.sqrt(c.d) if scale is None else scale
-    o, lse = sta.sta_prefix_fwd_paged(**c.dev(dev), scale=scale, **kw)
-    check_chunk(o, lse, c.ref(scale), int(c.q_indptr[-1]), f"{c.P} {kw}")
-    return o, lse
+    ref = c.ref(scale)
+    for n in splits:
+        o, lse = sta.sta_prefix_fwd_paged(**c.dev(dev), scale=scale, num_splits=n)
+        check_chunk(o, lse, ref, int(c.q_indptr[-1]), f"{c.P} {n}")
 
 
 def _whole_pages(tokens, P):
     return [t // P * P for t in tokens]
 
 
-@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (4, 4, 64), (7, 1, 128), (12, 4, 64), (16, 1, 64), (130, 2, 64)])
-@pytest.mark.parametrize("P", [1, 8, 16, 17, 48, 100, 128])
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (4, 4, 64), (7, 1, 128), (9, 3, 64), (16, 1, 64), (130, 2, 64), (24, 12, 64)])
+@pytest.mark.parametrize("P", [1, 8, 16, 48, 100, 128])
 def test_prefix_ragged(dev, Hq, Hkv, d, P):
     # groups of three, one, four and two requests; own parts of one token to many, chunks that end in the middle of tiles
     prefix = _whole_pages([1200, 900, 1100, 777], P)
     new = [1, 1, 5, 1, 0, 1, 33, 2, 1, 1]
     own = [1, 140, 5, 20, 9, 129, 40, 300, 128, 16]
     c = SharedCase(P + d, [3, 1, 4, 2], prefix, new, own, Hq, Hkv, d, P, pad_rows=2)
-    for splits in (0, 1, 3):
-        _run(dev, c, shared=None if Hq == 130 else True, num_splits=splits)  # (65 heads a KV head: as the plan chooses)
+    _run(dev, c, splits=(0, 1, 3, 40))
 
 
 @pytest.mark.parametrize("n", [2, 15, 16, 17, 33, 70])
@@ -81,16 +75,14 @@ def test_prefix_rows_are_those_of_the_chunk_attention_where_nothing_is_shared(de
         x.pop("group_indptr_host"), x.pop("prefix_host")
         want = sta.sta_chunk_fwd_paged(**x)
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
-        assert not _is_shared(c)
 
 
 def test_prefix_long_chunks(dev):
-    # whole query tiles of each request: shared or not as the plan chooses, and the same with the prefix cut
+    # whole query tiles of each request
     c = SharedCase(11, [3], [256], [150, 64, 257], [150, 70, 300], 8, 2, 64, 16)
-    _run(dev, c, shared=False)
+    _run(dev, c)
     c = SharedCase(12, [8], [1920], [40, 41, 40, 42, 40, 39, 38, 40], [40, 41, 50, 42, 60, 40, 150, 129], 8, 2, 64, 64)
-    for splits in (0, 1, 5):
-        _run(dev, c, num_splits=splits)
+    _run(dev, c, splits=(0, 1, 5))
 
 
 def test_prefix_many_requests_in_several_launches(dev):
@@ -115,14 +107,14 @@ def test_prefix_strides_padding_outputs_and_workspace(dev):
     wide[:, :1024] = x["q"].flatten(1)
     x["q"] = wide[:, :1024].unflatten(1, (8, 128))
     o, lse = torch.full((n + 5, 8, 128), 5.0, device=dev, dtype=torch.bfloat16), torch.full((n + 5, 8), 5.0, device=dev)
-    need = sta.prefix_workspace_bytes(c.q_indptr, c.kv_indptr, 4, c.group_indptr, c.prefix, 8, 2, 128, 16)
+    need = sta.prefix_workspace_bytes(c.q_indptr, c.kv_indptr, 4, c.group_indptr, c.prefix, 8, 2, 128, 16, num_splits=2)
     ws = torch.full((need + 256,), 255, dtype=torch.uint8, device=dev)
-    got = sta.sta_prefix_fwd_paged(**x, scale=scale, o=o, lse=lse, workspace=ws[:need])
+    got = sta.sta_prefix_fwd_paged(**x, scale=scale, num_splits=2, o=o, lse=lse, workspace=ws[:need])
     assert got[0] is o and got[1] is lse
     check_chunk(o, lse, ref, n)
     assert (o[n:] == 5.0).all() and (lse[n:] == 5.0).all() and (ws[need:] == 255).all()
     with pytest.raises(ValueError):
-        sta.sta_prefix_fwd_paged(**x, workspace=ws[:256])
+        sta.sta_prefix_fwd_paged(**x, num_splits=2, workspace=ws[:256])
 
 
 def test_prefix_streams_and_repeats(dev):
@@ -142,7 +134,8 @@ def test_prefix_streams_and_repeats(dev):
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
-def test_prefix_captured_and_replayed_with_other_lengths(dev):
+@pytest.mark.parametrize("splits", [0, 1, 4])
+def test_prefix_captured_and_replayed_with_other_lengths(dev, splits):
     import torch
 
     import split_kv_decode_bsr_gb300 as sta
@@ -155,7 +148,7 @@ def test_prefix_captured_and_replayed_with_other_lengths(dev):
     x["q"] = q
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        o, lse = sta.sta_prefix_fwd_paged(**x)
+        o, lse = sta.sta_prefix_fwd_paged(**x, num_splits=splits)
     for seed, new, own in ((1, [2] * n, [60] * n), (2, [1, 2, 0, 1, 0, 2], [1, 2, 0, 33, 17, 48]), (3, [1] * n, [20] * n),
                            (4, [0, 0, 0, 1, 0, 0], [0, 7, 0, 9, 0, 0])):
         c = SharedCase(16 + seed, [n], [prefix], new, own, 8, 2, 64, 16)
@@ -184,15 +177,14 @@ def test_prefix_damaged_lists_and_lengths_are_reported(dev):
     import split_kv_decode_bsr_gb300 as sta
 
     c = SharedCase(17, [4], [512], [1] * 4, [5, 6, 30, 9], 8, 2, 64, 16)
-    assert _is_shared(c)
-    good = sta.sta_prefix_fwd_paged(**c.dev(dev))
+    good = sta.sta_prefix_fwd_paged(**c.dev(dev), num_splits=2)
     torch.cuda.synchronize()
     assert sta.sta_device_error() == 0
 
     def broken(change):
         x = c.dev(dev)
         change(x)
-        got = sta.sta_prefix_fwd_paged(**x)
+        got = sta.sta_prefix_fwd_paged(**x, num_splits=2)
         torch.cuda.synchronize()
         return got, sta.sta_device_error(reset=True)
 
@@ -218,9 +210,9 @@ def test_prefix_a_query_that_is_no_number(dev):
 
     c = SharedCase(18, [3], [512], [1, 2, 1], [5, 20, 9], 4, 2, 64, 16)
     x = c.dev(dev)
-    want = sta.sta_prefix_fwd_paged(**x)
+    want = sta.sta_prefix_fwd_paged(**x, num_splits=2)
     x["q"][2, 1, 7] = float("nan")
-    got = sta.sta_prefix_fwd_paged(**x)
+    got = sta.sta_prefix_fwd_paged(**x, num_splits=2)
     dead = torch.zeros(4, 4, dtype=torch.bool, device=dev)
     dead[2, 1] = True
     assert torch.isnan(got[0][dead]).all() and torch.isnan(got[1][dead]).all()
@@ -265,7 +257,8 @@ def test_a_forked_batch_is_served_together(dev):
         qi, ki = indptr(new), indptr(after)
         qn = sta.sta_norm_rope_append_paged(q, k, v, kp, vp, ptr, idx, to(qi), to(ki), rope, qw, kw)
         if shared:
-            o, lse = sta.sta_prefix_fwd_paged(qn, kp, vp, ptr, idx, to(qi), qi, to(ki), ki, [0, n], [shared])
+            o, lse = sta.sta_prefix_fwd_paged(qn, kp, vp, ptr, idx, to(qi), qi, to(ki), ki, [0, n], [shared],
+                                              num_splits=2)
         else:
             o, lse = sta.sta_chunk_fwd_paged(qn, kp, vp, ptr, idx, to(qi), qi, to(ki), ki)
         for r in range(n):
