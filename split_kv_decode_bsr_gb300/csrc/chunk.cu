@@ -457,6 +457,12 @@ struct RowMaps<true> {
   CUtensorMap k, v;
 };
 
+// The launches with shared prefixes may start while the one before them ends. grid_wait(): it has ended, and what it wrote is
+// there. grid_go(): the next one may start (when all CTAs have come here). The first kernel touches no memory of the
+// call before its wait, and lets the merge start after it, since that looks its rows up before its own.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // A piece: the rank's rows of KV heads h0 .. , chunk c of its 16-key tiles (j0 .. j1 - 1).
 struct Piece {
   int rank, h0, c;      // rank -1: none
@@ -490,6 +496,8 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& A, const CUtensorMap& 
     fence_mbar_init();
   }
   __syncthreads();
+  grid_wait();
+  grid_go();
   const int P0 = A.page_size;
   auto page_no = [&](int tok) -> int { return A.page_shift < 0 ? tok : (int)(__umulhi((uint32_t)tok, A.page_mul) >> A.page_shift); };
 
@@ -803,7 +811,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if constexpr (SHARED) {
-    asm volatile("griddepcontrol.launch_dependents;");
     if ((int)blockIdx.x < P.row_ctas) {
       few_rows<D, CAP>(A, R.k, R.v, P, req0, smem);
       return;
@@ -840,6 +847,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  if constexpr (SHARED) {
+    grid_wait();
+    grid_go();
+  }
 
   // Every role runs over the same items: item k is in sh.item[k & 1]. A wait that runs out ends the
   // role's loop, and then, by their own waits, the others'.
@@ -1481,6 +1492,7 @@ __global__ void __launch_bounds__(128) chunk_merge_shared_kernel(const __grid_co
                                                                  const __grid_constant__ Plan<CAP, true> P, int req0, int n_rows) {
   constexpr int NV = D / 32, U = 4;  // 16-byte parts of a lane, partials on their way
   const int lane = threadIdx.x & 31, z = lane & 1, sub = (lane >> 3) * 2 + z;  // sub: of the 8 lanes of a row
+  grid_go();
   const int64_t mr = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * 4 + ((lane >> 1) & 3);
   bool some = mr < n_rows;
   int lo = 0, hi = P.n - 1;  // the first rank whose rows end behind this one
@@ -1510,7 +1522,7 @@ __global__ void __launch_bounds__(128) chunk_merge_shared_kernel(const __grid_co
         record_error(A.err, 0x609);
     }
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials
+  grid_wait();  // the partials
   const int s = some ? na + k.ns : 0;
   int most = s;
 #pragma unroll
@@ -1638,14 +1650,14 @@ constexpr double kItem = 2.0;    // an item's prologue and epilogue, in key tile
 constexpr double kMerge = 4.0;   // the merge launch
 
 // Chunks of a launch with shared prefixes, and the CTAs of few rows. The launch ends when its bytes have come, when the
-// last of the prefixes' items is done or the last CTA of few rows. Measured: a run of few rows takes 3.5 us and 0.6 a tile of 16
-// keys (and a piece 2 of them more); an item of query tiles 7.5 us and 1.5 a key tile (heads of 64: 1.0), 3 again for
+// last of the prefixes' items is done or the last CTA of few rows. Measured: a run of few rows takes 3.5 us and 1.0 a tile of 16 keys
+// of 8 heads of 128 (others 0.65; a piece 2 of them more); an item of query tiles 7.5 us and 1.5 a key tile (heads of 64: 1.0), 3 again for
 // each further one of its CTA. For each share of the SMs the length of the prefixes' pieces that ends soonest is taken, and
 // the best share.
 void plan_shared(const ChunkArgs& a, std::vector<Req>& reqs, int num_splits, int sms, Group& g) {
   constexpr int kTiles = 14, kKeys = 16;
-  const int heads = row_heads(a.Hkv), groups = (a.Hkv + heads - 1) / heads, turns = row_turns(a.Hkv);
-  const double tile_us = a.d == 128 ? 1.5 : 1.0, row_us = 0.6 / turns, key_bytes = 4.0 * a.d;
+  const int heads = row_heads(a.Hkv), groups = (a.Hkv + heads - 1) / heads;
+  const double tile_us = a.d == 128 ? 1.5 : 1.0, row_us = heads == 8 && a.d == 128 ? 1.0 : 0.65, key_bytes = 4.0 * a.d;
   int64_t row = 0;  // the tiles of few rows, one after the other
   double bytes = 0;
   int most = 1;
@@ -1654,36 +1666,41 @@ void plan_shared(const ChunkArgs& a, std::vector<Req>& reqs, int num_splits, int
     if (q.few) row += (q.few + kKeys - 1) / kKeys + kStart;
     else most = std::max(most, std::max(q.first, q.last));
   }
-  struct Tiles {  // the items of pieces of `tiles` key tiles: the longest one's time and that of all, us
+  struct Tiles {  // the items of pieces of `tiles` key tiles: the times of the longest one, of all and of the merge, us
     int tiles;
     int64_t items;
-    double longest, work;
+    double longest, work, merge;
   } t[kTiles];
   int nt = 0;
   for (int tiles = most; nt < kTiles; tiles = std::max(2, tiles * 3 / 4)) {
-    Tiles x{tiles, 0, 0, 0};
+    Tiles x{tiles, 0, 0, 0, 0};
+    int pieces = 0;
     for (const Req& q : reqs)
       if (!q.few) {
         const int len = std::max(q.first, q.last), ns = num_splits ? num_splits : std::min(kMaxAuto, (len + tiles - 1) / tiles);
         const int64_t items = (int64_t)q.units * a.Hkv * ns;
         x.items += items;
         x.work += (tile_us * 0.5 * (q.first + q.last) / ns + 3.0) * (double)items;
-        x.work += (double)q.n * a.Hq * ns * 8.0 * (a.d + 1) / 45e3;  // partials, 45 KB/us of an SM
+        x.merge += (double)q.n * a.Hq * ns * 4.0 * (a.d + 1) / 5e6;
         x.longest = std::max(x.longest, tile_us * len / ns);
+        pieces = std::max(pieces, ns);
       }
+    x.merge += 0.25 * pieces;  // (a row's are read four at a time)
     t[nt++] = x;
     if (tiles <= 2 || num_splits) break;
   }
   double best = 0;
   int best_tiles = 0, best_runs = 0;
-  const int shares = row > 0 ? 24 : 1;
+  constexpr int shares = 24;
   for (int c = 0; c < shares; ++c) {
-    const int runs = row > 0 ? std::max(1, std::min(sms - 1, sms * (c + 1) / (shares + 1)) / groups) : 0, m = std::max(1, sms - runs * groups);
-    const double t_rows = row > 0 ? 3.5 + row_us * (double)((row + runs - 1) / runs) : 0.0;
+    const int runs = std::max(1, std::min(sms - 1, sms * (c + 1) / (shares + 1)) / groups), m = std::max(1, sms - runs * groups);
+    const double t_rows = 3.5 + row_us * (double)((row + runs - 1) / runs);
     double t_tiles = 0;
     int bt = 0;
     for (int i = 0; i < nt; ++i) {
-      const double end = 4.5 + (t[i].items <= m ? t[i].longest + 3.0 : std::max(t[i].longest + 3.0, t[i].work / m + 0.3 * t[i].longest));
+      // whole rounds where there are few, else the share of a CTA and a half of the longest item
+      const double rounds = (double)((t[i].items + m - 1) / m), each = t[i].work / (double)t[i].items;
+      const double end = 4.5 + std::max(t[i].longest + 3.0, rounds <= 3.0 ? rounds * each : t[i].work / m + 0.5 * t[i].longest) + t[i].merge;
       if (i == 0 || end < t_tiles) {
         t_tiles = end;
         bt = i;
@@ -1699,8 +1716,8 @@ void plan_shared(const ChunkArgs& a, std::vector<Req>& reqs, int num_splits, int
   for (Req& q : reqs)
     if (!q.few && num_splits == 0)
       q.ns = std::min(kMaxAuto, std::max(1, (std::max(q.first, q.last) + t[best_tiles].tiles - 1) / t[best_tiles].tiles));
-  if (row > 0) {
-    // runs of a third of a tile's worth would only cut more; a request is cut into no more than 256 pieces
+  {
+    // a run longer than what a piece costs of itself; a request is cut into no more than 256 pieces
     int longest = 1;
     for (const Req& q : reqs) longest = std::max(longest, q.few);
     if (num_splits) best_runs = num_splits;
@@ -1783,10 +1800,17 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
       if (qi[r + 1] > qi[r]) add(r, 0, -1, 0);
   }
   bool rows = false;
+  int64_t items = 0;
   for (Req& q : reqs) {
     // (pages that hold no boxes of 8 tokens, copied token by token: 44 us for a case that takes 33 in items)
     if (!g.shared || a.row_box == 0) q.few = 0;
     rows = rows || q.few > 0;
+    items += q.few ? 0 : (int64_t)q.units * a.Hkv;
+  }
+  // three rounds of items and more: those of few rows are dealt out with them, by CTAs that take over one another's
+  if (num_splits == 0 && items > 3 * sms) {
+    for (Req& q : reqs) q.few = 0;
+    rows = false;
   }
   if (rows) plan_shared(a, reqs, num_splits, sms, g);
   // Chunks. The launch ends when the SM with the most to do does: with the items sorted by length and
@@ -1871,6 +1895,22 @@ struct Maps {
   RowMaps<true> rows;
 };
 
+// A launch that may start while the one before it on the stream ends (see grid_wait).
+template <class... F, class... T>
+cudaError_t launch_early(void (*kern)(F...), unsigned grid, int threads, int smem, cudaStream_t st, const T&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 template <int D, int CAP, bool SHARED>
 sta_status launch_group(const Maps& m, const ChunkArgs& a, const Group& g, cudaStream_t st) {
   Plan<CAP, SHARED> p;
@@ -1900,22 +1940,15 @@ sta_status launch_group(const Maps& m, const ChunkArgs& a, const Group& g, cudaS
   }
   auto kern = chunk_kernel<D, CAP, SHARED>;
   STA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM));
-  RowMaps<SHARED> rows;
-  if constexpr (SHARED) rows = m.rows;
-  kern<<<grid, kThreads, Cfg<D>::SMEM, st>>>(m.q, m.k, m.v, m.k4, m.v4, rows, a, p, g.r0);
-  STA_LAUNCH_CHECK();
+  if constexpr (SHARED) {
+    STA_CUDA_TRY(launch_early(kern, grid, kThreads, Cfg<D>::SMEM, st, m.q, m.k, m.v, m.k4, m.v4, m.rows, a, p, g.r0));
+  } else {
+    kern<<<grid, kThreads, Cfg<D>::SMEM, st>>>(m.q, m.k, m.v, m.k4, m.v4, RowMaps<false>{}, a, p, g.r0);
+    STA_LAUNCH_CHECK();
+  }
   if (g.rows > 0) {
     if constexpr (SHARED) {
-      cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3((unsigned)cdiv(g.rows, 16));
-      cfg.blockDim = dim3(128);
-      cfg.stream = st;
-      cudaLaunchAttribute early{};
-      early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      early.val.programmaticStreamSerializationAllowed = 1;
-      cfg.attrs = &early;
-      cfg.numAttrs = 1;
-      STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, chunk_merge_shared_kernel<D, CAP>, a, p, g.r0, (int)g.rows));
+      STA_CUDA_TRY(launch_early(chunk_merge_shared_kernel<D, CAP>, (unsigned)cdiv(g.rows, 16), 128, 0, st, a, p, g.r0, (int)g.rows));
     } else {
       chunk_merge_kernel<D, CAP><<<(unsigned)cdiv(g.rows, 8), 256, 0, st>>>(a, p, g.r0, (int)g.rows);
       STA_LAUNCH_CHECK();
