@@ -13,6 +13,8 @@
 // again), and puts the cosines and sines of the token that it has come to into a table of its own. A head is read once
 // and written once; the products in between stay in fp32 and are rounded once. The turns are exact at any position, as
 // in the rotary kernel.
+#include <type_traits>
+
 #include "rope.inl"
 
 namespace sta {
@@ -21,10 +23,13 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 template <typename T> constexpr int kMany = sizeof(T) == 2 ? 2 : 4;  // units of a lane where a head has more than 32 (at most 64, 128)
 constexpr int kMaxGrid = 152 * 2;  // CTAs of a backward pass, each with a row of partial sums for dw
+// What a lane holds of a head's turning part: vectors half a rotation apart; neighbouring pairs; or vectors as they come,
+// whose partners half a rotation away, where that is no whole number of vectors, it reads from the other lanes' copies.
+enum Layout { kHalves, kPairs, kPlain };
 template <int NU> constexpr int kSlots = NU <= 2 ? 3 : 2;  // pieces that a warp has on their way
-template <int W, bool IL, int NU>
+template <int W, int LY, int NU>
 constexpr int ctas_an_sm(bool backward) {
-  return W == 1 || NU * (IL ? 1 : 2) > 2 ? 1 : (backward ? 2 : 3);
+  return W == 1 || NU * (LY == kHalves ? 2 : 1) > 2 ? 1 : (backward || (LY == kPlain && NU == 2) ? 2 : 3);
 }
 enum Mode { kForward, kAppend, kBackward };
 
@@ -155,8 +160,9 @@ __device__ __forceinline__ void copy_wait() {
 // couples of pairs, first elements in A and second ones in B, for the packed instructions (twice the
 // products of an issue slot, which is what bounds these kernels first: 8192 tokens x 40 heads of 128 in
 // bf16 took 36.9 us with scalar ones). A unit that does not turn has its elements there just so (half layout: in A).
-template <typename T, int W, bool IL, int NU>
+template <typename T, int W, int LY, int NU>
 struct Units {
+  static constexpr bool IL = LY != kHalves, PL = LY == kPlain;  // a vector a unit; with partners elsewhere
   static constexpr int WI = IL && W == 1 ? 2 : W;  // elements of a vector: whole pairs when interleaved
   static constexpr int PP = IL ? WI / 2 : WI;      // pairs of a unit
   static constexpr int NP = (PP + 1) / 2;
@@ -164,6 +170,7 @@ struct Units {
   int off[NU];   // first element
   bool turn[NU];
   int half, d;
+  int partner[PL ? NU : 1][PL ? W : 1];  // byte of an element's partner in a slot
   static constexpr int V = NU * (IL ? 1 : 2);      // vectors of a head that a lane holds
   struct Row {  // elements that are not there are 0
     Vec<T, WI> a[NU], b[IL ? 1 : NU];
@@ -180,7 +187,40 @@ struct Units {
       const int u = l + (j << A.log_l);
       turn[j] = u < A.rot_units;
       unit[j] = u < A.units ? u : -1;
-      off[j] = turn[j] ? u * WI : (u < A.units ? A.rot + (u - A.rot_units) * WI : 0);
+      off[j] = IL || turn[j] ? u * WI : A.rot + (u - A.rot_units) * WI;
+      if (unit[j] < 0) off[j] = 0;
+      if constexpr (PL) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const int p = partner_of(off[j] + e, A.rot), v = p / W;
+          partner[j][e] = (v >> A.log_l) * 512 + ((threadIdx.x & 31) - l + (v & ((1 << A.log_l) - 1))) * 16 + p % W * (int)sizeof(T);
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ int partner_of(int e, int rot) {
+    return e >= rot ? e : (e < rot >> 1 ? e + (rot >> 1) : e - (rot >> 1));
+  }
+  // the partners of unit j's elements, out of a slot that the warp has filled
+  __device__ __forceinline__ Half2 partners(const uint8_t* slot, int j) const {
+    auto at = [&](int e) { return to_f(*reinterpret_cast<const T*>(slot + partner[PL ? j : 0][PL ? e : 0])); };
+    Half2 x;
+#pragma unroll
+    for (int m = 0; m < NP; ++m) {
+      x.a[m] = f32x2_pack(at(4 * m), at(4 * m + 2));
+      x.b[m] = f32x2_pack(at(4 * m + 1), at(4 * m + 3));
+    }
+    return x;
+  }
+  // x turned with its partners p, or back: [NP][cosines, signed sines][units that turn] of 4
+  __device__ __forceinline__ void rotate(const NormArgs& A, const float2* s_cs, int j, Half2& x, const Half2& p, bool back) const {
+#pragma unroll
+    for (int m = 0; m < NP; ++m) {
+      const float4 c = reinterpret_cast<const float4*>(s_cs)[2 * m * A.rot_units + unit[j]];
+      float4 s = reinterpret_cast<const float4*>(s_cs)[(2 * m + 1) * A.rot_units + unit[j]];
+      if (back) s = make_float4(-s.x, -s.y, -s.z, -s.w);
+      x.a[m] = f32x2_fma(p.a[m], f32x2_pack(s.x, s.y), f32x2_mul(x.a[m], f32x2_pack(c.x, c.y)));
+      x.b[m] = f32x2_fma(p.b[m], f32x2_pack(s.z, s.w), f32x2_mul(x.b[m], f32x2_pack(c.z, c.w)));
     }
   }
   // places in the head of a unit's couple m: first and second element of its pairs (-1: there is none)
@@ -293,13 +333,15 @@ struct Units {
     }
   }
   // the weights of this lane's elements (1 where there is none)
-  __device__ __forceinline__ void weights(const float* w, Half2* to) const {
+  __device__ __forceinline__ void weights(const float* w, Half2* to, bool of_partners = false) const {
 #pragma unroll
     for (int j = 0; j < NU; ++j)
 #pragma unroll
       for (int m = 0; m < NP; ++m) {
         const Places p = places(off[j], turn[j], m, half, d);
-        auto at = [&](int x) { return w && unit[j] >= 0 && x >= 0 ? __ldg(w + x) : 1.f; };
+        auto at = [&](int x) {
+          return w && unit[j] >= 0 && x >= 0 ? __ldg(w + (PL && of_partners ? partner_of(x, 2 * half) : x)) : 1.f;
+        };
         to[j].a[m] = f32x2_pack(at(p.a0), at(p.a1));
         to[j].b[m] = f32x2_pack(at(p.b0), at(p.b1));
       }
@@ -326,19 +368,39 @@ struct Units {
       x.a[m] = t;
     }
   }
-  // The cosines and sines (times the magnitude) of a position, by a warp.
+  // The cosines and sines (times the magnitude) of a position, by a warp; 1 and 0 for what a unit holds past the rotation.
   static __device__ __forceinline__ void table(const NormArgs& A, const RopeTable& tab, int pos, float2* s_cs) {
-    for (int p = threadIdx.x & 31; p < A.rot >> 1; p += 32) {
-      const uint64_t phase = (uint64_t)(int64_t)pos * tab.turn[p];
-      float s, c;
-      sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-      if constexpr (PP == 1) {
-        s_cs[p] = make_float2(c * A.mscale, s * A.mscale);
+    const int pairs = A.rot >> 1, all = PP == 1 || !IL ? pairs : (PL ? A.rot_units * W - pairs : A.rot_units * PP);
+    for (int p = threadIdx.x & 31; p < all; p += 32) {
+      float s = 0.f, c = 1.f;
+      if (p < pairs) {
+        const uint64_t phase = (uint64_t)(int64_t)pos * tab.turn[p];
+        sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
+        c *= A.mscale;
+        s *= A.mscale;
+      }
+      float* to = reinterpret_cast<float*>(s_cs);
+      if constexpr (PL) {
+        // element e of a unit: couple e / 4, place (0, 2, 1, 3)[e % 4] of its four
+        auto put = [&](int e, float sine) {
+          const int in = e % W;
+          float* at = to + ((in >> 2) * 2 * A.rot_units + e / W) * 4 + ((in & 1) * 2 + ((in >> 1) & 1));
+          at[0] = c;
+          at[A.rot_units * 4] = sine;
+        };
+        if (p < pairs) {
+          put(p, -s);
+          put(p + pairs, s);
+        } else {
+          put(p + pairs, 0.f);
+        }
+      } else if constexpr (PP == 1) {
+        s_cs[p] = make_float2(c, s);
       } else {
         const int e = p % PP;  // place of the pair in its unit
-        float* to = reinterpret_cast<float*>(s_cs) + ((e >> 1) * A.rot_units + p / PP) * 4 + (e & 1);
-        to[0] = c * A.mscale;
-        to[2] = s * A.mscale;
+        to += ((e >> 1) * A.rot_units + p / PP) * 4 + (e & 1);
+        to[0] = c;
+        to[2] = s;
       }
     }
   }
@@ -355,12 +417,12 @@ __device__ __forceinline__ void lanes_sum(float* x, int log_l) {
     }
 }
 
-// W: elements of a vector (1: unaligned data, element by element); IL: interleaved pairs; NU: units of a lane.
+// W: elements of a vector (1: unaligned data, element by element); LY: layout; NU: units of a lane.
 // Backward: a thread's part of dw stays in registers throughout.
-template <typename T, int W, bool IL, int NU, int MODE>
-__global__ void __launch_bounds__(kThreads, ctas_an_sm<W, IL, NU>(MODE == kBackward))
+template <typename T, int W, int LY, int NU, int MODE>
+__global__ void __launch_bounds__(kThreads, ctas_an_sm<W, LY, NU>(MODE == kBackward))
     norm_rope_kernel(const __grid_constant__ NormArgs A, const __grid_constant__ RopeTable tab) {
-  using U = Units<T, W, IL, NU>;
+  using U = Units<T, W, LY, NU>;
   constexpr bool BWD = MODE == kBackward;
   constexpr int S = W == 1 ? 0 : kSlots<NU>, SLOT = U::V * 512 * (BWD ? 2 : 1);
   extern __shared__ __align__(16) uint8_t smem[];
@@ -425,7 +487,8 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm<W, IL, NU>(MODE == kBackw
 #pragma unroll
     for (int i = 0; i < S; ++i) copy(i);
   }
-  typename U::Half2 w[NU], dw[BWD ? NU : 1] = {};
+  constexpr bool PL = U::PL;
+  typename U::Half2 w[NU], wp[PL && !BWD ? NU : 1], dw[BWD ? NU : 1] = {};
   if (BWD) u.weights(A.weight[role], w);
   Place place;
   uint8_t* out = nullptr;  // where this lane's head goes
@@ -442,7 +505,10 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm<W, IL, NU>(MODE == kBackw
       U::table(A, tab, pos, s_cs);
       __syncwarp();
     }
-    if (!BWD && at.g < 2) u.weights(A.weight[at.g], w);
+    if (!BWD && at.g < 2) {
+      u.weights(A.weight[at.g], w);
+      if constexpr (PL && !BWD) u.weights(A.weight[at.g], wp, true);
+    }
     out = A.dst[at.g] + (MODE == kAppend && at.g > 0 ? place.row : at.t) * A.dst_stride[at.g] + (int64_t)at.h * A.d * (int)sizeof(T);
   };
   if (count > 0) enter(true);
@@ -452,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm<W, IL, NU>(MODE == kBackw
     typename U::Row x, dy;
     if constexpr (W > 1) {
       copy_wait<S - 1>();
+      if (PL) __syncwarp();  // the other lanes' copies
       U::take(mine + lane * 16 + slot * SLOT, x);
       if (BWD) U::take(mine + lane * 16 + slot * SLOT + U::V * 512, dy);
     } else {
@@ -465,7 +532,11 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm<W, IL, NU>(MODE == kBackw
       const typename U::Half2 v = U::get(x, j);
       if (BWD) {
         gr[j] = U::get(dy, j);
-        if (u.turn[j]) u.rotate(A, s_cs, j, gr[j], true);
+        if constexpr (PL) {
+          if (u.turn[j]) u.rotate(A, s_cs, j, gr[j], u.partners(mine + slot * SLOT + U::V * 512, j), true);
+        } else {
+          if (u.turn[j]) u.rotate(A, s_cs, j, gr[j], true);
+        }
       }
 #pragma unroll
       for (int m = 0; m < U::NP; ++m) {
@@ -479,7 +550,13 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm<W, IL, NU>(MODE == kBackw
     }
     float sums[2] = {f32x2_sum(f32x2_add(sa, sb)), BWD ? f32x2_sum(f32x2_add(ga, gb)) : 0.f};
     lanes_sum<BWD ? 2 : 1>(sums, A.log_l);
+    typename U::Half2 xp[PL && !BWD ? NU : 1];
+    if constexpr (PL && !BWD) {
+#pragma unroll
+      for (int j = 0; j < NU; ++j) xp[j] = u.partners(mine + slot * SLOT, j);
+    }
     if constexpr (W > 1) {  // x and dy have been read
+      if (PL) __syncwarp();
       copy(slot);
       slot = slot + 1 == S ? 0 : slot + 1;
     }
@@ -513,7 +590,16 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm<W, IL, NU>(MODE == kBackw
             v.a[m] = f32x2_mul(f32x2_mul(v.a[m], rms), w[j].a[m]);
             v.b[m] = f32x2_mul(f32x2_mul(v.b[m], rms), w[j].b[m]);
           }
-          if (u.turn[j]) u.rotate(A, s_cs, j, v, false);
+          if constexpr (PL && !BWD) {
+#pragma unroll
+            for (int m = 0; m < U::NP; ++m) {
+              xp[j].a[m] = f32x2_mul(f32x2_mul(xp[j].a[m], rms), wp[j].a[m]);
+              xp[j].b[m] = f32x2_mul(f32x2_mul(xp[j].b[m], rms), wp[j].b[m]);
+            }
+            if (u.turn[j]) u.rotate(A, s_cs, j, v, xp[j], false);
+          } else if constexpr (!PL) {
+            if (u.turn[j]) u.rotate(A, s_cs, j, v, false);
+          }
           U::put(x, j, v);
         }
       }
@@ -585,24 +671,29 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int nq
   }
 }
 
-// Shape of a launch: vectors, units and lanes, the pieces of a token, and the shared memory of a warp.
-void set_shape(NormArgs& a, int size, bool interleaved, bool backward, int& nu) {
+// Shape of a launch: vectors, layout, units and lanes, the pieces of a token, and the shared memory of a warp.
+void set_shape(NormArgs& a, int size, bool interleaved, bool backward, int& layout, int& nu) {
   const int W = 16 / size;
-  // 16-byte vectors when every vector lies whole on one side of each border and starts on a 16-byte
-  // boundary; else element by element
-  bool wide = a.d % W == 0 && (interleaved ? a.rot % W == 0 : (a.rot / 2) % W == 0);
+  // 16-byte vectors when heads are whole numbers of them that start on 16-byte boundaries; else element by element (8192
+  // tokens of 32 + 8 heads of 128 in bf16, 42 elements of which turn, forward: 44 us; element by element 456; backward 57
+  // and 1377). The half layout takes pairs of vectors where half a rotation is a whole number of them (30 us), else plain
+  // ones with the partners out of shared memory (the 44).
+  bool wide = a.d % W == 0;
   for (int g = 0; g < 3; ++g)
     if (a.heads[g]) {
       wide = wide && !(((uintptr_t)a.src[g] | (uintptr_t)a.dst[g] | (uint64_t)a.src_stride[g] | (uint64_t)a.dst_stride[g]) & 15);
       if (backward) wide = wide && !(((uintptr_t)a.dy[g] | (uint64_t)a.dy_stride[g]) & 15);
     }
+  layout = interleaved ? kPairs : (!wide || a.rot / 2 % W == 0 ? kHalves : kPlain);
+  const bool halves = layout == kHalves;
   const int wi = wide ? W : (interleaved ? 2 : 1);
-  a.rot_units = interleaved ? a.rot / wi : a.rot / 2 / wi;
-  a.units = a.rot_units + (a.d - a.rot + wi - 1) / wi;
+  a.rot_units = halves ? a.rot / 2 / wi : (int)cdiv(a.rot, wi);
+  a.units = halves ? a.rot_units + (a.d - a.rot + wi - 1) / wi : (int)cdiv(a.d, wi);
   a.log_l = 0;
   while (a.log_l < 5 && (1 << a.log_l) < a.units) ++a.log_l;
   nu = !wide ? 16 : (a.units <= 32 ? 1 : (size == 2 ? kMany<__nv_bfloat16> : kMany<float>));
-  if (wide && interleaved && size == 2 && a.units > 8 && a.log_l > 0) {
+  // two vectors a lane where a unit is one, and half the lanes (pairs of neighbours, forward: 30.5 us against 35.5)
+  if (wide && !halves && size == 2 && a.units > 8) {
     nu = 2;
     a.log_l -= a.units <= 32;
   }
@@ -610,14 +701,16 @@ void set_shape(NormArgs& a, int size, bool interleaved, bool backward, int& nu) 
   for (int g = 0; g < 3; ++g) a.pieces[g] = (int)cdiv(a.heads[g], 32 >> a.log_l);
   a.inv_d = 1.f / (float)a.d;
   const int slots = !wide ? 0 : (nu <= 2 ? kSlots<1> : kSlots<4>);
-  a.warp_bytes = slots * nu * (interleaved ? 1 : 2) * 512 * (backward ? 2 : 1) + ((a.rot / 2 * (int)sizeof(float2) + 15) & ~15);
+  const int angles = halves || !wide ? a.rot / 2 : a.rot_units * (layout == kPlain ? W : W / 2);
+  a.warp_bytes = slots * nu * (halves ? 2 : 1) * 512 * (backward ? 2 : 1) + ((angles * (int)sizeof(float2) + 15) & ~15);
 }
 
 template <typename T, int MODE>
 sta_status launch_norm(NormArgs& a, const RopeTable& tab, bool il, cudaStream_t st, int* ctas = nullptr) {
   constexpr int W = 16 / (int)sizeof(T);
-  int nu;
-  set_shape(a, (int)sizeof(T), il, MODE == kBackward, nu);
+  int layout, nu;
+  set_shape(a, (int)sizeof(T), il, MODE == kBackward, layout, nu);
+  const bool light = nu * (layout == kHalves ? 2 : 1) <= 2;  // (registers: ctas_an_sm)
   const int64_t H = MODE == kAppend ? 3 : 2;
   int64_t pieces = 0;
   for (int g = 0; g < H; ++g) pieces += a.pieces[g];
@@ -625,7 +718,7 @@ sta_status launch_norm(NormArgs& a, const RopeTable& tab, bool il, cudaStream_t 
   unsigned grid;
   if (MODE == kBackward) {
     // CTAs by the heads of q and k, one a tensor at least, and none without a piece for each of its warps
-    const int most = nu * (il ? 1 : 2) <= 2 ? kMaxGrid : kMaxGrid / 2;
+    const int most = light ? kMaxGrid : kMaxGrid / 2;
     int n[2];
     for (int g = 0; g < 2; ++g) {
       int64_t share = (int64_t)(most * (double)a.pieces[g] / (double)pieces + 0.5);
@@ -638,7 +731,7 @@ sta_status launch_norm(NormArgs& a, const RopeTable& tab, bool il, cudaStream_t 
     grid = (unsigned)(n[0] + n[1]);
     smem = std::max(smem, (size_t)kWarps * a.d * sizeof(float));
   } else {
-    grid = (unsigned)std::min<int64_t>(152 * (nu * (il ? 1 : 2) <= 2 ? 3 : 1), cdiv(a.n_tokens * pieces, kWarps));
+    grid = (unsigned)std::min<int64_t>(152 * (!light ? 1 : (layout == kPlain && nu == 2 ? 2 : 3)), cdiv(a.n_tokens * pieces, kWarps));
   }
   if (a.n_tokens * pieces / ((int64_t)grid * kWarps) >= INT32_MAX) return STA_ERR_INVALID_ARG;
   auto go = [&](auto kern) -> sta_status {
@@ -647,9 +740,14 @@ sta_status launch_norm(NormArgs& a, const RopeTable& tab, bool il, cudaStream_t 
     STA_LAUNCH_CHECK();
     return STA_OK;
   };
-  if (nu == 1) return il ? go(norm_rope_kernel<T, W, true, 1, MODE>) : go(norm_rope_kernel<T, W, false, 1, MODE>);
-  if (nu == 16) return il ? go(norm_rope_kernel<T, 1, true, 16, MODE>) : go(norm_rope_kernel<T, 1, false, 16, MODE>);
-  return il ? go(norm_rope_kernel<T, W, true, kMany<T>, MODE>) : go(norm_rope_kernel<T, W, false, kMany<T>, MODE>);
+  if (nu == 16) return il ? go(norm_rope_kernel<T, 1, kPairs, 16, MODE>) : go(norm_rope_kernel<T, 1, kHalves, 16, MODE>);
+  auto of = [&](auto n) -> sta_status {
+    constexpr int NU = decltype(n)::value;
+    if (layout == kPairs) return go(norm_rope_kernel<T, W, kPairs, NU, MODE>);
+    if (layout == kPlain) return go(norm_rope_kernel<T, W, kPlain, NU, MODE>);
+    return go(norm_rope_kernel<T, W, kHalves, NU, MODE>);
+  };
+  return nu == 1 ? of(std::integral_constant<int, 1>{}) : of(std::integral_constant<int, kMany<T>>{});
 }
 
 template <typename T>

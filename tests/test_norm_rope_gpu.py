@@ -89,7 +89,8 @@ class Case:
 
 SHAPES = [(1, 1, 0, 2, 2, 0), (3, 5, 2, 128, 128, 0), (70, 32, 8, 128, 64, 8), (33, 3, 3, 80, 40, 16), (17, 2, 1, 96, 30, 3),
           (5, 7, 2, 63, 6, 0), (9, 1, 1, 512, 512, 1), (4, 2, 3, 512, 512, 8), (4, 1, 1, 512, 16, 0), (300, 2, 0, 64, 64, 24),
-          (6, 0, 4, 64, 32, 0), (2, 3, 1, 256, 0, 0), (1, 3, 1, 7, 0, 5), (50, 1, 1, 2, 2, 0)]
+          (6, 0, 4, 64, 32, 0), (2, 3, 1, 256, 0, 0), (1, 3, 1, 7, 0, 5), (50, 1, 1, 2, 2, 0), (50, 6, 2, 128, 42, 8),
+          (7, 2, 2, 64, 62, 0), (5, 1, 3, 256, 2, 16), (3, 2, 1, 512, 510, 0), (9, 3, 1, 40, 36, 8), (90, 5, 1, 32, 10, 0)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -289,7 +290,7 @@ def test_norm_rope_as_an_autograd_function(dev):
 
 @pytest.mark.parametrize("P", [1, 7, 16, 100])
 @pytest.mark.parametrize("interleaved,rot,d,Hq,Hkv", [(False, 128, 128, 8, 2), (True, 32, 64, 3, 3), (False, 0, 64, 0, 1),
-                                                      (True, 20, 72, 5, 5), (False, 30, 60, 4, 1)])
+                                                      (True, 20, 72, 5, 5), (False, 30, 60, 4, 1), (False, 50, 96, 4, 2)])
 def test_norm_append(dev, P, interleaved, rot, d, Hq, Hkv):
     import torch
 
