@@ -23,9 +23,10 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 template <typename T> constexpr int kMany = sizeof(T) == 2 ? 2 : 4;  // units of a lane where a head has more than 32 (at most 64, 128)
 constexpr int kMaxGrid = 152 * 2;  // CTAs of a backward pass, each with a row of partial sums for dw
-// What a lane holds of a head's turning part: vectors half a rotation apart; neighbouring pairs; or vectors as they come,
-// whose partners half a rotation away, where that is no whole number of vectors, it reads from the other lanes' copies.
-enum Layout { kHalves, kPairs, kPlain };
+// What a lane holds of a head's turning part: vectors half a rotation apart; neighbouring pairs; those where the rotation
+// ends inside a vector (looked at in kPairs too, that costs 3 of 30 us); or vectors as they come, whose partners half a
+// rotation away, where that is no whole number of vectors, it reads from the other lanes' copies.
+enum Layout { kHalves, kPairs, kPairsEnd, kPlain };
 template <int NU> constexpr int kSlots = NU <= 2 ? 3 : 2;  // pieces that a warp has on their way
 template <int W, int LY, int NU>
 constexpr int ctas_an_sm(bool backward) {
@@ -219,9 +220,19 @@ struct Units {
       const float4 c = reinterpret_cast<const float4*>(s_cs)[2 * m * A.rot_units + unit[j]];
       float4 s = reinterpret_cast<const float4*>(s_cs)[(2 * m + 1) * A.rot_units + unit[j]];
       if (back) s = make_float4(-s.x, -s.y, -s.z, -s.w);
-      x.a[m] = f32x2_fma(p.a[m], f32x2_pack(s.x, s.y), f32x2_mul(x.a[m], f32x2_pack(c.x, c.y)));
-      x.b[m] = f32x2_fma(p.b[m], f32x2_pack(s.z, s.w), f32x2_mul(x.b[m], f32x2_pack(c.z, c.w)));
+      const int e = off[j] + 4 * m;
+      x.a[m] = turned(f32x2_fma(p.a[m], f32x2_pack(s.x, s.y), f32x2_mul(x.a[m], f32x2_pack(c.x, c.y))), x.a[m], e, A.rot);
+      x.b[m] = turned(f32x2_fma(p.b[m], f32x2_pack(s.z, s.w), f32x2_mul(x.b[m], f32x2_pack(c.z, c.w))), x.b[m], e + 1, A.rot);
     }
+  }
+  // Elements e and e + 2 after the turn: as they were where they lie past the rotation (0 times an
+  // infinite partner would not be 0).
+  static __device__ __forceinline__ uint64_t turned(uint64_t to, uint64_t was, int e, int rot) {
+    if (LY < kPairsEnd || e + 2 < rot) return to;
+    float t0, t1, w0, w1;
+    f32x2_unpack(to, t0, t1);
+    f32x2_unpack(was, w0, w1);
+    return f32x2_pack(e < rot ? t0 : w0, w1);
   }
   // places in the head of a unit's couple m: first and second element of its pairs (-1: there is none)
   struct Places {
@@ -363,9 +374,10 @@ struct Units {
         s = f32x2_pack(v.z, v.w);
         n = f32x2_pack(-v.z, -v.w);
       }
+      const int e = off[j] + 4 * m;
       const uint64_t t = f32x2_fma(x.b[m], back ? s : n, f32x2_mul(x.a[m], c));
-      x.b[m] = f32x2_fma(x.a[m], back ? n : s, f32x2_mul(x.b[m], c));
-      x.a[m] = t;
+      x.b[m] = turned(f32x2_fma(x.a[m], back ? n : s, f32x2_mul(x.b[m], c)), x.b[m], e + 1, A.rot);
+      x.a[m] = turned(t, x.a[m], e, A.rot);
     }
   }
   // The cosines and sines (times the magnitude) of a position, by a warp; 1 and 0 for what a unit holds past the rotation.
@@ -684,7 +696,7 @@ void set_shape(NormArgs& a, int size, bool interleaved, bool backward, int& layo
       wide = wide && !(((uintptr_t)a.src[g] | (uintptr_t)a.dst[g] | (uint64_t)a.src_stride[g] | (uint64_t)a.dst_stride[g]) & 15);
       if (backward) wide = wide && !(((uintptr_t)a.dy[g] | (uint64_t)a.dy_stride[g]) & 15);
     }
-  layout = interleaved ? kPairs : (!wide || a.rot / 2 % W == 0 ? kHalves : kPlain);
+  layout = interleaved ? (wide && a.rot % W != 0 ? kPairsEnd : kPairs) : (!wide || a.rot / 2 % W == 0 ? kHalves : kPlain);
   const bool halves = layout == kHalves;
   const int wi = wide ? W : (interleaved ? 2 : 1);
   a.rot_units = halves ? a.rot / 2 / wi : (int)cdiv(a.rot, wi);
@@ -744,6 +756,7 @@ sta_status launch_norm(NormArgs& a, const RopeTable& tab, bool il, cudaStream_t 
   auto of = [&](auto n) -> sta_status {
     constexpr int NU = decltype(n)::value;
     if (layout == kPairs) return go(norm_rope_kernel<T, W, kPairs, NU, MODE>);
+    if (layout == kPairsEnd) return go(norm_rope_kernel<T, W, kPairsEnd, NU, MODE>);
     if (layout == kPlain) return go(norm_rope_kernel<T, W, kPlain, NU, MODE>);
     return go(norm_rope_kernel<T, W, kHalves, NU, MODE>);
   };

@@ -173,6 +173,43 @@ def test_norm_rope_far_positions(dev, kw):
     c.check_forward(sta.sta_norm_rope(c.q, c.k, *c.args(), **c.kw_args()))
 
 
+@pytest.mark.parametrize("interleaved,rot", [(False, 42), (False, 64), (True, 42), (True, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_rope_what_is_infinite_past_the_rotation_stays_there(dev, interleaved, rot, dtype):
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = Case(dev, 5, 3, 2, 128, rot, interleaved, dtype, seed=rot)
+    c.dy[0][2, 1, rot] = float("inf")
+    dqw = sta.sta_norm_rope_bwd(*c.dy, c.q, c.k, *c.args(), **c.kw_args())[2]
+    assert torch.isinf(dqw[rot]) and torch.isfinite(dqw).sum() == 127
+    c.qw[rot] = float("inf")
+    y = sta.sta_norm_rope(c.q, c.k, *c.args(), **c.kw_args())[0]
+    assert torch.isinf(y[..., rot]).all() and torch.isfinite(y).sum() == 5 * 3 * 127
+
+
+def test_norm_rope_a_refused_call_raises_and_leaves_the_device_as_it_was(dev):
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = Case(dev, 5, 3, 2, 64, 64, False, "bf16")
+    for call in (lambda **kw: sta.sta_norm_rope(c.q, c.k, *c.args(), **kw),
+                 lambda **kw: sta.sta_norm_rope_bwd(*c.dy, c.q, c.k, *c.args(), **kw)):
+        for kw in (dict(eps=0.0), dict(eps=float("nan")), dict(eps=float("inf"))):
+            with pytest.raises(sta.StaError):
+                call(**kw)
+        with pytest.raises(ValueError):
+            call(q_weight=c.qw[:32])
+        with pytest.raises(ValueError):
+            call(q_weight=c.qw.cpu())
+    with pytest.raises(sta.StaError):  # more turns than the head has
+        sta.sta_norm_rope(c.q, c.k, c.pos, sta.Rope(66))
+    torch.cuda.synchronize()
+    c.check_forward(sta.sta_norm_rope(c.q, c.k, *c.args(), **c.kw_args()))
+
+
 def test_norm_rope_no_weights_zero_rows_and_sizes(dev):
     import torch
 
