@@ -654,16 +654,16 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& A, const CUtensorMap& 
     const int hk = p.h0 + head;
     const bool mine = hk < A.Hkv, live0 = mine && t0 < p.n, live1 = mine && t1 < p.n;  // (rows past the last: zeros)
     uint32_t qa[D / 16][4];
-    {
+    {  // (q may be what the merge before this launch wrote while it ran already: not by way of the cache for what is constant)
       auto q_row = [&](int t, int g) { return A.q + (int64_t)(p.q0 + t) * A.q_stride + ((int64_t)hk * A.G + g) * D; };
       const __nv_bfloat16 *a0 = q_row(t0, g0), *a1 = q_row(t1, g1);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const int e = i * 16 + (lane & 3) * 2;
-        qa[i][0] = live0 ? __ldg(reinterpret_cast<const uint32_t*>(a0 + e)) : 0u;
-        qa[i][1] = live1 ? __ldg(reinterpret_cast<const uint32_t*>(a1 + e)) : 0u;
-        qa[i][2] = live0 ? __ldg(reinterpret_cast<const uint32_t*>(a0 + e + 8)) : 0u;
-        qa[i][3] = live1 ? __ldg(reinterpret_cast<const uint32_t*>(a1 + e + 8)) : 0u;
+        qa[i][0] = live0 ? *reinterpret_cast<const uint32_t*>(a0 + e) : 0u;
+        qa[i][1] = live1 ? *reinterpret_cast<const uint32_t*>(a1 + e) : 0u;
+        qa[i][2] = live0 ? *reinterpret_cast<const uint32_t*>(a0 + e + 8) : 0u;
+        qa[i][3] = live1 ? *reinterpret_cast<const uint32_t*>(a1 + e + 8) : 0u;
       }
     }
     float o[D / 8][4];
@@ -1522,18 +1522,18 @@ __global__ void __launch_bounds__(128) chunk_merge_shared_kernel(const __grid_co
         record_error(A.err, 0x609);
     }
   }
-  grid_wait();  // the partials
+  grid_wait();  // the partials: written while this kernel ran, so not by way of the cache for what is constant
   const int s = some ? na + k.ns : 0;
   int most = s;
 #pragma unroll
   for (int d = 2; d <= 4; d <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
   auto lse_at = [&](int i) {
-    return i < s ? __ldg(A.part_lse + (i < na ? pre.lse() + (int64_t)i * pre.rows : own.lse() + (int64_t)(i - na) * own.rows)) : -INFINITY;
+    return i < s ? A.part_lse[i < na ? pre.lse() + (int64_t)i * pre.rows : own.lse() + (int64_t)(i - na) * own.rows] : -INFINITY;
   };
   auto value = [&](int i, int v) {
     const SharedPart& p = i < na ? pre : own;
     const int64_t c = (int64_t)(i < na ? i : i - na) * p.rows;  // rows of the chunks before
-    return __ldg(reinterpret_cast<const float4*>(A.part_o + p.values(D, (lane >> 3) + 4 * v) + c * D + z * 4));
+    return *reinterpret_cast<const float4*>(A.part_o + p.values(D, (lane >> 3) + 4 * v) + c * D + z * 4);
   };
   float M = -INFINITY;
   for (int i = sub; i < most; i += 8) M = fmaxf(M, lse_at(i));

@@ -134,6 +134,35 @@ def test_prefix_streams_and_repeats(dev):
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("splits", [0, 2])
+def test_prefix_calls_that_read_what_the_last_one_wrote(dev, splits):
+    # each call's queries are the last one's results, in two buffers by turns or in one; its kernels may start before the
+    # last one's have ended
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = SharedCase(17, [40, 24], [1024, 512], [1] * 60 + [3] * 4, [4 + 11 * i % 60 for i in range(64)], 16, 8, 128, 16)
+    x = c.dev(dev)
+    q = x.pop("q")
+    ws = torch.empty(sta.prefix_workspace_bytes(c.q_indptr, c.kv_indptr, 64, c.group_indptr, c.prefix, 16, 8, 128, 16,
+                                                num_splits=splits), dtype=torch.uint8, device=dev)
+
+    def chain(buffers, wait):
+        at = buffers[0].copy_(q)
+        for i in range(12):
+            at, _ = sta.sta_prefix_fwd_paged(q=at, **x, scale=3.0, num_splits=splits, o=buffers[(i + 1) % len(buffers)], workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+        return at.clone()
+
+    two = [torch.empty_like(q) for _ in range(2)]
+    want = chain(two, True)
+    for _ in range(5):
+        assert torch.equal(chain(two, False), want)
+        assert torch.equal(chain(two[:1], False), want)
+
+
 @pytest.mark.parametrize("splits", [0, 1, 4])
 def test_prefix_captured_and_replayed_with_other_lengths(dev, splits):
     import torch
