@@ -1649,15 +1649,35 @@ constexpr int kMaxAuto = 256;    // chunks that the plan cuts a list into at mos
 constexpr double kItem = 2.0;    // an item's prologue and epilogue, in key tiles
 constexpr double kMerge = 4.0;   // the merge launch
 
-// Chunks of a launch with shared prefixes, and the CTAs of few rows. The launch ends when its bytes have come, when the
-// last of the prefixes' items is done or the last CTA of few rows. Measured: a run of few rows takes 3.5 us and 1.0 a tile of 16 keys
-// of 8 heads of 128 (others 0.65; a piece 2 of them more); an item of query tiles 7.5 us and 1.5 a key tile (heads of 64: 1.0), 3 again for
-// each further one of its CTA. For each share of the SMs the length of the prefixes' pieces that ends soonest is taken, and
-// the best share.
-void plan_shared(const ChunkArgs& a, std::vector<Req>& reqs, int num_splits, int sms, Group& g) {
+constexpr double kPieceUs = 0.25;  // merge: a partial of a row (it reads four at a time)
+// Nothing shared is estimated too where sharing saves less than 20 tiles an SM; it takes less than its estimate, since what requests
+// share lies in L2 then. (344 batches of all sizes, few rows by CTAs of their own, in items, or nothing shared: the choice takes
+// 1.02 times the best of the three on average, 1.5 at most, and 0.79 of what the chunk attention takes.)
+constexpr double kNone = 0.25, kClear = 20.0;  // (a quarter: no estimate, 1 us of host time; sharing won 3 us there at most)
+double apart(const ChunkArgs& a) { return (a.d == 128 ? 0.85 : 0.7) + (a.box > 0 ? 0.0 : 0.15); }
+
+// Measured: a run of few rows takes 3.5 us and 1.0 a tile of 16 keys
+// of 8 heads of 128 (others 0.65; a piece 2 of them more); an item of query tiles 7.5 us and 1.5 a key tile (heads of 64: 1.25), 3 again for
+// each further one of its CTA.
+struct RowTimes {
+  int heads;  // of a CTA of few rows
+  double tile_us, row_us;
+  explicit RowTimes(const ChunkArgs& a)
+      : heads(row_heads(a.Hkv)), tile_us(a.d == 128 ? 1.5 : 1.25), row_us(heads == 8 && a.d == 128 ? 1.0 : 0.65) {}
+  bool few(int keys) const {
+    const int t = (keys + 15) / 16;
+    return row_us * (t + kStart) < heads * (tile_us * t / 8 + 3.0);
+  }
+};
+
+// Chunks of a launch with shared prefixes, and the CTAs of few rows; its time. The launch ends when its bytes have come, when the
+// last of the prefixes' items is done or the last CTA of few rows. For each share of the SMs
+// the length of the prefixes' pieces that ends soonest is taken, and the best share.
+double plan_shared(const ChunkArgs& a, std::vector<Req>& reqs, int num_splits, int sms, Group& g) {
   constexpr int kTiles = 14, kKeys = 16;
-  const int heads = row_heads(a.Hkv), groups = (a.Hkv + heads - 1) / heads;
-  const double tile_us = a.d == 128 ? 1.5 : 1.0, row_us = heads == 8 && a.d == 128 ? 1.0 : 0.65, key_bytes = 4.0 * a.d;
+  const RowTimes times(a);
+  const int heads = times.heads, groups = (a.Hkv + heads - 1) / heads;
+  const double tile_us = times.tile_us, row_us = times.row_us, key_bytes = 4.0 * a.d;
   int64_t row = 0;  // the tiles of few rows, one after the other
   double bytes = 0;
   int most = 1;
@@ -1666,47 +1686,74 @@ void plan_shared(const ChunkArgs& a, std::vector<Req>& reqs, int num_splits, int
     if (q.few) row += (q.few + kKeys - 1) / kKeys + kStart;
     else most = std::max(most, std::max(q.first, q.last));
   }
+  std::vector<const Req*> by_len;  // the others, longest first
+  int longest_few = 1;
+  for (const Req& q : reqs)
+    if (q.few) longest_few = std::max(longest_few, q.few);
+    else by_len.push_back(&q);
+  std::stable_sort(by_len.begin(), by_len.end(),
+                   [](const Req* x, const Req* y) { return std::max(x->first, x->last) > std::max(y->first, y->last); });
+  struct Cut {  // items of one length, us
+    int64_t end;
+    double each;
+  };
   struct Tiles {  // the items of pieces of `tiles` key tiles: the times of the longest one, of all and of the merge, us
     int tiles;
     int64_t items;
     double longest, work, merge;
+    size_t c0;  // its first among the cuts
   } t[kTiles];
+  std::vector<Cut> cuts;
+  cuts.reserve(kTiles * by_len.size());
   int nt = 0;
   for (int tiles = most; nt < kTiles; tiles = std::max(2, tiles * 3 / 4)) {
-    Tiles x{tiles, 0, 0, 0, 0};
+    Tiles& x = t[nt++];
+    x = Tiles{tiles, 0, 0, 0, 0, cuts.size()};
     int pieces = 0;
-    for (const Req& q : reqs)
-      if (!q.few) {
-        const int len = std::max(q.first, q.last), ns = num_splits ? num_splits : std::min(kMaxAuto, (len + tiles - 1) / tiles);
-        const int64_t items = (int64_t)q.units * a.Hkv * ns;
-        x.items += items;
-        x.work += (tile_us * 0.5 * (q.first + q.last) / ns + 3.0) * (double)items;
-        x.merge += (double)q.n * a.Hq * ns * 4.0 * (a.d + 1) / 5e6;
-        x.longest = std::max(x.longest, tile_us * len / ns);
-        pieces = std::max(pieces, ns);
-      }
-    x.merge += 0.25 * pieces;  // (a row's are read four at a time)
-    t[nt++] = x;
+    for (const Req* r : by_len) {
+      const Req& q = *r;
+      const int len = std::max(q.first, q.last), ns = num_splits ? num_splits : std::min(kMaxAuto, (len + tiles - 1) / tiles);
+      const int64_t items = (int64_t)q.units * a.Hkv * ns;
+      const double each = tile_us * 0.5 * (q.first + q.last) / ns + 3.0;
+      x.items += items;
+      if (cuts.size() > x.c0 && cuts.back().each == each) cuts.back().end = x.items;
+      else cuts.push_back(Cut{x.items, each});
+      x.work += each * (double)items;
+      x.merge += (double)q.n * a.Hq * ns * 4.0 * (a.d + 1) / 5e6;
+      x.longest = std::max(x.longest, tile_us * len / ns);
+      pieces = std::max(pieces, ns);
+    }
+    x.merge += kPieceUs * pieces;
     if (tiles <= 2 || num_splits) break;
   }
+  // what the CTA with the most to do of m takes: items 0, m, 2 m, ..
+  auto rounds = [&](const Tiles& x, int m) {
+    if (x.items > 8 * (int64_t)m) return x.work / m + 0.5 * x.longest;
+    double sum = 0;
+    size_t c = x.c0;
+    for (int64_t i = 0; i < x.items; i += m) {
+      while (cuts[c].end <= i) ++c;
+      sum += cuts[c].each;
+    }
+    return sum;
+  };
   double best = 0;
   int best_tiles = 0, best_runs = 0;
   constexpr int shares = 24;
   for (int c = 0; c < shares; ++c) {
     const int runs = std::max(1, std::min(sms - 1, sms * (c + 1) / (shares + 1)) / groups), m = std::max(1, sms - runs * groups);
-    const double t_rows = 3.5 + row_us * (double)((row + runs - 1) / runs);
+    const int64_t run = (row + runs - 1) / runs;
+    const double t_rows = 3.5 + row_us * (double)run, merge = kPieceUs * row_turns(a.Hkv) * ((longest_few / kKeys + kStart) / (double)run + 1.0);
     double t_tiles = 0;
     int bt = 0;
     for (int i = 0; i < nt; ++i) {
-      // whole rounds where there are few, else the share of a CTA and a half of the longest item
-      const double rounds = (double)((t[i].items + m - 1) / m), each = t[i].work / (double)t[i].items;
-      const double end = 4.5 + std::max(t[i].longest + 3.0, rounds <= 3.0 ? rounds * each : t[i].work / m + 0.5 * t[i].longest) + t[i].merge;
+      const double end = 4.5 + std::max(t[i].longest + 3.0, rounds(t[i], m)) + t[i].merge;
       if (i == 0 || end < t_tiles) {
         t_tiles = end;
         bt = i;
       }
     }
-    const double end = std::max(bytes / 6.5e6 + 5.0, std::max(t_rows, t_tiles)) + 0.05 * (t_rows + t_tiles);
+    const double end = std::max(bytes / 6.5e6 + 5.0, std::max(t_rows, t_tiles)) + 0.05 * (t_rows + t_tiles) + merge;
     if (c == 0 || end < best) {
       best = end;
       best_tiles = bt;
@@ -1718,14 +1765,91 @@ void plan_shared(const ChunkArgs& a, std::vector<Req>& reqs, int num_splits, int
       q.ns = std::min(kMaxAuto, std::max(1, (std::max(q.first, q.last) + t[best_tiles].tiles - 1) / t[best_tiles].tiles));
   {
     // a run longer than what a piece costs of itself; a request is cut into no more than 256 pieces
-    int longest = 1;
-    for (const Req& q : reqs) longest = std::max(longest, q.few);
     if (num_splits) best_runs = num_splits;
-    g.run = (int)std::max<int64_t>({(row + best_runs - 1) / best_runs, kStart + 1, (longest / kKeys + kStart) / (kMaxAuto - 2) + 1});
+    g.run = (int)std::max<int64_t>({(row + best_runs - 1) / best_runs, kStart + 1, (longest_few / kKeys + kStart) / (kMaxAuto - 2) + 1});
     g.runs = (int)((row + g.run - 1) / g.run);
     g.row_ctas = g.runs * groups;
   }
   g.ctas = (int)std::min<int64_t>(std::max(sms / 8, sms - g.row_ctas), t[best_tiles].items);
+  return 1.1 * best;  // (what it took against this and the other estimate, in the batches of apart())
+}
+
+// Chunks of a launch without CTAs of few rows, and its time in us. The launch ends when the SM with the most to do does: with
+// the items sorted by length and handed out one by one that is about the largest of an SM's share, the longest item, and
+// k times the item number (k - 1) * SMs + 1 (some SM has k items of at least that length). Cutting shortens items
+// and adds to the share: a prologue each, fp32 partials written and read, and a merge. Lengths of
+// pieces from the longest list down are tried and the best estimate is kept. (64 single tokens over
+// 522,892 cached ones: 345 us whole, 333 in the pieces found, 421 in 16 pieces each; a 2048-token
+// prompt: 79 us in pieces of 8 tiles, 40 whole.)
+double plan_items(const ChunkArgs& a, std::vector<Req>& reqs, bool shared, int sms) {
+  const double tile_us = RowTimes(a).tile_us;
+  int most = 0;
+  struct Same {  // requests of one length (beside shared prefixes the short ones are counted together: most of 64 are)
+    int tiles;
+    double len;
+    int64_t units, rows;
+    bool part;
+  };
+  std::vector<Same> all;
+  all.reserve(reqs.size());
+  constexpr int kShort = 64;
+  int at[2 * kShort];
+  std::fill(at, at + 2 * kShort, -1);
+  for (const Req& q : reqs) {
+    const int tiles = std::max(q.first, q.last);
+    most = std::max(most, tiles);
+    if (shared && q.first == q.last && tiles < kShort) {
+      int& i = at[tiles + (q.pre != -1 ? kShort : 0)];
+      if (i >= 0) {
+        all[i].units += q.units;
+        all[i].rows += q.n;
+        continue;
+      }
+      i = (int)all.size();
+    }
+    all.push_back(Same{tiles, 0.5 * (q.first + q.last), q.units, q.n, q.pre != -1});
+  }
+  auto chunks = [&](int tiles, int piece) { return std::min(kMaxAuto, std::max(1, (tiles + piece - 1) / piece)); };
+  auto estimate = [&](int piece) {
+    constexpr int kBins = 32;
+    double work = 0, longest = 0;
+    int pieces = 1;
+    int64_t bins[kBins] = {0};  // items by length, in steps of the longest possible one / 32
+    const double step = (std::min(piece, most) + kItem) / kBins;
+    bool cut = false;
+    for (const Same& q : all) {
+      const int ns = chunks(q.tiles, piece);
+      const int64_t items = q.units * a.Hkv * ns;
+      const double len = q.len / ns + kItem;
+      work += len * (double)items;
+      longest = std::max(longest, (double)q.tiles / ns + kItem);
+      bins[std::min(kBins - 1, (int)(len / step))] += items;
+      if (ns > 1 || q.part) {
+        cut = true;
+        pieces = std::max(pieces, ns);
+        work += (double)q.rows * a.Hq * ns * 8.0 * (a.d + 1) / 65536.0;  // (a tile of K and V is 64 KB at most)
+      }
+    }
+    double end = std::max(work / sms, longest);
+    int64_t before = 0, k = 1;
+    for (int b = kBins - 1; b >= 0 && k <= 8; --b) {
+      for (; k <= 8 && (k - 1) * sms < before + bins[b]; ++k) end = std::max(end, (double)k * (b + 0.5) * step);
+      before += bins[b];
+    }
+    return end + (cut ? kMerge : 0.0) + (shared ? kPieceUs * pieces / tile_us : 0.0);
+  };
+  int best = most;
+  double best_end = estimate(most);
+  for (int piece = most; piece > 2;) {
+    piece = std::max(2, piece * 2 / 3);
+    const double end = estimate(piece);
+    if (end < 0.97 * best_end) {
+      best = piece;
+      best_end = end;
+    }
+  }
+  for (Req& q : reqs) q.ns = chunks(std::max(q.first, q.last), best);
+  return 4.5 + tile_us * best_end;
 }
 
 sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, const Prefixes& pf, int r0, int r1,
@@ -1755,110 +1879,86 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
     if (some < 2 || skip == 0) return kNot;
     return apart - own - items(n, skip) - 2.0 * n * a.Hq * 8.0 * (a.d + 1) / 65536.0;
   };
-  // It has to save the time of the merge, 4 us, or 2.5 tiles of each SM. (num_splits asks for it.)
-  bool worth = num_splits > 0;
-  if (pf.n > 0 && !worth) {
-    double sum = 0;
-    for (int i = 0; i < pf.n; ++i) {
-      const int from = std::max(r0, (int)pf.indptr[i]), to = std::min(r1, (int)pf.indptr[i + 1]);
-      if (from < to) sum += std::max(0.0, saves(from, to, pf.prefix[i]));
-    }
-    worth = sum > 2.5 * sms;
+  double sum = 0;
+  for (int i = 0; i < pf.n; ++i) {
+    const int from = std::max(r0, (int)pf.indptr[i]), to = std::min(r1, (int)pf.indptr[i + 1]);
+    if (from < to) sum += std::max(0.0, saves(from, to, pf.prefix[i]));
   }
   auto tiles_of = [&](int n, int64_t len, int u) {  // key tiles of pair u
     int gt, wl;
     const int64_t t0 = (int64_t)2 * u * a.TQ, te = std::min<int64_t>(n, t0 + 2 * a.TQ), p0 = len - n;
     return tile_list(seen(a, p0 + t0, p0 + te - 1, len), gt, wl);
   };
-  int most = 0;
   auto units_of = [&](int n) { return ((n + a.TQ - 1) / a.TQ + 1) / 2; };
   auto add = [&](int r, int64_t skip, int pre, int lead) {  // request r's keys from token `skip` on
     const int n = qi[r + 1] - qi[r], units = units_of(n);
     const int64_t len = (int64_t)ki[r + 1] - ki[r] - skip;
     reqs.push_back(Req{r - r0, n, units, tiles_of(n, len, 0), tiles_of(n, len, units - 1), std::max(num_splits, 1), (int)skip, pre,
                        r - r0 + 1, lead, (int64_t)n * a.G <= 16 ? (int)len : 0});
-    most = std::max(most, std::max(reqs.back().first, reqs.back().last));
   };
-  for (int r = r0, i = 0; r < r1;) {
-    int end = r + 1;
-    if (pf.n > 0) {
-      while (pf.indptr[i + 1] <= r) ++i;
-      end = std::min(r1, (int)pf.indptr[i + 1]);  // (a group that two launches meet in is two groups)
-      if (const double saved = worth ? saves(r, end, pf.prefix[i]) : kNot; num_splits > 0 ? saved > kNot : saved > 0) {
-        int lead = r;
-        while (qi[lead + 1] == qi[lead]) ++lead;
-        const int n = qi[end] - qi[r], tiles = (pf.prefix[i] + kBN - 1) / kBN, me = (int)reqs.size();
-        reqs.push_back(Req{r - r0, n, units_of(n), tiles, tiles, std::max(num_splits, 1), pf.prefix[i], -2, end - r0, lead - r0, 0});
-        most = std::max(most, tiles);
-        g.shared = true;
-        for (; r < end; ++r)
-          if (qi[r + 1] > qi[r]) add(r, pf.prefix[i], me, lead - r0);
-        continue;
+  auto fill = [&](bool share) {
+    reqs.clear();
+    g.shared = false;
+    for (int r = r0, i = 0; r < r1;) {
+      int end = r + 1;
+      if (pf.n > 0) {
+        while (pf.indptr[i + 1] <= r) ++i;
+        end = std::min(r1, (int)pf.indptr[i + 1]);  // (a group that two launches meet in is two groups)
+        if (const double saved = share ? saves(r, end, pf.prefix[i]) : kNot; num_splits > 0 ? saved > kNot : saved > 0) {
+          int lead = r;
+          while (qi[lead + 1] == qi[lead]) ++lead;
+          const int n = qi[end] - qi[r], tiles = (pf.prefix[i] + kBN - 1) / kBN, me = (int)reqs.size();
+          reqs.push_back(Req{r - r0, n, units_of(n), tiles, tiles, std::max(num_splits, 1), pf.prefix[i], -2, end - r0, lead - r0, 0});
+          g.shared = true;
+          for (; r < end; ++r)
+            if (qi[r + 1] > qi[r]) add(r, pf.prefix[i], me, lead - r0);
+          continue;
+        }
       }
+      for (; r < end; ++r)
+        if (qi[r + 1] > qi[r]) add(r, 0, -1, 0);
     }
-    for (; r < end; ++r)
-      if (qi[r + 1] > qi[r]) add(r, 0, -1, 0);
-  }
+  };
+  fill(num_splits > 0 ? pf.n > 0 : sum > kNone * sms);
+  // Few rows: pages that hold no boxes of 8 tokens are copied token by token (44 us for a case that takes 33 in items); and
+  // a request takes the time of a tile of 16 keys of all of its CTA's heads, or an item for each.
+  const RowTimes times(a);
   bool rows = false;
   int64_t items = 0;
   for (Req& q : reqs) {
-    // (pages that hold no boxes of 8 tokens, copied token by token: 44 us for a case that takes 33 in items)
-    if (!g.shared || a.row_box == 0) q.few = 0;
+    if (!g.shared || a.row_box == 0 || (num_splits == 0 && !times.few(q.few))) q.few = 0;
     rows = rows || q.few > 0;
     items += q.few ? 0 : (int64_t)q.units * a.Hkv;
   }
-  // three rounds of items and more: those of few rows are dealt out with them, by CTAs that take over one another's
-  if (num_splits == 0 && items > 3 * sms) {
-    for (Req& q : reqs) q.few = 0;
-    rows = false;
-  }
-  if (rows) plan_shared(a, reqs, num_splits, sms, g);
-  // Chunks. The launch ends when the SM with the most to do does: with the items sorted by length and
-  // handed out one by one that is about the largest of an SM's share, the longest item, and k times the
-  // item number (k - 1) * SMs + 1 (some SM has k items of at least that length). Cutting shortens items
-  // and adds to the share: a prologue each, fp32 partials written and read, and a merge. Lengths of
-  // pieces from the longest list down are tried and the best estimate is kept. (64 single tokens over
-  // 522,892 cached ones: 345 us whole, 333 in the pieces found, 421 in 16 pieces each; a 2048-token
-  // prompt: 79 us in pieces of 8 tiles, 40 whole.)
-  if (!rows && num_splits == 0 && most > 2) {
-    auto chunks = [&](int tiles, int piece) { return std::min(kMaxAuto, std::max(1, (tiles + piece - 1) / piece)); };
-    auto estimate = [&](int piece) {
-      constexpr int kBins = 32;
-      double work = 0, longest = 0;
-      int64_t bins[kBins] = {0};  // items by length, in steps of the longest possible one / 32
-      const double step = (std::min(piece, most) + kItem) / kBins;
-      bool cut = false;
-      for (const Req& q : reqs) {
-        const int tiles = std::max(q.first, q.last), ns = chunks(tiles, piece);
-        const int64_t items = (int64_t)q.units * a.Hkv * ns;
-        const double len = 0.5 * (q.first + q.last) / ns + kItem;
-        work += len * (double)items;
-        longest = std::max(longest, (double)tiles / ns + kItem);
-        bins[std::min(kBins - 1, (int)(len / step))] += items;
-        if (ns > 1 || q.pre != -1) {
-          cut = true;
-          work += (double)q.n * a.Hq * ns * 8.0 * (a.d + 1) / 65536.0;  // (a tile of K and V is 64 KB at most)
-        }
-      }
-      double end = std::max(work / sms, longest);
-      int64_t before = 0, k = 1;
-      for (int b = kBins - 1; b >= 0 && k <= 8; --b) {
-        for (; k <= 8 && (k - 1) * sms < before + bins[b]; ++k) end = std::max(end, (double)k * (b + 0.5) * step);
-        before += bins[b];
-      }
-      return end + (cut ? kMerge : 0.0);
-    };
-    int best = most;
-    double best_end = estimate(most);
-    for (int piece = most; piece > 2;) {
-      piece = std::max(2, piece * 2 / 3);
-      const double end = estimate(piece);
-      if (end < 0.97 * best_end) {
-        best = piece;
-        best_end = end;
+  if (num_splits > 0) {
+    if (rows) plan_shared(a, reqs, num_splits, sms, g);
+  } else {
+    double end = plan_items(a, reqs, g.shared, sms);
+    // three rounds of items and more: those of few rows are dealt out with them, by CTAs that take over one another's
+    rows = rows && items <= 3 * sms;
+    if (rows) {
+      const std::vector<Req> whole = reqs;
+      const double t = plan_shared(a, reqs, 0, sms, g);
+      rows = t < end;
+      if (rows) end = t;
+      else reqs = whole;
+    }
+    if (!rows) {
+      for (Req& q : reqs) q.few = 0;
+      g.run = g.runs = g.row_ctas = g.ctas = 0;
+    }
+    if (g.shared && sum < kClear * sms) {  // or nothing shared
+      std::vector<Req> shared;
+      reqs.swap(shared);
+      fill(false);
+      for (Req& q : reqs) q.few = 0;
+      if (apart(a) * plan_items(a, reqs, false, sms) > end) {
+        reqs.swap(shared);
+        g.shared = true;
+      } else {
+        g.run = g.runs = g.row_ctas = g.ctas = 0;
       }
     }
-    for (Req& q : reqs) q.ns = chunks(std::max(q.first, q.last), best);
   }
   auto longest = [](const Req& q) { return q.few ? 1e9 : (double)std::max(q.first, q.last) / q.ns; };
   std::vector<int> order(reqs.size()), rank(reqs.size());
