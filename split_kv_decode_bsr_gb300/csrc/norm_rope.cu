@@ -438,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm<W, LY, NU>(MODE == kBackw
   constexpr bool BWD = MODE == kBackward;
   constexpr int S = W == 1 ? 0 : kSlots<NU>, SLOT = U::V * 512 * (BWD ? 2 : 1);
   extern __shared__ __align__(16) uint8_t smem[];
+  if (BWD) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // norm_dw_kernel may start, and wait
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint8_t* mine = smem + warp * A.warp_bytes;  // S slots, then the table
   const uint32_t ring = smem_u32(mine) + lane * 16;
@@ -660,27 +661,41 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm<W, LY, NU>(MODE == kBackw
   }
 }
 
-// dw from the CTAs' sums, always in the same order: 32 columns a block, 32 slices of the CTAs; q, then k.
+// dw from the CTAs' sums, always in the same order: 32 columns a block, 32 slices of the CTAs; q, then k. It starts while they
+// are still at work and waits for them (8192 tokens 51.8 us, one after the other 52.8; 40 heads of 128 of 300 tokens in fp32 9.7, 10.1).
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int nq, int nk, int d, float* dqw, float* dkw) {
   __shared__ float s[32][33];
   const int c = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
   float* out = blockIdx.y ? dkw : dqw;
-  if (!out) return;
   const int n = blockIdx.y ? nk : nq;
   if (blockIdx.y) part += (int64_t)nq * d;
   float v = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (col < d) {
 #pragma unroll 4
-    for (int i = y; i < n; i += 32) v += __ldg(part + (int64_t)i * d + col);
+    for (int i = y; i < n; i += 32) v += part[(int64_t)i * d + col];
   }
   s[y][c] = v;
   __syncthreads();
-  if (y == 0 && col < d) {
+  if (y == 0 && col < d && out) {
     v = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) v += s[i][c];
     out[col] = v;
   }
+}
+
+cudaError_t launch_dw(cudaStream_t st, const float* part, int nq, int nk, int d, float* dqw, float* dkw) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)cdiv(d, 32), 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_dw_kernel, part, nq, nk, d, dqw, dkw);
 }
 
 // Shape of a launch: vectors, layout, units and lanes, the pieces of a token, and the shared memory of a warp.
@@ -769,8 +784,7 @@ sta_status launch_bwd(NormArgs& a, const RopeTable& tab, bool il, float* dqw, fl
   const sta_status status = launch_norm<T, kBackward>(a, tab, il, st, ctas);
   if (status != STA_OK) return status;
   if (dqw || dkw) {
-    norm_dw_kernel<<<dim3((unsigned)cdiv(a.d, 32), 2), 1024, 0, st>>>(a.part, ctas[0], ctas[1], a.d, dqw, dkw);
-    STA_LAUNCH_CHECK();
+    STA_CUDA_TRY(launch_dw(st, a.part, ctas[0], ctas[1], a.d, dqw, dkw));
   }
   return STA_OK;
 }
@@ -891,8 +905,7 @@ extern "C" sta_status sta_norm_rope_bwd(const void* dq_out, const void* dk_out, 
   const cudaStream_t s = (cudaStream_t)stream;
   if (n_tokens == 0) {  // no rows: the weights' gradients are 0
     if (dq_weight || dk_weight) {
-      norm_dw_kernel<<<dim3((unsigned)cdiv(d, 32), 2), 1024, 0, s>>>(a.part, 0, 0, d, dq_weight, dk_weight);
-      STA_LAUNCH_CHECK();
+      STA_CUDA_TRY(launch_dw(s, a.part, 0, 0, d, dq_weight, dk_weight));
     }
     return STA_OK;
   }

@@ -73,10 +73,11 @@ sta_status rope_table(const sta_rope_params* r, int d, RopeTable& tab) {
         f = g * f + (1.0 - g) * f / r->factor;
       }
     }
-    double turns = std::fmod(f / two_pi, 1.0);
+    double turns = f / two_pi;
+    if (!(turns >= 0.0 && turns < 1.0)) turns = std::fmod(turns, 1.0);
     if (turns < 0.0) turns += 1.0;
     if (turns >= 1.0) turns = 0.0;  // a tiny negative turn rounds up to a whole one
-    tab.turn[p] = (uint64_t)std::ldexp(turns, 64);
+    tab.turn[p] = (uint64_t)(turns * 0x1p64);
   }
   return STA_OK;
 }
