@@ -1,6 +1,7 @@
 """Python binding of libsta (masked MHA over a two-level BSR + bitmap mask, split-KV decode).
 
-Thin ctypes marshalling over the C ABI in ``include/sta.h``: every function of the
+Thin marshalling over the C ABI in ``include/sta.h`` (ctypes; ``csrc/bind.cpp`` for the calls
+whose kernels take no longer than that would): every function of the
 same name calls the CUDA library, on the current torch stream, with device memory
 held in torch tensors. There is no fallback: when ``libsta.so`` has not been built
 (``python -m split_kv_decode_bsr_gb300.build`` or ``__graft_entry__.build()``) every
@@ -17,6 +18,9 @@ Operations (sources):
   * ``sta_rope``, ``sta_rope_append_paged``, ``sta_chunk_fwd_paged``, ``sta_pages_*`` --
     serving over the paged KV cache of the paged decode: rotary positions, the write of new
     tokens, the attention of chunks of new tokens, and the bookkeeping of pages.
+  * ``sta_norm_rope``, ``sta_norm_rope_bwd``, ``sta_norm_rope_append_paged`` -- root-mean-square norms of
+    query and key heads with the rotary positions in the same pass, their gradient, and the cache write.
+  * ``sta_prefix_fwd_paged`` -- the chunk attention of requests that share their first pages.
 """
 
 from __future__ import annotations

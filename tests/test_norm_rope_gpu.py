@@ -256,6 +256,23 @@ def test_norm_rope_many_tokens(dev, dtype):
     assert all(torch.equal(a, b) for a, b in zip(again, got))
 
 
+def test_norm_rope_tokens_far_apart(dev):
+    # offsets past 32 bits, in elements and bytes: the same numbers as side by side
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = Case(dev, 3, 2, 0, 64, 64, False, "bf16")
+    far = torch.empty(3 << 31, device=dev, dtype=torch.bfloat16)
+    at = lambda first: far[first:].as_strided((3, 2, 64), (1 << 31, 64, 1))  # noqa: E731
+    q, dy = at(0).copy_(c.q), at(1024).copy_(c.dy[0])
+    want = sta.sta_norm_rope(c.q.contiguous(), None, *c.args(), q_weight=c.qw)[0]
+    assert torch.equal(sta.sta_norm_rope(q, None, *c.args(), q_weight=c.qw, q_out=at(4096))[0], want)
+    want = sta.sta_norm_rope_bwd(c.dy[0], None, c.q.contiguous(), None, *c.args(), q_weight=c.qw)
+    got = sta.sta_norm_rope_bwd(dy, None, q, None, *c.args(), q_weight=c.qw, dq=at(8192))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+
+
 def test_norm_rope_streams_and_graphs(dev):
     import torch
 
@@ -414,3 +431,27 @@ def test_norm_append_positions_and_bad_pages(dev):
                                        x["page_indices_dev"], x["q_indptr_dev"], x["kv_indptr_dev"])
         assert sta.sta_device_error(reset=True) == code
         assert torch.equal(k0.view(torch.int16), x["k_pages"].view(torch.int16))
+
+
+def test_norm_append_into_far_pages(dev):
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = PagedCase(77, [1, 30, 5], [90, 30, 41], 4, 8, 128, 16)
+    x, N = c.dev(dev), c.q.shape[0]
+    k, v = (torch.randn(N, 8, 128, device=dev).to(torch.bfloat16) for _ in "kv")
+    pages = lambda big: dict(x, k_pages=big[0], v_pages=big[1])  # noqa: E731
+
+    def append(x, indices):
+        sta.sta_norm_rope_append_paged(None, k, v, x["k_pages"], x["v_pages"], x["page_indptr_dev"], indices, x["q_indptr_dev"],
+                                       x["kv_indptr_dev"], rope=sta.Rope(128))
+        return x["k_pages"], x["v_pages"]
+
+    n = x["k_pages"].shape[0]
+    big = [torch.empty(135000, 16, 8, 128, device=dev, dtype=torch.bfloat16) for _ in "kv"]  # 4.4 GB each
+    for b, a in zip(big, (x["k_pages"], x["v_pages"])):
+        b[-n:] = a
+    got = append(pages(big), x["page_indices_dev"] + 135000 - n)
+    for a, b in zip(got, append(x, x["page_indices_dev"])):
+        assert torch.equal(a[-n:].view(torch.int16), b.view(torch.int16))

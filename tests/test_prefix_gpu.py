@@ -117,6 +117,27 @@ def test_prefix_strides_padding_outputs_and_workspace(dev):
         sta.sta_prefix_fwd_paged(**x, num_splits=2, workspace=ws[:256])
 
 
+@pytest.mark.parametrize("P", [16, 100])
+def test_prefix_in_far_pages(dev, P):
+    # offsets past 32 bits in the cache: the same numbers as at its start
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = SharedCase(18, [40], [1200 // P * P], [1] * 39 + [20], [3 + 5 * i % 70 for i in range(39)] + [55], 32, 8, 128, P)
+    x = c.dev(dev)
+    want = [sta.sta_prefix_fwd_paged(**x, num_splits=s) for s in (0, 2)]
+    n, far = x["k_pages"].shape[0], (1 << 31) // (P * 8 * 128) + 1000
+    for name in ("k_pages", "v_pages"):
+        big = torch.empty(far + n, P, 8, 128, device=dev, dtype=torch.bfloat16)  # 4.3 GB and more
+        big[far:] = x[name]
+        x[name] = big
+    x["page_indices_dev"] = x["page_indices_dev"] + far
+    for s, (o, lse) in zip((0, 2), want):
+        got = sta.sta_prefix_fwd_paged(**x, num_splits=s)
+        assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+
+
 def test_prefix_streams_and_repeats(dev):
     import torch
 
