@@ -31,6 +31,7 @@ import functools
 import importlib
 import math
 import os
+import struct
 import threading
 from dataclasses import dataclass
 from typing import List, Optional, Sequence
@@ -90,6 +91,7 @@ class _RopeParams(C.Structure):
                 ("high_turns", C.c_double), ("freqs", C.c_void_p)]
 
 
+_pack_rope = struct.Struct("@iiif5dP").pack  # a _RopeParams
 _lock = threading.Lock()
 _lib_handle = None
 _bound_calls = None  # csrc/bind.cpp, once a call of it is made
@@ -725,11 +727,24 @@ class Rope:
             if len(freqs) != rot_dim // 2:
                 raise ValueError("freqs: rot_dim / 2 values")
             self._freqs = (C.c_double * len(freqs))(*[float(f) for f in freqs])
-        self.rot_dim = int(rot_dim)
-        self.struct = _RopeParams(int(rot_dim), STA_ROPE_INTERLEAVED if interleaved else STA_ROPE_HALF, kind,
-                                  float(mscale), float(base), float(factor), float(orig_len), float(low_turns),
-                                  float(high_turns), C.cast(self._freqs, C.c_void_p) if self._freqs else None)
-        self.at = C.addressof(self.struct)
+        self.rot_dim = rot = int(rot_dim)
+        fields = (rot, STA_ROPE_INTERLEAVED if interleaved else STA_ROPE_HALF, kind, float(mscale), float(base), float(factor),
+                  float(orig_len), float(low_turns), float(high_turns), C.addressof(self._freqs) if self._freqs else 0)
+        try:
+            self._bytes, self._struct = _pack_rope(*fields), None
+        except (OverflowError, struct.error):  # more than the field holds: as ctypes takes it
+            self._struct = _RopeParams(*fields)
+
+    @property
+    def struct(self):
+        if self._struct is None:
+            self._struct = _RopeParams.from_buffer_copy(self._bytes)
+        return self._struct
+
+    def packed(self) -> bytes:
+        """The parameters as the C struct lays them out (a tenth of the time of a ctypes struct: a program may make its Rope
+        at every call)."""
+        return self._bytes if self._struct is None else bytes(self._struct)
 
 
 def _heads_view(t: torch.Tensor, what: str):
@@ -802,7 +817,7 @@ def sta_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], position
     None: the other alone. rope None: normed alone. q_out / k_out may be q / k (in place). Returns
     (q_out, k_out), new [n, H, d] tensors where none are given.
     """
-    return _bound("norm_rope", stream, q if q is not None else k, q, k, positions, 0 if rope is None else rope.at, q_weight,
+    return _bound("norm_rope", stream, q if q is not None else k, q, k, positions, None if rope is None else rope.packed(), q_weight,
                   k_weight, eps, q_out, k_out)
 
 
@@ -818,7 +833,7 @@ def sta_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Ten
     (that of a factor of 1); None where q or k is.
     """
     return _bound("norm_rope_bwd", stream, q if q is not None else k, dq_out, dk_out, q, k, positions,
-                  0 if rope is None else rope.at, q_weight, k_weight, eps, dq, dk, workspace)
+                  None if rope is None else rope.packed(), q_weight, k_weight, eps, dq, dk, workspace)
 
 
 def sta_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
@@ -883,7 +898,7 @@ def sta_norm_rope_append_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: to
     """sta_rope_append_paged with each head of q and k normed first (as in sta_norm_rope: weights float32
     [d] or None, eps). rope None: normed alone. Returns the normed and turned q."""
     return _bound("norm_rope_append_paged", stream, k, q, k, v, k_pages, v_pages, page_indptr_dev, page_indices_dev, q_indptr_dev,
-                  kv_indptr_dev, 0 if rope is None else rope.at, q_weight, k_weight, eps, positions, q_out)
+                  kv_indptr_dev, None if rope is None else rope.packed(), q_weight, k_weight, eps, positions, q_out)
 
 
 def sta_chunk_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_indptr_dev: torch.Tensor,

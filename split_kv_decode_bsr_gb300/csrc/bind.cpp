@@ -117,7 +117,12 @@ const Tensor& first(const Maybe& q, const Maybe& k) {
   return *x;
 }
 
-const sta_rope_params* params(uintptr_t rope) { return reinterpret_cast<const sta_rope_params*>(rope); }
+// A Rope's parameters: the bytes of the C struct (aligned: what precedes them in a bytes object is whole words), or None.
+const sta_rope_params* params(const py::object& rope) {
+  if (rope.is_none()) return nullptr;
+  if (!PyBytes_Check(rope.ptr()) || PyBytes_GET_SIZE(rope.ptr()) != (Py_ssize_t)sizeof(sta_rope_params)) refuse("rope: a Rope");
+  return reinterpret_cast<const sta_rope_params*>(PyBytes_AS_STRING(rope.ptr()));
+}
 
 // The tensors' device, made current where it is not, and its current stream.
 struct On {
@@ -146,27 +151,29 @@ void* workspace_at(const Maybe& given, size_t need, const Tensor& like, Tensor& 
   return given->data_ptr();
 }
 
-std::tuple<Maybe, Maybe> norm_rope(const Maybe& q, const Maybe& k, const Maybe& positions, uintptr_t rope, const Maybe& q_weight,
+std::tuple<Maybe, Maybe> norm_rope(const Maybe& q, const Maybe& k, const Maybe& positions, const py::object& rope, const Maybe& q_weight,
                                    const Maybe& k_weight, double eps, Maybe q_out, Maybe k_out) {
   const Tensor& x = first(q, k);
   const int code = dtype_code(x);
-  const int32_t* pos = rope ? token_positions(positions, x, true) : nullptr;
+  const sta_rope_params* turn = params(rope);
+  const int32_t* pos = turn ? token_positions(positions, x, true) : nullptr;
   const Heads a = heads(q, "q", x), b = heads(k, "k", x);
   const float *qw = norm_weight(q_weight, "q_weight", x), *kw = norm_weight(k_weight, "k_weight", x);
   On on(x);
   const Heads c = result(q_out, q, "q_out"), d = result(k_out, k, "k_out");
   check("sta_norm_rope", sta_norm_rope(a.at, b.at, a.stride, b.stride, c.at, d.at, c.stride, d.stride, qw, kw, (float)eps, pos,
-                                       params(rope), x.size(0), a.H, b.H, (int)x.size(2), code, on.stream));
+                                       turn, x.size(0), a.H, b.H, (int)x.size(2), code, on.stream));
   return {q_out, k_out};
 }
 
 std::tuple<Maybe, Maybe, Maybe, Maybe> norm_rope_bwd(const Maybe& dq_out, const Maybe& dk_out, const Maybe& q, const Maybe& k,
-                                                     const Maybe& positions, uintptr_t rope, const Maybe& q_weight,
+                                                     const Maybe& positions, const py::object& rope, const Maybe& q_weight,
                                                      const Maybe& k_weight, double eps, Maybe dq, Maybe dk,
                                                      const Maybe& workspace) {
   const Tensor& x = first(q, k);
   const int code = dtype_code(x);
-  const int32_t* pos = rope ? token_positions(positions, x, true) : nullptr;
+  const sta_rope_params* turn = params(rope);
+  const int32_t* pos = turn ? token_positions(positions, x, true) : nullptr;
   const Heads a = heads(q, "q", x), b = heads(k, "k", x), y = heads(dq_out, "dq_out", x), z = heads(dk_out, "dk_out", x);
   if (!(y.H == a.H && z.H == b.H)) refuse("dq_out, dk_out: the shapes of q and k");
   const float *qw = norm_weight(q_weight, "q_weight", x), *kw = norm_weight(k_weight, "k_weight", x);
@@ -186,7 +193,7 @@ std::tuple<Maybe, Maybe, Maybe, Maybe> norm_rope_bwd(const Maybe& dq_out, const 
   check("sta_norm_rope_bwd",
         sta_norm_rope_bwd(y.at, z.at, y.stride, z.stride, a.at, b.at, a.stride, b.stride, g.at, h.at, g.stride, h.stride, qw, kw,
                           dqw ? dqw->data_ptr<float>() : nullptr, dkw ? dkw->data_ptr<float>() : nullptr, (float)eps, pos,
-                          params(rope), x.size(0), a.H, b.H, d, code, ws, &bytes, on.stream));
+                          turn, x.size(0), a.H, b.H, d, code, ws, &bytes, on.stream));
   return {dq, dk, dqw, dkw};
 }
 
@@ -197,7 +204,7 @@ void pages_of(const Tensor& k_pages, const Tensor& v_pages) {
 
 Maybe norm_rope_append_paged(const Maybe& q, const Tensor& k, const Tensor& v, const Tensor& k_pages, const Tensor& v_pages,
                              const Tensor& page_indptr, const Tensor& page_indices, const Tensor& q_indptr,
-                             const Tensor& kv_indptr, uintptr_t rope, const Maybe& q_weight, const Maybe& k_weight, double eps,
+                             const Tensor& kv_indptr, const py::object& rope, const Maybe& q_weight, const Maybe& k_weight, double eps,
                              const Maybe& positions, Maybe q_out) {
   on_cuda(k);
   pages_of(k_pages, v_pages);
