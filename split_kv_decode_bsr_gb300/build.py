@@ -56,7 +56,7 @@ def _bind_commands(obj: str, out: str):
     cc = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           *[f"-I{i}" for i in inc], "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj]
     ld = ["g++", "-shared", "-o", out, obj, f"-L{os.path.join(root, 'lib')}", f"-L{HERE}", "-l:libsta.so", "-lc10", "-lc10_cuda",
-          "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+          "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     return cc, ld
 
 

@@ -2,7 +2,7 @@
 // allocate, the current stream and the call of libsta, without an interpreter's step for each (64 single tokens behind
 // a shared prefix: some 40 us of host time a call through ctypes, whose kernels take as long).
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -50,6 +50,11 @@ int64_t token_stride(const Tensor& t, const char* what) {
   return n > 1 ? t.stride(0) : H * d;
 }
 
+// A new contiguous tensor beside `like`, without the dispatcher's steps (0.5 us less for each, in calls of 7 to 15).
+Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const Tensor& like) {
+  return Tensor(at::detail::empty_cuda(sizes, type, like.device(), std::nullopt));
+}
+
 struct Heads {
   void* at = nullptr;
   int H = 0;
@@ -74,7 +79,7 @@ Heads result(Maybe& given, const Maybe& x, const char* what) {
     return h;
   }
   if (!given) {
-    given = at::empty(x->sizes(), x->options());
+    given = fresh(x->sizes(), x->scalar_type(), *x);
     h.stride = x->size(1) * x->size(2);
   } else {
     if (!(given->sizes() == x->sizes() && given->scalar_type() == x->scalar_type() && given->device() == x->device()))
@@ -135,7 +140,7 @@ struct On {
 };
 
 Tensor scratch(size_t bytes, const Tensor& like) {
-  return at::empty({(int64_t)bytes}, like.options().dtype(at::kByte));
+  return fresh({(int64_t)bytes}, at::kByte, like);
 }
 void* workspace_at(const Maybe& given, size_t need, const Tensor& like, Tensor& own, size_t& bytes) {
   if (!given) {
@@ -181,9 +186,8 @@ std::tuple<Maybe, Maybe, Maybe, Maybe> norm_rope_bwd(const Maybe& dq_out, const 
   On on(x);
   const Heads g = result(dq, q, "dq"), h = result(dk, k, "dk");
   Maybe dqw, dkw;
-  const auto f32 = x.options().dtype(at::kFloat);
-  if (q) dqw = at::empty({d}, f32);
-  if (k) dkw = at::empty({d}, f32);
+  if (q) dqw = fresh({d}, at::kFloat, x);
+  if (k) dkw = fresh({d}, at::kFloat, x);
   size_t need = 0, bytes = 0;
   check("sta_norm_rope_bwd", sta_norm_rope_bwd(nullptr, nullptr, d, 0, nullptr, nullptr, d, 0, nullptr, nullptr, d, 0, nullptr,
                                                nullptr, nullptr, nullptr, 1.f, nullptr, nullptr, 0, 1, 0, d, STA_BF16, nullptr,
@@ -300,10 +304,10 @@ std::tuple<Tensor, Tensor> prefix_fwd_paged(const Tensor& q, const Tensor& k_pag
   if (!(rows >= 0 && rows <= n)) refuse("q_indptr: past q's rows");
   const float by = scale ? (float)*scale : 1.f / std::sqrt((float)d);
   On on(q);
-  if (!o) o = at::empty(q.sizes(), q.options());
+  if (!o) o = fresh(q.sizes(), q.scalar_type(), q);
   else if (!(o->sizes() == q.sizes() && o->scalar_type() == q.scalar_type() && o->is_contiguous() && o->device() == q.device()))
     refuse("o: contiguous, q's shape, dtype and device");
-  if (!lse) lse = at::empty({n, Hq}, q.options().dtype(at::kFloat));
+  if (!lse) lse = fresh({n, Hq}, at::kFloat, q);
   else if (!(lse->dim() == 2 && lse->size(0) == n && lse->size(1) == Hq && lse->scalar_type() == at::kFloat && lse->is_contiguous() &&
              lse->device() == q.device()))
     refuse("lse: contiguous float32 [n, Hq]");

@@ -2187,7 +2187,9 @@ sta_status chunk_fwd(const void* q, int64_t q_stride, const void* k_pages, const
     m.k4 = m.k;
     m.v4 = m.v;
   }
-  if (pf.n > 0 && a.row_box > 0)
+  bool few = false;
+  for (const Group& g : groups) few = few || g.row_ctas > 0;
+  if (few)
     maps = maps && make_row_map(&m.rows.k, k_pages, d, Hkv, rows, a.row_box) && make_row_map(&m.rows.v, v_pages, d, Hkv, rows, a.row_box);
   else
     m.rows.k = m.rows.v = m.k;  // not used
