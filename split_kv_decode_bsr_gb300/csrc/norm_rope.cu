@@ -14,11 +14,11 @@
 // and written once; the products in between stay in fp32 and are rounded once. The turns are exact at any position, as
 // in the rotary kernel.
 //
-// What bounds it (8192 tokens of 32 + 8 heads of 128 in bf16, graph of calls back to back). Forward 29.9 us, 5.6 TB/s of the
-// 168 MB it has to move where a copy reaches 6.78 (24.7 us); HBM, with 64 % of the issue slots taken. Backward 51.8 us
+// What bounds it (8192 tokens of 32 + 8 heads of 128 in bf16, graph of calls back to back). Forward 29.6 us, 5.7 TB/s of the
+// 168 MB it has to move where a copy reaches 6.78 (24.7 us); HBM, with 64 % of the issue slots taken. Backward 51.5 us
 // (37.1 at copy speed): 125 registers allow 16 warps an SM, which take 58 % of the issue slots, and each waits for its
-// loads, its sums' shuffles and its results in turn (3 CTAs an SM spill: 84). The 11975 tokens of 24 prompts, 32 + 4 + 4
-// heads, into pages of 100: 46.5 (36.2). Small calls are the launch: 64 tokens into the cache 4.4 us, one step's norms 2.9.
+// loads, its sums' shuffles and its results in turn (3 CTAs an SM spill: 84; 20 warps with the weights in shared memory 54). The 11975 tokens of 24 prompts, 32 + 4 + 4
+// heads, into pages of 100: 45.9 (36.2). Small calls are the launch: 64 tokens into the cache 4.1 us, one step's norms 2.4.
 #include <type_traits>
 
 #include "rope.inl"
@@ -444,13 +444,14 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm<W, LY, NU>(MODE == kBackw
   constexpr bool BWD = MODE == kBackward;
   constexpr int S = W == 1 ? 0 : kSlots<NU>, SLOT = U::V * 512 * (BWD ? 2 : 1);
   extern __shared__ __align__(16) uint8_t smem[];
-  if (BWD) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // norm_dw_kernel may start, and wait
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint8_t* mine = smem + warp * A.warp_bytes;  // S slots, then the table
   const uint32_t ring = smem_u32(mine) + lane * 16;
   float2* s_cs = reinterpret_cast<float2*>(mine + S * SLOT);
   U u;
   u.set(A);
+  // the kernel before this one has ended; the next one may start, and wait
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
   const int role = BWD && (int)blockIdx.x >= A.ctas_q;  // backward: the tensor of this CTA
   const int n_pieces = BWD ? A.pieces[role] : A.pieces[0] + A.pieces[1] + (MODE == kAppend ? A.pieces[2] : 0);
   const int64_t total = A.n_tokens * n_pieces;
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int nq
   const int n = blockIdx.y ? nk : nq;
   if (blockIdx.y) part += (int64_t)nq * d;
   float v = 0.f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
   if (col < d) {
 #pragma unroll 4
     for (int i = y; i < n; i += 32) v += part[(int64_t)i * d + col];
@@ -691,17 +692,25 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int nq
   }
 }
 
-cudaError_t launch_dw(cudaStream_t st, const float* part, int nq, int nk, int d, float* dqw, float* dkw) {
+// A launch that may start while the kernel before it on the stream ends, and waits for that before it reads anything (one
+// step's norms after one another 2.4 us, 2.9 without; the gradient of 1999 tokens of 16 heads of 64 9.0, 9.6).
+template <class... F, class... T>
+cudaError_t launch_early(void (*kern)(F...), dim3 grid, int threads, size_t smem, cudaStream_t st, const T&... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)cdiv(d, 32), 2);
-  cfg.blockDim = dim3(1024);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_dw_kernel, part, nq, nk, d, dqw, dkw);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+cudaError_t launch_dw(cudaStream_t st, const float* part, int nq, int nk, int d, float* dqw, float* dkw) {
+  return launch_early(norm_dw_kernel, dim3((unsigned)cdiv(d, 32), 2), 1024, 0, st, part, nq, nk, d, dqw, dkw);
 }
 
 // Shape of a launch: vectors, layout, units and lanes, the pieces of a token, and the shared memory of a warp.
@@ -769,8 +778,7 @@ sta_status launch_norm(NormArgs& a, const RopeTable& tab, bool il, cudaStream_t 
   if (a.n_tokens * pieces / ((int64_t)grid * kWarps) >= INT32_MAX) return STA_ERR_INVALID_ARG;
   auto go = [&](auto kern) -> sta_status {
     if (smem > 48 * 1024) STA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-    kern<<<grid, kThreads, smem, st>>>(a, tab);
-    STA_LAUNCH_CHECK();
+    STA_CUDA_TRY(launch_early(kern, dim3(grid), kThreads, smem, st, a, tab));
     return STA_OK;
   };
   if (nu == 16) return il ? go(norm_rope_kernel<T, 1, kPairs, 16, MODE>) : go(norm_rope_kernel<T, 1, kHalves, 16, MODE>);

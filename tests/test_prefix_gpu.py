@@ -184,6 +184,40 @@ def test_prefix_calls_that_read_what_the_last_one_wrote(dev, splits):
         assert torch.equal(chain(two[:1], False), want)
 
 
+@pytest.mark.parametrize("P", [16, 20])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefix_steps_one_after_the_other(dev, d, P):
+    # norms and the cache write, then the attention of what was written, whose results are the next step's queries; each of the
+    # kernels may start before the one before it has ended
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = SharedCase(d, [30, 1, 20], [640, 0, 960], [1] * 49 + [4, 2], [5 + 9 * i % 70 for i in range(51)], 8, 4, d, P)
+    x = c.dev(dev)
+    q, groups = x.pop("q"), {n: x.pop(n) for n in ("group_indptr_host", "prefix_host")}
+    hosts = {n: x.pop(n) for n in ("q_indptr_host", "kv_indptr_host")}
+    k, v = (torch.randn(q.shape[0], 4, d, device=dev).to(torch.bfloat16) for _ in "kv")
+    rope, w = sta.Rope(d), torch.rand(d, device=dev) + 0.5
+
+    def steps(wait):
+        at, cache = q, dict(x, k_pages=x["k_pages"].clone(), v_pages=x["v_pages"].clone())
+        for i in range(10):
+            at = sta.sta_norm_rope_append_paged(at, k.roll(i, 0), v.roll(i, 1), cache["k_pages"], cache["v_pages"],
+                                                *(cache[n] for n in ("page_indptr_dev", "page_indices_dev", "q_indptr_dev",
+                                                                     "kv_indptr_dev")), rope=rope, q_weight=w, k_weight=w)
+            if wait:
+                torch.cuda.synchronize()
+            at, _ = sta.sta_prefix_fwd_paged(q=at, **cache, **hosts, **groups, num_splits=i % 3)
+            if wait:
+                torch.cuda.synchronize()
+        return at
+
+    want = steps(True)
+    for _ in range(5):
+        assert torch.equal(steps(False), want)
+
+
 @pytest.mark.parametrize("splits", [0, 1, 4])
 def test_prefix_captured_and_replayed_with_other_lengths(dev, splits):
     import torch
