@@ -3,11 +3,14 @@
 // a shared prefix: some 40 us of host time a call through ctypes, whose kernels take as long).
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/pybind.h>
+
+#include <pybind11/numpy.h>
 
 #include <algorithm>
 #include <cmath>
@@ -139,14 +142,12 @@ struct On {
   }
 };
 
-Tensor scratch(size_t bytes, const Tensor& like) {
-  return fresh({(int64_t)bytes}, at::kByte, like);
-}
-void* workspace_at(const Maybe& given, size_t need, const Tensor& like, Tensor& own, size_t& bytes) {
+// Scratch of the current device's current stream, to which it goes back; without a tensor around it.
+void* workspace_at(const Maybe& given, size_t need, const Tensor& like, c10::DataPtr& own, size_t& bytes) {
   if (!given) {
-    own = scratch(need, like);
+    own = c10::cuda::CUDACachingAllocator::get()->allocate(need);
     bytes = need;
-    return own.data_ptr();
+    return own.get();
   }
   if (!(given->scalar_type() == at::kByte && given->is_contiguous() && given->device() == like.device()))
     refuse("workspace: contiguous uint8 on " + like.device().str());
@@ -192,7 +193,7 @@ std::tuple<Maybe, Maybe, Maybe, Maybe> norm_rope_bwd(const Maybe& dq_out, const 
   check("sta_norm_rope_bwd", sta_norm_rope_bwd(nullptr, nullptr, d, 0, nullptr, nullptr, d, 0, nullptr, nullptr, d, 0, nullptr,
                                                nullptr, nullptr, nullptr, 1.f, nullptr, nullptr, 0, 1, 0, d, STA_BF16, nullptr,
                                                &need, nullptr));
-  Tensor own;
+  c10::DataPtr own;
   void* ws = workspace_at(workspace, need, x, own, bytes);
   check("sta_norm_rope_bwd",
         sta_norm_rope_bwd(y.at, z.at, y.stride, z.stride, a.at, b.at, a.stride, b.stride, g.at, h.at, g.stride, h.stride, qw, kw,
@@ -236,45 +237,34 @@ Maybe norm_rope_append_paged(const Maybe& q, const Tensor& k, const Tensor& v, c
   return q_out;
 }
 
-// Host int32 values [n]: their address, kept alive by this object.
+// Host int32 values [n]: their address, kept alive by this object and the argument.
 struct HostInts {
+  using Array = py::array_t<int32_t, py::array::c_style>;
   const int32_t* at = nullptr;
-  Py_ssize_t n = 0;
-  Py_buffer view{};
-  bool viewed = false;
+  int64_t n = 0;
   py::object kept;
-  HostInts(py::handle x, Py_ssize_t want, const char* what) {
-    auto number = [&](py::handle o) {
-      if (PyObject_GetBuffer(o.ptr(), &view, PyBUF_C_CONTIGUOUS | PyBUF_FORMAT) != 0) {
-        PyErr_Clear();
-        return false;
-      }
-      viewed = true;
-      if (!(view.ndim == 1 && view.itemsize == 4 && view.format && (view.format[0] == 'i' || view.format[0] == 'l') && !view.format[1])) {
-        PyBuffer_Release(&view);
-        viewed = false;
-        return false;
-      }
-      at = static_cast<const int32_t*>(view.buf);
-      n = view.shape[0];
+  HostInts(py::handle x, int64_t want, const char* what) {
+    auto numbers = [&](py::handle o) {
+      if (!Array::check_(o)) return false;
+      const auto& a = reinterpret_cast<const py::array&>(o);
+      if (a.ndim() != 1) return false;
+      at = static_cast<const int32_t*>(a.data());
+      n = a.shape(0);
       return true;
     };
-    if (THPVariable_Check(x.ptr()) && THPVariable_Unpack(x.ptr()).scalar_type() == at::kInt && THPVariable_Unpack(x.ptr()).is_cpu() &&
-        THPVariable_Unpack(x.ptr()).is_contiguous() && THPVariable_Unpack(x.ptr()).dim() == 1) {
+    if (THPVariable_Check(x.ptr())) {
       const Tensor& t = THPVariable_Unpack(x.ptr());
-      at = t.data_ptr<int32_t>();
-      n = t.size(0);
-    } else if (THPVariable_Check(x.ptr()) || !number(x)) {
-      py::module_ np = py::module_::import("numpy");
-      kept = np.attr("ascontiguousarray")(x, py::arg("dtype") = np.attr("int32"));
-      if (!number(kept)) refuse(std::string(what) + ": a list of whole numbers");
+      if (t.scalar_type() == at::kInt && t.is_cpu() && t.is_contiguous() && t.dim() == 1) {
+        at = t.data_ptr<int32_t>();
+        n = t.size(0);
+      }
+    }
+    if (!at && !numbers(x)) {
+      kept = py::module_::import("numpy").attr("ascontiguousarray")(x, py::arg("dtype") = "int32");
+      if (!numbers(kept)) refuse(std::string(what) + ": a list of whole numbers");
     }
     if (want < 1 || n != want) refuse(std::string(what) + ": " + std::to_string(want) + " values, at least one");
   }
-  ~HostInts() {
-    if (viewed) PyBuffer_Release(&view);
-  }
-  HostInts(const HostInts&) = delete;
 };
 
 std::tuple<Tensor, Tensor> prefix_fwd_paged(const Tensor& q, const Tensor& k_pages, const Tensor& v_pages,
@@ -313,7 +303,7 @@ std::tuple<Tensor, Tensor> prefix_fwd_paged(const Tensor& q, const Tensor& k_pag
     refuse("lse: contiguous float32 [n, Hq]");
   // scratch for 16 pieces a row, which does for most calls; one that needs more says how much
   size_t bytes = 0;
-  Tensor own;
+  c10::DataPtr own;
   void* ws = workspace_at(workspace, workspace ? 256 : std::max<int64_t>(256, std::min<int64_t>(16 * rows * Hq * (d + 2) * 4, 1 << 26)), q,
                           own, bytes);
   auto call = [&]() {

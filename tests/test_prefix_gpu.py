@@ -184,6 +184,30 @@ def test_prefix_calls_that_read_what_the_last_one_wrote(dev, splits):
         assert torch.equal(chain(two[:1], False), want)
 
 
+def test_prefix_host_values_of_any_kind(dev):
+    import array
+
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = SharedCase(20, [3, 2], [256, 128], [1, 2, 1, 1, 4], [5, 20, 9, 30, 7], 4, 2, 64, 16)
+    x, names = c.dev(dev), ("q_indptr_host", "kv_indptr_host", "group_indptr_host", "prefix_host")
+    host = {n: np.asarray(x.pop(n)) for n in names}
+    want = sta.sta_prefix_fwd_paged(**x, **host, num_splits=1)
+    strided = lambda a: np.repeat(a, 2)[::2]  # noqa: E731
+    for kind in (list, tuple, torch.from_numpy, lambda a: torch.from_numpy(a).long(), lambda a: a.astype(np.int64), strided,
+                 lambda a: array.array("i", a.tolist()), lambda a: memoryview(a)):
+        got = sta.sta_prefix_fwd_paged(**x, **{n: kind(a) for n, a in host.items()}, num_splits=1)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for name in names:
+        for bad in (lambda a: a[:-1], lambda a: np.concatenate([a, a[-1:]]), lambda a: np.stack([a, a]), lambda a: a[:0]):
+            with pytest.raises((ValueError, sta.StaError)):
+                sta.sta_prefix_fwd_paged(**x, **dict(host, **{name: bad(host[name])}))
+        with pytest.raises(TypeError):
+            sta.sta_prefix_fwd_paged(**x, **dict(host, **{name: torch.from_numpy(host[name]).to(dev)}))
+
+
 @pytest.mark.parametrize("P", [16, 20])
 @pytest.mark.parametrize("d", [64, 128])
 def test_prefix_steps_one_after_the_other(dev, d, P):
