@@ -48,7 +48,7 @@
 // alone 222; 17.5 are the cache once at copy speed): 5 or so until the first tiles are there, 20 for 85 CTAs' runs of 17 tiles of
 // 16 keys and, beside them, 64 items of 8 key tiles of the prefix, and the merge. 120 forks of 32768 tokens: 83 (1380 alone; 58.6 the cache, 0.40
 // GB of DRAM reads counted). Questions of up to 1024 tokens behind a document of 12000: 576 (612; 439 at cuBLAS' rate), 77 % of the tensor
-// pipe in the attention's 522, and 49 of the merge, which reads 136 MB of partials. With heads of 32 / 8, 128 elements each.
+// pipe in the attention's 522, and 35 of the merge, which reads 136 MB of partials. With heads of 32 / 8, 128 elements each.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -1499,10 +1499,14 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
 // Four merged rows a warp: a rank's own partials, and before them its prefix's. Lane (eighth x of 4, row y of 4, half z):
 // 16 bytes of its row's eighths x, x + 4, .., so that four rows side by side are whole lines. It starts as the first
 // kernel's CTAs end, finds its rows, then waits for the last of them.
-template <int D, int CAP>
-__global__ void __launch_bounds__(128) chunk_merge_shared_kernel(const __grid_constant__ ChunkArgs A,
-                                                                 const __grid_constant__ Plan<CAP, true> P, int req0, int n_rows) {
-  constexpr int NV = D / 32, U = 4;  // 16-byte parts of a lane, partials on their way
+// U partials of a row are on their way at once: 4, or 2 with twice the warps, for more rows than the SMs take at once otherwise
+// that have three partials or fewer on average (132224 rows of two 35 us, 49 by four; calls of 16384 rows of more 67 us, 64
+// by four, of 2048 rows 45.7 and 37.3).
+template <int D, int CAP, int U>
+__global__ void __launch_bounds__(128, U == 2 ? 8 : 1) chunk_merge_shared_kernel(const __grid_constant__ ChunkArgs A,
+                                                                                 const __grid_constant__ Plan<CAP, true> P, int req0,
+                                                                                 int n_rows) {
+  constexpr int NV = D / 32;  // 16-byte parts of a lane
   const int lane = threadIdx.x & 31, z = lane & 1, sub = (lane >> 3) * 2 + z;  // sub: of the 8 lanes of a row
   grid_go();
   const int64_t mr = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * 4 + ((lane >> 1) & 3);
@@ -1547,6 +1551,18 @@ __global__ void __launch_bounds__(128) chunk_merge_shared_kernel(const __grid_co
     const int64_t c = (int64_t)(i < na ? i : i - na) * p.rows;  // rows of the chunks before
     return *reinterpret_cast<const float4*>(A.part_o + p.values(D, (lane >> 3) + 4 * v) + c * D + z * 4);
   };
+  float4 x[U][NV];
+  float w[U];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      w[u] = lse_at(i0 + u);
+      if (i0 + u < s)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) x[u][v] = value(i0 + u, v);
+    }
+  };
+  load(0);  // (before the maximum is known)
   float M = -INFINITY;
   for (int i = sub; i < most; i += 8) M = fmaxf(M, lse_at(i));
 #pragma unroll
@@ -1556,15 +1572,7 @@ __global__ void __launch_bounds__(128) chunk_merge_shared_kernel(const __grid_co
   for (int v = 0; v < NV; ++v) out[v] = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
   for (int i0 = 0; i0 < most; i0 += U) {
-    float4 x[U][NV];
-    float w[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      w[u] = lse_at(i0 + u);
-      if (i0 + u < s)
-#pragma unroll
-        for (int v = 0; v < NV; ++v) x[u][v] = value(i0 + u, v);
-    }
+    if (i0 > 0) load(i0);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (i0 + u < s && M != -INFINITY) {
@@ -2002,6 +2010,8 @@ sta_status plan_group(const ChunkArgs& a, const int32_t* qi, const int32_t* ki, 
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+constexpr unsigned kManyRows = 152 * 4;  // CTAs of the merge that an SM takes at once, with four partials on their way
+
 struct Maps {
   CUtensorMap q, k, v, k4, v4;  // k4, v4: boxes of 32 tokens, beside those of 8
   RowMaps<true> rows;
@@ -2060,7 +2070,9 @@ sta_status launch_group(const Maps& m, const ChunkArgs& a, const Group& g, cudaS
   }
   if (g.rows > 0) {
     if constexpr (SHARED) {
-      STA_CUDA_TRY(launch_early(chunk_merge_shared_kernel<D, CAP>, (unsigned)cdiv(g.rows, 16), 128, 0, st, a, p, g.r0, (int)g.rows));
+      const unsigned ctas = (unsigned)cdiv(g.rows, 16);
+      const auto merge = ctas > kManyRows && g.parts <= 3 * g.rows ? chunk_merge_shared_kernel<D, CAP, 2> : chunk_merge_shared_kernel<D, CAP, 4>;
+      STA_CUDA_TRY(launch_early(merge, ctas, 128, 0, st, a, p, g.r0, (int)g.rows));
     } else {
       chunk_merge_kernel<D, CAP><<<(unsigned)cdiv(g.rows, 8), 256, 0, st>>>(a, p, g.r0, (int)g.rows);
       STA_LAUNCH_CHECK();

@@ -85,6 +85,13 @@ def test_prefix_long_chunks(dev):
     _run(dev, c, splits=(0, 1, 5))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefix_many_rows_to_merge(dev, d):
+    # more rows than the merge has warps for at once; pieces of both kinds and requests without a prefix between them
+    c = SharedCase(22, [3, 1, 2], [320, 0, 192], [90, 1, 120, 60, 70, 3], [95, 30, 120, 80, 70, 200], 48, 6, d, 32)
+    _run(dev, c, splits=(0, 1, 3))
+
+
 def test_prefix_many_requests_in_several_launches(dev):
     # 1500 requests in groups of 1 to 400, which the launches' parts cut
     sizes = [400, 1, 300, 2, 397, 400]
