@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libsta.so")
 BIND = os.path.join(HERE, "_bind.so")  # some of the Python calls
 SOURCES = ["api.cu", "encode.cu", "mha_row.cu", "mha_block.cu", "decode.cu", "decode_noalloc.cu", "epilogue.cu", "validate.cu", "mla.cu",
            "diag.cu", "rope.cu", "norm_rope.cu", "chunk.cu", "pages.cu"]
-HEADERS = ["common.cuh", "internal.h", "ptx.cuh", "rope.inl"]
+HEADERS = ["common.cuh", "internal.h", "ptx.cuh", "rope.inl", "shares.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "rope.inl"
+#include "shares.h"
 
 namespace sta {
 namespace {
@@ -759,14 +760,8 @@ sta_status launch_norm(NormArgs& a, const RopeTable& tab, bool il, cudaStream_t 
   size_t smem = (size_t)kWarps * a.warp_bytes;
   unsigned grid;
   if (MODE == kBackward) {
-    // CTAs by the heads of q and k, one a tensor at least, and none without a piece for each of its warps
-    const int most = light ? kMaxGrid : kMaxGrid / 2;
     int n[2];
-    for (int g = 0; g < 2; ++g) {
-      int64_t share = (int64_t)(most * (double)a.pieces[g] / (double)pieces + 0.5);
-      share = std::max<int64_t>(1, a.pieces[1 - g] ? std::min<int64_t>(share, most - 1) : share);
-      n[g] = a.pieces[g] ? (int)std::min(share, cdiv(a.n_tokens * a.pieces[g], kWarps)) : 0;
-    }
+    norm_ctas(light ? kMaxGrid : kMaxGrid / 2, a.pieces, a.n_tokens, kWarps, n);
     a.ctas_q = n[0];
     ctas[0] = n[0];
     ctas[1] = n[1];

@@ -455,3 +455,24 @@ def test_norm_append_into_far_pages(dev):
     got = append(pages(big), x["page_indices_dev"] + 135000 - n)
     for a, b in zip(got, append(x, x["page_indices_dev"])):
         assert torch.equal(a[-n:].view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("n,Hq,Hk,d,rot,dtype", [(200, 31, 1, 256, 256, "f32"), (90, 25, 7, 256, 256, "f32"), (130, 27, 5, 256, 128, "bf16"),
+                                                 (300, 42, 21, 128, 64, "bf16"), (170, 29, 3, 256, 0, "bf16")])
+def test_norm_rope_gradients_stay_in_their_workspace(dev, n, Hq, Hk, d, rot, dtype):
+    # q's and k's shares of the CTAs end in one half: together they still have a row of scratch each
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = Case(dev, n, Hq, Hk, d, rot, False, dtype, seed=n, eps=1e-3)
+    need = 304 * d * 4
+    ws = torch.full((need + 8 * d * 4,), 255, dtype=torch.uint8, device=dev)
+    with pytest.raises(ValueError):
+        sta.sta_norm_rope_bwd(*c.dy, c.q, c.k, *c.args(), **c.kw_args(), workspace=ws[:need - 1])
+    got = sta.sta_norm_rope_bwd(*c.dy, c.q, c.k, *c.args(), **c.kw_args(), workspace=ws[:need])
+    assert (ws[need:] == 255).all()
+    for i, (x, w, dy) in enumerate(c.parts()):
+        dx, dw, tol, dw_tol = norm_bwd_ref(_np(dy), _np(x), _np(w), c.eps, c.pos.cpu().numpy(), c.f, c.il)
+        _close(got[i], dx, tol, c.step, "dx")
+        _close(got[2 + i], dw, dw_tol, F32_HALF_STEP, "dw")
