@@ -58,6 +58,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "shares.h"
 
 namespace sta {
 namespace {
@@ -443,11 +444,15 @@ struct RowCfg {
   static constexpr int KEYS = 16;              // of a tile
   static constexpr int KH = D / 64;            // 128-byte column blocks of a row
   static constexpr int HEAD = KEYS * 128;      // a head's part of such a block
-  static constexpr int BYTES = 192 * 1024;     // of the ring
-  static constexpr int MAX_STAGES = 16, WARPS = 8, PIECES = 4;
+  static constexpr int BYTES = kRowRing;
+  static constexpr int WARPS = 8, PIECES = 4;
+  static constexpr bool turns_divide_stages() {
+    for (int heads = 1; heads <= 8; ++heads)
+      if (row_stages(D, heads) % row_turns(heads)) return false;
+    return true;
+  }
+  static_assert(turns_divide_stages(), "see row_first");
 };
-constexpr int row_heads(int Hkv) { return Hkv < 8 ? Hkv : 8; }       // KV heads of a CTA
-constexpr int row_turns(int Hkv) { return 8 / row_heads(Hkv); }      // warps of a head
 
 // Partials beside shared prefixes: those of chunk c of a rank are [D / 8][rows][8], rows by KV head, token and head of the
 // group, so that the threads of a warp, a row each, write whole lines (a row's 512 bytes by one thread took an item of two
@@ -495,7 +500,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& A, const CUtensorMap& 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   RowShared& sh = *reinterpret_cast<RowShared*>(smem + C::BYTES);
   const int HB = row_heads(A.Hkv), turns = row_turns(A.Hkv), half = HB * C::KH * C::HEAD;  // K's or V's part of a stage
-  const int ST = min(C::MAX_STAGES, C::BYTES / (2 * half));
+  const int ST = row_stages(D, HB);
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(&sh.full[s], 2);
@@ -683,7 +688,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& A, const CUtensorMap& 
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     const int nt = p.j1 - p.j0;
-    for (int i = turn; i < nt; i += turns) {
+    for (int i = row_first(T, turn, turns); i < nt; i += turns) {
       const int j = p.j0 + i, tail = p.len - j * C::KEYS, st = (T + i) % ST;  // tail: keys of this tile
       if (!(ok = mbar_wait_warp(&sh.full[st], ((T + i) / ST) & 1u, A.err, 0x639))) break;
       const uint8_t* kt = smem + st * 2 * half + at_head;

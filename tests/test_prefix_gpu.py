@@ -401,3 +401,25 @@ def test_a_forked_batch_is_served_together(dev):
     for _ in range(3):
         step(np.ones(n, np.int64), L // P * P)
     assert sta.sta_device_error() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 1, 128), (16, 2, 128), (4, 1, 64), (8, 2, 64), (12, 3, 128), (8, 4, 128)])
+@pytest.mark.parametrize("own", [(40, 40, 40, 200), (17, 100, 33, 260), (1, 16, 1, 16, 1, 16, 700)])
+def test_prefix_short_own_parts_before_long_ones(dev, Hq, Hkv, d, own):
+    # several warps a head: some have no tile of the short pieces, and come first to the long ones, past the ring's first turn
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    n = 8 * len(own)
+    c = SharedCase(23, [n], [512], [1] * n, list(own) * 8, Hq, Hkv, d, 16)
+    x, scale = c.dev(dev), 1 / math.sqrt(d)
+    ref, cold = c.ref(scale), torch.empty(1 << 28, dtype=torch.uint8, device=dev)
+    for splits in (0, 1, 2):
+        first = None
+        for _ in range(4):
+            cold.fill_(1)  # K and V come from memory, the lists too
+            got = sta.sta_prefix_fwd_paged(**x, scale=scale, num_splits=splits)
+            check_chunk(*got, ref, n, f"{splits}")
+            first = first or got
+            assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])

@@ -33,3 +33,35 @@ def test_the_backward_norms_have_a_row_of_scratch_for_each_cta(tmp_path):
         }
 """)
     assert out == "", out[:400]
+
+
+def test_a_warp_of_few_rows_has_read_a_stage_before_it_waits_for_the_next_tile_there(tmp_path):
+    # a wait for phase n of a stage passes while phase n - 1 is still open: a warp may wait for tile t of the run only where it
+    # has waited for tile t - stages itself. Each tile by one warp of a head, whatever the pieces' lengths.
+    out = _run(tmp_path, """
+  unsigned seed = 1;
+  for (int d : {64, 128})
+    for (int Hkv = 1; Hkv <= 12; ++Hkv) {
+      const int turns = row_turns(Hkv), stages = row_stages(d, row_heads(Hkv));
+      if (stages < 2 || stages * row_heads(Hkv) * d * 64 > kRowRing) std::printf("%d heads of %d: %d stages\\n", Hkv, d, stages);
+      for (int round = 0; round < 200; ++round) {
+        int by[4096] = {}, n = 0;  // warp of a tile, + 1
+        for (int piece = 0; piece < 20 && n < 3000; ++piece) {
+          seed = seed * 1664525u + 1013904223u;
+          const int tiles = (seed >> 16) % (round % 3 ? 5 : 40);
+          for (int turn = 0; turn < turns; ++turn)
+            for (int i = row_first((unsigned)n, turn, turns); i < tiles; i += turns) {
+              if (i < 0 || by[n + i]) std::printf("%d heads of %d: tile %d taken twice\\n", Hkv, d, n + i);
+              by[n + i] = turn + 1;
+            }
+          n += tiles;
+        }
+        for (int t = 0; t < n; ++t) {
+          if (!by[t]) std::printf("%d heads of %d: tile %d by none\\n", Hkv, d, t);
+          if (t >= stages && by[t] != by[t - stages])
+            std::printf("%d heads of %d: tile %d by warp %d, the one before it in its stage by %d\\n", Hkv, d, t, by[t], by[t - stages]);
+        }
+      }
+    }
+""")
+    assert out == "", out[:400]
