@@ -33,6 +33,14 @@ void check(const char* fn, sta_status status) {
   if (status != STA_OK) py::module_::import("split_kv_decode_bsr_gb300").attr("_check")(fn, status);
 }
 
+// A call of the library without the interpreter's lock, as through ctypes: where the stream has no room for another launch it
+// waits, and other threads, and what the stream may be waiting for in one of them, go on.
+template <class F>
+sta_status unlocked(const F& call) {
+  py::gil_scoped_release free;
+  return call();
+}
+
 void on_cuda(const Tensor& t) {
   if (!t.is_cuda()) refuse("tensors must be on a CUDA device, not " + t.device().str());
 }
@@ -167,8 +175,10 @@ std::tuple<Maybe, Maybe> norm_rope(const Maybe& q, const Maybe& k, const Maybe& 
   const float *qw = norm_weight(q_weight, "q_weight", x), *kw = norm_weight(k_weight, "k_weight", x);
   On on(x);
   const Heads c = result(q_out, q, "q_out"), d = result(k_out, k, "k_out");
-  check("sta_norm_rope", sta_norm_rope(a.at, b.at, a.stride, b.stride, c.at, d.at, c.stride, d.stride, qw, kw, (float)eps, pos,
-                                       turn, x.size(0), a.H, b.H, (int)x.size(2), code, on.stream));
+  check("sta_norm_rope", unlocked([&] {
+    return sta_norm_rope(a.at, b.at, a.stride, b.stride, c.at, d.at, c.stride, d.stride, qw, kw, (float)eps, pos, turn, x.size(0),
+                         a.H, b.H, (int)x.size(2), code, on.stream);
+  }));
   return {q_out, k_out};
 }
 
@@ -195,10 +205,11 @@ std::tuple<Maybe, Maybe, Maybe, Maybe> norm_rope_bwd(const Maybe& dq_out, const 
                                                &need, nullptr));
   c10::DataPtr own;
   void* ws = workspace_at(workspace, need, x, own, bytes);
-  check("sta_norm_rope_bwd",
-        sta_norm_rope_bwd(y.at, z.at, y.stride, z.stride, a.at, b.at, a.stride, b.stride, g.at, h.at, g.stride, h.stride, qw, kw,
-                          dqw ? dqw->data_ptr<float>() : nullptr, dkw ? dkw->data_ptr<float>() : nullptr, (float)eps, pos,
-                          turn, x.size(0), a.H, b.H, d, code, ws, &bytes, on.stream));
+  float *dqw_at = dqw ? dqw->data_ptr<float>() : nullptr, *dkw_at = dkw ? dkw->data_ptr<float>() : nullptr;
+  check("sta_norm_rope_bwd", unlocked([&] {
+    return sta_norm_rope_bwd(y.at, z.at, y.stride, z.stride, a.at, b.at, a.stride, b.stride, g.at, h.at, g.stride, h.stride, qw, kw,
+                             dqw_at, dkw_at, (float)eps, pos, turn, x.size(0), a.H, b.H, d, code, ws, &bytes, on.stream);
+  }));
   return {dq, dk, dqw, dkw};
 }
 
@@ -230,10 +241,12 @@ Maybe norm_rope_append_paged(const Maybe& q, const Tensor& k, const Tensor& v, c
   if (q_out && !(q && q_out->is_contiguous())) refuse("q_out: contiguous, q's shape");
   On on(k);
   const Heads c = result(q_out, q, "q_out");
-  check("sta_norm_rope_append_paged",
-        sta_norm_rope_append_paged(a.at, k.data_ptr(), v.data_ptr(), a.stride, ks, vs, c.at, k_pages.data_ptr(),
-                                   v_pages.data_ptr(), (int)k_pages.size(1), (int)k_pages.size(0), pp, pi, qp, kp, pos, qw, kw,
-                                   (float)eps, params(rope), n, (int)n_req, a.H, (int)Hkv, (int)d, STA_BF16, on.stream));
+  const sta_rope_params* turn = params(rope);
+  check("sta_norm_rope_append_paged", unlocked([&] {
+    return sta_norm_rope_append_paged(a.at, k.data_ptr(), v.data_ptr(), a.stride, ks, vs, c.at, k_pages.data_ptr(), v_pages.data_ptr(),
+                                      (int)k_pages.size(1), (int)k_pages.size(0), pp, pi, qp, kp, pos, qw, kw, (float)eps, turn, n,
+                                      (int)n_req, a.H, (int)Hkv, (int)d, STA_BF16, on.stream);
+  }));
   return q_out;
 }
 
@@ -311,11 +324,11 @@ std::tuple<Tensor, Tensor> prefix_fwd_paged(const Tensor& q, const Tensor& k_pag
                                 pp, pi, qp, qh.at, kp, kh.at, (int)n_req, gh.at, ph.at, (int)n_groups, (int)Hq, (int)k_pages.size(2),
                                 (int)d, code, by, num_splits, o->data_ptr(), lse->data_ptr<float>(), ws, &bytes, on.stream);
   };
-  sta_status status = call();
+  sta_status status = unlocked(call);
   if (status == STA_ERR_WORKSPACE) {
     const size_t need = bytes;
     ws = workspace_at(workspace, need, q, own, bytes);
-    status = call();
+    status = unlocked(call);
   }
   check("sta_prefix_fwd_paged", status);
   return {*o, *lse};
