@@ -746,6 +746,22 @@ class Rope:
         at every call)."""
         return self._bytes if self._struct is None else bytes(self._struct)
 
+    def __getstate__(self):
+        """What a copy is made of: the parameters without their address of the speeds, and the speeds."""
+        p = _RopeParams.from_buffer_copy(self.packed())
+        if (p.freqs or 0) != (C.addressof(self._freqs) if self._freqs else 0):
+            raise ValueError("freqs: an address that is not this Rope's cannot be copied")
+        p.freqs = None
+        return dict(self.__dict__, _bytes=bytes(p), _struct=None, _freqs=None if self._freqs is None else list(self._freqs))
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        if self._freqs is not None:
+            self._freqs = (C.c_double * len(self._freqs))(*self._freqs)
+            p = _RopeParams.from_buffer_copy(self._bytes)
+            p.freqs = C.addressof(self._freqs)
+            self._bytes = bytes(p)
+
 
 def _heads_view(t: torch.Tensor, what: str):
     """[n, H, d] with contiguous heads: the token stride."""
