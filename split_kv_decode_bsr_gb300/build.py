@@ -60,6 +60,15 @@ def _bind_commands(obj: str, out: str):
     return cc, ld
 
 
+def _bind_made_for(cc) -> str:
+    """What _bind.so was compiled for: its classes are those of this torch's headers, its name's form is this Python's."""
+    import sysconfig
+
+    import torch
+
+    return "\n".join([torch.__version__, str(sysconfig.get_config_var("SOABI")), " ".join(cc)])
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "sta.h")]
@@ -71,7 +80,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             jobs.append([nvcc(), *_flags(extra_flags), "-c", s, "-o", o])
     bind_obj, bind_tmp = os.path.join(BUILD, "bind.o"), BIND + f".tmp{os.getpid()}"
     cc, ld = _bind_commands(bind_obj, bind_tmp)
-    if force or _stale(bind_obj, [os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "sta.h")]):
+    key_file, key = os.path.join(BUILD, "bind.key"), _bind_made_for(cc)
+    made_for = ""
+    if os.path.exists(key_file):
+        with open(key_file, encoding="utf-8") as f:
+            made_for = f.read()
+    if force or made_for != key or _stale(bind_obj, [os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "sta.h")]):
         jobs.append(cc)
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
@@ -96,6 +110,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link of _bind.so failed")
         os.replace(bind_tmp, BIND)
+        with open(key_file, "w", encoding="utf-8") as f:
+            f.write(key)
     return LIB
 
 
