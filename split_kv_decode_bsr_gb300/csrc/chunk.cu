@@ -193,6 +193,14 @@ __host__ __device__ inline int tile_list(const Seen& s, int& gt, int& wl) {
   return gt + (wh >= wl ? wh - wl + 1 : 0);
 }
 
+// A word of the lists and lengths. As a constant (__ldg) only where the launch does not start before the one before it has
+// ended, which may have written it.
+template <bool SHARED>
+__device__ __forceinline__ int32_t list_word(const int32_t* p) {
+  if constexpr (SHARED) return *p;
+  else return __ldg(p);
+}
+
 template <int CAP, bool SHARED>
 __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP, SHARED>& P, int req0, int item, Item& it) {
   int lo = 0, hi = P.n;
@@ -215,10 +223,10 @@ __device__ __forceinline__ bool get_item(const ChunkArgs& A, const Plan<CAP, SHA
     q_end = req0 + k.end;
     if (k.pre == -2) kr = req0 + k.lead;
   }
-  const int q0 = __ldg(A.q_indptr + it.r), q1 = __ldg(A.q_indptr + q_end);
-  int64_t len = (int64_t)__ldg(A.kv_indptr + kr + 1) - __ldg(A.kv_indptr + kr);
-  it.pb = __ldg(A.page_indptr + kr);  // (with the lengths, not later by the loaders: a 2048-token prompt 36 us, 39)
-  it.pe = __ldg(A.page_indptr + kr + 1);
+  const int q0 = list_word<SHARED>(A.q_indptr + it.r), q1 = list_word<SHARED>(A.q_indptr + q_end);
+  int64_t len = (int64_t)list_word<SHARED>(A.kv_indptr + kr + 1) - list_word<SHARED>(A.kv_indptr + kr);
+  it.pb = list_word<SHARED>(A.page_indptr + kr);  // (with the lengths, not later by the loaders: a 2048-token prompt 36 us, 39)
+  it.pe = list_word<SHARED>(A.page_indptr + kr + 1);
   int n = q1 - q0;
   int64_t pos0 = len - n;
   if constexpr (SHARED) {
@@ -546,7 +554,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& A, const CUtensorMap& 
       ++lo;
       from = to;
       const int32_t* in = lane < 2 ? A.q_indptr : (lane < 4 ? A.kv_indptr : A.page_indptr);
-      return lane < 6 ? __ldg(in + req0 + k.req + (lane & 1)) : 0;
+      return lane < 6 ? list_word<true>(in + req0 + k.req + (lane & 1)) : 0;
     };
     auto settle = [&](Piece& p, int loaded) {
       const int q0 = __shfl_sync(0xffffffffu, loaded, 0), q1 = __shfl_sync(0xffffffffu, loaded, 1);
@@ -601,7 +609,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& A, const CUtensorMap& 
       // A lane holds one entry of the page list, and one of the 32 after them; -1 behind the list.
       auto entry = [&](int e) -> int {
         const int o = p.pb + e;
-        return o >= 0 && o < p.pe && (int64_t)e * P0 < p.len && A.page_indices ? __ldg(A.page_indices + o) : -1;
+        return o >= 0 && o < p.pe && (int64_t)e * P0 < p.len && A.page_indices ? list_word<true>(A.page_indices + o) : -1;
       };
       int window = page_no(p.j0 * C::KEYS), pages = -1, later = -1;
       if (p.j0 < p.j1) {
@@ -936,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto page_at = [&](int tok) -> int {  // list entry of a token, unchecked; -1 behind the list
       const int o = pb + page_no(tok);
-      return o >= 0 && o < pe && A.page_indices ? __ldg(A.page_indices + o) : -1;
+      return o >= 0 && o < pe && A.page_indices ? list_word<SHARED>(A.page_indices + o) : -1;
     };
     auto row_at = [&](int page, int tok) -> int {  // cache row; a page outside the cache reads page 0
       if (page < 0 || page >= A.n_pages) {
@@ -1525,21 +1533,21 @@ __global__ void __launch_bounds__(128, U == 2 ? 8 : 1) chunk_merge_shared_kernel
   const Rank k = rank_of(P, lo);
   const int y = some ? (int)mr - (lo > 0 ? P.rows[lo - 1] : 0) : 0, r = req0 + k.req;
   const int g = y % A.G, ht = y / A.G, hk = ht / k.qn, t = ht - hk * k.qn;
-  const int q0 = __ldg(A.q_indptr + r), n = __ldg(A.q_indptr + r + 1) - q0;
+  const int q0 = list_word<true>(A.q_indptr + r), n = list_word<true>(A.q_indptr + r + 1) - q0;
   some = some && q0 >= 0 && t < n && q0 <= A.N - min(n, k.qn);
   SharedPart own(k, A.Hq, A.G, 0, hk, t, g), pre = own;
   int na = 0;  // the prefix's partials
   if (k.pre >= 0) {
     const Rank kp = rank_of(P, k.pre);
-    const int64_t tg = (int64_t)q0 + t - __ldg(A.q_indptr + req0 + kp.req);  // its token of the group's
+    const int64_t tg = (int64_t)q0 + t - list_word<true>(A.q_indptr + req0 + kp.req);  // its token of the group's
     some = some && tg >= 0 && tg < kp.qn;
     if (some) pre = SharedPart(kp, A.Hq, A.G, 0, hk, (int)tg, g);
     na = kp.ns;
     if (some && y == 0 && sub == 0) {  // the request's list holds the pages that were read for it
       const int e = k.skip / A.page_size - 1, lead = req0 + k.lead;
-      const int a = __ldg(A.page_indptr + r) + e, b = __ldg(A.page_indptr + lead) + e;
-      if (a < 0 || a >= __ldg(A.page_indptr + r + 1) || b < 0 || b >= __ldg(A.page_indptr + lead + 1) ||
-          __ldg(A.page_indices + a) != __ldg(A.page_indices + b))
+      const int a = list_word<true>(A.page_indptr + r) + e, b = list_word<true>(A.page_indptr + lead) + e;
+      if (a < 0 || a >= list_word<true>(A.page_indptr + r + 1) || b < 0 || b >= list_word<true>(A.page_indptr + lead + 1) ||
+          list_word<true>(A.page_indices + a) != list_word<true>(A.page_indices + b))
         record_error(A.err, 0x609);
     }
   }

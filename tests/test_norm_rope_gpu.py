@@ -476,3 +476,41 @@ def test_norm_rope_gradients_stay_in_their_workspace(dev, n, Hq, Hk, d, rot, dty
         dx, dw, tol, dw_tol = norm_bwd_ref(_np(dy), _np(x), _np(w), c.eps, c.pos.cpu().numpy(), c.f, c.il)
         _close(got[i], dx, tol, c.step, "dx")
         _close(got[2 + i], dw, dw_tol, F32_HALF_STEP, "dw")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,Hq", [(48, 16), (3000, 8)])
+def test_norm_rope_by_weights_that_the_last_call_wrote(dev, n, Hq, dtype):
+    # each step's weights are the gradient of the step before, in one place; a kernel may start before the one that writes them
+    # has ended
+    import ctypes as C
+
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    d = 128
+    c = Case(dev, n, Hq, 0, d, d, False, dtype)
+    w, x = torch.empty(d, device=dev), torch.empty(n, Hq, d, device=dev, dtype=c.dt)
+    ws, size = torch.empty(304 * d * 4, dtype=torch.uint8, device=dev), C.c_size_t(304 * d * 4)
+    dx, P = torch.empty_like(x), lambda t: C.c_void_p(t.data_ptr())  # noqa: E731
+    code = sta.STA_BF16 if dtype == "bf16" else sta.STA_F32
+
+    def chain(wait):
+        x.copy_(c.q)
+        w.copy_(c.qw)
+        for i in range(20):
+            sta.sta_norm_rope(x, None, *c.args(), q_weight=w, q_out=x)
+            if wait:
+                torch.cuda.synchronize()
+            assert sta.lib().sta_norm_rope_bwd(P(c.dy[0]), None, Hq * d, 0, P(x), None, Hq * d, 0, P(dx), None, Hq * d, 0, None, None,
+                                               P(w), None, 1e-6, P(c.pos), C.byref(c.rope.struct), n, Hq, 0, d, code, P(ws),
+                                               C.byref(size), C.c_void_p(torch.cuda.current_stream().cuda_stream)) == sta.STA_OK
+            if wait:
+                torch.cuda.synchronize()
+        return x.clone(), w.clone()
+
+    want = chain(True)
+    assert torch.isfinite(want[0]).all() and torch.isfinite(want[1]).all()
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
