@@ -1842,7 +1842,9 @@ double plan_items(const ChunkArgs& a, std::vector<Req>& reqs, bool shared, int s
     }
     all.push_back(Same{tiles, 0.5 * (q.first + q.last), q.units, q.n, q.pre != -1});
   }
-  auto chunks = [&](int tiles, int piece) { return std::min(kMaxAuto, std::max(1, (tiles + piece - 1) / piece)); };
+  auto chunks = [&](int tiles, int piece) {  // (piece is 0 where no token sees a key)
+    return std::min(kMaxAuto, std::max(1, (tiles + piece - 1) / std::max(1, piece)));
+  };
   auto estimate = [&](int piece) {
     constexpr int kBins = 32;
     double work = 0, longest = 0;

@@ -194,3 +194,22 @@ def test_chunk_nan_query_under_a_window(dev, new, kv, Hq, Hkv, win, sinks, d, sp
     assert o[new - 1, 0].isnan().all() and lse[new - 1, 0].isnan()
     o[new - 1, 0], lse[new - 1, 0] = clean[new - 1, 0], clean_lse[new - 1, 0]
     assert o.equal(clean) and lse.equal(clean_lse)
+
+
+@pytest.mark.parametrize("kv,pattern", [([1, 2, 9], dict(win_lo=5, win_hi=9)), ([0, 0, 0], {}), ([0, 2, 0], {}), ([40, 300, 2], dict(win_lo=1, win_hi=9))])
+def test_chunks_of_which_no_token_sees_a_key(dev, kv, pattern):
+    # nothing for the plan to cut
+    import torch
+
+    import split_kv_decode_bsr_gb300 as sta
+
+    c = PagedCase(5, [1, 2, 3], kv, 8, 2, 64, 16, spare_entries=1)
+    x = c.dev(dev)
+    got = sta.sta_chunk_fwd_paged(**x, pattern=sta.MaskSource.pattern(causal=True, **pattern) if pattern else None)
+    torch.cuda.synchronize()
+    o, lse = got
+    alone = torch.isneginf(lse).all(1)
+    for row, r in enumerate(np.repeat(np.arange(3), c.new)):
+        if pattern or kv[r] == 0:
+            assert alone[row] and (o[row] == 0).all()
+    assert torch.isfinite(o).all() and sta.sta_device_error(reset=True) == 0
