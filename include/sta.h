@@ -518,7 +518,8 @@ sta_status sta_rope(const void* x, void* y, const int32_t* positions_dev, const 
  *              may be NULL
  *   d          2 .. 512; Hq, Hk 0 .. 65536; dtype STA_BF16 or STA_F32
  * Any d, rot_dim and stride is taken; 16-byte vectors are used where heads and strides are
- * whole numbers of them on 16-byte boundaries, single elements else (several times the time).
+ * whole numbers of them on 16-byte boundaries, single elements else (15 times the time
+ * forward and 26 times backward for 8192 tokens of 40 heads of 128 in bf16).
  * n_tokens == 0 launches nothing. One launch, asynchronous on `stream`. */
 sta_status sta_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, void* q_out, void* k_out,
                          int64_t q_out_stride, int64_t k_out_stride, const float* q_weight, const float* k_weight,

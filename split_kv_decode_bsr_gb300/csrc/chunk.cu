@@ -484,7 +484,9 @@ struct RowMaps<true> {
 
 // The launches with shared prefixes may start while the one before them ends. grid_wait(): it has ended, and what it wrote is
 // there. grid_go(): the next one may start (when all CTAs have come here). The first kernel touches no memory of the
-// call before its wait, and lets the merge start after it, since that looks its rows up before its own.
+// call before its wait, and lets the merge start after it, since that looks its rows up before its own: what wrote the lists and
+// lengths has ended before the merge begins. The merge lets the next launch start at once, beside the first kernel's last
+// CTAs; that launch waits for the merge's end, which comes after theirs.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

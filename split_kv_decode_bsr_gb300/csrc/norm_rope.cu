@@ -18,7 +18,7 @@
 // 168 MB it has to move where a copy reaches 6.78 (24.7 us); HBM, with 64 % of the issue slots taken. Backward 51.5 us
 // (37.1 at copy speed): 125 registers allow 16 warps an SM, which take 58 % of the issue slots, and each waits for its
 // loads, its sums' shuffles and its results in turn (3 CTAs an SM spill: 84; 20 warps with the weights in shared memory 54). The 11975 tokens of 24 prompts, 32 + 4 + 4
-// heads, into pages of 100: 45.9 (36.2). Small calls are the launch: 64 tokens into the cache 4.1 us, one step's norms 2.4.
+// heads, into pages of 100: 45.9 (36.2). Small calls are the launch: 64 tokens into the cache 4.0 us, one step's norms 2.5.
 #include <type_traits>
 
 #include "rope.inl"
